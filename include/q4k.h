@@ -68,7 +68,9 @@ typedef enum q4k_status {
   Q4K_ERR_ALIGNMENT = 2,      /* a pointer is not 16-byte aligned          */
   Q4K_ERR_UNSUPPORTED = 3,    /* a valid request this build does not serve */
   Q4K_ERR_CUDA = 4,           /* a CUDA runtime call or launch failed      */
-  Q4K_ERR_DEVICE_TIMEOUT = 5  /* a kernel gave up a bounded wait           */
+  Q4K_ERR_DEVICE_TIMEOUT = 5, /* a kernel gave up a bounded wait           */
+  Q4K_ERR_DEVICE_INDEX = 6    /* a kernel met an index, read from device
+                                 memory, that is out of its range          */
 } q4k_status;
 
 typedef enum q4k_layout {
@@ -536,11 +538,161 @@ int q6k_gemm_f16(const void* w, int layout, int64_t rows, int64_t cols,
 int q6k_gemm_blockdots(const void* w, int layout, int64_t rows, int64_t cols,
                        const int8_t* q8, int64_t tokens, int32_t* p, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The attention block between the projections: norms and rotation of the
+ * heads with the store into a paged key/value cache, attention over that
+ * cache, and low-rank adapters beside the projections.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the calls below. */
+typedef enum q4k_type {
+  Q4K_F16 = 0,                /* IEEE binary16 */
+  Q4K_BF16 = 1,               /* bfloat16      */
+  Q4K_F32 = 2                 /* IEEE binary32 */
+} q4k_type;
+
+/*
+ * q4k_kv_cache - a paged key/value cache (HOST struct, read during the call
+ * only).  k and v are device arrays [num_pages][kv_heads][page_size][head_dim]
+ * of `type`; cache slot s is the cell s % page_size of page s / page_size.
+ * A request's keys lie in the pages that its page table lists, in order; the
+ * caller owns and assigns the pages (the pages' engine keeps its KV pool
+ * allocated for the whole run, genie-ai-runtime §4 "Memory-first").
+ */
+typedef struct q4k_kv_cache {
+  void* k;
+  void* v;
+  int64_t num_pages;          /* num_pages * page_size < 2^31                  */
+  int32_t page_size;          /* 16, 32, 64, 128 or 256                        */
+  int32_t kv_heads;           /* 1..256                                        */
+  int32_t head_dim;           /* 64 or 128 (else Q4K_ERR_UNSUPPORTED)          */
+  int32_t type;               /* Q4K_F16 or Q4K_BF16                           */
+} q4k_kv_cache;
+
+/*
+ * q4k_qk_norm_rope - per-head RMS norm and position rotation of queries and
+ * keys, and the store of keys and values into the cache, in one pass over
+ * the projections' outputs.  For every head row x of q and k:
+ *   n = x / sqrt(mean(x^2) + eps) * weight        (weight NULL: n = x)
+ *   the first rot_dim values of n are rotated by the angles of pos[t]; pair i
+ *   is (n[i], n[i + rot_dim/2]), or (n[2i], n[2i+1]) if `interleaved`:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * in fp32, rounded once to the cache's type.  v is rounded only.
+ *   q        : float [tokens][heads][head_dim]
+ *   k, v     : float [tokens][kv_heads][head_dim]
+ *   q_weight, k_weight : float [head_dim], both or neither NULL
+ *   cos_sin  : float [max_pos][rot_dim]: rot_dim/2 cosines, then the sines
+ *   rot_dim  : a multiple of 8, 0..head_dim (0: no rotation; cos_sin and pos
+ *              may be NULL)
+ *   pos      : int32 [tokens], 0..max_pos-1
+ *   slot     : int32 [tokens], the cache slot of token t; negative: the
+ *              token's key and value are not stored (padding)
+ *   q_out    : [tokens][heads][head_dim] of the cache's type
+ * Two tokens with one slot leave either's values there.  A pos or slot out
+ * of range is reported by q4k_device_error (Q4K_ERR_DEVICE_INDEX): a token
+ * with a bad pos gets no output at all, one with a bad slot stores no key
+ * and value.  pos and slot need 4-byte alignment.
+ * Errors: Q4K_ERR_INVALID_ARG, Q4K_ERR_ALIGNMENT, Q4K_ERR_UNSUPPORTED
+ * (head_dim).  tokens == 0 enqueues nothing.
+ */
+int q4k_qk_norm_rope(const float* q, const float* k, const float* v, int64_t tokens, int heads,
+                     const q4k_kv_cache* cache, const float* q_weight, const float* k_weight,
+                     float eps, const float* cos_sin, int64_t max_pos, int rot_dim,
+                     int interleaved, const int32_t* pos, const int32_t* slot, void* q_out,
+                     void* stream);
+
+/*
+ * q4k_paged_attn - attention of the new tokens of n_req requests over the
+ * paged cache, causal: token i of the n_i new tokens of request r sits at
+ * position p = kv_len[r] - n_r + i (the cache already holds the new tokens'
+ * keys and values) and sees the keys j of request r with
+ *   j <= p   and, if window > 0,   j > p - window
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k[j][h']) v[j][h'],
+ * h' = h / (heads / kv_heads).  A token that sees no key (p < 0) gets zeros.
+ *   q          : [tokens][heads][head_dim] of the cache's type
+ *   page_table : int32 [n_req][max_pages]
+ *   cu_q       : int32 [n_req + 1], non-decreasing, cu_q[0] = 0,
+ *                cu_q[n_req] = tokens: request r has tokens cu_q[r] ..
+ *                cu_q[r+1]-1 (none is allowed)
+ *   kv_len     : int32 [n_req], keys of each request in the cache, the new
+ *                ones included, 0..max_pages * page_size
+ *   max_q      : an upper bound of the requests' new tokens (it shapes the
+ *                launch)
+ *   out        : [tokens][heads][head_dim] of out_type: the cache's type, or
+ *                Q4K_F32
+ *   workspace  : device memory of at least q4k_paged_attn_workspace_bytes()
+ *                bytes, 16-byte aligned, zero-filled before its first use;
+ *                each call leaves it ready for the next.  Calls that share a
+ *                workspace must not overlap on the GPU.
+ * Cells past kv_len and pages that no token sees may hold anything (NaN and
+ * infinities too); the keys and values that some token of a request sees
+ * must be finite.  A page index out of range where a key is needed reads as
+ * zeros, a cu_q or kv_len out of range is cut to its range, and each is
+ * reported by q4k_device_error (Q4K_ERR_DEVICE_INDEX).  page_table, cu_q and
+ * kv_len need 4-byte alignment.
+ * Accuracy: scores, softmax statistics and sums are fp32.  With fp32 out the
+ * weights keep 16 bits or more beside the values, |out - exact| <= 1e-5 *
+ * max(1, z / 64) * max_j |v_j| with z = max_j |scale| sum |q||k_j| (fp32
+ * scores of large z are themselves that far off); with 16-bit out the weights may be rounded to that type
+ * before they meet the values, as the result is after.
+ * Deterministic on one device: the same inputs give the same bits.
+ */
+size_t q4k_paged_attn_workspace_bytes(const q4k_kv_cache* cache, int heads, int64_t tokens,
+                                      int64_t n_req, int64_t max_q, int64_t max_pages,
+                                      int out_type);
+int q4k_paged_attn(const void* q, int64_t tokens, int heads, const q4k_kv_cache* cache,
+                   const int32_t* page_table, int64_t max_pages, const int32_t* cu_q,
+                   const int32_t* kv_len, int64_t n_req, int64_t max_q, float scale, int window,
+                   void* out, int out_type, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * q4k_lora_add - low-rank adapters of many requests added beside 1..4
+ * projections that share the input x (the QKV triple, the gate/up pair):
+ *   y_m[t] = base_m[t] + scale[a] * B_m[a] (A_m[a] x[t]),   a = adapter of t,
+ * or y_m[t] = base_m[t] for a token without one.
+ *   mats      : HOST array of n entries, read during the call only
+ *   rank      : a multiple of 8, 8..128 (pad smaller adapters with zeros)
+ *   type      : of the A and B, Q4K_F16 or Q4K_BF16
+ *   cols      : a positive multiple of 256
+ *   x         : float [tokens][cols]
+ *   order     : int32 [tokens], a permutation of the tokens that groups them
+ *               by adapter: segment s is order[seg_start[s]] ..
+ *               order[seg_start[s+1]-1], all of adapter seg_adapter[s]
+ *   seg_start : int32 [n_seg + 1], non-decreasing, 0 first and tokens last
+ *   seg_adapter : int32 [n_seg], 0..n_adapters-1, or negative for tokens
+ *               without an adapter
+ *   scale     : float [n_adapters]
+ *   workspace : device memory of at least q4k_lora_workspace_bytes() bytes,
+ *               16-byte aligned; it needs no clearing.  Calls that share a
+ *               workspace must not overlap on the GPU.
+ * fp32 sums, A and B entries exact: |y - exact| <= 1e-5 * (|base| + |scale|
+ * sum |B||A||x|).  Deterministic on one device.  An index out of range is
+ * skipped and reported by q4k_device_error (Q4K_ERR_DEVICE_INDEX): a token
+ * out of range gets no output, an adapter out of range counts as none.
+ * order, seg_start and seg_adapter need 4-byte alignment.
+ */
+typedef struct q4k_lora_mat {
+  const void* a;              /* [n_adapters][rank][cols]                      */
+  const void* b;              /* [n_adapters][rows][rank]                      */
+  const float* base;          /* float [tokens][rows]; NULL: zeros             */
+  float* y;                   /* float [tokens][rows]; may be base             */
+  int64_t rows;               /* a matrix with 0 rows is skipped               */
+} q4k_lora_mat;
+size_t q4k_lora_workspace_bytes(int n, int rank, int64_t tokens);
+int q4k_lora_add(int n, const q4k_lora_mat* mats, int64_t n_adapters, int rank, int type,
+                 int64_t cols, const float* x, int64_t tokens, const int32_t* order,
+                 const int32_t* seg_start, const int32_t* seg_adapter, int64_t n_seg,
+                 const float* scale, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * q4k_device_error - synchronise `stream` and read (then clear) the
  * library's device-side error word on the current device.  Returns Q4K_OK,
  * Q4K_ERR_DEVICE_TIMEOUT if a kernel abandoned a bounded wait since the last
- * read, or Q4K_ERR_CUDA if the synchronisation itself failed.
+ * read, Q4K_ERR_DEVICE_INDEX if none did but a kernel met an index out of
+ * range in device memory (a page, a cache slot, a position, a token, an
+ * adapter; it made no access with it), or Q4K_ERR_CUDA if the
+ * synchronisation itself failed.
  */
 int q4k_device_error(void* stream);
 

@@ -25,7 +25,8 @@ QK_K = 256
 QK_SUB = 32
 
 _STATUS = {0: "Q4K_OK", 1: "Q4K_ERR_INVALID_ARG", 2: "Q4K_ERR_ALIGNMENT",
-           3: "Q4K_ERR_UNSUPPORTED", 4: "Q4K_ERR_CUDA", 5: "Q4K_ERR_DEVICE_TIMEOUT"}
+           3: "Q4K_ERR_UNSUPPORTED", 4: "Q4K_ERR_CUDA", 5: "Q4K_ERR_DEVICE_TIMEOUT",
+           6: "Q4K_ERR_DEVICE_INDEX"}
 
 _P, _I64, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
 GEMV_SEQ_MAX_JOBS = 256
@@ -35,6 +36,17 @@ class GemvJob(ctypes.Structure):
     """``q4k_gemv_job`` of the C ABI (one GEMV of a ``q4k_gemv_seq`` list)."""
     _fields_ = [("w", _P), ("rows", _I64), ("cols", _I64), ("x", _P), ("residual", _P), ("y", _P),
                 ("wait", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    """``q4k_kv_cache`` of the C ABI (a paged key/value cache)."""
+    _fields_ = [("k", _P), ("v", _P), ("num_pages", _I64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class LoraMat(ctypes.Structure):
+    """``q4k_lora_mat`` of the C ABI (one projection of a ``q4k_lora_add`` call)."""
+    _fields_ = [("a", _P), ("b", _P), ("base", _P), ("y", _P), ("rows", _I64)]
 
 
 # Every symbol the header declares, with its ctypes signature.
@@ -71,6 +83,12 @@ SIGNATURES = {
     "q6k_gemm": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _I64, _P, _P]),
     "q6k_gemm_blockdots": (_I, [_P, _I, _I64, _I64, _P, _I64, _P, _P]),
     "q6k_gemm_f16": (_I, [_P, _I, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P]),
+    "q4k_qk_norm_rope": (_I, [_P, _P, _P, _I64, _I, _P, _P, _P, ctypes.c_float, _P, _I64, _I, _I, _P, _P, _P, _P]),
+    "q4k_paged_attn_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I64, _I64, _I64, _I64, _I]),
+    "q4k_paged_attn": (_I, [_P, _I64, _I, _P, _P, _I64, _P, _P, _I64, _I64, ctypes.c_float, _I, _P, _I, _P,
+                            ctypes.c_size_t, _P]),
+    "q4k_lora_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I64]),
+    "q4k_lora_add": (_I, [_I, _P, _I64, _I, _I, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, ctypes.c_size_t, _P]),
     "q4k_device_error": (_I, [_P]),
     "q4k_selftest_wait_timeout": (_I, [_P]),
     "q4k_status_string": (ctypes.c_char_p, [_I]),
@@ -531,6 +549,174 @@ def q4k_gemm_blockdots(w, rows: int, cols: int, q8, p=None, layout: int = BLOCK1
     return p
 
 
+_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}     # q4k_type
+
+
+def _kv_cache(k_cache, v_cache) -> KvCache:
+    if k_cache.dtype not in (torch.float16, torch.bfloat16) or k_cache.dim() != 4:
+        raise TypeError("k_cache must be a float16 or bfloat16 tensor [num_pages][kv_heads][page_size][head_dim]")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have one shape")
+    pages, kv_heads, page_size, dim = k_cache.shape
+    return KvCache(_ptr(k_cache, k_cache.dtype, "k_cache"), _ptr(v_cache, k_cache.dtype, "v_cache"), pages, page_size,
+                   kv_heads, dim, _TYPES[k_cache.dtype])
+
+
+def _count(t, n, name):
+    """A tensor of exactly ``n`` elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if t.numel() != n:
+        raise ValueError(f"{name} must hold {n} elements, got {t.numel()}")
+    return t
+
+
+def q4k_qk_norm_rope(q, k, v, k_cache, v_cache, pos, slot, cos_sin, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     interleaved: bool = False, q_out=None, stream=None):
+    """Per-head RMS norm and rotation of ``q`` and ``k``, and the store of
+    keys and values into the paged cache, in one pass.
+
+    ``q`` [tokens][heads * head_dim] and ``k``, ``v`` [tokens][kv_heads *
+    head_dim] float32 (2-D projection outputs, or 3-D with the heads apart);
+    ``k_cache``, ``v_cache`` [num_pages][kv_heads][page_size][head_dim]
+    float16 or bfloat16, written at the int32 ``slot`` [tokens] (negative: not
+    stored); ``cos_sin`` [max_pos][rot_dim] float32 (cosines, then sines), read
+    at the int32 ``pos`` [tokens], or None for no rotation; the weights
+    [head_dim] float32, or both None for no norm.  Returns the queries
+    [tokens][heads][head_dim] in the cache's type."""
+    cache = _kv_cache(k_cache, v_cache)
+    tokens, dim = q.shape[0], cache.head_dim
+    heads = q.shape[1] if len(q.shape) == 3 else q.shape[1] // dim
+    _count(q, tokens * heads * dim, "q")
+    _count(k, tokens * cache.kv_heads * dim, "k")
+    _count(v, tokens * cache.kv_heads * dim, "v")
+    _count(slot, tokens, "slot")
+    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    if rot:
+        _count(pos, tokens, "pos")
+    if q_weight is not None:
+        _count(q_weight, dim, "q_weight")
+        _count(k_weight, dim, "k_weight")
+    if q_out is None:
+        q_out = torch.empty((tokens, heads, dim), dtype=k_cache.dtype, device=q.device)
+    _count(q_out, q.numel(), "q_out")
+    _check(lib().q4k_qk_norm_rope(_ptr(q, torch.float32, "q"), _ptr(k, torch.float32, "k"),
+                                  _ptr(v, torch.float32, "v"), tokens, heads, ctypes.byref(cache),
+                                  _ptr(q_weight, torch.float32, "q_weight"),
+                                  _ptr(k_weight, torch.float32, "k_weight"), eps,
+                                  _ptr(cos_sin, torch.float32, "cos_sin"), max_pos, rot, interleaved,
+                                  _ptr(pos, torch.int32, "pos"), _ptr(slot, torch.int32, "slot"),
+                                  _ptr(q_out, k_cache.dtype, "q_out"), _stream(stream)), "q4k_qk_norm_rope")
+    return q_out
+
+
+def q4k_paged_attn_workspace(q, k_cache, page_table, max_q: int, out_dtype=torch.float32, tokens=None):
+    """A zeroed workspace for ``q4k_paged_attn`` calls of these shapes (``tokens``: in
+    place of ``q``'s, for the most tokens of any step)."""
+    cache = _kv_cache(k_cache, k_cache)
+    n_req, max_pages = page_table.shape
+    need = int(lib().q4k_paged_attn_workspace_bytes(ctypes.byref(cache), q.shape[1],
+                                                    q.shape[0] if tokens is None else tokens, n_req, max_q, max_pages,
+                                                    _TYPES[out_dtype]))
+    return torch.zeros(max(need, 16), dtype=torch.uint8, device=k_cache.device)
+
+
+def q4k_paged_attn(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int, scale=None, window: int = 0, out=None,
+                   out_dtype=torch.float32, workspace=None, stream=None):
+    """Causal attention of the new tokens ``q`` [tokens][heads][head_dim] (in
+    the cache's type) over the paged cache; returns ``out``
+    [tokens][heads][head_dim] of ``out_dtype`` (float32 or the cache's type).
+
+    Request r has the tokens ``cu_q[r]`` .. ``cu_q[r+1]-1`` (int32 [n_req+1]),
+    ``kv_len[r]`` keys with the new ones (int32) in the pages
+    ``page_table[r]`` (int32 [n_req][max_pages]), and at most ``max_q`` new
+    tokens.  ``scale`` is head_dim ** -0.5 by default; ``window`` > 0 limits a
+    token to its last ``window`` keys.  Keep a ``workspace``
+    (``q4k_paged_attn_workspace``) for repeated calls."""
+    cache = _kv_cache(k_cache, v_cache)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError(f"q must be [tokens][heads][{cache.head_dim}]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [n_req][max_pages]")
+    tokens, heads, dim = q.shape
+    n_req, max_pages = page_table.shape
+    _count(cu_q, n_req + 1, "cu_q")
+    _count(kv_len, n_req, "kv_len")
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype not in _TYPES:
+        raise ValueError("out must have q's shape and be float32 or of the cache's type")
+    if workspace is None:
+        workspace = q4k_paged_attn_workspace(q, k_cache, page_table, max_q, out.dtype)
+    _check(lib().q4k_paged_attn(_ptr(q, k_cache.dtype, "q"), tokens, heads, ctypes.byref(cache),
+                                _ptr(page_table, torch.int32, "page_table"), max_pages,
+                                _ptr(cu_q, torch.int32, "cu_q"), _ptr(kv_len, torch.int32, "kv_len"), n_req, max_q,
+                                dim ** -0.5 if scale is None else scale, window, _ptr(out, out.dtype, "out"),
+                                _TYPES[out.dtype], _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
+                                _stream(stream)), "q4k_paged_attn")
+    return out
+
+
+def q4k_lora_segments(adapters, device="cuda"):
+    """``(order, seg_start, seg_adapter)`` of ``q4k_lora_add`` (int32 on
+    ``device``) for a list of each token's adapter (negative: none); one per
+    step serves every projection of every layer."""
+    ids = [max(int(a), -1) for a in adapters]
+    order = sorted(range(len(ids)), key=ids.__getitem__)
+    starts = [i for i in range(len(ids)) if i == 0 or ids[order[i]] != ids[order[i - 1]]]
+    make = lambda v: torch.tensor(v, dtype=torch.int32, device=device)  # noqa: E731
+    return make(order), make(starts + [len(ids)]), make([ids[order[i]] for i in starts])
+
+
+def q4k_lora_workspace(tokens: int, rank: int, n_mats: int = 1, device="cuda"):
+    """A workspace for ``q4k_lora_add`` calls of up to these sizes."""
+    need = int(lib().q4k_lora_workspace_bytes(n_mats, rank, tokens))
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+
+def q4k_lora_add(x, a, b, base, order, seg_start, seg_adapter, scale, y=None, workspace=None, stream=None):
+    """Add low-rank adapters beside projections that share the input ``x``
+    [tokens][cols] float32: ``y[m][t] = base[m][t] + scale[i] * b[m][i] @
+    (a[m][i] @ x[t])`` with i the adapter of token t.
+
+    ``a``, ``b``, ``base``, ``y`` are lists with an entry for each of 1..4
+    projections: ``a[m]`` [n_adapters][rank][cols] and ``b[m]``
+    [n_adapters][rows][rank] float16 or bfloat16, ``base[m]`` [tokens][rows]
+    float32 (or None for zeros), ``y[m]`` likewise (may be ``base[m]``; made
+    here when ``y`` is None).  ``order``, ``seg_start``, ``seg_adapter``: the
+    tokens grouped by adapter (``q4k_lora_segments``); ``scale`` [n_adapters]
+    float32.  Returns the list ``y``."""
+    n, (tokens, cols) = len(a), x.shape
+    if not (len(b) == len(base) == n and (y is None or len(y) == n)) or n == 0:
+        raise ValueError("a, b, base and y must be lists of one length")
+    adapters, rank, dtype = a[0].shape[0], a[0].shape[1], a[0].dtype
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError("a must be float16 or bfloat16")
+    if y is None:
+        y = [torch.empty((tokens, w.shape[1]), dtype=torch.float32, device=x.device) for w in b]
+    mats = (LoraMat * n)()
+    for m in range(n):
+        rows = b[m].shape[1]
+        if a[m].shape != (adapters, rank, cols) or b[m].shape != (adapters, rows, rank):
+            raise ValueError(f"a[{m}] must be [{adapters}][{rank}][{cols}] and b[{m}] [{adapters}][rows][{rank}]")
+        if y[m].shape != (tokens, rows) or (base[m] is not None and base[m].shape != (tokens, rows)):
+            raise ValueError(f"base[{m}] and y[{m}] must be [{tokens}][{rows}]")
+        mats[m] = LoraMat(_ptr(a[m], dtype, "a"), _ptr(b[m], dtype, "b"), _ptr(base[m], torch.float32, "base"),
+                          _ptr(y[m], torch.float32, "y"), rows)
+    n_seg = seg_adapter.numel()
+    _count(order, tokens, "order")
+    _count(seg_start, n_seg + 1, "seg_start")
+    _count(scale, adapters, "scale")
+    if workspace is None:
+        workspace = q4k_lora_workspace(tokens, rank, n, x.device)
+    _check(lib().q4k_lora_add(n, mats, adapters, rank, _TYPES[dtype], cols, _ptr(x, torch.float32, "x"), tokens,
+                              _ptr(order, torch.int32, "order"), _ptr(seg_start, torch.int32, "seg_start"),
+                              _ptr(seg_adapter, torch.int32, "seg_adapter"), n_seg,
+                              _ptr(scale, torch.float32, "scale"), _ptr(workspace, torch.uint8, "workspace"),
+                              workspace.numel(), _stream(stream)), "q4k_lora_add")
+    return y
+
+
 def q4k_device_error(stream=None) -> int:
     """Synchronise ``stream`` and return (and clear) the device error status."""
     return int(lib().q4k_device_error(_stream(stream)))
@@ -551,5 +737,7 @@ __all__ = ["build", "lib", "Q4KError", "BLOCK144", "LAYOUT_GPU", "q4k_packed_byt
            "q8_1_bytes", "q8_quantize", "q8_quantize_h16", "q4k_gemm_h16", "q4k_gemm_blockdots_h16",
            "q4k_gemv", "q4k_gemv_multi", "GemvJob", "GemvSeq", "q4k_gemv_seq", "q4k_gemv_seq_static", "q4k_gemm",
            "q4k_gemm_blockdots", "q4k_device_error",
+           "KvCache", "LoraMat", "q4k_qk_norm_rope", "q4k_paged_attn_workspace", "q4k_paged_attn",
+           "q4k_lora_segments", "q4k_lora_workspace", "q4k_lora_add",
            "q4k_selftest_wait_timeout", "q4k_version",
            "SIGNATURES"]

@@ -33,6 +33,7 @@ int record_cuda(cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_cols(int64_t cols) {
   if (cols <= 0 || cols % kQK != 0 || cols > (int64_t(1) << 24)) return Q4K_ERR_INVALID_ARG;
@@ -45,6 +46,42 @@ int check_layout(int layout) {
 
 int check_rows(int64_t rows) {
   return (rows < 0 || rows > (int64_t(1) << 24)) ? Q4K_ERR_INVALID_ARG : Q4K_OK;
+}
+
+int check_kv_cache(const q4k_kv_cache* c, int heads) {
+  if (!c) return Q4K_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return Q4K_ERR_INVALID_ARG;
+  if (c->num_pages < 0 || c->num_pages > (int64_t(1) << 31) / c->page_size - 1) return Q4K_ERR_INVALID_ARG;
+  if (c->kv_heads < 1 || c->kv_heads > 256 || heads < 1 || heads > 4096 || heads % c->kv_heads != 0)
+    return Q4K_ERR_INVALID_ARG;
+  if (c->type != Q4K_F16 && c->type != Q4K_BF16) return Q4K_ERR_INVALID_ARG;
+  return (c->head_dim == 64 || c->head_dim == 128) ? Q4K_OK : Q4K_ERR_UNSUPPORTED;
+}
+
+constexpr int64_t kMaxTokens = int64_t(1) << 22;
+
+// The sizes of an attention call, checked; `p` gets them.
+int check_attn(const q4k_kv_cache* c, int heads, int64_t tokens, int64_t n_req, int64_t max_q, int64_t max_pages,
+               int out_type, AttnParams* p) {
+  if (int e = check_kv_cache(c, heads)) return e;
+  if (tokens < 0 || tokens > kMaxTokens || n_req < 0 || n_req > kMaxTokens || max_q < 0 || max_q > kMaxTokens)
+    return Q4K_ERR_INVALID_ARG;
+  if (max_pages < 0 || max_pages > (int64_t(1) << 31) / c->page_size - 1) return Q4K_ERR_INVALID_ARG;
+  if (out_type != c->type && out_type != Q4K_F32) return Q4K_ERR_INVALID_ARG;
+  p->tokens = tokens;
+  p->num_pages = c->num_pages;
+  p->n_req = n_req;
+  p->max_pages = max_pages;
+  p->max_q = std::min(max_q, tokens);
+  p->heads = heads;
+  p->kv_heads = c->kv_heads;
+  p->dim = c->head_dim;
+  p->page_size = c->page_size;
+  p->bf16 = c->type == Q4K_BF16;
+  p->out_f32 = out_type == Q4K_F32;
+  p->k_cache = c->k;
+  p->v_cache = c->v;
+  return Q4K_OK;
 }
 
 }  // namespace
@@ -646,6 +683,108 @@ int q4k_gemv_seq_static(const q4k_gemv_job* jobs, int n_jobs, int layout, int64_
   return st;
 }
 
+int q4k_qk_norm_rope(const float* q, const float* k, const float* v, int64_t tokens, int heads,
+                     const q4k_kv_cache* cache, const float* q_weight, const float* k_weight, float eps,
+                     const float* cos_sin, int64_t max_pos, int rot_dim, int interleaved, const int32_t* pos,
+                     const int32_t* slot, void* q_out, void* stream) {
+  if (int e = check_kv_cache(cache, heads)) return e;
+  if (tokens < 0 || tokens > kMaxTokens || max_pos < 0 || max_pos > (int64_t(1) << 31)) return Q4K_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > cache->head_dim || rot_dim % 8 != 0) return Q4K_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || (q_weight == nullptr) != (k_weight == nullptr)) return Q4K_ERR_INVALID_ARG;
+  if (tokens == 0) return Q4K_OK;
+  if (!q || !k || !v || !slot || !q_out || !cache->k || !cache->v) return Q4K_ERR_INVALID_ARG;
+  if (rot_dim && (!cos_sin || !pos)) return Q4K_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)q, (const void*)k, (const void*)v, (const void*)q_weight, (const void*)k_weight,
+                        (const void*)cos_sin, (const void*)q_out, (const void*)cache->k, (const void*)cache->v})
+    if (!aligned16(p)) return Q4K_ERR_ALIGNMENT;
+  if (!aligned4(pos) || !aligned4(slot)) return Q4K_ERR_ALIGNMENT;
+  HeadsParams p{};
+  p.q = q, p.k = k, p.v = v, p.q_weight = q_weight, p.k_weight = k_weight, p.cos_sin = cos_sin;
+  p.pos = pos, p.slot = slot, p.q_out = q_out, p.k_cache = cache->k, p.v_cache = cache->v;
+  p.tokens = tokens, p.max_pos = max_pos, p.num_slots = cache->num_pages * cache->page_size;
+  p.heads = heads, p.kv_heads = cache->kv_heads, p.dim = cache->head_dim, p.rot = rot_dim;
+  p.page_size = cache->page_size, p.interleaved = interleaved != 0, p.bf16 = cache->type == Q4K_BF16, p.eps = eps;
+  if (!(p.err = device_error_word())) return record_cuda(cudaGetLastError());
+  cudaError_t e = launch_qk_norm_rope(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? Q4K_OK : record_cuda(e);
+}
+
+size_t q4k_paged_attn_workspace_bytes(const q4k_kv_cache* cache, int heads, int64_t tokens, int64_t n_req,
+                                      int64_t max_q, int64_t max_pages, int out_type) {
+  AttnParams p{};
+  if (check_attn(cache, heads, tokens, n_req, max_q, max_pages, out_type, &p) || tokens == 0 || n_req == 0) return 0;
+  return paged_attn_workspace(p);
+}
+
+int q4k_paged_attn(const void* q, int64_t tokens, int heads, const q4k_kv_cache* cache, const int32_t* page_table,
+                   int64_t max_pages, const int32_t* cu_q, const int32_t* kv_len, int64_t n_req, int64_t max_q,
+                   float scale, int window, void* out, int out_type, void* workspace, size_t workspace_bytes,
+                   void* stream) {
+  AttnParams p{};
+  if (int e = check_attn(cache, heads, tokens, n_req, max_q, max_pages, out_type, &p)) return e;
+  if (window < 0 || !(scale > -3.0e38f && scale < 3.0e38f)) return Q4K_ERR_INVALID_ARG;
+  if (tokens == 0) return Q4K_OK;
+  if (n_req == 0 || max_q == 0) return Q4K_ERR_INVALID_ARG;   // tokens that belong to no request
+  if (!q || !cache->k || !cache->v || (!page_table && max_pages) || !cu_q || !kv_len || !out || !workspace)
+    return Q4K_ERR_INVALID_ARG;
+  for (const void* a : {q, (const void*)cache->k, (const void*)cache->v, (const void*)out, (const void*)workspace})
+    if (!aligned16(a)) return Q4K_ERR_ALIGNMENT;
+  if (!aligned4(page_table) || !aligned4(cu_q) || !aligned4(kv_len)) return Q4K_ERR_ALIGNMENT;
+  p.q = q, p.page_table = page_table, p.cu_q = cu_q, p.kv_len = kv_len, p.out = out, p.workspace = workspace;
+  p.scale = scale, p.window = window;
+  if (workspace_bytes < paged_attn_workspace(p)) return Q4K_ERR_INVALID_ARG;
+  if (!(p.err = device_error_word())) return record_cuda(cudaGetLastError());
+  cudaError_t e = launch_paged_attn(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? Q4K_OK : record_cuda(e);
+}
+
+static int check_lora(int n, int rank, int64_t tokens) {
+  if (n < 0 || rank < 8 || rank > 128 || rank % 8 != 0 || tokens < 0 || tokens > kMaxTokens)
+    return Q4K_ERR_INVALID_ARG;
+  return n > kLoraMaxMats ? Q4K_ERR_UNSUPPORTED : Q4K_OK;
+}
+
+size_t q4k_lora_workspace_bytes(int n, int rank, int64_t tokens) {
+  if (check_lora(n, rank, tokens) || n == 0 || tokens == 0) return 0;
+  return lora_workspace(n, rank, tokens);
+}
+
+int q4k_lora_add(int n, const q4k_lora_mat* mats, int64_t n_adapters, int rank, int type, int64_t cols,
+                 const float* x, int64_t tokens, const int32_t* order, const int32_t* seg_start,
+                 const int32_t* seg_adapter, int64_t n_seg, const float* scale, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  if (int e = check_lora(n, rank, tokens)) return e;
+  if (int e = check_cols(cols)) return e;
+  if (type != Q4K_F16 && type != Q4K_BF16) return Q4K_ERR_INVALID_ARG;
+  if (n_adapters < 0 || n_adapters > (int64_t(1) << 24) || n_seg < 0 || n_seg > kMaxTokens) return Q4K_ERR_INVALID_ARG;
+  if (n && !mats) return Q4K_ERR_INVALID_ARG;
+  LoraParams p{};
+  for (int m = 0; m < n; ++m) {
+    if (int e = check_rows(mats[m].rows)) return e;
+    if (mats[m].rows == 0) continue;
+    p.mat[p.n++] = {mats[m].a, mats[m].b, mats[m].base, mats[m].y, mats[m].rows};
+  }
+  if (p.n == 0 || tokens == 0) return Q4K_OK;
+  if (n_seg == 0) return Q4K_ERR_INVALID_ARG;                 // tokens that belong to no segment
+  if (!x || !order || !seg_start || !seg_adapter || !workspace || (n_adapters && !scale)) return Q4K_ERR_INVALID_ARG;
+  for (int m = 0; m < p.n; ++m) {
+    const LoraMat& w = p.mat[m];
+    if (!w.y || (n_adapters && (!w.a || !w.b))) return Q4K_ERR_INVALID_ARG;
+    if (!aligned16(w.a) || !aligned16(w.b) || !aligned16(w.base) || !aligned16(w.y)) return Q4K_ERR_ALIGNMENT;
+  }
+  if (!aligned16(x) || !aligned16(scale) || !aligned16(workspace) || !aligned4(order) || !aligned4(seg_start) ||
+      !aligned4(seg_adapter))
+    return Q4K_ERR_ALIGNMENT;
+  if (workspace_bytes < lora_workspace(p.n, rank, tokens)) return Q4K_ERR_INVALID_ARG;
+  p.x = x, p.scale = scale, p.order = order, p.seg_start = seg_start, p.seg_adapter = seg_adapter;
+  p.work = static_cast<float*>(workspace);
+  p.n_adapters = n_adapters, p.tokens = tokens, p.n_seg = n_seg, p.cols = cols, p.rank = rank;
+  p.bf16 = type == Q4K_BF16;
+  if (!(p.err = device_error_word())) return record_cuda(cudaGetLastError());
+  cudaError_t e = launch_lora_add(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? Q4K_OK : record_cuda(e);
+}
+
 int q4k_selftest_wait_timeout(void* stream) {
   int* err = device_error_word();
   if (!err) return record_cuda(cudaGetLastError());
@@ -665,7 +804,7 @@ int q4k_device_error(void* stream) {
     const int zero = 0;
     e = cudaMemcpy(word, &zero, sizeof(int), cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return record_cuda(e);
-    return Q4K_ERR_DEVICE_TIMEOUT;
+    return (value & ~kErrIndex) ? Q4K_ERR_DEVICE_TIMEOUT : Q4K_ERR_DEVICE_INDEX;
   }
   return Q4K_OK;
 }
@@ -678,6 +817,7 @@ const char* q4k_status_string(int status) {
     case Q4K_ERR_UNSUPPORTED: return "Q4K_ERR_UNSUPPORTED";
     case Q4K_ERR_CUDA: return "Q4K_ERR_CUDA";
     case Q4K_ERR_DEVICE_TIMEOUT: return "Q4K_ERR_DEVICE_TIMEOUT";
+    case Q4K_ERR_DEVICE_INDEX: return "Q4K_ERR_DEVICE_INDEX";
     default: return "Q4K_ERR_UNKNOWN";
   }
 }

@@ -120,6 +120,58 @@ cudaError_t launch_gemm_f16(const uint8_t* w, int64_t rows, int64_t cols, const 
 cudaError_t launch_gemm_q6k_f16(const uint8_t* w, int64_t rows, int64_t cols, const uint16_t* hi, const uint16_t* lo,
                                 const float* inv_scale, int64_t tokens, float* y, int* err, cudaStream_t s);
 
+// Bit of the device error word: a kernel met an index out of range in device
+// memory (the other bits are waits that gave up).
+constexpr int kErrIndex = 1 << 8;
+
+// Head norms, rotation and the store into the paged cache (q4k_qk_norm_rope).
+struct HeadsParams {
+  const float *q, *k, *v, *q_weight, *k_weight, *cos_sin;
+  const int32_t *pos, *slot;
+  void *q_out, *k_cache, *v_cache;
+  int* err;
+  int64_t tokens, max_pos, num_slots;
+  int heads, kv_heads, dim, rot, page_size;
+  bool interleaved, bf16;
+  float eps;
+};
+cudaError_t launch_qk_norm_rope(const HeadsParams& p, cudaStream_t s);
+
+// Attention over the paged cache (q4k_paged_attn).
+struct AttnParams {
+  const void *q, *k_cache, *v_cache;
+  const int32_t *page_table, *cu_q, *kv_len;
+  void *out, *workspace;
+  int* err;
+  int64_t tokens, num_pages, n_req, max_pages, max_q;
+  int heads, kv_heads, dim, page_size, window;
+  float scale;
+  bool bf16, out_f32;
+};
+size_t paged_attn_workspace(const AttnParams& p);
+cudaError_t launch_paged_attn(const AttnParams& p, cudaStream_t s);
+
+// Low-rank adapters beside up to kLoraMaxMats projections (q4k_lora_add).
+constexpr int kLoraMaxMats = 4;
+struct LoraMat {
+  const void *a, *b;
+  const float* base;
+  float* y;
+  int64_t rows;
+};
+struct LoraParams {
+  LoraMat mat[kLoraMaxMats];
+  const float *x, *scale;
+  const int32_t *order, *seg_start, *seg_adapter;
+  float* work;
+  int* err;
+  int64_t n_adapters, tokens, n_seg, cols;
+  int n, rank;
+  bool bf16;
+};
+size_t lora_workspace(int n, int rank, int64_t tokens);
+cudaError_t launch_lora_add(const LoraParams& p, cudaStream_t s);
+
 // One-thread kernel whose only (bounded) wait can never complete: after the
 // library's wait limit it records a timeout in `err` and returns.
 cudaError_t launch_wait_timeout_selftest(int* err, cudaStream_t s);
