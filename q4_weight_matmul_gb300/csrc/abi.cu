@@ -144,6 +144,24 @@ bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
   return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();
+  if (!encode) return false;
+  const cuuint32_t estride[5] = {1, 1, 1, 1, 1};
+  cuuint64_t gdim[5], gstride[4];
+  cuuint32_t bdim[5];
+  for (int i = 0; i < rank; ++i) {
+    gdim[i] = dims[i];
+    bdim[i] = box[i];
+    if (i + 1 < rank) gstride[i] = strides[i];
+  }
+  CUresult r = encode(map, dtype, rank, const_cast<void*>(base), gdim, gstride, bdim, estride,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 bool encode_tmap_u8_3d(CUtensorMap* map, const void* base, const uint64_t dims[3],
                        const uint64_t strides[2], const uint32_t box[3]) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tmap_encoder();

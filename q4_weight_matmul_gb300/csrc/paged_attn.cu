@@ -1,106 +1,65 @@
-// q4k_paged_attn: causal attention of new tokens over the paged cache.
-//
-// One warp per (token, head): its lanes share the head's values, the keys
-// come one after another with the running maximum and sum of their softmax.
-#include "q4k_internal.h"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+// q4k_paged_attn: causal attention of new tokens over the paged cache (host
+// side: the kernel, its workspace and its tensor maps).
+#include "paged_attn_few.cuh"
+#include "tmap.h"
 
 #include <algorithm>
 
 namespace q4k {
 namespace {
 
-template <bool BF16>
-__device__ __forceinline__ float to_float(uint16_t v) {
-  if constexpr (BF16) return __bfloat162float(__ushort_as_bfloat16(v));
-  else return __half2float(__ushort_as_half(v));
+using namespace attn;
+
+// Few-row variant (see launch_few) and the rows of its tiles.
+int few_variant(const AttnParams& p, int* rows) {
+  const int64_t n = p.max_q * (p.heads / p.kv_heads);
+  const int v = n <= 8 ? 0 : n <= 16 ? 1 : n <= 32 ? 2 : 3;
+  constexpr int kRows[4] = {8, 16, 32, 64};
+  *rows = kRows[v];
+  return v;
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(128) paged_attn_kernel(const AttnParams P) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= P.tokens * P.heads) return;
-  const int t = (int)(row / P.heads), h = (int)(row - (int64_t)t * P.heads);
-  const int hk = h / (P.heads / P.kv_heads);
-  // the request: the last one that starts at or before t
-  int lo = 0, hi = (int)P.n_req - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) / 2;
-    if (P.cu_q[mid] <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  int64_t kv = P.kv_len[lo];
-  const int64_t most = P.max_pages * P.page_size;
-  if (kv < 0 || kv > most || P.cu_q[lo] > t || P.cu_q[lo + 1] <= t || P.cu_q[lo + 1] > P.tokens) {
-    if (lane == 0) atomicOr(P.err, kErrIndex);
-    kv = kv < 0 ? 0 : min(kv, most);
-  }
-  const int64_t pos = min(kv - (P.cu_q[lo + 1] - t), kv - 1);   // in range whatever cu_q holds
-  const int64_t first = P.window ? max((int64_t)0, pos - P.window + 1) : 0;
+int cta_count() {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return std::min(device_info(dev).sm_count, kMaxCtas);
+}
 
-  float q[E], o[E], ob[E], m = -INFINITY, l = 0.f, lb = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    q[e] = to_float<BF16>(static_cast<const uint16_t*>(P.q)[row * D + lane * E + e]) * P.scale;
-    o[e] = ob[e] = 0.f;
-  }
-  for (int64_t j = first; j <= pos; ++j) {
-    const int page = P.page_table[lo * P.max_pages + j / P.page_size];
-    float kk[E], vv[E];
-    const bool ok = page >= 0 && page < P.num_pages;
-    if (!ok && lane == 0) atomicOr(P.err, kErrIndex);
-    const int64_t at = (((int64_t)page * P.kv_heads + hk) * P.page_size + j % P.page_size) * D + lane * E;
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      kk[e] = ok ? to_float<BF16>(static_cast<const uint16_t*>(P.k_cache)[at + e]) : 0.f;
-      vv[e] = ok ? to_float<BF16>(static_cast<const uint16_t*>(P.v_cache)[at + e]) : 0.f;
-      s = fmaf(q[e], kk[e], s);
-    }
-    for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-    const float top = fmaxf(m, s), a = expf(m - top), p = expf(s - top);
-    m = top;
-    // sums of 64 keys each, added up: a single running sum of a long context would lose bits
-    const bool last = (j & 63) == 63 || j == pos;
-    lb = lb * a + p;
-    l = l * a + (last ? lb : 0.f);
-    if (last) lb = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      ob[e] = ob[e] * a + p * vv[e];
-      o[e] = o[e] * a + (last ? ob[e] : 0.f);
-      if (last) ob[e] = 0.f;
-    }
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const float v = o[e] * inv;
-    const int64_t at = row * D + lane * E + e;
-    if (P.out_f32) static_cast<float*>(P.out)[at] = v;
-    else if constexpr (BF16) static_cast<__nv_bfloat16*>(P.out)[at] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(P.out)[at] = __float2half_rn(v);
-  }
+// A cache array as [num_pages][kv_heads][page_size][head_dim], copied 64
+// values by `box` cells at a time.
+bool cache_map(CUtensorMap* map, const AttnParams& p, const void* base, int box) {
+  const uint64_t cell = (uint64_t)p.dim * 2;
+  const uint64_t dims[4] = {(uint64_t)p.dim, (uint64_t)p.page_size, (uint64_t)p.kv_heads,
+                            (uint64_t)std::max<int64_t>(p.num_pages, 1)};
+  const uint64_t strides[3] = {cell, cell * p.page_size, cell * p.page_size * p.kv_heads};
+  const uint32_t boxes[4] = {64, (uint32_t)box, 1, 1};
+  return encode_tmap(map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims,
+                     strides, boxes, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 }  // namespace
 
-size_t paged_attn_workspace(const AttnParams&) { return 16; }
+size_t paged_attn_workspace(const AttnParams& p) {
+  int rows;
+  few_variant(p, &rows);
+  return kTicketBytes + (size_t)cta_count() * 2 * rows * (p.dim + 2) * sizeof(float);
+}
 
 cudaError_t launch_paged_attn(const AttnParams& p, cudaStream_t s) {
-  const unsigned grid = (unsigned)((p.tokens * p.heads + 3) / 4);
-  if (p.dim == 128) {
-    if (p.bf16) paged_attn_kernel<128, true><<<grid, 128, 0, s>>>(p);
-    else paged_attn_kernel<128, false><<<grid, 128, 0, s>>>(p);
-  } else {
-    if (p.bf16) paged_attn_kernel<64, true><<<grid, 128, 0, s>>>(p);
-    else paged_attn_kernel<64, false><<<grid, 128, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  FewParams f{};
+  f.a = p;
+  f.box = std::min(p.page_size, kUnit);
+  for (f.page_shift = 4; (1 << f.page_shift) < p.page_size; ++f.page_shift) {}
+  f.min_units = 2;
+  CUtensorMap kmap, vmap;
+  if (!cache_map(&kmap, p, p.k_cache, f.box) || !cache_map(&vmap, p, p.v_cache, f.box)) return cudaErrorInvalidValue;
+  int rows;
+  const int variant = few_variant(p, &rows), ctas = cta_count();
+  if (p.dim == 128)
+    return p.bf16 ? launch_few<128, true>(kmap, vmap, f, variant, ctas, s)
+                  : launch_few<128, false>(kmap, vmap, f, variant, ctas, s);
+  return p.bf16 ? launch_few<64, true>(kmap, vmap, f, variant, ctas, s)
+                : launch_few<64, false>(kmap, vmap, f, variant, ctas, s);
 }
 
 }  // namespace q4k

@@ -19,4 +19,9 @@ bool encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* bas
                     uint64_t dim1, uint64_t row_stride_bytes, uint32_t box0, uint32_t box1,
                     CUtensorMapSwizzle swizzle);
 
+// Tensor of `rank` (2..5) dimensions, dims[0] innermost (elements of `dtype`),
+// strides[i] = byte stride of dims[i+1], box[i] elements per copy.
+bool encode_tmap(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* base, const uint64_t* dims,
+                 const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
+
 }  // namespace q4k
