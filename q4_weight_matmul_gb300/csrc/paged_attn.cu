@@ -1,5 +1,6 @@
 // q4k_paged_attn: causal attention of new tokens over the paged cache (host
 // side: the kernel, its workspace and its tensor maps).
+#include "paged_attn_chunk.cuh"
 #include "paged_attn_few.cuh"
 #include "tmap.h"
 
@@ -18,6 +19,9 @@ int few_variant(const AttnParams& p, int* rows) {
   *rows = kRows[v];
   return v;
 }
+
+// The many-row kernel keeps its weights at 16 bits, so it gives 16-bit results.
+bool many_rows(const AttnParams& p) { return !p.out_f32 && p.max_q * (p.heads / p.kv_heads) > 64; }
 
 int cta_count() {
   int dev = 0;
@@ -42,19 +46,26 @@ bool cache_map(CUtensorMap* map, const AttnParams& p, const void* base, int box)
 size_t paged_attn_workspace(const AttnParams& p) {
   int rows;
   few_variant(p, &rows);
+  if (many_rows(p)) rows = kChunkRows;
   return kTicketBytes + (size_t)cta_count() * 2 * rows * (p.dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const AttnParams& p, cudaStream_t s) {
-  FewParams f{};
-  f.a = p;
-  f.box = std::min(p.page_size, kUnit);
-  for (f.page_shift = 4; (1 << f.page_shift) < p.page_size; ++f.page_shift) {}
-  f.min_units = 2;
+  const bool many = many_rows(p);
+  const int box = std::min(p.page_size, many ? kChunkKeys : kUnit), ctas = cta_count();
+  int shift = 4;
+  while ((1 << shift) < p.page_size) ++shift;
   CUtensorMap kmap, vmap;
-  if (!cache_map(&kmap, p, p.k_cache, f.box) || !cache_map(&vmap, p, p.v_cache, f.box)) return cudaErrorInvalidValue;
+  if (!cache_map(&kmap, p, p.k_cache, box) || !cache_map(&vmap, p, p.v_cache, box)) return cudaErrorInvalidValue;
+  if (many) {
+    const ChunkParams f{p, shift, box, 2};
+    if (p.dim == 128)
+      return p.bf16 ? launch_chunk<128, true>(kmap, vmap, f, ctas, s) : launch_chunk<128, false>(kmap, vmap, f, ctas, s);
+    return p.bf16 ? launch_chunk<64, true>(kmap, vmap, f, ctas, s) : launch_chunk<64, false>(kmap, vmap, f, ctas, s);
+  }
   int rows;
-  const int variant = few_variant(p, &rows), ctas = cta_count();
+  const int variant = few_variant(p, &rows);
+  const FewParams f{p, shift, box, 2};
   if (p.dim == 128)
     return p.bf16 ? launch_few<128, true>(kmap, vmap, f, variant, ctas, s)
                   : launch_few<128, false>(kmap, vmap, f, variant, ctas, s);

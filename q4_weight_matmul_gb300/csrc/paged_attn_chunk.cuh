@@ -1,0 +1,490 @@
+// Attention over the paged cache for many query rows per key head: chunks of
+// prompts, with 16-bit results.
+//
+// 4 D operations per row and key on the tensor cores against an exponential
+// and a handful of fp32 operations, so the tensor pipe bounds it, closely
+// followed by the softmax.  One CTA per SM takes its share of the (row tile,
+// 128 keys) units (paged_attn_common.cuh).  A row tile is 256 rows in two
+// halves of 128, each with its own four softmax warps, one thread per row:
+// while one half's softmax runs, the tensor core works for the other half.
+//
+//   warp 8   streams key and value tiles (128 x D, tensor copies of pages or
+//            page parts, 128-byte swizzled) into a ring of five
+//   warp 9   issues the products: S = Q K^T (both operands from shared
+//            memory, S in tensor memory), O += P V (P from tensor memory,
+//            V read with its keys as the K dimension, O in tensor memory)
+//   warps 0-3, 4-7   load Q, turn S into P = exp2(S c - m) in place, rescale
+//            O when a row's maximum grows, write the results
+//
+// P is rounded to the cache's type for the second product (16 bits: 2^-11 or
+// 2^-8 of each weight, as the result itself is); its sum is taken in fp32
+// before that.  m is a row's maximum as of its last rescale: O is rescaled
+// only when the maximum has grown by more than 2^6 since, so almost never
+// after a row's first tiles, and P, lifted by 2^8, stays below binary16's
+// largest value and above its subnormals down to 2^-22 of the largest weight.
+#pragma once
+
+#include "paged_attn_common.cuh"
+#include "tc_ptx.cuh"
+
+#include <cuda.h>
+
+namespace q4k {
+namespace attn {
+
+constexpr int kChunkRows = 256;
+constexpr int kChunkKeys = 128;
+constexpr int kChunkThreads = 320;
+constexpr float kChunkLift = 8.0f, kChunkGrow = 6.0f;
+
+template <int D>
+struct ChunkLayout {
+  static constexpr int kHalf = kChunkKeys * 128;            // 64 values of 128 keys (or rows)
+  static constexpr int kTile = kHalf * (D / 64);
+  static constexpr int kRing = 5;
+  static constexpr int kQ = 2 * kTile;
+  static constexpr int kSmem = kQ + kRing * kTile + 512 + 1024;     // barriers; base alignment
+};
+
+struct ChunkParams {
+  AttnParams a;
+  int page_shift, box;          // box: keys of one copy, min(page size, 128)
+  int min_units;
+};
+
+// D[tmem] (+)= A[tmem] B[smem]: A's rows are lanes, two 16-bit values a column.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// Descriptor of an operand whose K dimension is the slow one in memory: rows
+// (k) of 64 values, 128-byte swizzled, 8-row groups 1024 bytes apart, the
+// next 64 values `next` bytes on.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t next) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(next >> 4) << 16;
+  d |= (uint64_t)(1024 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int c0, int c1, int c2, int c3,
+                                              uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(bar)) : "memory");
+}
+
+// Whether the phase with `parity` has passed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const __grid_constant__ ChunkParams F) {
+  using L = ChunkLayout<D>;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  const AttnParams& P = F.a;
+  const uint32_t q_smem = tc::smem_u32(smem), ring = q_smem + L::kQ;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kQ + L::kRing * L::kTile);
+  uint64_t* empty = full + L::kRing;
+  uint64_t* q_full = empty + L::kRing;               // [2]
+  uint64_t* s_full = q_full + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* o_full = p_full + 2;
+  uint64_t* pv_done = o_full + 2;
+  uint64_t* drained = pv_done + 2;
+  uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_at + 1);
+  int* last = reinterpret_cast<int*>(tmem_at + 2);
+  int64_t* scratch = reinterpret_cast<int64_t*>(smem + L::kQ + L::kRing * L::kTile + 256);   // 16 words
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int group = P.heads / P.kv_heads;
+  if (tid == 0) {
+    for (int i = 0; i < L::kRing; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&q_full[i], 4);
+      tc::mbar_init(&s_full[i], 1);
+      tc::mbar_init(&p_full[i], 4);
+      tc::mbar_init(&o_full[i], 1);
+      tc::mbar_init(&pv_done[i], 1);
+    }
+    tc::mbar_init(drained, 1);
+    *gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  const Range R = share_out<kChunkRows, kChunkKeys, kChunkThreads>(P, group, F.min_units, scratch);
+  if ((int)blockIdx.x >= R.ctas) return;
+  if (warp == 9) {
+    tc::tmem_alloc(tmem_at, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_at;
+  // columns: S (and P) of the halves at 0 and 128, O at 256 and 384
+  auto s_at = [&](int h) { return tmem + 128u * h; };
+  auto o_at = [&](int h) { return tmem + 256u + 128u * h; };
+
+  auto wait = [&](uint64_t* bar, int64_t phase) {
+    if (!tc::mbar_wait(bar, (uint32_t)(phase & 1), gave_up) && !*gave_up) {
+      *gave_up = 1;
+      atomicOr(P.err, 1);
+    }
+  };
+
+  Walk<kChunkRows, kChunkKeys> w;
+  w.first(P, R, group);
+
+  if (warp == 8) {
+    // ------------------------------------------------ key and value tiles
+    const int none = P.num_pages > 0 ? (int)P.num_pages : 1;        // a page past the end reads as zeros
+    const int parts = kChunkKeys / F.box, copies = parts * (D / 64); // of one tile
+    int64_t n = 0;                                                   // tiles issued
+    do {
+      const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
+      const int32_t* table = P.page_table + w.req * P.max_pages;
+      for (int u = w.u0; u < w.u1; ++u) {
+        // lane i has part i's page (parts <= 8)
+        const int64_t key = key0 + (int64_t)u * kChunkKeys;
+        int page = none;
+        if (lane < parts) {
+          const int64_t p = (key + (int64_t)lane * F.box) >> F.page_shift, from = p << F.page_shift;
+          if (from < w.hi && from + P.page_size > w.lo) {
+            page = table[p];
+            if (page < 0 || page >= P.num_pages) {
+              atomicOr(P.err, kErrIndex);
+              page = none;
+            }
+          }
+        }
+        const int part = lane % parts, half = lane / parts;
+        page = __shfl_sync(0xffffffffu, page, part);
+        const int cell = (int)((key + (int64_t)part * F.box) & (P.page_size - 1));
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++n) {
+          const int slot = (int)(n % L::kRing);
+          const int64_t use = n / L::kRing;
+          if (use > 0) wait(&empty[slot], use - 1);
+          const bool go = !*gave_up;
+          if (lane == 0 && go) tc::mbar_arrive_expect_tx(&full[slot], L::kTile);
+          __syncwarp();
+          if (lane < copies && go)
+            tma_load_page(ring + slot * L::kTile + half * L::kHalf + part * F.box * 128, kv ? &vmap : &kmap, half * 64,
+                          cell, w.head, page, &full[slot]);
+        }
+      }
+    } while (w.next(P, R, group));
+    // after a wait gave up, the copies still in flight end before the block does
+    if (lane == 0 && *gave_up) {
+      const int64_t m = n < L::kRing ? n : L::kRing;
+      for (int64_t j = n - m; j < n; ++j)
+        if (!tc::mbar_wait_sleep(&full[j % L::kRing], (uint32_t)((j / L::kRing) & 1))) break;
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------ products
+    // Each half goes its own way: when its P is there, O += P V; when that is
+    // done (P lies where the next S goes), S = Q K^T of the next keys.
+    constexpr uint32_t kQK = tc::idesc_f16(128, kChunkKeys, BF16);
+    constexpr uint32_t kPV = tc::idesc_f16(128, D, BF16) | (1u << 16);        // B: K is its slow dimension
+    int64_t n0 = 0;                       // ring tiles before this item: K of unit u is n0 + 2 u, V the next
+    int64_t items[2] = {0, 0}, p_seen[2] = {0, 0}, pv_seen[2] = {0, 0};       // phases passed
+    auto ready = [&](uint64_t* bar, int64_t phase) {
+      return __shfl_sync(0xffffffffu, (int)mbar_test(bar, (uint32_t)(phase & 1)), 0) != 0;
+    };
+    // Never a wait in here while a half has work: the half that is ahead may need a tile whose place only the
+    // other half's progress frees.
+    auto landed = [&](int64_t n) { return ready(&full[n % L::kRing], n / L::kRing); };
+    auto release = [&](int64_t n) {
+      if (lane == 0) tc::mbar_arrive(&empty[n % L::kRing]);
+    };
+    auto qk = [&](int h, int64_t n) {
+      if (lane == 0) {
+        const uint32_t k_tile = ring + (uint32_t)(n % L::kRing) * L::kTile;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (uint32_t)(k >> 2) * L::kHalf + (uint32_t)(k & 3) * 32;
+          tc::mma_f16_ss(s_at(h), tc::desc_sw128(q_smem + h * L::kTile + off), tc::desc_sw128(k_tile + off), kQK,
+                         k > 0);
+        }
+        tc::mma_commit(&s_full[h]);
+      }
+      __syncwarp();
+    };
+    do {
+      const int halves = w.s.n * group - w.tile * kChunkRows > 128 ? 2 : 1, units = w.u1 - w.u0;
+      const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
+      wait(&full[n0 % L::kRing], n0 / L::kRing);      // every tile before it has been released
+      for (int h = 0; h < halves; ++h) {
+        wait(&q_full[h], items[h]++);
+        tc::fence_after_sync();
+        qk(h, n0);
+      }
+      int unit[2] = {0, halves == 2 ? 0 : units};   // of each half: the unit whose P (or P V) is next
+      int got_p[2] = {0, unit[1]};                  // units whose P has been seen
+      bool busy[2] = {false, false};                // its P V is under way
+      int clean = 0;                                // units whose V holds no stray values
+      long long since = clock64();
+      while ((unit[0] < units || unit[1] < units) && !*gave_up) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (unit[h] >= units) continue;
+          const int u = unit[h];
+          const int64_t n = n0 + 2 * u;
+          if (!busy[h]) {
+            if (!ready(&p_full[h], p_seen[h]) || !landed(n + 1)) continue;
+            ++p_seen[h];
+            got_p[h] = u + 1;
+            if (got_p[1 - h] > u) release(n);       // both halves are past this unit's S: its keys may go
+            const int64_t key = key0 + (int64_t)(w.u0 + u) * kChunkKeys;
+            if (u == clean) {
+              ++clean;
+              // values that no row of the tile sees may be anything: they become zeros
+              if (key < w.lo || key + kChunkKeys > w.hi) {
+                uint8_t* v = smem + L::kQ + (n + 1) % L::kRing * L::kTile;
+                for (int r = 0; r < kChunkKeys; ++r) {
+                  if (key + r >= w.lo && key + r < w.hi) continue;
+                  if (lane < D / 8) *reinterpret_cast<uint4*>(v + (lane >> 3) * L::kHalf + r * 128 + (lane & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+              }
+            }
+            tc::fence_after_sync();
+            if (lane == 0) {
+              const uint32_t v_tile = ring + (uint32_t)((n + 1) % L::kRing) * L::kTile;
+#pragma unroll
+              for (int k = 0; k < kChunkKeys / 16; ++k)
+                mma_f16_ts(o_at(h), s_at(h) + 8 * k, desc_mn_sw128(v_tile + k * 2048, L::kHalf), kPV, u > 0 || k > 0);
+              tc::mma_commit(&pv_done[h]);
+            }
+            __syncwarp();
+            busy[h] = true;
+          } else {
+            if (!ready(&pv_done[h], pv_seen[h]) || (u + 1 < units && !landed(n + 2))) continue;
+            ++pv_seen[h];
+            tc::fence_after_sync();
+            busy[h] = false;
+            ++unit[h];
+            if (unit[1 - h] > u) release(n + 1);
+            if (u + 1 < units) {
+              qk(h, n + 2);
+            } else {
+              tc::fence_before_sync();
+              if (lane == 0) tc::mbar_arrive(&o_full[h]);
+            }
+          }
+          since = clock64();
+        }
+        if (clock64() - since > tc::kTimeoutCycles) {
+          *gave_up = 1;
+          atomicOr(P.err, 1);
+        }
+      }
+      if (*gave_up) break;
+      n0 += 2 * units;
+    } while (w.next(P, R, group));
+    if (lane == 0) tc::mma_commit(drained);
+    __syncwarp();
+    if (!tc::mbar_wait_sleep(drained, 0)) atomicOr(P.err, 1);
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int h = warp >> 2, row = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const float c = fmaxf(fabsf(P.scale) * 1.4426950408889634f, 1e-30f);   // a scale of 0 must not meet -inf
+    const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
+    float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
+    auto sync = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    int64_t item = 0, tile = 0;
+    do {
+      const int row0 = w.tile * kChunkRows, rows = min(kChunkRows, w.s.n * group - row0);
+      const int halves = rows > 128 ? 2 : 1, r = h * 128 + row;
+      const bool mine = r < rows;
+      float m = -INFINITY, l = 0.f;
+      const int64_t out_at = mine ? out_row(P, w.s, w.head, group, row0 + r) * D : 0;
+      if (h < halves) {
+        // Q, negated where the scale is, so that the largest score has the largest weight
+        uint8_t* dst = smem + h * L::kTile;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + out_at);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          uint4 v = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * L::kHalf + tc::sw128_offset(row, i & 7)) = v;
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&q_full[h]);
+
+        // the keys this row sees, as positions within the item
+        const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
+        const int64_t pos = w.s.kv - w.s.n + (row0 + r) / group, from = P.window ? pos - P.window + 1 : 0;
+        const int hi = mine && pos + 1 > key0 ? (int)(pos + 1 - key0) : 0, lo = from > key0 ? (int)(from - key0) : 0;
+        for (int u = w.u0; u < w.u1; ++u, ++tile) {
+          wait(&s_full[h], tile);
+          tc::fence_after_sync();
+          float s[kChunkKeys];
+#pragma unroll
+          for (int i = 0; i < kChunkKeys / 32; ++i)
+            tc::tmem_ld32(s_at(h) + lanes + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+          tc::tmem_wait_ld();
+          const int at = u * kChunkKeys;
+          if (lo > at || hi < at + kChunkKeys) {
+            const int a = lo - at, b = hi - at;
+#pragma unroll
+            for (int i = 0; i < kChunkKeys; ++i) s[i] = i >= a && i < b ? s[i] : -INFINITY;
+          }
+          float t[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int i = 4; i < kChunkKeys; i += 4) {
+            t[0] = fmaxf(t[0], s[i]), t[1] = fmaxf(t[1], s[i + 1]);
+            t[2] = fmaxf(t[2], s[i + 2]), t[3] = fmaxf(t[3], s[i + 3]);
+          }
+          const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;     // c >= 0
+          float f = 1.f;
+          bool grow = false;
+          if (m == -INFINITY) {
+            m = top;                       // nothing seen so far: O and l are zero
+          } else if (top > m + kChunkGrow) {
+            f = ex2(m - top);
+            m = top;
+            grow = true;
+          }
+          l *= f;
+          if (__any_sync(0xffffffffu, grow) && u > w.u0) {
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t o[16];
+              tc::tmem_ld16(o_at(h) + lanes + 16 * i, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc::tmem_st16(o_at(h) + lanes + 16 * i, o);
+            }
+          }
+          const float sub = m == -INFINITY ? 0.f : m - kChunkLift;
+          float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < kChunkKeys / 32; ++i) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = ex2(fmaf(s[32 * i + 2 * e], c, -sub)), y = ex2(fmaf(s[32 * i + 2 * e + 1], c, -sub));
+              add[(2 * e) & 3] += x, add[(2 * e + 1) & 3] += y;
+              p[e] = pack2<BF16>(x, y);
+            }
+            tc::tmem_st16(s_at(h) + lanes + 16 * i, p);
+          }
+          l += (add[0] + add[1]) + (add[2] + add[3]);
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&p_full[h]);
+        }
+        wait(&o_full[h], item++);
+        tc::fence_after_sync();
+      }
+      const bool whole = w.u0 == 0 && w.u1 == w.units;
+      if (whole) {
+        if (h < halves) {
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          uint16_t* out = static_cast<uint16_t*>(P.out) + out_at;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tc::tmem_ld32(o_at(h) + lanes + 32 * i, o);
+            tc::tmem_wait_ld();
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  v[k] = pack2<BF16>(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                *reinterpret_cast<uint4*>(out + 32 * i + 8 * e) = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+            }
+          }
+          tc::fence_before_sync();
+        }
+      } else {
+        float* piece = pieces + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * piece_floats<kChunkRows, D>();
+        if (h < halves) {
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tc::tmem_ld32(o_at(h) + lanes + 32 * i, o);
+            tc::tmem_wait_ld();
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                __stcg(reinterpret_cast<uint4*>(piece + (size_t)r * D + 32 * i + 4 * e),
+                       make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+            }
+          }
+          tc::fence_before_sync();
+          if (mine) {
+            __stcg(piece + kChunkRows * D + r, m);
+            __stcg(piece + kChunkRows * D + kChunkRows + r, l);
+          }
+        }
+        const int c0 = owner(w.at, R), c1 = owner(w.at + w.units - 1, R);
+        // Q's place is free: every product with it is done (both halves have waited for theirs)
+        if (arrive(static_cast<unsigned*>(P.workspace) + c0, c1 - c0 + 1, last, tid == 0, sync))
+          combine_many<kChunkRows, D, BF16>(P, pieces, c0, c1, w.s, w.head, group, row0, rows,
+                                            reinterpret_cast<float*>(smem), tid, 256, sync);
+      }
+    } while (w.next(P, R, group));
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 9) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_chunk(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& f, int ctas,
+                         cudaStream_t s);
+
+template <int D, bool BF16>
+cudaError_t launch_chunk_kernel(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& f, int ctas,
+                                cudaStream_t s) {
+  auto kernel = paged_attn_chunk_kernel<D, BF16>;
+  constexpr int smem = ChunkLayout<D>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<ctas, kChunkThreads, smem, s>>>(kmap, vmap, f);
+  return cudaGetLastError();
+}
+
+}  // namespace attn
+}  // namespace q4k

@@ -96,7 +96,7 @@ def test_matches_the_oracle(case, dtype, out_dtype):
     assert q4k.q4k_device_error() == 0
 
 
-@pytest.mark.parametrize("new,kv", [([1], [40000]), ([3], [20001]), ([70], [5000])])
+@pytest.mark.parametrize("new,kv", [([1], [40000]), ([3], [20001]), ([70], [5000]), ([300], [20000])])
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 def test_long_contexts(new, kv, dtype):
     q4k.build()
