@@ -60,17 +60,26 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// Descriptor of an operand whose K dimension is the slow one in memory: rows
-// (k) of 64 values, 128-byte swizzled, 8-row groups 1024 bytes apart, the
-// next 64 values `next` bytes on.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t addr, uint32_t next) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(next >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Shared-memory operand descriptors, 128-byte swizzled, in two words: the low
+// one has the address (in units of 16 bytes) and, for an operand whose K
+// dimension is the slow one in memory (rows of 64 values, one row per k), the
+// distance to its next 64 values; the high one is the same for both: 8-row
+// groups 1024 bytes apart, version, swizzle.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint64_t desc(uint32_t low) { return ((uint64_t)kDescHigh << 32) | low; }
+
+// One lane of the (converged) warp.  With this and warp-wide votes in the
+// conditions around it, the operands of the tensor instructions stay in
+// uniform registers; under `lane == 0` each instruction's operands were moved
+// there one by one, and issuing them took longer than running them.
+__device__ __forceinline__ bool elect() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
 }
 
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int c0, int c1, int c2, int c3,
@@ -147,13 +156,14 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_at;
+  constexpr uint32_t tmem = 0;               // all 512 columns are this block's, so they begin at 0
   // columns: S (and P) of the halves at 0 and 128, O at 256 and 384
   auto s_at = [&](int h) { return tmem + 128u * h; };
   auto o_at = [&](int h) { return tmem + 256u + 128u * h; };
 
-  auto wait = [&](uint64_t* bar, int64_t phase) {
-    if (!tc::mbar_wait(bar, (uint32_t)(phase & 1), gave_up) && !*gave_up) {
+  // counts of tiles and phases are 32-bit (a range has fewer), whose division by the ring's length is cheap
+  auto wait = [&](uint64_t* bar, uint32_t phase) {
+    if (!tc::mbar_wait(bar, phase & 1, gave_up) && !*gave_up) {
       *gave_up = 1;
       atomicOr(P.err, 1);
     }
@@ -166,7 +176,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     // ------------------------------------------------ key and value tiles
     const int none = P.num_pages > 0 ? (int)P.num_pages : 1;        // a page past the end reads as zeros
     const int parts = kChunkKeys / F.box, copies = parts * (D / 64); // of one tile
-    int64_t n = 0;                                                   // tiles issued
+    uint32_t n = 0;                                                  // tiles issued
     do {
       const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
       const int32_t* table = P.page_table + w.req * P.max_pages;
@@ -189,8 +199,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         const int cell = (int)((key + (int64_t)part * F.box) & (P.page_size - 1));
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++n) {
-          const int slot = (int)(n % L::kRing);
-          const int64_t use = n / L::kRing;
+          const uint32_t slot = n % L::kRing, use = n / L::kRing;
           if (use > 0) wait(&empty[slot], use - 1);
           const bool go = !*gave_up;
           if (lane == 0 && go) tc::mbar_arrive_expect_tx(&full[slot], L::kTile);
@@ -203,9 +212,8 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     } while (w.next(P, R, group));
     // after a wait gave up, the copies still in flight end before the block does
     if (lane == 0 && *gave_up) {
-      const int64_t m = n < L::kRing ? n : L::kRing;
-      for (int64_t j = n - m; j < n; ++j)
-        if (!tc::mbar_wait_sleep(&full[j % L::kRing], (uint32_t)((j / L::kRing) & 1))) break;
+      for (uint32_t j = n < L::kRing ? 0 : n - L::kRing; j < n; ++j)
+        if (!tc::mbar_wait_sleep(&full[j % L::kRing], (j / L::kRing) & 1)) break;
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------ products
@@ -213,25 +221,25 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     // done (P lies where the next S goes), S = Q K^T of the next keys.
     constexpr uint32_t kQK = tc::idesc_f16(128, kChunkKeys, BF16);
     constexpr uint32_t kPV = tc::idesc_f16(128, D, BF16) | (1u << 16);        // B: K is its slow dimension
-    int64_t n0 = 0;                       // ring tiles before this item: K of unit u is n0 + 2 u, V the next
-    int64_t items[2] = {0, 0}, p_seen[2] = {0, 0}, pv_seen[2] = {0, 0};       // phases passed
-    auto ready = [&](uint64_t* bar, int64_t phase) {
-      return __shfl_sync(0xffffffffu, (int)mbar_test(bar, (uint32_t)(phase & 1)), 0) != 0;
+    uint32_t n0 = 0;                      // ring tiles before this item: K of unit u is n0 + 2 u, V the next
+    uint32_t items[2] = {0, 0}, p_seen[2] = {0, 0}, pv_seen[2] = {0, 0};      // phases passed
+    auto ready = [&](uint64_t* bar, uint32_t phase) {
+      return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0;
     };
     // Never a wait in here while a half has work: the half that is ahead may need a tile whose place only the
     // other half's progress frees.
-    auto landed = [&](int64_t n) { return ready(&full[n % L::kRing], n / L::kRing); };
-    auto release = [&](int64_t n) {
+    auto landed = [&](uint32_t n) { return ready(&full[n % L::kRing], n / L::kRing); };
+    auto release = [&](uint32_t n) {
       if (lane == 0) tc::mbar_arrive(&empty[n % L::kRing]);
     };
-    auto qk = [&](int h, int64_t n) {
-      if (lane == 0) {
-        const uint32_t k_tile = ring + (uint32_t)(n % L::kRing) * L::kTile;
+    auto qk = [&](int h, uint32_t n) {
+      const uint32_t q_low = (q_smem + h * L::kTile) >> 4 | 1u << 16;
+      const uint32_t k_low = (ring + n % L::kRing * L::kTile) >> 4 | 1u << 16;
+      if (elect()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (uint32_t)(k >> 2) * L::kHalf + (uint32_t)(k & 3) * 32;
-          tc::mma_f16_ss(s_at(h), tc::desc_sw128(q_smem + h * L::kTile + off), tc::desc_sw128(k_tile + off), kQK,
-                         k > 0);
+          const uint32_t off = ((k >> 2) * L::kHalf + (k & 3) * 32) >> 4;
+          tc::mma_f16_ss(s_at(h), desc(q_low + off), desc(k_low + off), kQK, k > 0);
         }
         tc::mma_commit(&s_full[h]);
       }
@@ -251,12 +259,12 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
       bool busy[2] = {false, false};                // its P V is under way
       int clean = 0;                                // units whose V holds no stray values
       long long since = clock64();
-      while ((unit[0] < units || unit[1] < units) && !*gave_up) {
+      while (__all_sync(0xffffffffu, (unit[0] < units || unit[1] < units) && !*gave_up)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (unit[h] >= units) continue;
           const int u = unit[h];
-          const int64_t n = n0 + 2 * u;
+          const uint32_t n = n0 + 2 * u;
           if (!busy[h]) {
             if (!ready(&p_full[h], p_seen[h]) || !landed(n + 1)) continue;
             ++p_seen[h];
@@ -278,11 +286,12 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
               }
             }
             tc::fence_after_sync();
-            if (lane == 0) {
-              const uint32_t v_tile = ring + (uint32_t)((n + 1) % L::kRing) * L::kTile;
+            const uint32_t v_low = (ring + (n + 1) % L::kRing * L::kTile) >> 4 | (uint32_t)(L::kHalf >> 4) << 16;
+            if (elect()) {
+              mma_f16_ts(o_at(h), s_at(h), desc(v_low), kPV, u > 0);
 #pragma unroll
-              for (int k = 0; k < kChunkKeys / 16; ++k)
-                mma_f16_ts(o_at(h), s_at(h) + 8 * k, desc_mn_sw128(v_tile + k * 2048, L::kHalf), kPV, u > 0 || k > 0);
+              for (int k = 1; k < kChunkKeys / 16; ++k)
+                mma_f16_ts(o_at(h), s_at(h) + 8 * k, desc(v_low + k * (2048 >> 4)), kPV, 1);
               tc::mma_commit(&pv_done[h]);
             }
             __syncwarp();
@@ -308,10 +317,10 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           atomicOr(P.err, 1);
         }
       }
-      if (*gave_up) break;
+      if (__any_sync(0xffffffffu, *gave_up)) break;
       n0 += 2 * units;
     } while (w.next(P, R, group));
-    if (lane == 0) tc::mma_commit(drained);
+    if (elect()) tc::mma_commit(drained);
     __syncwarp();
     if (!tc::mbar_wait_sleep(drained, 0)) atomicOr(P.err, 1);
   } else {
@@ -322,7 +331,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
     float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
     auto sync = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-    int64_t item = 0, tile = 0;
+    uint32_t item = 0, tile = 0;
     do {
       const int row0 = w.tile * kChunkRows, rows = min(kChunkRows, w.s.n * group - row0);
       const int halves = rows > 128 ? 2 : 1, r = h * 128 + row;
@@ -445,7 +454,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
             if (mine) {
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                __stcg(reinterpret_cast<uint4*>(piece + (size_t)r * D + 32 * i + 4 * e),
+                __stcg(reinterpret_cast<uint4*>(piece + ((8 * i + e) * kChunkRows + r) * 4),
                        make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
             }
           }
@@ -456,10 +465,8 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           }
         }
         const int c0 = owner(w.at, R), c1 = owner(w.at + w.units - 1, R);
-        // Q's place is free: every product with it is done (both halves have waited for theirs)
         if (arrive(static_cast<unsigned*>(P.workspace) + c0, c1 - c0 + 1, last, tid == 0, sync))
-          combine_many<kChunkRows, D, BF16>(P, pieces, c0, c1, w.s, w.head, group, row0, rows,
-                                            reinterpret_cast<float*>(smem), tid, 256, sync);
+          combine_rows<kChunkRows, D, BF16>(P, pieces, c0, c1, mine, r, out_at);
       }
     } while (w.next(P, R, group));
   }

@@ -278,40 +278,41 @@ __device__ __forceinline__ void combine(const AttnParams& P, const float* pieces
   sync();
 }
 
-// The same for large tiles: the maxima and inverse sums of the rows are kept
-// (2 * ROWS shared floats), the pieces' weights made where they are used.
-template <int ROWS, int D, bool BF16, class SYNC>
-__device__ __forceinline__ void combine_many(const AttnParams& P, const float* pieces, int c0, int c1, const Shape& s,
-                                             int head, int group, int row0, int rows, float* stats, int t, int n,
-                                             SYNC sync) {
+// The same with one thread per row (row r, its output at out_at) and pieces
+// laid out [D/4][ROWS][4], so that the threads of a warp read whole lines.
+template <int ROWS, int D, bool BF16>
+__device__ __forceinline__ void combine_rows(const AttnParams& P, const float* pieces, int c0, int c1, bool mine,
+                                             int r, int64_t out_at) {
+  if (!mine) return;
   auto piece = [&](int c) { return pieces + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * piece_floats<ROWS, D>(); };
-  for (int r = t; r < rows; r += n) {
-    float m = -INFINITY, l = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float mc = __ldcg(piece(c) + ROWS * D + r), lc = __ldcg(piece(c) + ROWS * D + ROWS + r);
-      if (mc == -INFINITY) continue;
-      const float top = fmaxf(m, mc);
-      l = l * (m == -INFINITY ? 0.f : exp2f(m - top)) + lc * exp2f(mc - top);
-      m = top;
-    }
-    stats[r] = m;
-    stats[ROWS + r] = l > 0.f ? 1.f / l : 0.f;
+  float m = -INFINITY, l = 0.f;
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(piece(c) + ROWS * D + r));
+  for (int c = c0; c <= c1; ++c) {
+    const float mc = __ldcg(piece(c) + ROWS * D + r);
+    if (mc != -INFINITY) l += exp2f(mc - m) * __ldcg(piece(c) + ROWS * D + ROWS + r);
   }
-  sync();
-  for (int e = t; e < rows * (D / 4); e += n) {
-    const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-    const float m = stats[r], inv = stats[ROWS + r];
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+  for (int d = 0; d < D; d += 32) {
+    float4 a[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int c = c0; c <= c1; ++c) {
-      const float mc = __ldcg(piece(c) + ROWS * D + r);
-      const float w = mc == -INFINITY ? 0.f : exp2f(mc - m) * inv;
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(c) + (size_t)r * D + d));
-      a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
+      const float* from = piece(c) + (d / 4 * ROWS + r) * 4;
+      float4 v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = __ldcg(reinterpret_cast<const float4*>(from + q * ROWS * 4));
+      const float mc = __ldcg(piece(c) + ROWS * D + r), w = mc == -INFINITY ? 0.f : exp2f(mc - m) * inv;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        a[q].x = fmaf(w, v[q].x, a[q].x), a[q].y = fmaf(w, v[q].y, a[q].y);
+        a[q].z = fmaf(w, v[q].z, a[q].z), a[q].w = fmaf(w, v[q].w, a[q].w);
+      }
     }
-    store4<BF16>(P.out, P.out_f32, out_row(P, s, head, group, row0 + r) * D + d, a);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) store4<BF16>(P.out, P.out_f32, out_at + d + 4 * q, a[q]);
   }
-  sync();
 }
 
 }  // namespace attn

@@ -138,7 +138,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
 
   Walk<ROWS, kUnit> w;
   w.first(P, R, group);
-  int64_t issued = 0;                                // slots before this item, the same count in every warp
+  uint32_t issued = 0;                               // slots before this item, the same count in every warp
 
   if (warp == kConsumers) {
     // ---------------------------------------------------------- producer
@@ -150,7 +150,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       int64_t cached = -1;                           // page index that lane 0's entry is for
       int entry = none;
       for (int u = w.u0; u < w.u1; ++u, ++issued) {
-        const int slot = (int)(issued % C::kSlots);
+        const int slot = issued % C::kSlots;
         const int64_t key = key0 + (int64_t)u * kUnit;
         const int64_t p0 = key >> F.page_shift;
         if (cached < 0 || p0 + pages_slot > cached + 32) {
@@ -165,7 +165,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
             }
           }
         }
-        if (issued >= C::kSlots) wait(&empty[slot], (uint32_t)((issued / C::kSlots - 1) & 1));
+        if (issued >= C::kSlots) wait(&empty[slot], (issued / C::kSlots - 1) & 1);
         if (lane == 0 && !*gave_up) tc::mbar_arrive_expect_tx(&full[slot], L::kSlot);
         for (int i = 0; i < pages_slot; ++i) {
           const int page = __shfl_sync(0xffffffffu, entry, (int)(p0 + i - cached));
@@ -184,16 +184,16 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     } while (w.next(P, R, group));
     // after a wait gave up, the copies still in flight end before the block does
     if (lane == 0 && *gave_up) {
-      const int64_t n = issued < C::kSlots ? issued : C::kSlots;
-      for (int64_t j = issued - n; j < issued; ++j)
-        if (!tc::mbar_wait_sleep(&full[j % C::kSlots], (uint32_t)((j / C::kSlots) & 1))) break;
+      for (uint32_t j = issued < C::kSlots ? 0 : issued - C::kSlots; j < issued; ++j)
+        if (!tc::mbar_wait_sleep(&full[j % C::kSlots], (j / C::kSlots) & 1)) break;
     }
     return;
   }
 
   // ------------------------------------------------------------ consumers
   auto sync = [&] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); };
-  const int wr = warp % WR, grp = warp / WR;
+  const uint32_t grp = warp / WR;
+  const int wr = warp % WR;
   const int g = lane >> 2, c2 = (lane & 3) * 2;
   const float to_log2 = P.scale * 1.4426950408889634f;
   float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
@@ -248,9 +248,9 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
 
     for (int u = w.u0; u < w.u1; ++u, ++issued) {
-      if ((int)(issued % C::kGroups) != grp) continue;
-      const int slot = (int)(issued % C::kSlots);
-      wait(&full[slot], (uint32_t)((issued / C::kSlots) & 1));
+      if (issued % C::kGroups != grp) continue;
+      const int slot = issued % C::kSlots;
+      wait(&full[slot], (issued / C::kSlots) & 1);
       if (active) {
         const uint32_t ks = ring + slot * L::kSlot, vs = ks + L::kTile;
         // S: 4 tiles of 8 keys

@@ -9,6 +9,10 @@
     python -m q4_weight_matmul_gb300.profile_case q6k_gemv --rows 151936 --cols 2560 --batch 1 --reps 3
     python -m q4_weight_matmul_gb300.profile_case gemm_f16 --rows 9728 --cols 2560 --tokens 512
     python -m q4_weight_matmul_gb300.profile_case q6k_gemm_f16 --rows 2560 --cols 9728 --tokens 512
+    python -m q4_weight_matmul_gb300.profile_case heads --tokens 8192 --reps 3
+    python -m q4_weight_matmul_gb300.profile_case attn --requests 1 --new 512 --context 8192 --reps 3
+    python -m q4_weight_matmul_gb300.profile_case attn --requests 16 --new 1 --context 8192 --f32-out --reps 3
+    python -m q4_weight_matmul_gb300.profile_case lora --rows 2560 --cols 9728 --tokens 2048 --rank 32 --reps 3
 
 ``seq`` runs --layers Qwen3-4B-shaped decode linear sets (q, k, v, o, gate,
 up, down; independent inputs) as one q4k_gemv_seq launch per rep, as the
@@ -59,15 +63,59 @@ def run_seq(a, dev, gen):
     print("profile case done: seq", a.layers, "layers, batch", a.batch, a.reps, "reps")
 
 
+def run_heads(a, dev, gen):
+    t = a.tokens
+    r = lambda *s: torch.randn(s, device=dev, generator=gen)  # noqa: E731
+    kc = torch.zeros((t // 64 + 1, 8, 64, 128), dtype=torch.bfloat16, device=dev)
+    vc, slot = torch.zeros_like(kc), torch.arange(t, dtype=torch.int32, device=dev)
+    q, k, v, cs, w = r(t, 32, 128), r(t, 8, 128), r(t, 8, 128), r(t, 128), r(128)
+    for _ in range(a.reps):
+        q4k.q4k_qk_norm_rope(q, k, v, kc, vc, slot, slot, cs, w, w)
+
+
+def run_attn(a, dev, gen):
+    """--requests of --new tokens each over --context keys; 32 query and 8 key heads of 128, bfloat16, pages of 64."""
+    page = 64
+    per = -(-a.context // page)
+    kc = torch.randn((a.requests * per, 8, page, 128), device=dev, generator=gen).bfloat16()
+    vc = torch.randn((a.requests * per, 8, page, 128), device=dev, generator=gen).bfloat16()
+    table = torch.randperm(a.requests * per, device=dev, generator=gen).to(torch.int32).view(a.requests, per)
+    q = torch.randn((a.requests * a.new, 32, 128), device=dev, generator=gen).bfloat16()
+    cu = torch.arange(a.requests + 1, dtype=torch.int32, device=dev) * a.new
+    kv = torch.full((a.requests,), a.context, dtype=torch.int32, device=dev)
+    dtype = torch.float32 if a.f32_out else torch.bfloat16
+    ws = q4k.q4k_paged_attn_workspace(q, kc, table, a.new, dtype)
+    for _ in range(a.reps):
+        q4k.q4k_paged_attn(q, kc, vc, table, cu, kv, a.new, out_dtype=dtype, workspace=ws)
+
+
+def run_lora(a, dev, gen):
+    """--tokens spread over --adapters adapters of --rank beside one --rows x --cols projection, bfloat16."""
+    r = lambda *s: torch.randn(s, device=dev, generator=gen)  # noqa: E731
+    seg = q4k.q4k_lora_segments([i * a.adapters // a.tokens for i in range(a.tokens)], dev)
+    x, base = r(a.tokens, a.cols), r(a.tokens, a.rows)
+    w1, w2 = r(a.adapters, a.rank, a.cols).bfloat16(), r(a.adapters, a.rows, a.rank).bfloat16()
+    scale = torch.ones(a.adapters, device=dev)
+    ws = q4k.q4k_lora_workspace(a.tokens, a.rank)
+    for _ in range(a.reps):
+        q4k.q4k_lora_add(x, [w1], [w2], [base], *seg, scale, workspace=ws)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("kernel", choices=["gemv", "gemm", "gemm_h16", "gemm_f16", "q8", "pack", "seq", "q6k_gemv",
-                                       "q6k_gemm_f16"])
+                                       "q6k_gemm_f16", "heads", "attn", "lora"])
     ap.add_argument("--layers", type=int, default=13)
     ap.add_argument("--rows", type=int, default=9728)
     ap.add_argument("--cols", type=int, default=2560)
     ap.add_argument("--batch", type=int, default=1)
     ap.add_argument("--tokens", type=int, default=512)
+    ap.add_argument("--requests", type=int, default=1)
+    ap.add_argument("--new", type=int, default=1)
+    ap.add_argument("--context", type=int, default=4096)
+    ap.add_argument("--f32-out", action="store_true")
+    ap.add_argument("--rank", type=int, default=32)
+    ap.add_argument("--adapters", type=int, default=4)
     ap.add_argument("--reps", type=int, default=5)
     a = ap.parse_args()
     q4k.build()
@@ -76,6 +124,13 @@ def main():
     gen.manual_seed(0)
     if a.kernel == "seq":
         run_seq(a, dev, gen)
+        return
+    if a.kernel in ("heads", "attn", "lora"):
+        {"heads": run_heads, "attn": run_attn, "lora": run_lora}[a.kernel](a, dev, gen)
+        torch.cuda.synchronize()
+        if q4k.q4k_device_error() != 0:
+            raise RuntimeError("a kernel reported an error")
+        print("profile case done:", a.kernel)
         return
     l2 = getattr(torch.cuda.get_device_properties(dev), "L2_cache_size", 126 * 2 ** 20)
     if a.kernel in ("q6k_gemv", "q6k_gemm_f16"):
