@@ -4,17 +4,23 @@
 // 4 D operations per row and key on the tensor cores against an exponential
 // and a handful of fp32 operations, so the tensor pipe bounds it, closely
 // followed by the softmax.  One CTA per SM takes its share of the (row tile,
-// 128 keys) units (paged_attn_common.cuh).  A row tile is 256 rows in two
-// halves of 128, each with its own four softmax warps, one thread per row:
-// while one half's softmax runs, the tensor core works for the other half.
+// 64 keys) units (paged_attn_common.cuh).  A row tile is 256 rows in two
+// halves of 128, each with its own four softmax warps, one thread per row.
 //
-//   warp 8   streams key and value tiles (128 x D, tensor copies of pages or
-//            page parts, 128-byte swizzled) into a ring of five
-//   warp 9   issues the products: S = Q K^T (both operands from shared
-//            memory, S in tensor memory), O += P V (P from tensor memory,
-//            V read with its keys as the K dimension, O in tensor memory)
+//   warp 8   streams key and value tiles (64 x D, tensor copies of pages or
+//            page parts, 128-byte swizzled) into a ring of ten
+//   warps 9, 10   issue a half's products: S = Q K^T (both operands from
+//            shared memory, S in tensor memory), O += P V (P from tensor
+//            memory, V read with its keys as the K dimension, O in tensor
+//            memory); one warp polling for both halves was the bottleneck
 //   warps 0-3, 4-7   load Q, turn S into P = exp2(S c - m) in place, rescale
 //            O when a row's maximum grows, write the results
+//
+// Each half has two S tiles: while its softmax works on one, the products of
+// the next are made in the other, so neither waits for the other's latency
+// (tiles of 128 keys with one S per half spent half of the time in that
+// chain: 4400 cycles per 128 keys against 2048 of tensor work).  64 keys is
+// what tensor memory has room for: 2 (halves) x (2 x 64 + D) columns of 512.
 //
 // P is rounded to the cache's type for the second product (16 bits: 2^-11 or
 // 2^-8 of each weight, as the result itself is); its sum is taken in fp32
@@ -33,22 +39,24 @@ namespace q4k {
 namespace attn {
 
 constexpr int kChunkRows = 256;
-constexpr int kChunkKeys = 128;
-constexpr int kChunkThreads = 320;
+constexpr int kChunkKeys = 64;
+constexpr int kChunkThreads = 352;
 constexpr float kChunkLift = 8.0f, kChunkGrow = 6.0f;
 
 template <int D>
 struct ChunkLayout {
-  static constexpr int kHalf = kChunkKeys * 128;            // 64 values of 128 keys (or rows)
+  static constexpr int kHalf = kChunkKeys * 128;            // 64 values of a tile's keys
   static constexpr int kTile = kHalf * (D / 64);
-  static constexpr int kRing = 5;
-  static constexpr int kQ = 2 * kTile;
+  static constexpr int kQHalf = 128 * 128;                  // 64 values of 128 rows of Q
+  static constexpr int kQTile = kQHalf * (D / 64);
+  static constexpr int kRing = 10;
+  static constexpr int kQ = 2 * kQTile;
   static constexpr int kSmem = kQ + kRing * kTile + 512 + 1024;     // barriers; base alignment
 };
 
 struct ChunkParams {
   AttnParams a;
-  int page_shift, box;          // box: keys of one copy, min(page size, 128)
+  int page_shift, box;          // box: keys of one copy, min(page size, 64)
   int min_units;
 };
 
@@ -90,17 +98,6 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int
       ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(bar)) : "memory");
 }
 
-// Whether the phase with `parity` has passed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -119,31 +116,29 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kQ + L::kRing * L::kTile);
   uint64_t* empty = full + L::kRing;
   uint64_t* q_full = empty + L::kRing;               // [2]
-  uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_full = p_full + 2;
-  uint64_t* pv_done = o_full + 2;
-  uint64_t* drained = pv_done + 2;
+  uint64_t* s_full = q_full + 2;                     // [half * 2 + S tile], as the next two
+  uint64_t* p_full = s_full + 4;
+  uint64_t* pv_done = p_full + 4;
+  uint64_t* drained = pv_done + 4;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_at + 1);
   int* last = reinterpret_cast<int*>(tmem_at + 2);
-  int64_t* scratch = reinterpret_cast<int64_t*>(smem + L::kQ + L::kRing * L::kTile + 256);   // 16 words
+  int64_t* scratch = reinterpret_cast<int64_t*>(smem + L::kQ + L::kRing * L::kTile + 320);   // 16 words
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = P.heads / P.kv_heads;
   if (tid == 0) {
     for (int i = 0; i < L::kRing; ++i) {
       tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], 1);
+      tc::mbar_init(&empty[i], 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&q_full[i], 4);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&q_full[i], 4);
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&s_full[i], 1);
       tc::mbar_init(&p_full[i], 4);
-      tc::mbar_init(&o_full[i], 1);
       tc::mbar_init(&pv_done[i], 1);
     }
-    tc::mbar_init(drained, 1);
+    tc::mbar_init(drained, 2);
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -157,8 +152,8 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
   __syncthreads();
   tc::fence_after_sync();
   constexpr uint32_t tmem = 0;               // all 512 columns are this block's, so they begin at 0
-  // columns: S (and P) of the halves at 0 and 128, O at 256 and 384
-  auto s_at = [&](int h) { return tmem + 128u * h; };
+  // columns: S (and in its place P) of half h, tile b at 128 h + 64 b, O at 256 and 384
+  auto s_at = [&](int h, int b) { return tmem + 128u * h + 64u * b; };
   auto o_at = [&](int h) { return tmem + 256u + 128u * h; };
 
   // counts of tiles and phases are 32-bit (a range has fewer), whose division by the ring's length is cheap
@@ -215,110 +210,87 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
       for (uint32_t j = n < L::kRing ? 0 : n - L::kRing; j < n; ++j)
         if (!tc::mbar_wait_sleep(&full[j % L::kRing], (j / L::kRing) & 1)) break;
     }
-  } else if (warp == 9) {
+  } else if (warp >= 9) {
     // ------------------------------------------------------------ products
-    // Each half goes its own way: when its P is there, O += P V; when that is
-    // done (P lies where the next S goes), S = Q K^T of the next keys.
+    // S = Q K^T of a unit when its S tile is free (the P V of two units before is done), O += P V when its P is
+    // there.  Each half goes at its own pace; a ring tile is free when both have let it go.
     constexpr uint32_t kQK = tc::idesc_f16(128, kChunkKeys, BF16);
     constexpr uint32_t kPV = tc::idesc_f16(128, D, BF16) | (1u << 16);        // B: K is its slow dimension
-    uint32_t n0 = 0;                      // ring tiles before this item: K of unit u is n0 + 2 u, V the next
-    uint32_t items[2] = {0, 0}, p_seen[2] = {0, 0}, pv_seen[2] = {0, 0};      // phases passed
-    auto ready = [&](uint64_t* bar, uint32_t phase) {
-      return __all_sync(0xffffffffu, mbar_test(bar, phase & 1)) != 0;
-    };
-    // Never a wait in here while a half has work: the half that is ahead may need a tile whose place only the
-    // other half's progress frees.
-    auto landed = [&](uint32_t n) { return ready(&full[n % L::kRing], n / L::kRing); };
+    const int h = warp - 9;
+    const uint32_t q_low = (q_smem + h * L::kQTile) >> 4 | 1u << 16;
+    uint32_t n0 = 0, item = 0;            // ring tiles before this item: K of unit u is n0 + 2 u, V the next
+    uint32_t uses0 = 0, uses1 = 0;        // of this half's S tiles, before this item
+    auto landed = [&](uint32_t n) { wait(&full[n % L::kRing], n / L::kRing); };
     auto release = [&](uint32_t n) {
       if (lane == 0) tc::mbar_arrive(&empty[n % L::kRing]);
     };
-    auto qk = [&](int h, uint32_t n) {
-      const uint32_t q_low = (q_smem + h * L::kTile) >> 4 | 1u << 16;
-      const uint32_t k_low = (ring + n % L::kRing * L::kTile) >> 4 | 1u << 16;
+    auto qk = [&](int u) {
+      const int b = u & 1;
+      const uint32_t n = n0 + 2 * u, k_low = (ring + n % L::kRing * L::kTile) >> 4 | 1u << 16;
+      landed(n);
       if (elect()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * L::kHalf + (k & 3) * 32) >> 4;
-          tc::mma_f16_ss(s_at(h), desc(q_low + off), desc(k_low + off), kQK, k > 0);
-        }
-        tc::mma_commit(&s_full[h]);
+        for (int k = 0; k < D / 16; ++k)
+          tc::mma_f16_ss(s_at(h, b), desc(q_low + (((k >> 2) * L::kQHalf + (k & 3) * 32) >> 4)),
+                         desc(k_low + (((k >> 2) * L::kHalf + (k & 3) * 32) >> 4)), kQK, k > 0);
+        tc::mma_commit(&s_full[2 * h + b]);
       }
       __syncwarp();
     };
     do {
       const int halves = w.s.n * group - w.tile * kChunkRows > 128 ? 2 : 1, units = w.u1 - w.u0;
+      if (h >= halves) {                  // no rows: only let the tiles go
+        for (int i = 0; i < 2 * units; ++i) {
+          landed(n0 + i);
+          release(n0 + i);
+        }
+        n0 += 2 * units;
+        continue;
+      }
       const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
-      wait(&full[n0 % L::kRing], n0 / L::kRing);      // every tile before it has been released
-      for (int h = 0; h < halves; ++h) {
-        wait(&q_full[h], items[h]++);
-        tc::fence_after_sync();
-        qk(h, n0);
-      }
-      int unit[2] = {0, halves == 2 ? 0 : units};   // of each half: the unit whose P (or P V) is next
-      int got_p[2] = {0, unit[1]};                  // units whose P has been seen
-      bool busy[2] = {false, false};                // its P V is under way
-      int clean = 0;                                // units whose V holds no stray values
-      long long since = clock64();
-      while (__all_sync(0xffffffffu, (unit[0] < units || unit[1] < units) && !*gave_up)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (unit[h] >= units) continue;
-          const int u = unit[h];
-          const uint32_t n = n0 + 2 * u;
-          if (!busy[h]) {
-            if (!ready(&p_full[h], p_seen[h]) || !landed(n + 1)) continue;
-            ++p_seen[h];
-            got_p[h] = u + 1;
-            if (got_p[1 - h] > u) release(n);       // both halves are past this unit's S: its keys may go
-            const int64_t key = key0 + (int64_t)(w.u0 + u) * kChunkKeys;
-            if (u == clean) {
-              ++clean;
-              // values that no row of the tile sees may be anything: they become zeros
-              if (key < w.lo || key + kChunkKeys > w.hi) {
-                uint8_t* v = smem + L::kQ + (n + 1) % L::kRing * L::kTile;
-                for (int r = 0; r < kChunkKeys; ++r) {
-                  if (key + r >= w.lo && key + r < w.hi) continue;
-                  if (lane < D / 8) *reinterpret_cast<uint4*>(v + (lane >> 3) * L::kHalf + r * 128 + (lane & 7) * 16) =
-                      make_uint4(0, 0, 0, 0);
-                }
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-              }
-            }
-            tc::fence_after_sync();
-            const uint32_t v_low = (ring + (n + 1) % L::kRing * L::kTile) >> 4 | (uint32_t)(L::kHalf >> 4) << 16;
-            if (elect()) {
-              mma_f16_ts(o_at(h), s_at(h), desc(v_low), kPV, u > 0);
-#pragma unroll
-              for (int k = 1; k < kChunkKeys / 16; ++k)
-                mma_f16_ts(o_at(h), s_at(h) + 8 * k, desc(v_low + k * (2048 >> 4)), kPV, 1);
-              tc::mma_commit(&pv_done[h]);
-            }
-            __syncwarp();
-            busy[h] = true;
-          } else {
-            if (!ready(&pv_done[h], pv_seen[h]) || (u + 1 < units && !landed(n + 2))) continue;
-            ++pv_seen[h];
-            tc::fence_after_sync();
-            busy[h] = false;
-            ++unit[h];
-            if (unit[1 - h] > u) release(n + 1);
-            if (u + 1 < units) {
-              qk(h, n + 2);
-            } else {
-              tc::fence_before_sync();
-              if (lane == 0) tc::mbar_arrive(&o_full[h]);
-            }
+      wait(&q_full[h], item++);
+      tc::fence_after_sync();
+      qk(0);
+      if (units > 1) qk(1);
+      for (int u = 0; u < units && !*gave_up; ++u) {
+        const int b = u & 1;
+        const uint32_t n = n0 + 2 * u, use = (b ? uses1 : uses0) + (u >> 1);
+        landed(n + 1);
+        const int64_t key = key0 + (int64_t)(w.u0 + u) * kChunkKeys;
+        if (key < w.lo || key + kChunkKeys > w.hi) {
+          // values that no row of the tile sees may be anything: they become zeros (both halves write them)
+          const int first = w.lo > key ? (int)min(w.lo - key, (int64_t)kChunkKeys) : 0;
+          const int end = w.hi > key ? (int)min(w.hi - key, (int64_t)kChunkKeys) : 0;
+          uint8_t* v = smem + L::kQ + (n + 1) % L::kRing * L::kTile;
+          for (int i = lane; i < kChunkKeys * (D / 8); i += 32) {
+            const int r = i / (D / 8), c = i % (D / 8);
+            if (r < first || r >= end)
+              *reinterpret_cast<uint4*>(v + (c >> 3) * L::kHalf + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
-          since = clock64();
+          tc::fence_proxy_async_smem();
+          __syncwarp();
         }
-        if (clock64() - since > tc::kTimeoutCycles) {
-          *gave_up = 1;
-          atomicOr(P.err, 1);
+        wait(&p_full[2 * h + b], use);
+        tc::fence_after_sync();
+        const uint32_t v_low = (ring + (n + 1) % L::kRing * L::kTile) >> 4 | (uint32_t)(L::kHalf >> 4) << 16;
+        if (elect()) {
+          mma_f16_ts(o_at(h), s_at(h, b), desc(v_low), kPV, u > 0);
+#pragma unroll
+          for (int k = 1; k < kChunkKeys / 16; ++k)
+            mma_f16_ts(o_at(h), s_at(h, b) + 8 * k, desc(v_low + k * (2048 >> 4)), kPV, 1);
+          tc::mma_commit(&pv_done[2 * h + b]);
         }
+        __syncwarp();
+        release(n);                       // P is there, so S is done
+        wait(&pv_done[2 * h + b], use);
+        tc::fence_after_sync();
+        release(n + 1);
+        if (u + 2 < units) qk(u + 2);
       }
-      if (__any_sync(0xffffffffu, *gave_up)) break;
       n0 += 2 * units;
+      uses0 += (units + 1) >> 1;
+      uses1 += units >> 1;
+      if (__any_sync(0xffffffffu, *gave_up)) break;
     } while (w.next(P, R, group));
     if (elect()) tc::mma_commit(drained);
     __syncwarp();
@@ -331,22 +303,22 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
     float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
     auto sync = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
-    uint32_t item = 0, tile = 0;
+    uint32_t uses0 = 0, uses1 = 0;              // of this half's S tiles, before this item
     do {
       const int row0 = w.tile * kChunkRows, rows = min(kChunkRows, w.s.n * group - row0);
-      const int halves = rows > 128 ? 2 : 1, r = h * 128 + row;
+      const int halves = rows > 128 ? 2 : 1, r = h * 128 + row, units = w.u1 - w.u0;
       const bool mine = r < rows;
       float m = -INFINITY, l = 0.f;
       const int64_t out_at = mine ? out_row(P, w.s, w.head, group, row0 + r) * D : 0;
       if (h < halves) {
         // Q, negated where the scale is, so that the largest score has the largest weight
-        uint8_t* dst = smem + h * L::kTile;
+        uint8_t* dst = smem + h * L::kQTile;
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + out_at);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
           uint4 v = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
           v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * L::kHalf + tc::sw128_offset(row, i & 7)) = v;
+          *reinterpret_cast<uint4*>(dst + (i >> 3) * L::kQHalf + tc::sw128_offset(row, i & 7)) = v;
         }
         tc::fence_proxy_async_smem();
         __syncwarp();
@@ -356,25 +328,27 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
         const int64_t pos = w.s.kv - w.s.n + (row0 + r) / group, from = P.window ? pos - P.window + 1 : 0;
         const int hi = mine && pos + 1 > key0 ? (int)(pos + 1 - key0) : 0, lo = from > key0 ? (int)(from - key0) : 0;
-        for (int u = w.u0; u < w.u1; ++u, ++tile) {
-          wait(&s_full[h], tile);
+        for (int i = 0; i < units; ++i) {
+          const int b = i & 1;
+          const uint32_t use = (b ? uses1 : uses0) + (i >> 1);
+          wait(&s_full[2 * h + b], use);
           tc::fence_after_sync();
           float s[kChunkKeys];
 #pragma unroll
-          for (int i = 0; i < kChunkKeys / 32; ++i)
-            tc::tmem_ld32(s_at(h) + lanes + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * i));
+          for (int k = 0; k < kChunkKeys / 32; ++k)
+            tc::tmem_ld32(s_at(h, b) + lanes + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * k));
           tc::tmem_wait_ld();
-          const int at = u * kChunkKeys;
+          const int at = (w.u0 + i) * kChunkKeys;
           if (lo > at || hi < at + kChunkKeys) {
-            const int a = lo - at, b = hi - at;
+            const int x = lo - at, y = hi - at;
 #pragma unroll
-            for (int i = 0; i < kChunkKeys; ++i) s[i] = i >= a && i < b ? s[i] : -INFINITY;
+            for (int k = 0; k < kChunkKeys; ++k) s[k] = k >= x && k < y ? s[k] : -INFINITY;
           }
           float t[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int i = 4; i < kChunkKeys; i += 4) {
-            t[0] = fmaxf(t[0], s[i]), t[1] = fmaxf(t[1], s[i + 1]);
-            t[2] = fmaxf(t[2], s[i + 2]), t[3] = fmaxf(t[3], s[i + 3]);
+          for (int k = 4; k < kChunkKeys; k += 4) {
+            t[0] = fmaxf(t[0], s[k]), t[1] = fmaxf(t[1], s[k + 1]);
+            t[2] = fmaxf(t[2], s[k + 2]), t[3] = fmaxf(t[3], s[k + 3]);
           }
           const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;     // c >= 0
           float f = 1.f;
@@ -387,38 +361,41 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
             grow = true;
           }
           l *= f;
-          if (__any_sync(0xffffffffu, grow) && u > w.u0) {
+          if (__any_sync(0xffffffffu, grow) && i > 0) {
+            // O holds every unit before this one: wait for the last of their products
+            wait(&pv_done[2 * h + 1 - b], (b ? uses0 : uses1) + ((i - 1) >> 1));
+            tc::fence_after_sync();
 #pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
+            for (int k = 0; k < D / 16; ++k) {
               uint32_t o[16];
-              tc::tmem_ld16(o_at(h) + lanes + 16 * i, o);
+              tc::tmem_ld16(o_at(h) + lanes + 16 * k, o);
               tc::tmem_wait_ld();
 #pragma unroll
               for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tc::tmem_st16(o_at(h) + lanes + 16 * i, o);
+              tc::tmem_st16(o_at(h) + lanes + 16 * k, o);
             }
           }
           const float sub = m == -INFINITY ? 0.f : m - kChunkLift;
           float add[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t p[kChunkKeys / 2];
 #pragma unroll
-          for (int i = 0; i < kChunkKeys / 32; ++i) {
-            uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float x = ex2(fmaf(s[32 * i + 2 * e], c, -sub)), y = ex2(fmaf(s[32 * i + 2 * e + 1], c, -sub));
-              add[(2 * e) & 3] += x, add[(2 * e + 1) & 3] += y;
-              p[e] = pack2<BF16>(x, y);
-            }
-            tc::tmem_st16(s_at(h) + lanes + 16 * i, p);
+          for (int e = 0; e < kChunkKeys / 2; ++e) {
+            const float x = ex2(fmaf(s[2 * e], c, -sub)), y = ex2(fmaf(s[2 * e + 1], c, -sub));
+            add[(2 * e) & 3] += x, add[(2 * e + 1) & 3] += y;
+            p[e] = pack2<BF16>(x, y);
           }
+          tc::tmem_st32(s_at(h, b) + lanes, p);
           l += (add[0] + add[1]) + (add[2] + add[3]);
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&p_full[h]);
+          if (lane == 0) tc::mbar_arrive(&p_full[2 * h + b]);
         }
-        wait(&o_full[h], item++);
+        // the item's last product (the ones before it are done when it is)
+        wait(&pv_done[2 * h + ((units - 1) & 1)], ((units - 1) & 1 ? uses1 : uses0) + ((units - 1) >> 1));
         tc::fence_after_sync();
+        uses0 += (units + 1) >> 1;
+        uses1 += units >> 1;
       }
       const bool whole = w.u0 == 0 && w.u1 == w.units;
       if (whole) {
