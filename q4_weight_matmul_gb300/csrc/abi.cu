@@ -52,6 +52,7 @@ int check_kv_cache(const q4k_kv_cache* c, int heads) {
   if (!c) return Q4K_ERR_INVALID_ARG;
   if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return Q4K_ERR_INVALID_ARG;
   if (c->num_pages < 0 || c->num_pages > (int64_t(1) << 31) / c->page_size - 1) return Q4K_ERR_INVALID_ARG;
+  if (c->num_pages * std::max(c->kv_heads, 1) >= (int64_t(1) << 31) - 256) return Q4K_ERR_INVALID_ARG;
   if (c->kv_heads < 1 || c->kv_heads > 256 || heads < 1 || heads > 4096 || heads % c->kv_heads != 0)
     return Q4K_ERR_INVALID_ARG;
   if (c->type != Q4K_F16 && c->type != Q4K_BF16) return Q4K_ERR_INVALID_ARG;

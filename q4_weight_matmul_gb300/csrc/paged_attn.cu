@@ -29,15 +29,15 @@ int cta_count() {
   return std::min(device_info(dev).sm_count, kMaxCtas);
 }
 
-// A cache array as [num_pages][kv_heads][page_size][head_dim], copied 64
-// values by `box` cells at a time.
+// A cache array as (64 values, 8 cells, 64s of values, groups of 8 cells,
+// pages and heads), copied `box` cells of a page at a time (see Cells).
 bool cache_map(CUtensorMap* map, const AttnParams& p, const void* base, int box) {
-  const uint64_t cell = (uint64_t)p.dim * 2;
-  const uint64_t dims[4] = {(uint64_t)p.dim, (uint64_t)p.page_size, (uint64_t)p.kv_heads,
-                            (uint64_t)std::max<int64_t>(p.num_pages, 1)};
-  const uint64_t strides[3] = {cell, cell * p.page_size, cell * p.page_size * p.kv_heads};
-  const uint32_t boxes[4] = {64, (uint32_t)box, 1, 1};
-  return encode_tmap(map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base, dims,
+  const uint64_t cell = (uint64_t)p.dim * 2, halves = p.dim / 64;
+  const uint64_t dims[5] = {64, 8, halves, (uint64_t)p.page_size / 8,
+                            (uint64_t)std::max<int64_t>(p.num_pages, 1) * p.kv_heads};
+  const uint64_t strides[4] = {cell, 128, 8 * cell, cell * p.page_size};
+  const uint32_t boxes[5] = {64, 8, (uint32_t)halves, (uint32_t)box / 8, 1};
+  return encode_tmap(map, p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, base, dims,
                      strides, boxes, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 

@@ -45,8 +45,7 @@ constexpr float kChunkLift = 8.0f, kChunkGrow = 6.0f;
 
 template <int D>
 struct ChunkLayout {
-  static constexpr int kHalf = kChunkKeys * 128;            // 64 values of a tile's keys
-  static constexpr int kTile = kHalf * (D / 64);
+  static constexpr int kTile = kChunkKeys * D * 2;          // keys (or values) of a unit
   static constexpr int kQHalf = 128 * 128;                  // 64 values of 128 rows of Q
   static constexpr int kQTile = kQHalf * (D / 64);
   static constexpr int kRing = 10;
@@ -68,13 +67,13 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// Shared-memory operand descriptors, 128-byte swizzled, in two words: the low
-// one has the address (in units of 16 bytes) and, for an operand whose K
-// dimension is the slow one in memory (rows of 64 values, one row per k), the
-// distance to its next 64 values; the high one is the same for both: 8-row
-// groups 1024 bytes apart, version, swizzle.
-constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint64_t desc(uint32_t low) { return ((uint64_t)kDescHigh << 32) | low; }
+// Shared-memory operand descriptors, 128-byte swizzled: the address (in units
+// of 16 bytes, as all below), the distance to the next 64 values where the K
+// dimension is the slow one in memory (V), the distance of 8-row groups.
+__device__ __forceinline__ uint64_t desc(uint32_t addr16, uint32_t next, uint32_t group) {
+  const uint32_t low = addr16 | (next >> 4) << 16, high = (group >> 4) | (1u << 14) | (2u << 29);
+  return ((uint64_t)high << 32) | low;
+}
 
 // One lane of the (converged) warp.  With this and warp-wide votes in the
 // conditions around it, the operands of the tensor instructions stay in
@@ -90,14 +89,6 @@ __device__ __forceinline__ bool elect() {
   return e != 0;
 }
 
-__device__ __forceinline__ void tma_load_page(uint32_t dst, const void* map, int c0, int c1, int c2, int c3,
-                                              uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(bar)) : "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -109,6 +100,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ ChunkParams F) {
   using L = ChunkLayout<D>;
+  using C = Cells<D>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const AttnParams& P = F.a;
@@ -170,7 +162,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
   if (warp == 8) {
     // ------------------------------------------------ key and value tiles
     const int none = P.num_pages > 0 ? (int)P.num_pages : 1;        // a page past the end reads as zeros
-    const int parts = kChunkKeys / F.box, copies = parts * (D / 64); // of one tile
+    const int parts = kChunkKeys / F.box;                            // of one tile
     uint32_t n = 0;                                                  // tiles issued
     do {
       const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
@@ -189,9 +181,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
             }
           }
         }
-        const int part = lane % parts, half = lane / parts;
-        page = __shfl_sync(0xffffffffu, page, part);
-        const int cell = (int)((key + (int64_t)part * F.box) & (P.page_size - 1));
+        const int cell = (int)((key + (int64_t)lane * F.box) & (P.page_size - 1));
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++n) {
           const uint32_t slot = n % L::kRing, use = n / L::kRing;
@@ -199,9 +189,9 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           const bool go = !*gave_up;
           if (lane == 0 && go) tc::mbar_arrive_expect_tx(&full[slot], L::kTile);
           __syncwarp();
-          if (lane < copies && go)
-            tma_load_page(ring + slot * L::kTile + half * L::kHalf + part * F.box * 128, kv ? &vmap : &kmap, half * 64,
-                          cell, w.head, page, &full[slot]);
+          if (lane < parts && go)
+            load_cells(ring + slot * L::kTile + lane * F.box * D * 2, kv ? &vmap : &kmap, cell >> 3, page, P.kv_heads,
+                       w.head, &full[slot]);
         }
       }
     } while (w.next(P, R, group));
@@ -217,7 +207,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     constexpr uint32_t kQK = tc::idesc_f16(128, kChunkKeys, BF16);
     constexpr uint32_t kPV = tc::idesc_f16(128, D, BF16) | (1u << 16);        // B: K is its slow dimension
     const int h = warp - 9;
-    const uint32_t q_low = (q_smem + h * L::kQTile) >> 4 | 1u << 16;
+    const uint32_t q_at = (q_smem + h * L::kQTile) >> 4;
     uint32_t n0 = 0, item = 0;            // ring tiles before this item: K of unit u is n0 + 2 u, V the next
     uint32_t uses0 = 0, uses1 = 0;        // of this half's S tiles, before this item
     auto landed = [&](uint32_t n) { wait(&full[n % L::kRing], n / L::kRing); };
@@ -226,13 +216,13 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     };
     auto qk = [&](int u) {
       const int b = u & 1;
-      const uint32_t n = n0 + 2 * u, k_low = (ring + n % L::kRing * L::kTile) >> 4 | 1u << 16;
+      const uint32_t n = n0 + 2 * u, k_at = (ring + n % L::kRing * L::kTile) >> 4;
       landed(n);
       if (elect()) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          tc::mma_f16_ss(s_at(h, b), desc(q_low + (((k >> 2) * L::kQHalf + (k & 3) * 32) >> 4)),
-                         desc(k_low + (((k >> 2) * L::kHalf + (k & 3) * 32) >> 4)), kQK, k > 0);
+          tc::mma_f16_ss(s_at(h, b), desc(q_at + (((k >> 2) * L::kQHalf + (k & 3) * 32) >> 4), 16, 1024),
+                         desc(k_at + (((k >> 2) * C::kNext + (k & 3) * 32) >> 4), 16, C::kGroup), kQK, k > 0);
         tc::mma_commit(&s_full[2 * h + b]);
       }
       __syncwarp();
@@ -265,19 +255,19 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           for (int i = lane; i < kChunkKeys * (D / 8); i += 32) {
             const int r = i / (D / 8), c = i % (D / 8);
             if (r < first || r >= end)
-              *reinterpret_cast<uint4*>(v + (c >> 3) * L::kHalf + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(v + C::at(r, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
           }
           tc::fence_proxy_async_smem();
           __syncwarp();
         }
         wait(&p_full[2 * h + b], use);
         tc::fence_after_sync();
-        const uint32_t v_low = (ring + (n + 1) % L::kRing * L::kTile) >> 4 | (uint32_t)(L::kHalf >> 4) << 16;
+        const uint32_t v_at = (ring + (n + 1) % L::kRing * L::kTile) >> 4;
         if (elect()) {
-          mma_f16_ts(o_at(h), s_at(h, b), desc(v_low), kPV, u > 0);
+          mma_f16_ts(o_at(h), s_at(h, b), desc(v_at, C::kNext, C::kGroup), kPV, u > 0);
 #pragma unroll
           for (int k = 1; k < kChunkKeys / 16; ++k)
-            mma_f16_ts(o_at(h), s_at(h, b) + 8 * k, desc(v_low + k * (2048 >> 4)), kPV, 1);
+            mma_f16_ts(o_at(h), s_at(h, b) + 8 * k, desc(v_at + (k * 2 * C::kGroup >> 4), C::kNext, C::kGroup), kPV, 1);
           tc::mma_commit(&pv_done[2 * h + b]);
         }
         __syncwarp();
@@ -304,6 +294,27 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
     auto sync = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
     uint32_t uses0 = 0, uses1 = 0;              // of this half's S tiles, before this item
+    // This thread's row of the item's Q, negated where the scale is, so that the largest score has the largest weight
+    auto load_q = [&](const Walk<kChunkRows, kChunkKeys>& x) {
+      const int r = h * 128 + row, rows = min(kChunkRows, x.s.n * group - x.tile * kChunkRows);
+      if (h * 128 >= rows) return;
+      uint8_t* dst = smem + h * L::kQTile;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q)) +
+                         (r < rows ? out_row(P, x.s, x.head, group, x.tile * kChunkRows + r) * (D / 8) : 0);
+      uint4 v[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) v[i] = r < rows ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        v[i].x ^= flip, v[i].y ^= flip, v[i].z ^= flip, v[i].w ^= flip;
+        *reinterpret_cast<uint4*>(dst + (i >> 3) * L::kQHalf + tc::sw128_offset(row, i & 7)) = v[i];
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&q_full[h]);
+    };
+    load_q(w);
+    bool more;
     do {
       const int row0 = w.tile * kChunkRows, rows = min(kChunkRows, w.s.n * group - row0);
       const int halves = rows > 128 ? 2 : 1, r = h * 128 + row, units = w.u1 - w.u0;
@@ -311,19 +322,6 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
       float m = -INFINITY, l = 0.f;
       const int64_t out_at = mine ? out_row(P, w.s, w.head, group, row0 + r) * D : 0;
       if (h < halves) {
-        // Q, negated where the scale is, so that the largest score has the largest weight
-        uint8_t* dst = smem + h * L::kQTile;
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.q) + out_at);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          uint4 v = mine ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-          *reinterpret_cast<uint4*>(dst + (i >> 3) * L::kQHalf + tc::sw128_offset(row, i & 7)) = v;
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&q_full[h]);
-
         // the keys this row sees, as positions within the item
         const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
         const int64_t pos = w.s.kv - w.s.n + (row0 + r) / group, from = P.window ? pos - P.window + 1 : 0;
@@ -391,6 +389,13 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&p_full[2 * h + b]);
         }
+      }
+      // every score of this item is there, so Q's place is free: the next item's first scores are made while this
+      // item's results are written
+      auto x = w;
+      more = x.next(P, R, group);
+      if (more) load_q(x);
+      if (h < halves) {
         // the item's last product (the ones before it are done when it is)
         wait(&pv_done[2 * h + ((units - 1) & 1)], ((units - 1) & 1 ? uses1 : uses0) + ((units - 1) >> 1));
         tc::fence_after_sync();
@@ -445,7 +450,8 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         if (arrive(static_cast<unsigned*>(P.workspace) + c0, c1 - c0 + 1, last, tid == 0, sync))
           combine_rows<kChunkRows, D, BF16>(P, pieces, c0, c1, mine, r, out_at);
       }
-    } while (w.next(P, R, group));
+      w = x;
+    } while (more);
   }
   tc::fence_before_sync();
   __syncthreads();

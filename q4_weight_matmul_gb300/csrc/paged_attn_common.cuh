@@ -15,6 +15,7 @@
 #pragma once
 
 #include "q4k_internal.h"
+#include "tc_ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,6 +25,31 @@ namespace attn {
 
 constexpr int kMaxCtas = 160;           // of a launch
 constexpr int kTicketBytes = 1024;      // leading workspace bytes: one counter per CTA
+
+// Keys (or values) in shared memory: groups of 8 cells, per group the first
+// 64 values of its cells, then the next 64; a cell's 64 values are 128 bytes,
+// 128-byte swizzled.  The cache's tensor map has the same dimensions (values,
+// cell of the group, 64s of values, group of the page, page and head), so one
+// copy brings up to a whole page of a head.
+template <int D>
+struct Cells {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kNext = 1024;                    // bytes to the next 64 values
+  static constexpr int kGroup = kNext * kHalves;        // bytes of 8 cells
+  static __device__ __forceinline__ uint32_t at(int cell, int half, int chunk) {
+    return (uint32_t)((cell >> 3) * kGroup + half * kNext + (cell & 7) * 128 + ((chunk ^ (cell & 7)) << 4));
+  }
+};
+
+// Copy cells of page `page` (num_pages or more: zeros) and key head `head`,
+// from 8-cell group `group` of the page on.
+__device__ __forceinline__ void load_cells(uint32_t dst, const void* map, int group, int page, int kv_heads, int head,
+                                           uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %2, %2, %3, %4}], [%5];"
+      ::"r"(dst), "l"(map), "r"(0), "r"(group), "r"(page * kv_heads + head), "r"(tc::smem_u32(bar)) : "memory");
+}
 
 struct Shape {             // of one request
   int q0, n;               // first token, new tokens

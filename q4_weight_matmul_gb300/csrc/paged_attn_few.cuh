@@ -36,9 +36,7 @@ constexpr float kLift = 14.0f;          // weights are held times 2^14
 
 template <int D>
 struct FewLayout {
-  static constexpr int kHalf = kUnit * 128;                // bytes of 64 values of every key of a slot
-  static constexpr int kHalves = D / 64;
-  static constexpr int kTile = kHalf * kHalves;            // keys (or values) of a slot
+  static constexpr int kTile = kUnit * D * 2;              // keys (or values) of a slot
   static constexpr int kSlot = 2 * kTile;
 };
 
@@ -80,14 +78,6 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c0, int c1, int c2, int c3,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5}], [%6];"
-      ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_u32(bar)) : "memory");
 }
 
 struct FewParams {
@@ -171,13 +161,10 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
           const int page = __shfl_sync(0xffffffffu, entry, (int)(p0 + i - cached));
           const int cell = (int)(key & (P.page_size - 1));
           if (lane == 0 && !*gave_up) {
-            const uint32_t dst = ring + slot * L::kSlot + i * F.box * 128;
-#pragma unroll
-            for (int h = 0; h < L::kHalves; ++h) {
-              tma_load_4d(dst + h * L::kHalf, &kmap, h * 64, F.box < kUnit ? 0 : cell, w.head, page, &full[slot]);
-              tma_load_4d(dst + L::kTile + h * L::kHalf, &vmap, h * 64, F.box < kUnit ? 0 : cell, w.head, page,
-                          &full[slot]);
-            }
+            const uint32_t dst = ring + slot * L::kSlot + i * F.box * D * 2;
+            const int from = F.box < kUnit ? 0 : cell >> 3;
+            load_cells(dst, &kmap, from, page, P.kv_heads, w.head, &full[slot]);
+            load_cells(dst + L::kTile, &vmap, from, page, P.kv_heads, w.head, &full[slot]);
           }
         }
       }
@@ -265,7 +252,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
           for (int t = 0; t < 4; ++t) {
             uint32_t b[4];
             const int key = 8 * t + (lane & 7), chunk = 4 * (k & 1) + (lane >> 3);
-            ldsm4(b, ks + (k >> 1) * L::kHalf + tc::sw128_offset(key, chunk));
+            ldsm4(b, ks + Cells<D>::at(key, k >> 1, chunk));
             mma16816<BF16>(s[t], q[2 * k], b[0], b[1]);
             mma16816<BF16>(s[t], q[2 * k + 1], b[2], b[3]);
           }
@@ -347,7 +334,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
           for (int k = 0; k < 2; ++k) {
             uint32_t b[4];   // (keys 0-7, values 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
             const int key = 16 * k + (lane & 15), chunk = 2 * (n & 3) + (lane >> 4);
-            ldsm4t(b, vs + (n >> 2) * L::kHalf + tc::sw128_offset(key, chunk));
+            ldsm4t(b, vs + Cells<D>::at(key, n >> 2, chunk));
             b[0] &= keep[k][0], b[1] &= keep[k][1], b[2] &= keep[k][0], b[3] &= keep[k][1];
             if constexpr (PACK) {
 #pragma unroll
