@@ -166,7 +166,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     uint32_t n = 0;                                                  // tiles issued
     do {
       const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
-      const int32_t* table = P.page_table + w.req * P.max_pages;
+      const int32_t* table = P.page_table + (int64_t)w.req * P.max_pages;
       for (int u = w.u0; u < w.u1; ++u) {
         // lane i has part i's page (parts <= 8)
         const int64_t key = key0 + (int64_t)u * kChunkKeys;

@@ -53,133 +53,200 @@ __device__ __forceinline__ void load_cells(uint32_t dst, const void* map, int gr
 
 struct Shape {             // of one request
   int q0, n;               // first token, new tokens
-  int64_t kv;              // keys
+  int kv;                  // keys
 };
 
 // The request's shape, cut to what the call's arrays hold; what was out of
 // range is reported.
-__device__ __forceinline__ Shape request(const AttnParams& P, int64_t r) {
-  int a = P.cu_q[r], b = P.cu_q[r + 1];
-  int64_t kv = P.kv_len[r];
-  const int64_t most = P.max_pages * P.page_size;
+__device__ __forceinline__ Shape request(const AttnParams& P, int r) {
+  int a = P.cu_q[r], b = P.cu_q[r + 1], kv = P.kv_len[r];
+  const int most = (int)(P.max_pages * P.page_size);                  // below 2^31
   if (a < 0 || b < a || b > P.tokens || b - a > P.max_q || kv < 0 || kv > most) {
     atomicOr(P.err, kErrIndex);
     a = max(0, min(a, (int)P.tokens));
     b = max(a, min(b, (int)P.tokens));
     b = min(b, a + (int)P.max_q);
-    kv = kv < 0 ? 0 : min(kv, most);
+    kv = max(0, min(kv, most));
   }
   return {a, b - a, kv};
 }
 
 // The keys lo <= j < hi that some row of rows r0 .. r1-1 (of the request's
 // n * group rows) sees.
-__device__ __forceinline__ void key_range(const Shape& s, int group, int window, int r0, int r1, int64_t& lo,
-                                          int64_t& hi) {
-  const int64_t first = s.kv - s.n + r0 / group, last = s.kv - s.n + (r1 - 1) / group;
-  hi = last + 1 > 0 ? last + 1 : 0;
-  lo = window ? first - window + 1 : 0;
-  if (lo < 0) lo = 0;
-  if (lo > hi) lo = hi;
+__device__ __forceinline__ void key_range(const Shape& s, int group, int window, int r0, int r1, int& lo, int& hi) {
+  const int first = s.kv - s.n + r0 / group, last = s.kv - s.n + (r1 - 1) / group;
+  hi = max(last + 1, 0);
+  lo = window && first >= window ? first - window + 1 : 0;
+  lo = min(lo, hi);
 }
 
 // Units of row tile m (0 .. tiles-1): at least one, so that a tile that sees
 // no key is still written.
 template <int ROWS, int UNIT>
-__device__ __forceinline__ int tile_units(const Shape& s, int group, int window, int m, int64_t& lo, int64_t& hi) {
+__device__ __forceinline__ int tile_units(const Shape& s, int group, int window, int m, int& lo, int& hi) {
   const int rows = s.n * group;
   key_range(s, group, window, m * ROWS, min((m + 1) * ROWS, rows), lo, hi);
-  const int64_t u = (hi + UNIT - 1) / UNIT - lo / UNIT;
-  return u > 0 ? (int)u : 1;
+  return max((int)(((unsigned)hi + UNIT - 1) / UNIT) - lo / UNIT, 1);
 }
 
+// Units of all row tiles of one key head.  The lanes of the (converged) warp
+// share the tiles.
 template <int ROWS, int UNIT>
-__device__ __forceinline__ int64_t request_units(const AttnParams& P, const Shape& s, int group) {
-  if (s.n == 0) return 0;
+__device__ __forceinline__ int64_t head_units(const AttnParams& P, const Shape& s, int group) {
   const int tiles = (s.n * group + ROWS - 1) / ROWS;
-  int64_t sum = 0, lo, hi;
-  for (int m = 0; m < tiles; ++m) sum += tile_units<ROWS, UNIT>(s, group, P.window, m, lo, hi);
+  int64_t sum = 0;
+  int lo, hi;
+  for (int m = threadIdx.x & 31; m < tiles; m += 32) sum += tile_units<ROWS, UNIT>(s, group, P.window, m, lo, hi);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum;
 }
 
 // This CTA's share of the work.
 struct Range {
   int64_t begin, end, total;
-  int64_t req, req_base;      // the request that holds `begin`, the units before it
+  int64_t share;              // units of a CTA; the first `longer` CTAs have one more
+  int longer;
+  int64_t req_base, per_head; // units before the request that holds `begin`, units of each of its heads
+  int req;
   int ctas;                   // CTAs that have work (the others have none)
 };
 
-// Collective over the block (THREADS threads, a multiple of 32).
+// a / b for a >= 0, b > 0: in 32 bits where they fit (a 64-bit division takes some hundred cycles).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+__device__ __forceinline__ void set_share(Range& R, int64_t total, int min_units) {
+  const int64_t n = divide(total + min_units - 1, min_units);
+  const int b = blockIdx.x;
+  R.total = total;
+  R.ctas = (int)(n < gridDim.x ? n : gridDim.x);
+  if (b >= R.ctas) return;
+  R.share = divide(total, R.ctas);
+  R.longer = (int)(total - R.share * R.ctas);
+  R.begin = R.share * b + min(b, R.longer);
+  R.end = R.begin + R.share + (b < R.longer ? 1 : 0);
+}
+
+__device__ __forceinline__ int64_t scan_up(int64_t v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += up;
+  }
+  return v;
+}
+
+// Collective over the block (THREADS threads, a multiple of 32); `scratch` is
+// W + 3 words.  Requests are looked at one per lane where none has more than
+// one row tile, else one per warp, whose lanes share its tiles.  Up to some
+// number of requests every warp does that by itself, without a barrier of the
+// block (2 us less for one request); beyond it the warps share the requests.
 template <int ROWS, int UNIT, int THREADS>
 __device__ __forceinline__ Range share_out(const AttnParams& P, int group, int min_units, int64_t* scratch) {
   constexpr int W = THREADS / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Range R{0, 0, 0, 0, 0, 0};
-  // all units
-  int64_t mine = 0;
-  for (int64_t r = tid; r < P.n_req; r += THREADS)
-    mine += P.kv_heads * request_units<ROWS, UNIT>(P, request(P, r), group);
-  int64_t v = mine;
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) scratch[warp] = v;
-  __syncthreads();
-  for (int w = 0; w < W; ++w) R.total += scratch[w];
-  const int64_t n = (R.total + min_units - 1) / min_units;
-  R.ctas = (int)(n < gridDim.x ? n : gridDim.x);
-  if (R.ctas < 1 || (int)blockIdx.x >= R.ctas) return R;      // the whole block
-  R.begin = R.total * blockIdx.x / R.ctas;
-  R.end = R.total * (blockIdx.x + 1) / R.ctas;
-  // the request that holds the first unit
-  int64_t base = 0;
-  for (int64_t r0 = 0; r0 < P.n_req; r0 += THREADS) {
-    const int64_t r = r0 + tid;
-    // with one request per thread the first pass has the units already
-    const int64_t own = P.n_req <= THREADS ? mine
-                        : r < P.n_req ? P.kv_heads * request_units<ROWS, UNIT>(P, request(P, r), group) : 0;
-    int64_t incl = own;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+  const int n_req = (int)P.n_req;
+  const bool single = P.max_q * group <= ROWS;
+  Range R{};
+  auto units = [&](int r) -> int64_t {                  // single: of the lane's request; else of the warp's
+    if (r >= n_req) return 0;
+    const Shape s = request(P, r);
+    int lo, hi;
+    if (single) return s.n ? (int64_t)P.kv_heads * tile_units<ROWS, UNIT>(s, group, P.window, 0, lo, hi) : 0;
+    return P.kv_heads * head_units<ROWS, UNIT>(P, s, group);
+  };
+
+  if (n_req <= (single ? 128 : 8)) {
+    int64_t mine = 0, all = 0;                          // !single: lane r keeps request r's units
+    if (single) {
+      for (int r = lane; r < n_req; r += 32) all += units(r);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    } else {
+      for (int r = 0; r < n_req; ++r) {
+        const int64_t u = units(r);
+        all += u;
+        if (lane == r) mine = u;
+      }
     }
+    set_share(R, all, min_units);
+    if ((int)blockIdx.x >= R.ctas) return R;
+    int64_t base = 0;
+    for (int r0 = 0; r0 < n_req; r0 += 32) {
+      const int64_t own = single ? units(r0 + lane) : mine, incl = scan_up(own);
+      const unsigned past = __ballot_sync(0xffffffffu, R.begin < base + incl);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        R.req = r0 + src;
+        R.req_base = base + __shfl_sync(0xffffffffu, incl - own, src);
+        R.per_head = divide(__shfl_sync(0xffffffffu, own, src), P.kv_heads);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return R;
+  }
+
+  const int step = single ? THREADS : W, index = single ? tid : warp;
+  int64_t all = 0;
+  for (int r = index; r < n_req; r += step) all += units(r);
+  if (single)
+    for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  if (lane == 0) scratch[warp] = all;
+  __syncthreads();
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) all += scratch[w];
+  set_share(R, all, min_units);
+  if ((int)blockIdx.x >= R.ctas) return R;              // the whole block
+  int64_t base = 0;
+  for (int r0 = 0; r0 < n_req; r0 += step) {
+    const int64_t own = units(r0 + index);
+    int64_t incl = single ? scan_up(own) : own;
     __syncthreads();
-    if (lane == 31) scratch[warp] = incl;
+    if (lane == (single ? 31 : 0)) scratch[warp] = incl;
     __syncthreads();
-    int64_t all = 0;
+    int64_t sum = 0;
+#pragma unroll
     for (int w = 0; w < W; ++w) {
       if (w < warp) incl += scratch[w];
-      all += scratch[w];
+      sum += scratch[w];
     }
     const int64_t at = base + incl - own;
-    if (own > 0 && R.begin >= at && R.begin < at + own) {
-      scratch[W] = r;
+    if ((single || lane == 0) && own > 0 && R.begin >= at && R.begin < at + own) {
+      scratch[W] = r0 + index;
       scratch[W + 1] = at;
+      scratch[W + 2] = own;
     }
-    base += all;
-    if (R.begin < base) break;                                // the same for every thread
+    base += sum;
+    if (R.begin < base) break;                          // the same for every thread
   }
   __syncthreads();
-  R.req = scratch[W];
+  R.req = (int)scratch[W];
   R.req_base = scratch[W + 1];
-  __syncthreads();
+  R.per_head = divide(scratch[W + 2], P.kv_heads);
   return R;
 }
 
 __device__ __forceinline__ int owner(int64_t unit, const Range& R) {
-  return (int)(((unit + 1) * R.ctas - 1) / R.total);
+  const int64_t past = unit - (R.share + 1) * R.longer;
+  return (int)(past < 0 ? divide(unit, R.share + 1) : R.longer + divide(past, R.share));
 }
 
 // The items of a CTA's range, one after another.
 template <int ROWS, int UNIT>
 struct Walk {
   Shape s;
-  int64_t req;
-  int head, tile, tiles;
+  int req, head, tile, tiles;
   int64_t at;              // first unit of the item in the order of all
   int units;               // of the item
-  int64_t lo, hi;          // its keys
+  int lo, hi;              // its keys
   int u0, u1;              // the item's units that this CTA has
 
-  __device__ __forceinline__ void load(const AttnParams& P, int64_t r, int group) {
+  __device__ __forceinline__ void load(const AttnParams& P, int r, int group) {
     req = r;
     s = request(P, r);
     tiles = (s.n * group + ROWS - 1) / ROWS;
@@ -188,16 +255,25 @@ struct Walk {
     u0 = (int)(R.begin > at ? R.begin - at : 0);
     u1 = (int)(R.end < at + units ? R.end - at : units);
   }
+  // Converged warps: the lanes look for the tile together.
   __device__ __forceinline__ void first(const AttnParams& P, const Range& R, int group) {
     load(P, R.req, group);
-    const int64_t per_head = request_units<ROWS, UNIT>(P, s, group);
-    head = (int)((R.begin - R.req_base) / per_head);
-    at = R.req_base + head * per_head;
-    for (tile = 0;; ++tile) {
-      units = tile_units<ROWS, UNIT>(s, group, P.window, tile, lo, hi);
-      if (R.begin < at + units) break;
-      at += units;
+    head = (int)divide(R.begin - R.req_base, R.per_head);
+    at = R.req_base + head * R.per_head;
+    const int lane = threadIdx.x & 31;
+    for (int m0 = 0;; m0 += 32) {
+      const int64_t own = m0 + lane < tiles ? tile_units<ROWS, UNIT>(s, group, P.window, m0 + lane, lo, hi) : 0;
+      const int64_t incl = scan_up(own);
+      const unsigned past = __ballot_sync(0xffffffffu, R.begin < at + incl);
+      if (past) {
+        const int src = __ffs(past) - 1;
+        tile = m0 + src;
+        at += __shfl_sync(0xffffffffu, incl - own, src);
+        break;
+      }
+      at += __shfl_sync(0xffffffffu, incl, 31);
     }
+    units = tile_units<ROWS, UNIT>(s, group, P.window, tile, lo, hi);
     cut(R);
   }
   // false: the range is done
@@ -252,12 +328,13 @@ __device__ __forceinline__ int64_t out_row(const AttnParams& P, const Shape& s, 
 
 // Arrive with this CTA's piece of an item held by CTAs c0..c1; true in every
 // thread of the last CTA.  `flag` is shared; SYNC is a barrier of the calling
-// threads, `leader` one of them.
+// threads, `leader` one of them: its fence covers the stores that the barrier
+// put before it.
 template <class SYNC>
 __device__ __forceinline__ bool arrive(unsigned* ticket, int pieces, int* flag, bool leader, SYNC sync) {
-  __threadfence();
   sync();
   if (leader) {
+    __threadfence();
     const bool last = atomicAdd(ticket, 1u) == (unsigned)(pieces - 1);
     if (last) *ticket = 0u;                      // ready for the next call
     __threadfence();
@@ -267,34 +344,57 @@ __device__ __forceinline__ bool arrive(unsigned* ticket, int pieces, int* flag, 
   return *flag != 0;
 }
 
-// Add the pieces of CTAs c0..c1 up and write the item's rows: `n` threads,
-// this one is `t`.  weights: kMaxCtas * ROWS shared floats.
-template <int ROWS, int D, bool BF16, class SYNC>
+// Add the pieces of CTAs c0..c1 up and write the item's rows: WARPS warps,
+// this thread is `t` of them.  weights: kMaxCtas * ROWS shared floats.
+template <int ROWS, int D, bool BF16, int WARPS, class SYNC>
 __device__ __forceinline__ void combine(const AttnParams& P, const float* pieces, int c0, int c1, const Shape& s,
-                                        int head, int group, int row0, int rows, float* weights, int t, int n,
-                                        SYNC sync) {
+                                        int head, int group, int row0, int rows, float* weights, int t, SYNC sync) {
   // piece of CTA c: slot 1 (the item starts in its range) for the first, slot 0 for the others
   auto piece = [&](int c) { return pieces + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * piece_floats<ROWS, D>(); };
-  const int np = c1 - c0 + 1;
-  for (int r = t; r < rows; r += n) {
-    float m = -INFINITY;
-    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(piece(c) + ROWS * D + r));
-    float l = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float mc = __ldcg(piece(c) + ROWS * D + r);
-      const float w = mc == -INFINITY ? 0.f : exp2f(mc - m);
-      l += w * __ldcg(piece(c) + ROWS * D + ROWS + r);
-      weights[(c - c0) * ROWS + r] = w;
+  const int np = c1 - c0 + 1, lane = t & 31;
+  // a warp per row: the lanes have its pieces' statistics
+  for (int r = t >> 5; r < rows; r += WARPS) {
+    constexpr int K = kMaxCtas / 32;
+    float m[K], l[K], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = c0 + 32 * k + lane;
+      m[k] = c <= c1 ? __ldcg(piece(c) + ROWS * D + r) : -INFINITY;
+      l[k] = c <= c1 ? __ldcg(piece(c) + ROWS * D + ROWS + r) : 0.f;
+      top = fmaxf(top, m[k]);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int c = 0; c < np; ++c) weights[c * ROWS + r] *= inv;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      m[k] = m[k] == -INFINITY ? 0.f : exp2f(m[k] - top);
+      sum += m[k] * l[k];
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (32 * k + lane < np) weights[(32 * k + lane) * ROWS + r] = m[k] * inv;
   }
   sync();
-  for (int e = t; e < rows * (D / 4); e += n) {
+  for (int e = t; e < rows * (D / 4); e += 32 * WARPS) {
     const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    int c = 0;
+    constexpr int B = 8;                       // loads in flight
+    for (; c + B <= np; c += B) {
+      float4 v[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(piece(c0 + c + k) + r * D + d));
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const float w = weights[(c + k) * ROWS + r];
+        a.x = fmaf(w, v[k].x, a.x), a.y = fmaf(w, v[k].y, a.y), a.z = fmaf(w, v[k].z, a.z), a.w = fmaf(w, v[k].w, a.w);
+      }
+    }
 #pragma unroll 4
-    for (int c = 0; c < np; ++c) {
+    for (; c < np; ++c) {
       const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(c0 + c) + r * D + d));
       const float w = weights[c * ROWS + r];
       a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
@@ -312,7 +412,9 @@ __device__ __forceinline__ void combine_rows(const AttnParams& P, const float* p
   if (!mine) return;
   auto piece = [&](int c) { return pieces + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * piece_floats<ROWS, D>(); };
   float m = -INFINITY, l = 0.f;
+#pragma unroll 4
   for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(piece(c) + ROWS * D + r));
+#pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     const float mc = __ldcg(piece(c) + ROWS * D + r);
     if (mc != -INFINITY) l += exp2f(mc - m) * __ldcg(piece(c) + ROWS * D + ROWS + r);

@@ -31,7 +31,7 @@ namespace attn {
 
 constexpr int kUnit = 32;               // keys of a slot
 constexpr int kConsumers = 8;           // consumer warps
-constexpr int kFewThreads = 32 * (kConsumers + 1);
+constexpr int kFewThreads = 32 * (kConsumers + 4);   // the producer's warpgroup: one warp works
 constexpr float kLift = 14.0f;          // weights are held times 2^14
 
 template <int D>
@@ -60,13 +60,11 @@ struct FewConfig {
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (BF16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -117,8 +115,9 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const Range R = share_out<ROWS, kUnit, kFewThreads>(P, group, F.min_units, scratch);   // syncs the block
+  const Range R = share_out<ROWS, kUnit, kFewThreads>(P, group, F.min_units, scratch);
   if ((int)blockIdx.x >= R.ctas) return;
+  __syncthreads();                                   // the barriers are there
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!tc::mbar_wait(bar, parity, gave_up) && !*gave_up) {
       *gave_up = 1;
@@ -130,13 +129,16 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   w.first(P, R, group);
   uint32_t issued = 0;                               // slots before this item, the same count in every warp
 
-  if (warp == kConsumers) {
+  // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+  if (warp >= kConsumers) {
     // ---------------------------------------------------------- producer
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp > kConsumers) return;
     const int pages_slot = F.box < kUnit ? kUnit / F.box : 1;
     const int none = P.num_pages > 0 ? (int)P.num_pages : 1;    // a page past the end reads as zeros
     do {
       const int64_t key0 = (w.lo / kUnit) * kUnit;
-      const int32_t* table = P.page_table + w.req * P.max_pages;
+      const int32_t* table = P.page_table + (int64_t)w.req * P.max_pages;
       int64_t cached = -1;                           // page index that lane 0's entry is for
       int entry = none;
       for (int u = w.u0; u < w.u1; ++u, ++issued) {
@@ -178,7 +180,9 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   }
 
   // ------------------------------------------------------------ consumers
-  auto sync = [&] { asm volatile("bar.sync 1, %0;" ::"n"(32 * kConsumers) : "memory"); };
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  constexpr int kThreads = 32 * kConsumers;
+  auto sync = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   const uint32_t grp = warp / WR;
   const int wr = warp % WR;
   const int g = lane >> 2, c2 = (lane & 3) * 2;
@@ -248,14 +252,13 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
           for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {              // 32 values: chunks 4k .. 4k+3
+          uint32_t b[4][4];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            uint32_t b[4];
-            const int key = 8 * t + (lane & 7), chunk = 4 * (k & 1) + (lane >> 3);
-            ldsm4(b, ks + Cells<D>::at(key, k >> 1, chunk));
-            mma16816<BF16>(s[t], q[2 * k], b[0], b[1]);
-            mma16816<BF16>(s[t], q[2 * k + 1], b[2], b[3]);
-          }
+          for (int t = 0; t < 4; ++t) ldsm4(b[t], ks + Cells<D>::at(8 * t + (lane & 7), k >> 1, 4 * (k & 1) + (lane >> 3)));
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma16816<BF16>(s[t], q[2 * k], b[t][0], b[t][1]);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma16816<BF16>(s[t], q[2 * k + 1], b[t][2], b[t][3]);
         }
         // scores in units of log 2, masked where a row does not see the key
         const int at = u * kUnit;
@@ -315,8 +318,9 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
         l_a = l_a * f_a + add_a;
         l_b = l_b * f_b + add_b;
         // values that no row of the tile sees may be anything: they become zeros
-        uint32_t keep[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
-        if (at < lo_item || at + kUnit > hi_item) {
+        uint32_t keep[2][2];
+        const bool edge = at < lo_item || at + kUnit > hi_item;
+        if (edge) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -326,35 +330,46 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
                            (j + 1 >= lo_item && j + 1 < hi_item ? 0xffff0000u : 0u);
             }
         }
-        // O += P V, 16 values (two tiles of 8) at a time
+        // O += P V, 32 values (four tiles of 8) at a time
 #pragma unroll
-        for (int n = 0; n < D / 16; ++n) {
-          float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        for (int n = 0; n < D / 32; ++n) {
+          float acc[4][4];
+          uint32_t b[2][2][4];   // [16 values][16 keys]: (keys 0-7, values 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              ldsm4t(b[j][k], vs + Cells<D>::at(16 * k + (lane & 15), n >> 1, 4 * (n & 1) + 2 * j + (lane >> 4)));
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) b[j][k][e] &= keep[k][e & 1];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            uint32_t b[4];   // (keys 0-7, values 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
-            const int key = 16 * k + (lane & 15), chunk = 2 * (n & 3) + (lane >> 4);
-            ldsm4t(b, vs + Cells<D>::at(key, n >> 2, chunk));
-            b[0] &= keep[k][0], b[1] &= keep[k][1], b[2] &= keep[k][0], b[3] &= keep[k][1];
-            if constexpr (PACK) {
+            constexpr int STEP = PACK ? 2 : 1;
 #pragma unroll
-              for (int i = 0; i < PARTS; i += 2) {
-                const uint32_t a[4] = {p[i][k][0], i + 1 < PARTS ? p[i + 1 < PARTS ? i + 1 : i][k][0] : 0u, p[i][k][2],
-                                       i + 1 < PARTS ? p[i + 1 < PARTS ? i + 1 : i][k][2] : 0u};
-                mma16816<BF16>(acc[0], a, b[0], b[1]);
-                mma16816<BF16>(acc[1], a, b[2], b[3]);
+            for (int i = 0; i < PARTS; i += STEP) {
+              uint32_t a[4];
+              if constexpr (PACK) {
+                const int lo = i + 1 < PARTS ? i + 1 : i;
+                a[0] = p[i][k][0], a[2] = p[i][k][2];
+                a[1] = i + 1 < PARTS ? p[lo][k][0] : 0u, a[3] = i + 1 < PARTS ? p[lo][k][2] : 0u;
+              } else {
+                a[0] = p[i][k][0], a[1] = p[i][k][1], a[2] = p[i][k][2], a[3] = p[i][k][3];
               }
-            } else {
 #pragma unroll
-              for (int i = 0; i < PARTS; ++i) {
-                mma16816<BF16>(acc[0], p[i][k], b[0], b[1]);
-                mma16816<BF16>(acc[1], p[i][k], b[2], b[3]);
-              }
+              for (int j = 0; j < 4; ++j) mma16816<BF16>(acc[j], a, b[j >> 1][k][2 * (j & 1)], b[j >> 1][k][2 * (j & 1) + 1]);
             }
           }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float(&x)[PACK ? 2 : 4] = o[2 * n + i];
+          for (int i = 0; i < 4; ++i) {
+            float(&x)[PACK ? 2 : 4] = o[4 * n + i];
             if constexpr (PACK) {
               x[0] = fmaf(x[0], f_a, acc[i][0] + acc[i][2]);
               x[1] = fmaf(x[1], f_a, acc[i][1] + acc[i][3]);
@@ -391,7 +406,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     sync();
     const bool whole = w.u0 == 0 && w.u1 == w.units;
     float* mine = pieces + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * piece_floats<ROWS, D>();
-    for (int e = tid; e < rows * (D / 4); e += 32 * kConsumers) {
+    for (int e = tid; e < rows * (D / 4); e += kThreads) {
       const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
       float m = -INFINITY;
 #pragma unroll
@@ -424,7 +439,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     } else {
       const int c0 = owner(w.at, R), c1 = owner(w.at + w.units - 1, R);
       if (arrive(static_cast<unsigned*>(P.workspace) + c0, c1 - c0 + 1, last, tid == 0, sync))
-        combine<ROWS, D, BF16>(P, pieces, c0, c1, w.s, w.head, group, row0, rows, sum, tid, 32 * kConsumers, sync);
+        combine<ROWS, D, BF16, kConsumers>(P, pieces, c0, c1, w.s, w.head, group, row0, rows, sum, tid, sync);
     }
   } while (w.next(P, R, group));
 }
