@@ -1,12 +1,16 @@
 // q4k_qk_norm_rope: per-head RMS norm and rotation of queries and keys, and
 // the store of keys and values into the paged cache.
 //
-// A row is one head of one token: 4 D bytes in, 2 D bytes out, and about six
-// operations a value between them, so HBM bounds it.  D/4 lanes share a row
-// (16-byte loads, 8-byte stores); a warp takes kRows row slots of one token
-// and has all their loads in flight at once, together with the token's
-// cosines and sines, which it then uses for every row.  A row's rotation
-// partner sits rot/8 lanes away (or in the same lane when interleaved).
+// A row is one head of one token: 4 D bytes in, 2 D bytes out, and some ten
+// instructions per 16 bytes between them, so HBM bounds it as long as the
+// instructions stay few.  D/8 lanes share a row, each with 4 values of its
+// lower half and the 4 at the same place of its upper half (16-byte loads,
+// 8-byte stores): where the whole head is rotated by halves, or neighbours
+// are, a lane then has both values of its pairs (PAIRS), and only the sum of
+// squares crosses lanes.  Rotating a part of the head by halves takes the
+// partner's value from another lane.  A warp takes kLoads rows per group of
+// lanes, all of one token, with their loads in flight at once, and reads the
+// token's cosines and sines once for all of them.
 #include "q4k_internal.h"
 
 #include <cuda_bf16.h>
@@ -15,48 +19,61 @@
 namespace q4k {
 namespace {
 
-constexpr int kLoads = 4;   // row loads in flight per lane
+constexpr int kLoads = 4;   // rows in flight per group of lanes
 
 template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
+__device__ __forceinline__ uint2 pack4(const float4& v) {
+  uint2 r;
   if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    r.x = *reinterpret_cast<const uint32_t*>(&a), r.y = *reinterpret_cast<const uint32_t*>(&b);
   } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
+    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+    r.x = *reinterpret_cast<const uint32_t*>(&a), r.y = *reinterpret_cast<const uint32_t*>(&b);
   }
+  return r;
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P) {
-  constexpr int kLanes = D / 4;             // lanes of a row
+__device__ __forceinline__ float4 mul(const float4& a, const float4& b) {
+  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+__device__ __forceinline__ float4 mul(const float4& a, float b) { return make_float4(a.x * b, a.y * b, a.z * b, a.w * b); }
+// a b + c d
+__device__ __forceinline__ float4 mul2(const float4& a, const float4& b, const float4& c, const float4& d) {
+  return make_float4(fmaf(a.x, b.x, c.x * d.x), fmaf(a.y, b.y, c.y * d.y), fmaf(a.z, b.z, c.z * d.z),
+                     fmaf(a.w, b.w, c.w * d.w));
+}
+__device__ __forceinline__ float squares(const float4& a) { return a.x * a.x + a.y * a.y + (a.z * a.z + a.w * a.w); }
+
+template <int D, bool BF16, bool PAIRS>
+__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P, int page_shift) {
+  constexpr int kLanes = D / 8;             // lanes of a row
   constexpr int kPerLoad = 32 / kLanes;     // rows of one warp-wide load
   constexpr int kRows = kLoads * kPerLoad;
   const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
-  const int rows = P.heads + 2 * P.kv_heads;
-  const int groups = (rows + kRows - 1) / kRows;
-  const int64_t task = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (task >= P.tokens * groups) return;    // whole warps leave
-  const int64_t t = task / groups;
-  const int first = (int)(task - t * groups) * kRows + sub;
+  const int rows = P.heads + 2 * P.kv_heads, groups = (rows + kRows - 1) / kRows;
+  const int task = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int t = task / groups, first = (task - t * groups) * kRows + sub;
+  if (t >= P.tokens) return;                // whole warps leave
 
-  float4 x[kLoads];
+  const float* q = P.q + (int64_t)t * P.heads * D + 4 * l;
+  const float* k = P.k + (int64_t)t * P.kv_heads * D + 4 * l;
+  const float* v = P.v + (int64_t)t * P.kv_heads * D + 4 * l;
+  float4 lo[kLoads], hi[kLoads];
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = first + i * kPerLoad;
-    x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r >= rows) continue;
-    const float* src;
-    if (r < P.heads) src = P.q + (t * P.heads + r) * D;
-    else if (r < P.heads + P.kv_heads) src = P.k + (t * P.kv_heads + (r - P.heads)) * D;
-    else src = P.v + (t * P.kv_heads + (r - P.heads - P.kv_heads)) * D;
-    x[i] = reinterpret_cast<const float4*>(src)[l];
+    const int r = first + i * kPerLoad, rk = r - P.heads, rv = rk - P.kv_heads;
+    const float* src = rk < 0 ? q + r * D : rv < 0 ? k + rk * D : v + rv * D;
+    if (r < rows) {
+      lo[i] = *reinterpret_cast<const float4*>(src);
+      hi[i] = *reinterpret_cast<const float4*>(src + D / 2);
+    } else {
+      lo[i] = hi[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
   }
 
   // where the token's key and value go, and whether its indices are in range
-  int64_t slot = P.slot[t];
-  int pos = 0;
+  int slot = P.slot[t], pos = 0;
   if (P.rot) {
     pos = P.pos[t];
     if (pos < 0 || pos >= P.max_pos) {
@@ -68,93 +85,120 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P) 
     if (lane == 0) atomicOr(P.err, kErrIndex);
     slot = -1;
   }
-  const int64_t page = slot / P.page_size;
-  const int cell = (int)(slot - page * P.page_size);
+  const int page = slot >> page_shift, cell = slot & (P.page_size - 1);
 
-  // the lane's four angles: values 4l..4l+3 of pair index 4l mod rot/2, or
-  // pairs 2l and 2l+1 when interleaved
-  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  int partner = lane;
-  if (4 * l < P.rot) {
-    const float* row = P.cos_sin + (int64_t)pos * P.rot;
-    const int half = P.rot / 2;
-    if (P.interleaved) {
-      const float2 cc = *reinterpret_cast<const float2*>(row + 2 * l);
-      const float2 ss = *reinterpret_cast<const float2*>(row + half + 2 * l);
-      c = make_float4(cc.x, cc.x, cc.y, cc.y);
-      s = make_float4(-ss.x, ss.x, -ss.y, ss.y);
-    } else {
-      const bool low = 4 * l < half;
-      const int i = low ? 4 * l : 4 * l - half;
-      c = *reinterpret_cast<const float4*>(row + i);
-      s = *reinterpret_cast<const float4*>(row + half + i);
-      if (low) s = make_float4(-s.x, -s.y, -s.z, -s.w);
-      partner = low ? lane + P.rot / 8 : lane - P.rot / 8;
-    }
+  // factors of the lane's values (c) and of their partners (s), lower and upper half
+  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 c0 = one, s0 = zero, c1 = one, s1 = zero;
+  const float* cs = P.cos_sin + (int64_t)pos * P.rot;
+  const int half = P.rot / 2;
+  int from0 = lane, from1 = lane;           // !PAIRS: the lanes of the partners,
+  bool up0 = false, up1 = false;            // and in which of its halves they are
+  auto neighbours = [&](int i, float4& c, float4& s) {      // values i .. i+3
+    if (i >= P.rot) return;
+    const float2 cc = *reinterpret_cast<const float2*>(cs + i / 2), ss = *reinterpret_cast<const float2*>(cs + half + i / 2);
+    c = make_float4(cc.x, cc.x, cc.y, cc.y);
+    s = make_float4(-ss.x, ss.x, -ss.y, ss.y);
+  };
+  auto halves = [&](int i, float4& c, float4& s, int& from, bool& up) {
+    if (i >= P.rot) return;
+    const int pair = i < half ? i : i - half, partner = i < half ? i + half : i - half;
+    c = *reinterpret_cast<const float4*>(cs + pair);
+    s = *reinterpret_cast<const float4*>(cs + half + pair);
+    if (i < half) s = mul(s, -1.f);
+    up = partner >= D / 2;
+    from = sub * kLanes + (partner - (up ? D / 2 : 0)) / 4;
+  };
+  if (P.interleaved) {
+    neighbours(4 * l, c0, s0);
+    neighbours(4 * l + D / 2, c1, s1);
+  } else {
+    halves(4 * l, c0, s0, from0, up0);
+    halves(4 * l + D / 2, c1, s1, from1, up1);
   }
   const bool norm = P.q_weight != nullptr;
-  float4 wq = make_float4(1.f, 1.f, 1.f, 1.f), wk = wq;
+  float4 wq0 = one, wq1 = one, wk0 = one, wk1 = one;
   if (norm) {
-    wq = reinterpret_cast<const float4*>(P.q_weight)[l];
-    wk = reinterpret_cast<const float4*>(P.k_weight)[l];
+    wq0 = *reinterpret_cast<const float4*>(P.q_weight + 4 * l);
+    wq1 = *reinterpret_cast<const float4*>(P.q_weight + 4 * l + D / 2);
+    wk0 = *reinterpret_cast<const float4*>(P.k_weight + 4 * l);
+    wk1 = *reinterpret_cast<const float4*>(P.k_weight + 4 * l + D / 2);
   }
+  uint16_t* q_out = static_cast<uint16_t*>(P.q_out) + (int64_t)t * P.heads * D + 4 * l;
+  const int64_t cell_at = (((int64_t)page * P.kv_heads) * P.page_size + cell) * D + 4 * l;
+  const int head_step = P.page_size * D;
 
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
-    const int r = first + i * kPerLoad;
-    float4 v = x[i];
-    const bool value_row = r >= P.heads + P.kv_heads;
+    const int r = first + i * kPerLoad, rk = r - P.heads, rv = rk - P.kv_heads;
+    float4 x = lo[i], y = hi[i];
+    // rows of one load may be of two kinds where the head counts are odd, so the lanes meet before they part
+    float sum = 0.f;
     if (norm) {
-      float ss = v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+      sum = squares(x) + squares(y);
 #pragma unroll
-      for (int o = kLanes / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (!value_row) {
-        const float inv = 1.0f / sqrtf(ss * (1.0f / D) + P.eps);
-        const float4 w = r < P.heads ? wq : wk;
-        v = make_float4(v.x * inv * w.x, v.y * inv * w.y, v.z * inv * w.z, v.w * inv * w.w);
-      }
+      for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     }
-    if (P.rot) {
-      float4 o;
-      if (P.interleaved) {
-        o = make_float4(v.y, v.x, v.w, v.z);
-      } else {
-        o.x = __shfl_sync(0xffffffffu, v.x, partner);
-        o.y = __shfl_sync(0xffffffffu, v.y, partner);
-        o.z = __shfl_sync(0xffffffffu, v.z, partner);
-        o.w = __shfl_sync(0xffffffffu, v.w, partner);
-      }
-      if (!value_row && 4 * l < P.rot)
-        v = make_float4(v.x * c.x + o.x * s.x, v.y * c.y + o.y * s.y, v.z * c.z + o.z * s.z, v.w * c.w + o.w * s.w);
+    if (norm && rv < 0) {
+      const float inv = rsqrtf(fmaf(sum, 1.0f / D, P.eps));
+      x = mul(mul(x, inv), rk < 0 ? wq0 : wk0);
+      y = mul(mul(y, inv), rk < 0 ? wq1 : wk1);
+    }
+    float4 px, py;
+    if (P.interleaved) {
+      px = make_float4(x.y, x.x, x.w, x.z), py = make_float4(y.y, y.x, y.w, y.z);
+    } else if (PAIRS) {
+      px = y, py = x;
+    } else {
+      auto partner = [&](float a, float b, int from, bool up) {
+        const float u = __shfl_sync(0xffffffffu, a, from), w = __shfl_sync(0xffffffffu, b, from);
+        return up ? w : u;
+      };
+      px = make_float4(partner(x.x, y.x, from0, up0), partner(x.y, y.y, from0, up0), partner(x.z, y.z, from0, up0),
+                       partner(x.w, y.w, from0, up0));
+      py = make_float4(partner(x.x, y.x, from1, up1), partner(x.y, y.y, from1, up1), partner(x.z, y.z, from1, up1),
+                       partner(x.w, y.w, from1, up1));
     }
     if (r >= rows) continue;
     uint16_t* dst;
-    if (r < P.heads) {
-      dst = static_cast<uint16_t*>(P.q_out) + (t * P.heads + r) * D;
+    if (rv < 0) {
+      x = mul2(x, c0, px, s0);
+      y = mul2(y, c1, py, s1);
+      dst = rk < 0 ? q_out + r * D : static_cast<uint16_t*>(P.k_cache) + cell_at + (int64_t)rk * head_step;
     } else {
-      if (slot < 0) continue;
-      const int h = value_row ? r - P.heads - P.kv_heads : r - P.heads;
-      dst = static_cast<uint16_t*>(value_row ? P.v_cache : P.k_cache) +
-            ((page * P.kv_heads + h) * P.page_size + cell) * D;
+      dst = static_cast<uint16_t*>(P.v_cache) + cell_at + (int64_t)rv * head_step;
     }
-    reinterpret_cast<uint2*>(dst)[l] = make_uint2(pack2<BF16>(v.x, v.y), pack2<BF16>(v.z, v.w));
+    if (rk >= 0 && slot < 0) continue;
+    *reinterpret_cast<uint2*>(dst) = pack4<BF16>(x);
+    *reinterpret_cast<uint2*>(dst + D / 2) = pack4<BF16>(y);
   }
+}
+
+template <int D, bool BF16>
+void launch(const HeadsParams& p, int page_shift, unsigned grid, int threads, cudaStream_t s) {
+  if (p.interleaved || p.rot == D || p.rot == 0)
+    qk_norm_rope_kernel<D, BF16, true><<<grid, threads, 0, s>>>(p, page_shift);
+  else
+    qk_norm_rope_kernel<D, BF16, false><<<grid, threads, 0, s>>>(p, page_shift);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const HeadsParams& p, cudaStream_t s) {
-  const int per = kLoads * (128 / p.dim);
+  const int per = kLoads * (256 / p.dim);
   const int64_t tasks = p.tokens * ((p.heads + 2 * p.kv_heads + per - 1) / per);
   // few tasks: one warp per CTA, so that they spread over the SMs
   const int warps = tasks <= 152 * 4 ? 1 : 8;
-  const unsigned grid = (unsigned)((tasks + warps - 1) / warps);
+  const int64_t grid = (tasks + warps - 1) / warps;
+  if (tasks > 0x7ffffff0) return cudaErrorInvalidValue;
+  int page_shift = 4;
+  while ((1 << page_shift) < p.page_size) ++page_shift;
   if (p.dim == 128) {
-    if (p.bf16) qk_norm_rope_kernel<128, true><<<grid, 32 * warps, 0, s>>>(p);
-    else qk_norm_rope_kernel<128, false><<<grid, 32 * warps, 0, s>>>(p);
+    if (p.bf16) launch<128, true>(p, page_shift, (unsigned)grid, 32 * warps, s);
+    else launch<128, false>(p, page_shift, (unsigned)grid, 32 * warps, s);
   } else {
-    if (p.bf16) qk_norm_rope_kernel<64, true><<<grid, 32 * warps, 0, s>>>(p);
-    else qk_norm_rope_kernel<64, false><<<grid, 32 * warps, 0, s>>>(p);
+    if (p.bf16) launch<64, true>(p, page_shift, (unsigned)grid, 32 * warps, s);
+    else launch<64, false>(p, page_shift, (unsigned)grid, 32 * warps, s);
   }
   return cudaGetLastError();
 }

@@ -39,7 +39,7 @@ int column_parts(int64_t tokens, int64_t cols) {
 }
 
 struct Tile {
-  int seg, adapter;              // adapter -1: none
+  int adapter;                   // -1: none
   int first, n;                  // places of the order
 };
 
@@ -49,10 +49,11 @@ __device__ __forceinline__ Tile find_tile(const LoraParams& P, int t) {
   int base = 0;
   for (int64_t s0 = 0; s0 < P.n_seg; s0 += 32) {
     const int64_t s = s0 + lane;
-    int a = 0, b = 0;
+    int a = 0, b = 0, adapter = -1;
     if (s < P.n_seg) {
       a = P.seg_start[s];
       b = P.seg_start[s + 1];
+      adapter = P.seg_adapter[s];
       if (a < 0 || b < a || b > P.tokens) {
         atomicOr(P.err, kErrIndex);
         a = b = 0;
@@ -69,17 +70,16 @@ __device__ __forceinline__ Tile find_tile(const LoraParams& P, int t) {
       const int src = __ffs(here) - 1;
       const int k = t - base - __shfl_sync(0xffffffffu, incl - own, src);
       const int sa = __shfl_sync(0xffffffffu, a, src), sb = __shfl_sync(0xffffffffu, b, src);
-      const int64_t seg = s0 + src;
-      int adapter = P.seg_adapter[seg];
+      adapter = __shfl_sync(0xffffffffu, adapter, src);
       if (adapter >= P.n_adapters) {
         if (lane == 0) atomicOr(P.err, kErrIndex);
         adapter = -1;
       }
-      return {(int)seg, max(adapter, -1), sa + k * kTile, min(kTile, sb - sa - k * kTile)};
+      return {max(adapter, -1), sa + k * kTile, min(kTile, sb - sa - k * kTile)};
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  return {0, -1, 0, 0};
+  return {-1, 0, 0};
 }
 
 // The token at place i of the order; -1 if it is out of range.
@@ -152,7 +152,7 @@ __device__ __forceinline__ void step32(float (&c)[NT][4], const float4 (&xa)[2],
 // h[part][place][m * rank + j], scaled.  Grid: tiles x column parts x groups
 // of NT rank tiles (8 ranks each); a CTA's warps split its columns.
 template <bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const LoraParams P) {
+__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraParams P) {
   __shared__ float part[kWarps][NT * 8][kTile + 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Tile T = find_tile(P, blockIdx.x);
@@ -216,107 +216,123 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(const LoraParams 
   }
 }
 
-// y = base + B h.  Grid: tiles x chunks of kWarps * 32 outputs over all
-// projections; a warp has 32 outputs of one projection for the tile's tokens.
-// Output 8 c + 2 q + e of the 32 is column 2 c + e of instruction tile q, so
-// a lane holds 8 consecutive outputs of two tokens.
-constexpr int kOuts = 32;
+// y = base + B h.  Grid: tiles x shares of the chunks of kWarps * 32 outputs
+// of all projections; a warp has 32 outputs of one projection for the tile's
+// tokens at a time.  Output 8 c + 2 q + e of the 32 is column 2 c + e of
+// instruction tile q, so a lane holds 8 consecutive outputs of two tokens.
+constexpr int kOuts = 32, kChunk = kWarps * kOuts;
+constexpr int kMaxRanks = kLoraMaxMats * 128;
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(const LoraParams P, int parts) {
-  __shared__ float h[kTile][128 + 4];
+__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraParams P, int parts, int chunks) {
+  __shared__ __align__(16) float h[kTile][kMaxRanks + 4];
   const Tile T = find_tile(P, blockIdx.x);
   if (T.n <= 0) return;
-  int chunk = blockIdx.y, m = 0;
-  for (;; ++m) {                                          // the host counted the chunks the same way
-    const int n = (int)((P.mat[m].rows + kWarps * kOuts - 1) / (kWarps * kOuts));
-    if (chunk < n) break;
-    chunk -= n;
-  }
-  const LoraMat w = P.mat[m];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int64_t o0 = ((int64_t)chunk * kWarps + warp) * kOuts;
-  const int kblocks = (P.rank + 31) / 32;
-  if (T.adapter < 0 && w.y == w.base) return;             // nothing to add, nothing to copy
+  const int kblocks = (P.rank + 31) / 32, all = P.n * P.rank;
+  const int token[2] = {g < T.n ? token_at(P, T.first + g) : -1, g + 8 < T.n ? token_at(P, T.first + g + 8) : -1};
 
-  // what does not wait for the first kernel: the first B values, base
+  // where the warp's outputs of a chunk are (projection m, outputs from o0 on), and what they need: base and B
+  int m = 0, first = 0;                                   // first chunk of projection m
+  int64_t o0 = 0;
   const uint16_t* bp[4];
-  bool has[4];
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t o = o0 + 8 * (g >> 1) + 2 * q + (g & 1);
-    has[q] = T.adapter >= 0 && o < w.rows;
-    bp[q] = static_cast<const uint16_t*>(w.b) + (has[q] ? ((int64_t)T.adapter * w.rows + o) * P.rank : 0) + 8 * c;
-  }
   uint4 b[4];
-  auto load = [&](int kb) {
+  float y[2][8];
+  bool vec = false;
+  auto load_b = [&](int kb) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      b[q] = has[q] && kb * 32 + 8 * c < P.rank ? __ldg(reinterpret_cast<const uint4*>(bp[q] + kb * 32))
-                                                : make_uint4(0, 0, 0, 0);
+      b[q] = bp[q] && kb * 32 + 8 * c < P.rank ? __ldg(reinterpret_cast<const uint4*>(bp[q] + kb * 32))
+                                               : make_uint4(0, 0, 0, 0);
   };
-  load(0);
-  const int token[2] = {g < T.n ? token_at(P, T.first + g) : -1, g + 8 < T.n ? token_at(P, T.first + g + 8) : -1};
-  const int64_t o = o0 + 8 * c;
-  const bool vec = (w.rows & 3) == 0;
-  float y[2][8];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[r][e] = 0.f;
-    if (token[r] < 0 || !w.base) continue;
-    const float* src = w.base + (int64_t)token[r] * w.rows + o;
-    if (vec) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (o + 4 * e < w.rows) *reinterpret_cast<float4*>(&y[r][4 * e]) = reinterpret_cast<const float4*>(src)[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (o + e < w.rows) y[r][e] = src[e];
+  auto load = [&](int chunk) {
+    for (;; ++m) {
+      const int n = (int)((P.mat[m].rows + kChunk - 1) / kChunk);
+      if (chunk < first + n) break;
+      first += n;
     }
-  }
-
-  float acc[4][4];
+    const LoraMat& w = P.mat[m];
+    o0 = ((int64_t)(chunk - first) * kWarps + warp) * kOuts;
+    vec = (w.rows & 3) == 0;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+    for (int q = 0; q < 4; ++q) {
+      const int64_t o = o0 + 8 * (g >> 1) + 2 * q + (g & 1);
+      bp[q] = T.adapter >= 0 && o < w.rows
+                  ? static_cast<const uint16_t*>(w.b) + ((int64_t)T.adapter * w.rows + o) * P.rank + 8 * c
+                  : nullptr;
+    }
+    load_b(0);
+    const int64_t o = o0 + 8 * c;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[r][e] = 0.f;
+      if (token[r] < 0 || !w.base) continue;
+      const float* src = w.base + (int64_t)token[r] * w.rows + o;
+      if (vec) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (o + 4 * e < w.rows) *reinterpret_cast<float4*>(&y[r][4 * e]) = reinterpret_cast<const float4*>(src)[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (o + e < w.rows) y[r][e] = src[e];
+      }
+    }
+  };
+
+  load(blockIdx.y);                                       // these do not wait for the first kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (T.adapter >= 0) {
-    const int all = P.n * P.rank;
-    for (int i = threadIdx.x; i < kTile * kblocks * 32; i += kThreads) {
-      const int place = i / (kblocks * 32), j = i - place * (kblocks * 32);
+    for (int i = threadIdx.x; i < kTile * all; i += kThreads) {
+      const int place = i / all, j = i - place * all;
       float v = 0.f;
-      if (place < T.n && j < P.rank)
-        for (int k = 0; k < parts; ++k)
-          v += __ldcg(P.work + ((int64_t)k * P.tokens + T.first + place) * all + m * P.rank + j);
+      if (place < T.n)
+        for (int k = 0; k < parts; ++k) v += __ldcg(P.work + ((int64_t)k * P.tokens + T.first + place) * all + j);
       h[place][j] = v;
     }
     __syncthreads();
-    for (int kb = 0; kb < kblocks; ++kb) {
-      const float4* ha = reinterpret_cast<const float4*>(&h[g][kb * 32 + 8 * c]);
-      const float4* hb = reinterpret_cast<const float4*>(&h[g + 8][kb * 32 + 8 * c]);
-      const float4 xa[2] = {ha[0], ha[1]}, xb[2] = {hb[0], hb[1]};
-      const uint4 now[4] = {b[0], b[1], b[2], b[3]};
-      if (kb + 1 < kblocks) load(kb + 1);
-      step32<BF16, 4>(acc, xa, xb, now, 4);
-    }
   }
+  for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
+    if (chunk != blockIdx.y) load(chunk);
+    const LoraMat& w = P.mat[m];
+    if (T.adapter >= 0) {
+      float acc[4][4];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    if (token[r] < 0) continue;
+      for (int q = 0; q < 4; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        const bool in = kb * 32 + 8 * c < P.rank;
+        const float4* ha = reinterpret_cast<const float4*>(&h[g][m * P.rank + kb * 32 + 8 * c]);
+        const float4* hb = reinterpret_cast<const float4*>(&h[g + 8][m * P.rank + kb * 32 + 8 * c]);
+        const float4 xa[2] = {in ? ha[0] : zero, in ? ha[1] : zero}, xb[2] = {in ? hb[0] : zero, in ? hb[1] : zero};
+        const uint4 now[4] = {b[0], b[1], b[2], b[3]};
+        if (kb + 1 < kblocks) load_b(kb + 1);
+        step32<BF16, 4>(acc, xa, xb, now, 4);
+      }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) y[r][2 * q + e] += acc[q][2 * r + e];
-    float* dst = w.y + (int64_t)token[r] * w.rows + o;
-    if (vec) {
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (o + 4 * e < w.rows) reinterpret_cast<float4*>(dst)[e] = *reinterpret_cast<const float4*>(&y[r][4 * e]);
-    } else {
+          for (int e = 0; e < 2; ++e) y[r][2 * q + e] += acc[q][2 * r + e];
+    } else if (w.y == w.base) {
+      continue;                                           // nothing to add, nothing to copy
+    }
+    const int64_t o = o0 + 8 * c;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (o + e < w.rows) dst[e] = y[r][e];
+    for (int r = 0; r < 2; ++r) {
+      if (token[r] < 0) continue;
+      float* dst = w.y + (int64_t)token[r] * w.rows + o;
+      if (vec) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (o + 4 * e < w.rows) reinterpret_cast<float4*>(dst)[e] = *reinterpret_cast<const float4*>(&y[r][4 * e]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (o + e < w.rows) dst[e] = y[r][e];
+      }
     }
   }
 }
@@ -331,17 +347,19 @@ template <bool BF16>
 cudaError_t launch(const LoraParams& p, cudaStream_t s) {
   const unsigned tiles = (unsigned)std::min<int64_t>(p.tokens, p.n_seg + p.tokens / kTile);
   const int parts = column_parts(p.tokens, p.cols);
-  // few tokens: one rank tile per CTA for the sake of latency; many: all of
-  // them together, so that x is read once (up to 64 ranks)
+  // few tokens: one rank tile per CTA for the sake of latency; many: four of
+  // them, so that x is read once for 32 ranks
   if (p.tokens <= 16) shrink<BF16, 1>(p, tiles, parts, s);
-  else if (p.n * p.rank <= 32) shrink<BF16, 4>(p, tiles, parts, s);
-  else shrink<BF16, 8>(p, tiles, parts, s);
+  else shrink<BF16, 4>(p, tiles, parts, s);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   unsigned chunks = 0;
-  for (int m = 0; m < p.n; ++m) chunks += (unsigned)((p.mat[m].rows + kWarps * kOuts - 1) / (kWarps * kOuts));
+  for (int m = 0; m < p.n; ++m) chunks += (unsigned)((p.mat[m].rows + kChunk - 1) / kChunk);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const unsigned want = (unsigned)std::max(1, 4 * device_info(dev).sm_count / (int)std::min(tiles, 1u << 20));
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(tiles, chunks);
+  cfg.gridDim = dim3(tiles, std::min(chunks, want));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute attr{};
@@ -349,7 +367,7 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_expand_kernel<BF16>, p, parts);
+  return cudaLaunchKernelEx(&cfg, lora_expand_kernel<BF16>, p, parts, (int)chunks);
 }
 
 }  // namespace
