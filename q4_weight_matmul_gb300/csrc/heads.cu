@@ -5,10 +5,10 @@
 // instructions per 16 bytes between them, so HBM bounds it as long as the
 // instructions stay few.  D/8 lanes share a row, each with 4 values of its
 // lower half and the 4 at the same place of its upper half (16-byte loads,
-// 8-byte stores): where the whole head is rotated by halves, or neighbours
-// are, a lane then has both values of its pairs (PAIRS), and only the sum of
-// squares crosses lanes.  Rotating a part of the head by halves takes the
-// partner's value from another lane.  A warp takes kLoads rows per group of
+// 8-byte stores): where the whole head is rotated by halves (kWhole), or
+// neighbours are (kNeighbours), a lane then has both values of its pairs, and
+// only the sum of squares crosses lanes.  Rotating a part of the head by
+// halves (kPart) takes the partner's value from another lane.  A warp takes kLoads rows per group of
 // lanes, all of one token, with their loads in flight at once, and reads the
 // token's cosines and sines once for all of them.
 #include "q4k_internal.h"
@@ -45,8 +45,10 @@ __device__ __forceinline__ float4 mul2(const float4& a, const float4& b, const f
 }
 __device__ __forceinline__ float squares(const float4& a) { return a.x * a.x + a.y * a.y + (a.z * a.z + a.w * a.w); }
 
-template <int D, bool BF16, bool PAIRS>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P, int page_shift) {
+enum Mode { kWhole, kNeighbours, kPart };
+
+template <int D, bool BF16, Mode MODE>
+__global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const HeadsParams P, int page_shift) {
   constexpr int kLanes = D / 8;             // lanes of a row
   constexpr int kPerLoad = 32 / kLanes;     // rows of one warp-wide load
   constexpr int kRows = kLoads * kPerLoad;
@@ -92,38 +94,36 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P, 
   float4 c0 = one, s0 = zero, c1 = one, s1 = zero;
   const float* cs = P.cos_sin + (int64_t)pos * P.rot;
   const int half = P.rot / 2;
-  int from0 = lane, from1 = lane;           // !PAIRS: the lanes of the partners,
+  int from0 = lane, from1 = lane;           // kPart: the lanes of the partners,
   bool up0 = false, up1 = false;            // and in which of its halves they are
-  auto neighbours = [&](int i, float4& c, float4& s) {      // values i .. i+3
-    if (i >= P.rot) return;
-    const float2 cc = *reinterpret_cast<const float2*>(cs + i / 2), ss = *reinterpret_cast<const float2*>(cs + half + i / 2);
-    c = make_float4(cc.x, cc.x, cc.y, cc.y);
-    s = make_float4(-ss.x, ss.x, -ss.y, ss.y);
-  };
-  auto halves = [&](int i, float4& c, float4& s, int& from, bool& up) {
-    if (i >= P.rot) return;
-    const int pair = i < half ? i : i - half, partner = i < half ? i + half : i - half;
-    c = *reinterpret_cast<const float4*>(cs + pair);
-    s = *reinterpret_cast<const float4*>(cs + half + pair);
-    if (i < half) s = mul(s, -1.f);
-    up = partner >= D / 2;
-    from = sub * kLanes + (partner - (up ? D / 2 : 0)) / 4;
-  };
-  if (P.interleaved) {
-    neighbours(4 * l, c0, s0);
-    neighbours(4 * l + D / 2, c1, s1);
+  if constexpr (MODE == kWhole) {
+    if (P.rot) {
+      c0 = *reinterpret_cast<const float4*>(cs + 4 * l);
+      s0 = *reinterpret_cast<const float4*>(cs + D / 2 + 4 * l);
+    }
+  } else if constexpr (MODE == kNeighbours) {
+    auto factors = [&](int i, float4& c, float4& s) {      // values i .. i+3
+      if (i >= P.rot) return;
+      const float2 cc = *reinterpret_cast<const float2*>(cs + i / 2), ss = *reinterpret_cast<const float2*>(cs + half + i / 2);
+      c = make_float4(cc.x, cc.x, cc.y, cc.y);
+      s = make_float4(-ss.x, ss.x, -ss.y, ss.y);
+    };
+    factors(4 * l, c0, s0);
+    factors(4 * l + D / 2, c1, s1);
   } else {
-    halves(4 * l, c0, s0, from0, up0);
-    halves(4 * l + D / 2, c1, s1, from1, up1);
+    auto factors = [&](int i, float4& c, float4& s, int& from, bool& up) {
+      if (i >= P.rot) return;
+      const int pair = i < half ? i : i - half, partner = i < half ? i + half : i - half;
+      c = *reinterpret_cast<const float4*>(cs + pair);
+      s = *reinterpret_cast<const float4*>(cs + half + pair);
+      if (i < half) s = mul(s, -1.f);
+      up = partner >= D / 2;
+      from = sub * kLanes + (partner - (up ? D / 2 : 0)) / 4;
+    };
+    factors(4 * l, c0, s0, from0, up0);
+    factors(4 * l + D / 2, c1, s1, from1, up1);
   }
   const bool norm = P.q_weight != nullptr;
-  float4 wq0 = one, wq1 = one, wk0 = one, wk1 = one;
-  if (norm) {
-    wq0 = *reinterpret_cast<const float4*>(P.q_weight + 4 * l);
-    wq1 = *reinterpret_cast<const float4*>(P.q_weight + 4 * l + D / 2);
-    wk0 = *reinterpret_cast<const float4*>(P.k_weight + 4 * l);
-    wk1 = *reinterpret_cast<const float4*>(P.k_weight + 4 * l + D / 2);
-  }
   uint16_t* q_out = static_cast<uint16_t*>(P.q_out) + (int64_t)t * P.heads * D + 4 * l;
   const int64_t cell_at = (((int64_t)page * P.kv_heads) * P.page_size + cell) * D + 4 * l;
   const int head_step = P.page_size * D;
@@ -141,15 +141,12 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P, 
     }
     if (norm && rv < 0) {
       const float inv = rsqrtf(fmaf(sum, 1.0f / D, P.eps));
-      x = mul(mul(x, inv), rk < 0 ? wq0 : wk0);
-      y = mul(mul(y, inv), rk < 0 ? wq1 : wk1);
+      const float* w = (rk < 0 ? P.q_weight : P.k_weight) + 4 * l;     // few lines, in L1 after the first rows
+      x = mul(mul(x, inv), __ldg(reinterpret_cast<const float4*>(w)));
+      y = mul(mul(y, inv), __ldg(reinterpret_cast<const float4*>(w + D / 2)));
     }
     float4 px, py;
-    if (P.interleaved) {
-      px = make_float4(x.y, x.x, x.w, x.z), py = make_float4(y.y, y.x, y.w, y.z);
-    } else if (PAIRS) {
-      px = y, py = x;
-    } else {
+    if constexpr (MODE == kPart) {
       auto partner = [&](float a, float b, int from, bool up) {
         const float u = __shfl_sync(0xffffffffu, a, from), w = __shfl_sync(0xffffffffu, b, from);
         return up ? w : u;
@@ -162,8 +159,16 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P, 
     if (r >= rows) continue;
     uint16_t* dst;
     if (rv < 0) {
-      x = mul2(x, c0, px, s0);
-      y = mul2(y, c1, py, s1);
+      if constexpr (MODE == kWhole) {
+        px = mul2(x, c0, mul(y, -1.f), s0);
+        y = mul2(y, c0, x, s0);
+        x = px;
+      } else {
+        if constexpr (MODE == kNeighbours)
+          px = make_float4(x.y, x.x, x.w, x.z), py = make_float4(y.y, y.x, y.w, y.z);
+        x = mul2(x, c0, px, s0);
+        y = mul2(y, c1, py, s1);
+      }
       dst = rk < 0 ? q_out + r * D : static_cast<uint16_t*>(P.k_cache) + cell_at + (int64_t)rk * head_step;
     } else {
       dst = static_cast<uint16_t*>(P.v_cache) + cell_at + (int64_t)rv * head_step;
@@ -176,10 +181,12 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const HeadsParams P, 
 
 template <int D, bool BF16>
 void launch(const HeadsParams& p, int page_shift, unsigned grid, int threads, cudaStream_t s) {
-  if (p.interleaved || p.rot == D || p.rot == 0)
-    qk_norm_rope_kernel<D, BF16, true><<<grid, threads, 0, s>>>(p, page_shift);
+  if (p.rot == 0 || (p.rot == D && !p.interleaved))
+    qk_norm_rope_kernel<D, BF16, kWhole><<<grid, threads, 0, s>>>(p, page_shift);
+  else if (p.interleaved)
+    qk_norm_rope_kernel<D, BF16, kNeighbours><<<grid, threads, 0, s>>>(p, page_shift);
   else
-    qk_norm_rope_kernel<D, BF16, false><<<grid, threads, 0, s>>>(p, page_shift);
+    qk_norm_rope_kernel<D, BF16, kPart><<<grid, threads, 0, s>>>(p, page_shift);
 }
 
 }  // namespace
