@@ -8,19 +8,18 @@
 // share an adapter share its loads; each warp finds its tile from seg_start
 // by itself.
 //
-// Products run on mma.sync m16n8k8 with tf32 operands: the adapters' 16-bit
-// values are exact in tf32, and a fp32 activation enters as two parts, hi
-// (rounded to 11 bits) + lo (the rest, 11 more bits), so products keep 22
-// bits or more over fp32's whole range.  The k index of an instruction is free
-// to permute, so every lane loads 8 consecutive k of its row (16 bytes of an
-// adapter, 32 of x) straight into registers and feeds them to four
-// instructions: no shared memory, no transposes.  Sums of 32 k start from
-// zero and are added up in fp32 registers (the tensor core's own running sum
-// truncates).
+// Products run on mma.sync m16n8k16 with the adapters' 16-bit values as they
+// are; a fp32 activation enters as a sum of values of their type: three
+// bfloat16 (24 bits), or two binary16 (22 bits) of the activations scaled by
+// a power of two, the same for 32 of a row, that puts the largest near 2^14
+// (smaller ones lose nothing until 2^-38 of it).  The k index of an
+// instruction is free to permute, so every lane loads 8 consecutive k of its
+// row (16 bytes of an adapter, 32 of x) and feeds them to two instructions
+// without a transpose.  Sums of 32 k start from zero and are added up in fp32
+// registers (the tensor core's own running sum truncates).
+#include "mma_sync.cuh"
 #include "q4k_internal.h"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include "tc_ptx.cuh"
 
 #include <algorithm>
 
@@ -33,8 +32,9 @@ constexpr int kThreads = 32 * kWarps;
 
 // Parts of the columns that the shrink's CTAs split among them: more for few
 // tokens, which have few tiles.
+constexpr int kMaxParts = 8;
 int column_parts(int64_t tokens, int64_t cols) {
-  const int64_t want = tokens <= 64 ? 8 : tokens <= 512 ? 4 : 2;
+  const int64_t want = tokens <= 64 ? kMaxParts : tokens <= 512 ? 4 : 2;
   return (int)std::max<int64_t>(1, std::min(want, cols / 256));
 }
 
@@ -90,29 +90,37 @@ __device__ __forceinline__ int token_at(const LoraParams& P, int i) {
   return -1;
 }
 
-__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// v = hi + lo: hi rounded to tf32's 11 bits, lo exact (read to 11 bits).
-__device__ __forceinline__ void split(float v, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(v) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(v - __uint_as_float(hi));
-}
-
+// The 16-bit parts of the two rows' 8 values each: p[part][i] is the A operand
+// of instruction i; `back`: what the products are to be multiplied by.
 template <bool BF16>
-__device__ __forceinline__ void widen(uint32_t v, uint32_t& x, uint32_t& y) {
-  if constexpr (BF16) {
-    x = v << 16;
-    y = v & 0xffff0000u;
-  } else {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-    x = __float_as_uint(f.x);
-    y = __float_as_uint(f.y);
+__device__ __forceinline__ void split(const float (&a)[8], const float (&b)[8], uint32_t (&p)[BF16 ? 3 : 2][2][4],
+                                      float (&back)[2]) {
+  float s[2] = {1.f, 1.f};
+  back[0] = back[1] = 1.f;
+  if constexpr (!BF16) {
+    float top[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top[0] = fmaxf(top[0], fabsf(a[e])), top[1] = fmaxf(top[1], fabsf(b[e]));
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));      // the row's other 24 values
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      const uint32_t e = max(__float_as_uint(top[r]) >> 23, 15u);           // biased exponent
+      s[r] = __uint_as_float((268u - e) << 23);                             // 2^(14 - exponent)
+      back[r] = __uint_as_float((e - 14u) << 23);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0 = a[2 * i] * s[0], x1 = a[2 * i + 1] * s[0], y0 = b[2 * i] * s[1], y1 = b[2 * i + 1] * s[1];
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 3 : 2); ++k) {
+      const uint32_t x = pack2<BF16>(x0, x1), y = pack2<BF16>(y0, y1);
+      const float2 fx = unpack2<BF16>(x), fy = unpack2<BF16>(y);
+      x0 -= fx.x, x1 -= fx.y, y0 -= fy.x, y1 -= fy.y;
+      p[k][i >> 1][2 * (i & 1)] = x;
+      p[k][i >> 1][2 * (i & 1) + 1] = y;
+    }
   }
 }
 
@@ -121,85 +129,34 @@ __device__ __forceinline__ void widen(uint32_t v, uint32_t& x, uint32_t& y) {
 template <bool BF16, int NT>
 __device__ __forceinline__ void step32(float (&c)[NT][4], const float4 (&xa)[2], const float4 (&xb)[2],
                                        const uint4 (&w)[NT], int tiles) {
-  float t[NT][4];
+  const float a[8] = {xa[0].x, xa[0].y, xa[0].z, xa[0].w, xa[1].x, xa[1].y, xa[1].z, xa[1].w};
+  const float b[8] = {xb[0].x, xb[0].y, xb[0].z, xb[0].w, xb[1].x, xb[1].y, xb[1].z, xb[1].w};
+  uint32_t p[BF16 ? 3 : 2][2][4];
+  float back[2];
+  split<BF16>(a, b, p, back);
 #pragma unroll
-  for (int q = 0; q < NT; ++q) t[q][0] = t[q][1] = t[q][2] = t[q][3] = 0.f;
-  const float* a = reinterpret_cast<const float*>(xa);
-  const float* b = reinterpret_cast<const float*>(xb);
+  for (int q = 0; q < NT; ++q) {
+    if (q < tiles) {
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h0, h1, h2, h3, l0, l1, l2, l3;
-    split(a[2 * i], h0, l0);
-    split(b[2 * i], h1, l1);
-    split(a[2 * i + 1], h2, l2);
-    split(b[2 * i + 1], h3, l3);
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      if (q < tiles) {
-        uint32_t w0, w1;
-        widen<BF16>(i == 0 ? w[q].x : i == 1 ? w[q].y : i == 2 ? w[q].z : w[q].w, w0, w1);
-        mma_tf32(t[q], h0, h1, h2, h3, w0, w1);
-        mma_tf32(t[q], l0, l1, l2, l3, w0, w1);
+      for (int k = 0; k < (BF16 ? 3 : 2); ++k) {
+        mma16816<BF16>(t, p[k][0], w[q].x, w[q].y);
+        mma16816<BF16>(t, p[k][1], w[q].z, w[q].w);
       }
+      c[q][0] = fmaf(t[0], back[0], c[q][0]), c[q][1] = fmaf(t[1], back[0], c[q][1]);
+      c[q][2] = fmaf(t[2], back[1], c[q][2]), c[q][3] = fmaf(t[3], back[1], c[q][3]);
     }
   }
-#pragma unroll
-  for (int q = 0; q < NT; ++q)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[q][e] += t[q][e];
 }
 
 // h[part][place][m * rank + j], scaled.  Grid: tiles x column parts x groups
 // of NT rank tiles (8 ranks each); a CTA's warps split its columns.
-template <bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraParams P) {
-  __shared__ float part[kWarps][NT * 8][kTile + 1];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const Tile T = find_tile(P, blockIdx.x);
-  if (T.n <= 0 || T.adapter < 0) return;                 // the whole block
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int all = P.n * P.rank, q0 = blockIdx.z * NT, tiles = min(NT, all / 8 - q0);
-  const int ta = g < T.n ? token_at(P, T.first + g) : -1, tb = g + 8 < T.n ? token_at(P, T.first + g + 8) : -1;
-  const float* xa = P.x + (int64_t)max(ta, 0) * P.cols + 8 * c;
-  const float* xb = P.x + (int64_t)max(tb, 0) * P.cols + 8 * c;
-  const uint16_t* wp[NT];
-#pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    const int col = min(q0 + q, all / 8 - 1) * 8, m = col / P.rank, j = col - m * P.rank;
-    wp[q] = static_cast<const uint16_t*>(P.mat[m].a) + ((int64_t)T.adapter * P.rank + j + g) * P.cols + 8 * c;
-  }
-  float acc[NT][4];
-#pragma unroll
-  for (int q = 0; q < NT; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
-  // this warp's steps of 32 columns: every (parts * kWarps)-th
-  const int steps = (int)(P.cols / 32), stride = gridDim.y * kWarps;
-  constexpr int kAhead = NT <= 2 ? 4 : 2;                // steps in flight
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 a[kAhead][2], b[kAhead][2];
-  uint4 w[kAhead][NT];
-  auto load = [&](int i, int s) {
-    const int64_t k = (int64_t)s * 32;
-    const bool in = s < steps;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      a[i][e] = in && ta >= 0 ? reinterpret_cast<const float4*>(xa + k)[e] : zero;
-      b[i][e] = in && tb >= 0 ? reinterpret_cast<const float4*>(xb + k)[e] : zero;
-    }
-#pragma unroll
-    for (int q = 0; q < NT; ++q)
-      if (q < tiles) w[i][q] = in ? __ldg(reinterpret_cast<const uint4*>(wp[q] + k)) : make_uint4(0, 0, 0, 0);
-  };
-  int s = blockIdx.y * kWarps + warp;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(i, s + i * stride);
-  for (; s < steps; s += kAhead * stride) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      step32<BF16, NT>(acc, a[i], b[i], w[i], tiles);
-      load(i, s + (i + kAhead) * stride);
-    }
-  }
-  // the warps' sums, added up in warp order
+
+// The warps' sums, added up in warp order; part: [warp][NT * 8][kTile + 1].
+template <int NT>
+__device__ __forceinline__ void store_h(const LoraParams& P, const Tile& T, float (*part)[NT * 8][kTile + 1],
+                                        const float (&acc)[NT][4], int q0, int tiles) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, all = P.n * P.rank;
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
 #pragma unroll
@@ -214,6 +171,143 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraPara
     for (int k = 0; k < kWarps; ++k) v += part[k][col][place];
     P.work[((int64_t)blockIdx.y * P.tokens + T.first + place) * all + q0 * 8 + col] = v * scale;
   }
+}
+
+// Row `col` of the adapter's A, all projections after one another.
+__device__ __forceinline__ const uint16_t* a_row(const LoraParams& P, int adapter, int col) {
+  const int m = col / P.rank, j = col - m * P.rank;
+  return static_cast<const uint16_t*>(P.mat[m].a) + ((int64_t)adapter * P.rank + j) * P.cols;
+}
+
+// Few tokens: latency counts.  Operands straight into registers, one rank
+// tile per CTA.
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const LoraParams P) {
+  __shared__ float part[kWarps][8][kTile + 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Tile T = find_tile(P, blockIdx.x);
+  if (T.n <= 0 || T.adapter < 0) return;                 // the whole block
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int ta = g < T.n ? token_at(P, T.first + g) : -1, tb = g + 8 < T.n ? token_at(P, T.first + g + 8) : -1;
+  const float* xa = P.x + (int64_t)max(ta, 0) * P.cols + 8 * c;
+  const float* xb = P.x + (int64_t)max(tb, 0) * P.cols + 8 * c;
+  const uint16_t* wp = a_row(P, T.adapter, blockIdx.z * 8 + g) + 8 * c;
+  float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+  // this warp's steps of 32 columns: every (parts * kWarps)-th
+  const int steps = (int)(P.cols / 32), stride = gridDim.y * kWarps;
+  constexpr int kAhead = 4;                              // steps in flight
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 a[kAhead][2], b[kAhead][2];
+  uint4 w[kAhead][1];
+  auto load = [&](int i, int s) {
+    const int64_t k = (int64_t)s * 32;
+    const bool in = s < steps;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      a[i][e] = in && ta >= 0 ? reinterpret_cast<const float4*>(xa + k)[e] : zero;
+      b[i][e] = in && tb >= 0 ? reinterpret_cast<const float4*>(xb + k)[e] : zero;
+    }
+    w[i][0] = in ? __ldg(reinterpret_cast<const uint4*>(wp + k)) : make_uint4(0, 0, 0, 0);
+  };
+  int s = blockIdx.y * kWarps + warp;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i, s + i * stride);
+  for (; s < steps; s += kAhead * stride) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      step32<BF16, 1>(acc, a[i], b[i], w[i], 1);
+      load(i, s + (i + kAhead) * stride);
+    }
+  }
+  store_h<1>(P, T, part, acc, blockIdx.z, 1);
+}
+
+// Many tokens: bandwidth counts.  Stages of 256 columns (the tile's rows of x
+// and the rank rows of A, from wherever a row lies) go through a ring in
+// shared memory by 16-byte asynchronous copies, all threads sharing them
+// (bulk copies of single rows, 48 to a stage, took longer to issue than to
+// arrive); warp w has columns 32 w .. of every stage.  Rows are padded so
+// that the lanes of a load meet different banks.
+constexpr int kCols = 256;
+constexpr int kXRow = kCols * 4 + 16, kARow = kCols * 2 + 64;      // bytes of a row in shared memory
+
+template <int NT>
+struct Shrink {
+  static constexpr int kStage = kTile * kXRow + NT * 8 * kARow;
+  static constexpr int kPart = kWarps * NT * 8 * (kTile + 1) * 4;
+  static constexpr int kStages = 112 * 1024 / kStage > 4 ? 4 : 112 * 1024 / kStage;      // two CTAs per SM
+  static constexpr int kSmem = kStages * kStage > kPart ? kStages * kStage : kPart;
+};
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+
+template <bool BF16, int NT>
+__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraParams P) {
+  using S = Shrink<NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const Tile T = find_tile(P, blockIdx.x);
+  if (T.n <= 0 || T.adapter < 0) return;                 // the whole block
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int q0 = blockIdx.z * NT, tiles = min(NT, P.n * P.rank / 8 - q0);
+  // this CTA's stages: blockIdx.y, + parts, ...
+  const int parts = gridDim.y, stages = (int)(P.cols / kCols), mine = (stages - (int)blockIdx.y + parts - 1) / parts;
+
+  // what a thread copies of a stage: 16 bytes of x rows tid / 64 + 4 i, and of A rows tid / 32 + 8 i
+  constexpr int XN = kTile / 4;
+  const float* xs[XN];
+  const uint16_t* as[NT];
+#pragma unroll
+  for (int i = 0; i < XN; ++i) {
+    const int r = tid / 64 + 4 * i, t = r < T.n ? token_at(P, T.first + r) : -1;
+    xs[i] = t >= 0 ? P.x + (int64_t)t * P.cols + 4 * (tid % 64) : nullptr;
+  }
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+    as[i] = i < tiles ? a_row(P, T.adapter, (q0 + i) * 8 + tid / 32) + 8 * (tid % 32) : nullptr;
+  // rows that are not there keep what shared memory held: an output row takes nothing from another's input row
+  auto copy = [&](int i) {
+    if (i < mine) {
+      uint8_t* at = smem + (i % S::kStages) * S::kStage;
+      const int64_t k = ((int64_t)blockIdx.y + (int64_t)i * parts) * kCols;
+#pragma unroll
+      for (int j = 0; j < XN; ++j)
+        if (xs[j]) copy16(at + (tid / 64 + 4 * j) * kXRow + 16 * (tid % 64), xs[j] + k);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (as[j]) copy16(at + kTile * kXRow + (8 * j + tid / 32) * kARow + 16 * (tid % 32), as[j] + k);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");       // an empty one past the last stage
+  };
+#pragma unroll
+  for (int i = 0; i < S::kStages - 1; ++i) copy(i);
+
+  float acc[NT][4];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
+  for (int i = 0; i < mine; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 2) : "memory");
+    __syncthreads();                                     // stage i is there, and stage i - 1 has been used
+    copy(i + S::kStages - 1);
+    const uint8_t* at = smem + (i % S::kStages) * S::kStage;
+    const uint8_t* x = at + g * kXRow + warp * 128 + c * 32;
+    const uint8_t* a = at + kTile * kXRow + g * kARow + warp * 64 + c * 16;
+    float4 xa[2], xb[2];
+    uint4 w[NT];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      xa[e] = reinterpret_cast<const float4*>(x)[e];
+      xb[e] = reinterpret_cast<const float4*>(x + 8 * kXRow)[e];
+    }
+#pragma unroll
+    for (int q = 0; q < NT; ++q) w[q] = *reinterpret_cast<const uint4*>(a + q * 8 * kARow);
+    step32<BF16, NT>(acc, xa, xb, w, tiles);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  store_h<NT>(P, T, reinterpret_cast<float(*)[NT * 8][kTile + 1]>(smem), acc, q0, tiles);
 }
 
 // y = base + B h.  Grid: tiles x shares of the chunks of kWarps * 32 outputs
@@ -232,126 +326,142 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
   const int kblocks = (P.rank + 31) / 32, all = P.n * P.rank;
   const int token[2] = {g < T.n ? token_at(P, T.first + g) : -1, g + 8 < T.n ? token_at(P, T.first + g + 8) : -1};
 
-  // where the warp's outputs of a chunk are (projection m, outputs from o0 on), and what they need: base and B
-  int m = 0, first = 0;                                   // first chunk of projection m
-  int64_t o0 = 0;
-  const uint16_t* bp[4];
-  uint4 b[4];
-  float y[2][8];
-  bool vec = false;
-  auto load_b = [&](int kb) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      b[q] = bp[q] && kb * 32 + 8 * c < P.rank ? __ldg(reinterpret_cast<const uint4*>(bp[q] + kb * 32))
-                                               : make_uint4(0, 0, 0, 0);
+  // what a warp's outputs of a chunk (projection m, outputs from o0 on) need: base and the first B values; the next
+  // chunk's are loaded while this one's are used
+  struct Work {
+    int m;
+    int64_t o0;
+    const uint16_t* bp;          // B row of the lane's output of tile 0, at its k
+    uint4 b[4];
+    float y[4][4];               // [instruction tile][token g: two outputs, token g + 8: two]
   };
-  auto load = [&](int chunk) {
+  int m = 0, first = 0;          // projection of the chunk loaded last, its first chunk
+  auto load_b = [&](Work& u, int kb) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool in = T.adapter >= 0 && u.o0 + 8 * (g >> 1) + 2 * q + (g & 1) < P.mat[u.m].rows && kb * 32 + 8 * c < P.rank;
+      u.b[q] = in ? __ldg(reinterpret_cast<const uint4*>(u.bp + 2 * q * P.rank + kb * 32)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto load = [&](Work& u, int chunk) {
     for (;; ++m) {
       const int n = (int)((P.mat[m].rows + kChunk - 1) / kChunk);
       if (chunk < first + n) break;
       first += n;
     }
     const LoraMat& w = P.mat[m];
-    o0 = ((int64_t)(chunk - first) * kWarps + warp) * kOuts;
-    vec = (w.rows & 3) == 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t o = o0 + 8 * (g >> 1) + 2 * q + (g & 1);
-      bp[q] = T.adapter >= 0 && o < w.rows
-                  ? static_cast<const uint16_t*>(w.b) + ((int64_t)T.adapter * w.rows + o) * P.rank + 8 * c
-                  : nullptr;
-    }
-    load_b(0);
-    const int64_t o = o0 + 8 * c;
+    u.m = m;
+    u.o0 = ((int64_t)(chunk - first) * kWarps + warp) * kOuts;
+    u.bp = static_cast<const uint16_t*>(w.b) +
+           ((int64_t)T.adapter * w.rows + u.o0 + 8 * (g >> 1) + (g & 1)) * P.rank + 8 * c;
+    load_b(u, 0);
+    const int64_t o = u.o0 + 8 * c;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      if (token[r] >= 0 && w.base) {
+        const float* src = w.base + (int64_t)token[r] * w.rows + o;
+        if ((w.rows & 3) == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[r][e] = 0.f;
-      if (token[r] < 0 || !w.base) continue;
-      const float* src = w.base + (int64_t)token[r] * w.rows + o;
-      if (vec) {
+          for (int e = 0; e < 2; ++e)
+            if (o + 4 * e < w.rows) v[e] = reinterpret_cast<const float4*>(src)[e];
+        } else {
+          float* f = reinterpret_cast<float*>(v);
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (o + 4 * e < w.rows) *reinterpret_cast<float4*>(&y[r][4 * e]) = reinterpret_cast<const float4*>(src)[e];
-      } else {
+          for (int e = 0; e < 8; ++e)
+            if (o + e < w.rows) f[e] = src[e];
+        }
+      }
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (o + e < w.rows) y[r][e] = src[e];
+      for (int e = 0; e < 2; ++e) {
+        u.y[2 * e][2 * r] = v[e].x, u.y[2 * e][2 * r + 1] = v[e].y;
+        u.y[2 * e + 1][2 * r] = v[e].z, u.y[2 * e + 1][2 * r + 1] = v[e].w;
       }
     }
   };
 
-  load(blockIdx.y);                                       // these do not wait for the first kernel
+  Work u;
+  load(u, blockIdx.y);                                    // these do not wait for the first kernel
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (T.adapter >= 0) {
-    for (int i = threadIdx.x; i < kTile * all; i += kThreads) {
-      const int place = i / all, j = i - place * all;
-      float v = 0.f;
-      if (place < T.n)
-        for (int k = 0; k < parts; ++k) v += __ldcg(P.work + ((int64_t)k * P.tokens + T.first + place) * all + j);
-      h[place][j] = v;
+    for (int i = threadIdx.x; i < kTile * all / 4; i += kThreads) {
+      const int place = i / (all / 4), j = 4 * (i - place * (all / 4));
+      float4 v[kMaxParts];
+#pragma unroll
+      for (int k = 0; k < kMaxParts; ++k)
+        v[k] = place < T.n && k < parts
+                   ? __ldcg(reinterpret_cast<const float4*>(P.work + ((int64_t)k * P.tokens + T.first + place) * all + j))
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 1; k < kMaxParts; ++k) v[0].x += v[k].x, v[0].y += v[k].y, v[0].z += v[k].z, v[0].w += v[k].w;
+      *reinterpret_cast<float4*>(&h[place][j]) = v[0];
     }
     __syncthreads();
   }
   for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
-    if (chunk != blockIdx.y) load(chunk);
-    const LoraMat& w = P.mat[m];
+    Work next;
+    const bool more = chunk + (int)gridDim.y < chunks;
+    if (more) load(next, chunk + gridDim.y);
+    const LoraMat& w = P.mat[u.m];
     if (T.adapter >= 0) {
-      float acc[4][4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
       const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int kb = 0; kb < kblocks; ++kb) {
         const bool in = kb * 32 + 8 * c < P.rank;
-        const float4* ha = reinterpret_cast<const float4*>(&h[g][m * P.rank + kb * 32 + 8 * c]);
-        const float4* hb = reinterpret_cast<const float4*>(&h[g + 8][m * P.rank + kb * 32 + 8 * c]);
+        const float4* ha = reinterpret_cast<const float4*>(&h[g][u.m * P.rank + kb * 32 + 8 * c]);
+        const float4* hb = reinterpret_cast<const float4*>(&h[g + 8][u.m * P.rank + kb * 32 + 8 * c]);
         const float4 xa[2] = {in ? ha[0] : zero, in ? ha[1] : zero}, xb[2] = {in ? hb[0] : zero, in ? hb[1] : zero};
-        const uint4 now[4] = {b[0], b[1], b[2], b[3]};
-        if (kb + 1 < kblocks) load_b(kb + 1);
-        step32<BF16, 4>(acc, xa, xb, now, 4);
-      }
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) y[r][2 * q + e] += acc[q][2 * r + e];
-    } else if (w.y == w.base) {
-      continue;                                           // nothing to add, nothing to copy
-    }
-    const int64_t o = o0 + 8 * c;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      if (token[r] < 0) continue;
-      float* dst = w.y + (int64_t)token[r] * w.rows + o;
-      if (vec) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (o + 4 * e < w.rows) reinterpret_cast<float4*>(dst)[e] = *reinterpret_cast<const float4*>(&y[r][4 * e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (o + e < w.rows) dst[e] = y[r][e];
+        const uint4 now[4] = {u.b[0], u.b[1], u.b[2], u.b[3]};
+        if (kb + 1 < kblocks) load_b(u, kb + 1);
+        step32<BF16, 4>(u.y, xa, xb, now, 4);
       }
     }
+    const int64_t o = u.o0 + 8 * c;
+    if (T.adapter >= 0 || w.y != w.base) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (token[r] < 0) continue;
+        float* dst = w.y + (int64_t)token[r] * w.rows + o;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 v = make_float4(u.y[2 * e][2 * r], u.y[2 * e][2 * r + 1], u.y[2 * e + 1][2 * r], u.y[2 * e + 1][2 * r + 1]);
+          if ((w.rows & 3) == 0) {
+            if (o + 4 * e < w.rows) reinterpret_cast<float4*>(dst)[e] = v;
+          } else {
+            const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (o + 4 * e + k < w.rows) dst[4 * e + k] = f[k];
+          }
+        }
+      }
+    }
+    if (more) u = next;
   }
 }
 
 template <bool BF16, int NT>
-void shrink(const LoraParams& p, unsigned tiles, int parts, cudaStream_t s) {
+cudaError_t shrink(const LoraParams& p, unsigned tiles, int parts, cudaStream_t s) {
+  auto kernel = lora_shrink_kernel<BF16, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shrink<NT>::kSmem);
+  if (e != cudaSuccess) return e;
   const int groups = (p.n * p.rank / 8 + NT - 1) / NT;
-  lora_shrink_kernel<BF16, NT><<<dim3(tiles, parts, groups), kThreads, 0, s>>>(p);
+  kernel<<<dim3(tiles, parts, groups), kThreads, Shrink<NT>::kSmem, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <bool BF16>
 cudaError_t launch(const LoraParams& p, cudaStream_t s) {
   const unsigned tiles = (unsigned)std::min<int64_t>(p.tokens, p.n_seg + p.tokens / kTile);
   const int parts = column_parts(p.tokens, p.cols);
-  // few tokens: one rank tile per CTA for the sake of latency; many: four of
-  // them, so that x is read once for 32 ranks
-  if (p.tokens <= 16) shrink<BF16, 1>(p, tiles, parts, s);
-  else shrink<BF16, 4>(p, tiles, parts, s);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e;
+  if (p.tokens <= 16) {
+    lora_shrink_few_kernel<BF16><<<dim3(tiles, parts, p.n * p.rank / 8), kThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+  } else if (p.n * p.rank <= 32) {
+    e = shrink<BF16, 4>(p, tiles, parts, s);
+  } else {
+    e = shrink<BF16, 8>(p, tiles, parts, s);             // x is read once for 64 ranks
+  }
   if (e != cudaSuccess) return e;
   unsigned chunks = 0;
   for (int m = 0; m < p.n; ++m) chunks += (unsigned)((p.mat[m].rows + kChunk - 1) / kChunk);

@@ -14,11 +14,9 @@
 // CTA order, so the result does not depend on who is last.
 #pragma once
 
+#include "mma_sync.cuh"
 #include "q4k_internal.h"
 #include "tc_ptx.cuh"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 namespace q4k {
 namespace attn {
@@ -297,22 +295,6 @@ struct Walk {
 // Floats of one piece: per row the sums, then all maxima, then all sums of weights.
 template <int ROWS, int D>
 __host__ __device__ constexpr size_t piece_floats() { return (size_t)ROWS * (D + 2); }
-
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (BF16) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-template <bool BF16>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-  if constexpr (BF16) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
-  else return __half22float2(*reinterpret_cast<const __half2*>(&v));
-}
 
 // Store four consecutive outputs of a row.
 template <bool BF16>
