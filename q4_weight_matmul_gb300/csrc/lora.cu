@@ -124,16 +124,11 @@ __device__ __forceinline__ void split(const float (&a)[8], const float (&b)[8], 
   }
 }
 
-// c += X W^T over 32 k: X rows g and g + 8 as 8 consecutive k each (xa, xb),
-// W row g of each tile as 8 consecutive k (w).
+// c += X W^T over 32 k: X as split() made it, W row g of each tile as 8
+// consecutive k (w).
 template <bool BF16, int NT>
-__device__ __forceinline__ void step32(float (&c)[NT][4], const float4 (&xa)[2], const float4 (&xb)[2],
-                                       const uint4 (&w)[NT], int tiles) {
-  const float a[8] = {xa[0].x, xa[0].y, xa[0].z, xa[0].w, xa[1].x, xa[1].y, xa[1].z, xa[1].w};
-  const float b[8] = {xb[0].x, xb[0].y, xb[0].z, xb[0].w, xb[1].x, xb[1].y, xb[1].z, xb[1].w};
-  uint32_t p[BF16 ? 3 : 2][2][4];
-  float back[2];
-  split<BF16>(a, b, p, back);
+__device__ __forceinline__ void products(float (&c)[NT][4], const uint32_t (&p)[BF16 ? 3 : 2][2][4],
+                                         const float (&back)[2], const uint4 (&w)[NT], int tiles) {
 #pragma unroll
   for (int q = 0; q < NT; ++q) {
     if (q < tiles) {
@@ -147,6 +142,18 @@ __device__ __forceinline__ void step32(float (&c)[NT][4], const float4 (&xa)[2],
       c[q][2] = fmaf(t[2], back[1], c[q][2]), c[q][3] = fmaf(t[3], back[1], c[q][3]);
     }
   }
+}
+
+// The same with X rows g and g + 8 as 8 consecutive k each (xa, xb).
+template <bool BF16, int NT>
+__device__ __forceinline__ void step32(float (&c)[NT][4], const float4 (&xa)[2], const float4 (&xb)[2],
+                                       const uint4 (&w)[NT], int tiles) {
+  const float a[8] = {xa[0].x, xa[0].y, xa[0].z, xa[0].w, xa[1].x, xa[1].y, xa[1].z, xa[1].w};
+  const float b[8] = {xb[0].x, xb[0].y, xb[0].z, xb[0].w, xb[1].x, xb[1].y, xb[1].z, xb[1].w};
+  uint32_t p[BF16 ? 3 : 2][2][4];
+  float back[2];
+  split<BF16>(a, b, p, back);
+  products<BF16, NT>(c, p, back, w, tiles);
 }
 
 // h[part][place][m * rank + j], scaled.  Grid: tiles x column parts x groups
@@ -314,117 +321,195 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraPara
 // of all projections; a warp has 32 outputs of one projection for the tile's
 // tokens at a time.  Output 8 c + 2 q + e of the 32 is column 2 c + e of
 // instruction tile q, so a lane holds 8 consecutive outputs of two tokens.
+// The parts of h are made once per CTA and lie in shared memory as the lanes
+// take them (making them again for every 32 outputs cost as many
+// instructions as all the rest).
 constexpr int kOuts = 32, kChunk = kWarps * kOuts;
-constexpr int kMaxRanks = kLoraMaxMats * 128;
+
+// Blocks of 32 ranks of all projections, and the bytes of one's parts.
+__host__ __device__ constexpr int rank_blocks(int n, int rank) { return n * ((rank + 31) / 32); }
+template <bool BF16>
+__host__ __device__ constexpr int block_bytes() { return (BF16 ? 3 : 2) * 2 * 32 * 16 + 2 * 32 * 4; }
+
+// A ring slot: base of the tile's tokens for a chunk (rows as in the shrink),
+// and 32 ranks of the chunk's rows of B.  The copies of two CTAs keep some
+// 130 KB in flight on an SM; with base and B loaded into registers one chunk
+// ahead (32 KB in flight) plain copying of base to y took 2.4 TB/s.
+constexpr int kBRow = 64;
+constexpr int kSlot = kTile * kXRow + kChunk * kBRow;
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraParams P, int parts, int chunks) {
-  __shared__ __align__(16) float h[kTile][kMaxRanks + 4];
+__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraParams P, int parts, int chunks, int slots) {
+  // [block]: parts [part][instruction][lane], back [row][lane]; then the ring
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int PARTS = BF16 ? 3 : 2;
   const Tile T = find_tile(P, blockIdx.x);
   if (T.n <= 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  const int kblocks = (P.rank + 31) / 32, all = P.n * P.rank;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  const int all = P.n * P.rank, rank_blocks_m = (P.rank + 31) / 32, kblocks = T.adapter >= 0 ? rank_blocks_m : 1;
+  uint8_t* ring = smem + P.n * rank_blocks_m * block_bytes<BF16>();
   const int token[2] = {g < T.n ? token_at(P, T.first + g) : -1, g + 8 < T.n ? token_at(P, T.first + g + 8) : -1};
+  int copy_token[kTile / 4];                             // of the base rows that this thread copies 16 bytes of
+#pragma unroll
+  for (int i = 0; i < kTile / 4; ++i)
+    copy_token[i] = tid / 64 + 4 * i < T.n ? token_at(P, T.first + tid / 64 + 4 * i) : -1;
 
-  // what a warp's outputs of a chunk (projection m, outputs from o0 on) need: base and the first B values; the next
-  // chunk's are loaded while this one's are used
-  struct Work {
-    int m;
-    int64_t o0;
-    const uint16_t* bp;          // B row of the lane's output of tile 0, at its k
-    uint4 b[4];
-    float y[4][4];               // [instruction tile][token g: two outputs, token g + 8: two]
+  // where a chunk is: projection m, whose first chunk is `first`
+  struct Place {
+    int chunk, m, first, kb;
   };
-  int m = 0, first = 0;          // projection of the chunk loaded last, its first chunk
-  auto load_b = [&](Work& u, int kb) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const bool in = T.adapter >= 0 && u.o0 + 8 * (g >> 1) + 2 * q + (g & 1) < P.mat[u.m].rows && kb * 32 + 8 * c < P.rank;
-      u.b[q] = in ? __ldg(reinterpret_cast<const uint4*>(u.bp + 2 * q * P.rank + kb * 32)) : make_uint4(0, 0, 0, 0);
+  auto find = [&](Place& at) {
+    for (;; ++at.m) {
+      const int n = (int)((P.mat[at.m].rows + kChunk - 1) / kChunk);
+      if (at.chunk < at.first + n) break;
+      at.first += n;
     }
   };
-  auto load = [&](Work& u, int chunk) {
-    for (;; ++m) {
-      const int n = (int)((P.mat[m].rows + kChunk - 1) / kChunk);
-      if (chunk < first + n) break;
-      first += n;
-    }
-    const LoraMat& w = P.mat[m];
-    u.m = m;
-    u.o0 = ((int64_t)(chunk - first) * kWarps + warp) * kOuts;
-    u.bp = static_cast<const uint16_t*>(w.b) +
-           ((int64_t)T.adapter * w.rows + u.o0 + 8 * (g >> 1) + (g & 1)) * P.rank + 8 * c;
-    load_b(u, 0);
-    const int64_t o = u.o0 + 8 * c;
+  auto advance = [&](Place& at) {
+    if (++at.kb < kblocks) return;
+    at.kb = 0;
+    at.chunk += gridDim.y;
+    if (at.chunk < chunks) find(at);
+  };
+  Place ahead{(int)blockIdx.y, 0, 0, 0};
+  find(ahead);
+  auto copy = [&](int slot) {
+    if (ahead.chunk < chunks) {
+      const LoraMat& w = P.mat[ahead.m];
+      const int64_t o0 = (int64_t)(ahead.chunk - ahead.first) * kChunk;
+      uint8_t* at = ring + slot * kSlot;
+      if (ahead.kb == 0 && w.base && (w.rows & 3) == 0 && o0 + 4 * (tid % 64) < w.rows) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-      if (token[r] >= 0 && w.base) {
-        const float* src = w.base + (int64_t)token[r] * w.rows + o;
-        if ((w.rows & 3) == 0) {
+        for (int i = 0; i < kTile / 4; ++i)
+          if (copy_token[i] >= 0)
+            copy16(at + (tid / 64 + 4 * i) * kXRow + 16 * (tid % 64),
+                   w.base + (int64_t)copy_token[i] * w.rows + o0 + 4 * (tid % 64));
+      }
+      if (T.adapter >= 0) {
+        const int j = ahead.kb * 32 + 8 * (tid % 4);
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (o + 4 * e < w.rows) v[e] = reinterpret_cast<const float4*>(src)[e];
-        } else {
-          float* f = reinterpret_cast<float*>(v);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (o + e < w.rows) f[e] = src[e];
+        for (int i = 0; i < kChunk / 64; ++i) {
+          const int r = tid / 4 + 64 * i;
+          const bool in = o0 + r < w.rows && j < P.rank;       // zeros elsewhere
+          const uint16_t* from = static_cast<const uint16_t*>(w.b) +
+                                 (in ? ((int64_t)T.adapter * w.rows + o0 + r) * P.rank + j : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                       ::"r"(tc::smem_u32(at + kTile * kXRow + r * kBRow + 16 * (tid % 4))), "l"(from), "r"(in ? 16 : 0)
+                       : "memory");
         }
       }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        u.y[2 * e][2 * r] = v[e].x, u.y[2 * e][2 * r + 1] = v[e].y;
-        u.y[2 * e + 1][2 * r] = v[e].z, u.y[2 * e + 1][2 * r + 1] = v[e].w;
-      }
+      advance(ahead);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");       // an empty one past the last step
   };
-
-  Work u;
-  load(u, blockIdx.y);                                    // these do not wait for the first kernel
+  // the first copies do not wait for the first kernel
+  int put = 0;
+  for (int i = 0; i < slots - 1; ++i) copy(put++);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (T.adapter >= 0) {
-    for (int i = threadIdx.x; i < kTile * all / 4; i += kThreads) {
-      const int place = i / (all / 4), j = 4 * (i - place * (all / 4));
-      float4 v[kMaxParts];
+    // a warp per block: lane (g, c) has 8 ranks of places g and g + 8
+    for (int i = warp; i < P.n * kblocks; i += kWarps) {
+      const int j = 32 * (i % kblocks) + 8 * c;
+      float x[2][8];
 #pragma unroll
-      for (int k = 0; k < kMaxParts; ++k)
-        v[k] = place < T.n && k < parts
-                   ? __ldcg(reinterpret_cast<const float4*>(P.work + ((int64_t)k * P.tokens + T.first + place) * all + j))
-                   : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < 2; ++r) {
+        const bool in = g + 8 * r < T.n && j < P.rank;
+        const float* from = P.work + ((int64_t)T.first + g + 8 * r) * all + i / kblocks * P.rank + j;
+        float4 v[kMaxParts][2];
 #pragma unroll
-      for (int k = 1; k < kMaxParts; ++k) v[0].x += v[k].x, v[0].y += v[k].y, v[0].z += v[k].z, v[0].w += v[k].w;
-      *reinterpret_cast<float4*>(&h[place][j]) = v[0];
+        for (int k = 0; k < kMaxParts; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            v[k][e] = in && k < parts ? __ldcg(reinterpret_cast<const float4*>(from + (int64_t)k * P.tokens * all) + e)
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int k = 1; k < kMaxParts; ++k)
+            v[0][e].x += v[k][e].x, v[0][e].y += v[k][e].y, v[0][e].z += v[k][e].z, v[0][e].w += v[k][e].w;
+          x[r][4 * e] = v[0][e].x, x[r][4 * e + 1] = v[0][e].y, x[r][4 * e + 2] = v[0][e].z, x[r][4 * e + 3] = v[0][e].w;
+        }
+      }
+      uint32_t p[PARTS][2][4];
+      float back[2];
+      split<BF16>(x[0], x[1], p, back);
+      uint8_t* at = smem + i * block_bytes<BF16>();
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          reinterpret_cast<uint4*>(at)[(k * 2 + e) * 32 + lane] = make_uint4(p[k][e][0], p[k][e][1], p[k][e][2], p[k][e][3]);
+      float* scale = reinterpret_cast<float*>(at + PARTS * 2 * 32 * 16);
+      scale[lane] = back[0];
+      scale[32 + lane] = back[1];
     }
-    __syncthreads();
   }
-  for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
-    Work next;
-    const bool more = chunk + (int)gridDim.y < chunks;
-    if (more) load(next, chunk + gridDim.y);
-    const LoraMat& w = P.mat[u.m];
-    if (T.adapter >= 0) {
-      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int kb = 0; kb < kblocks; ++kb) {
-        const bool in = kb * 32 + 8 * c < P.rank;
-        const float4* ha = reinterpret_cast<const float4*>(&h[g][u.m * P.rank + kb * 32 + 8 * c]);
-        const float4* hb = reinterpret_cast<const float4*>(&h[g + 8][u.m * P.rank + kb * 32 + 8 * c]);
-        const float4 xa[2] = {in ? ha[0] : zero, in ? ha[1] : zero}, xb[2] = {in ? hb[0] : zero, in ? hb[1] : zero};
-        const uint4 now[4] = {u.b[0], u.b[1], u.b[2], u.b[3]};
-        if (kb + 1 < kblocks) load_b(u, kb + 1);
-        step32<BF16, 4>(u.y, xa, xb, now, 4);
+
+  Place now{(int)blockIdx.y, 0, 0, 0};
+  find(now);
+  float y[4][4];                                          // [instruction tile][token g: two outputs, token g + 8: two]
+  int get = 0;
+  while (now.chunk < chunks) {
+    if (slots == 3) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();                                      // this step's copies are there, the last step's slot is free
+    copy(put);
+    put = put + 1 == slots ? 0 : put + 1;
+    const LoraMat& w = P.mat[now.m];
+    const int64_t o = (int64_t)(now.chunk - now.first) * kChunk + warp * kOuts + 8 * c;
+    const uint8_t* at = ring + get * kSlot;
+    const bool vec = (w.rows & 3) == 0;
+    if (now.kb == 0) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float4 v[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (token[r] >= 0 && w.base) {
+          if (vec) {
+            const float4* from = reinterpret_cast<const float4*>(at + (g + 8 * r) * kXRow + warp * 128 + c * 32);
+            v[0] = from[0], v[1] = from[1];
+          } else {
+            const float* src = w.base + (int64_t)token[r] * w.rows + o;
+            float* f = reinterpret_cast<float*>(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (o + e < w.rows) f[e] = src[e];
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          y[2 * e][2 * r] = v[e].x, y[2 * e][2 * r + 1] = v[e].y;
+          y[2 * e + 1][2 * r] = v[e].z, y[2 * e + 1][2 * r + 1] = v[e].w;
+        }
       }
     }
-    const int64_t o = u.o0 + 8 * c;
-    if (T.adapter >= 0 || w.y != w.base) {
+    if (T.adapter >= 0) {
+      const uint8_t* parts_at = smem + (now.m * kblocks + now.kb) * block_bytes<BF16>();
+      uint32_t p[PARTS][2][4];
+#pragma unroll
+      for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4 v = reinterpret_cast<const uint4*>(parts_at)[(k * 2 + e) * 32 + lane];
+          p[k][e][0] = v.x, p[k][e][1] = v.y, p[k][e][2] = v.z, p[k][e][3] = v.w;
+        }
+      const float* scale = reinterpret_cast<const float*>(parts_at + PARTS * 2 * 32 * 16);
+      const float back[2] = {scale[lane], scale[32 + lane]};
+      uint4 b[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        b[q] = *reinterpret_cast<const uint4*>(at + kTile * kXRow + (warp * kOuts + 8 * (g >> 1) + 2 * q + (g & 1)) * kBRow +
+                                               16 * c);
+      products<BF16, 4>(y, p, back, b, 4);
+    }
+    if (now.kb + 1 == kblocks && (T.adapter >= 0 || w.y != w.base)) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         if (token[r] < 0) continue;
         float* dst = w.y + (int64_t)token[r] * w.rows + o;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float4 v = make_float4(u.y[2 * e][2 * r], u.y[2 * e][2 * r + 1], u.y[2 * e + 1][2 * r], u.y[2 * e + 1][2 * r + 1]);
-          if ((w.rows & 3) == 0) {
+          const float4 v = make_float4(y[2 * e][2 * r], y[2 * e][2 * r + 1], y[2 * e + 1][2 * r], y[2 * e + 1][2 * r + 1]);
+          if (vec) {
             if (o + 4 * e < w.rows) reinterpret_cast<float4*>(dst)[e] = v;
           } else {
             const float f[4] = {v.x, v.y, v.z, v.w};
@@ -435,8 +520,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
         }
       }
     }
-    if (more) u = next;
+    advance(now);
+    get = get + 1 == slots ? 0 : get + 1;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <bool BF16, int NT>
@@ -467,17 +554,25 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
   for (int m = 0; m < p.n; ++m) chunks += (unsigned)((p.mat[m].rows + kChunk - 1) / kChunk);
   int dev = 0;
   cudaGetDevice(&dev);
-  const unsigned want = (unsigned)std::max(1, 4 * device_info(dev).sm_count / (int)std::min(tiles, 1u << 20));
+  // one wave of two CTAs per SM where the tiles allow
+  const unsigned want = (unsigned)std::max(1, 2 * device_info(dev).sm_count / (int)std::min(tiles, 1u << 20));
+  // three slots if two CTAs fit an SM with them, else two
+  const int parts_bytes = rank_blocks(p.n, p.rank) * block_bytes<BF16>();
+  const int slots = parts_bytes + 3 * kSlot <= 112 * 1024 ? 3 : 2, smem = parts_bytes + slots * kSlot;
+  e = cudaFuncSetAttribute(lora_expand_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           rank_blocks(kLoraMaxMats, 128) * block_bytes<BF16>() + 3 * kSlot);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles, std::min(chunks, want));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lora_expand_kernel<BF16>, p, parts, (int)chunks);
+  return cudaLaunchKernelEx(&cfg, lora_expand_kernel<BF16>, p, parts, (int)chunks, slots);
 }
 
 }  // namespace
