@@ -11,13 +11,12 @@ namespace {
 
 using namespace attn;
 
-// Few-row variant (see launch_few) and the rows of its tiles.
-int few_variant(const AttnParams& p, int* rows) {
+// The few-row kernel's kind (see FewConfig) and the rows of its tiles.
+int few_kind(const AttnParams& p, int* rows) {
   const int64_t n = p.max_q * (p.heads / p.kv_heads);
-  const int v = n <= 8 ? 0 : n <= 16 ? 1 : n <= 32 ? 2 : 3;
-  constexpr int kRows[4] = {8, 16, 32, 64};
-  *rows = kRows[v];
-  return v;
+  const int kind = n <= 4 ? 0 : n <= 8 ? 1 : n <= 16 ? 16 : n <= 32 ? 32 : 64;
+  *rows = kind == 0 ? 4 : kind == 1 ? 8 : kind;
+  return kind;
 }
 
 // The many-row kernel keeps its weights at 16 bits, so it gives 16-bit results.
@@ -45,7 +44,7 @@ bool cache_map(CUtensorMap* map, const AttnParams& p, const void* base, int box)
 
 size_t paged_attn_workspace(const AttnParams& p) {
   int rows;
-  few_variant(p, &rows);
+  few_kind(p, &rows);
   if (many_rows(p)) rows = kChunkRows;
   return kTicketBytes + (size_t)cta_count() * 2 * rows * (p.dim + 2) * sizeof(float);
 }
@@ -64,13 +63,13 @@ cudaError_t launch_paged_attn(const AttnParams& p, cudaStream_t s) {
     return p.bf16 ? launch_chunk<64, true>(kmap, vmap, f, ctas, s) : launch_chunk<64, false>(kmap, vmap, f, ctas, s);
   }
   int rows;
-  const int variant = few_variant(p, &rows);
+  const int kind = few_kind(p, &rows);
   const FewParams f{p, shift, box, 2};
   if (p.dim == 128)
-    return p.bf16 ? launch_few<128, true>(kmap, vmap, f, variant, ctas, s)
-                  : launch_few<128, false>(kmap, vmap, f, variant, ctas, s);
-  return p.bf16 ? launch_few<64, true>(kmap, vmap, f, variant, ctas, s)
-                : launch_few<64, false>(kmap, vmap, f, variant, ctas, s);
+    return p.bf16 ? launch_few<128, true>(kmap, vmap, f, kind, ctas, s)
+                  : launch_few<128, false>(kmap, vmap, f, kind, ctas, s);
+  return p.bf16 ? launch_few<64, true>(kmap, vmap, f, kind, ctas, s)
+                : launch_few<64, false>(kmap, vmap, f, kind, ctas, s);
 }
 
 }  // namespace q4k

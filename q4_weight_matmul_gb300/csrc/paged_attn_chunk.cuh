@@ -89,12 +89,6 @@ __device__ __forceinline__ bool elect() {
   return e != 0;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,

@@ -158,34 +158,38 @@ __device__ __forceinline__ Range share_out(const AttnParams& P, int group, int m
   };
 
   if (n_req <= (single ? 128 : 8)) {
-    int64_t mine = 0, all = 0;                          // !single: lane r keeps request r's units
+    // lane r has request r's units (of the first 32)
+    int64_t own = 0, all = 0;
     if (single) {
-      for (int r = lane; r < n_req; r += 32) all += units(r);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      own = units(lane);
+      for (int r = lane + 32; r < n_req; r += 32) all += units(r);
     } else {
       for (int r = 0; r < n_req; ++r) {
         const int64_t u = units(r);
-        all += u;
-        if (lane == r) mine = u;
+        if (lane == r) own = u;
       }
     }
-    set_share(R, all, min_units);
+    int64_t incl = scan_up(own), base = 0;
+    if (n_req > 32) {
+#pragma unroll
+      for (int o = 16; o; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    }
+    set_share(R, all + __shfl_sync(0xffffffffu, incl, 31), min_units);
     if ((int)blockIdx.x >= R.ctas) return R;
-    int64_t base = 0;
-    for (int r0 = 0; r0 < n_req; r0 += 32) {
-      const int64_t own = single ? units(r0 + lane) : mine, incl = scan_up(own);
+    for (int r0 = 0;;) {
       const unsigned past = __ballot_sync(0xffffffffu, R.begin < base + incl);
       if (past) {
         const int src = __ffs(past) - 1;
         R.req = r0 + src;
         R.req_base = base + __shfl_sync(0xffffffffu, incl - own, src);
         R.per_head = divide(__shfl_sync(0xffffffffu, own, src), P.kv_heads);
-        break;
+        return R;
       }
       base += __shfl_sync(0xffffffffu, incl, 31);
+      r0 += 32;
+      own = units(r0 + lane);
+      incl = scan_up(own);
     }
-    return R;
   }
 
   const int step = single ? THREADS : W, index = single ? tid : warp;
@@ -259,7 +263,8 @@ struct Walk {
     head = (int)divide(R.begin - R.req_base, R.per_head);
     at = R.req_base + head * R.per_head;
     const int lane = threadIdx.x & 31;
-    for (int m0 = 0;; m0 += 32) {
+    tile = 0;
+    for (int m0 = 0; tiles > 1; m0 += 32) {
       const int64_t own = m0 + lane < tiles ? tile_units<ROWS, UNIT>(s, group, P.window, m0 + lane, lo, hi) : 0;
       const int64_t incl = scan_up(own);
       const unsigned past = __ballot_sync(0xffffffffu, R.begin < at + incl);
@@ -296,6 +301,12 @@ struct Walk {
 template <int ROWS, int D>
 __host__ __device__ constexpr size_t piece_floats() { return (size_t)ROWS * (D + 2); }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Store four consecutive outputs of a row.
 template <bool BF16>
 __device__ __forceinline__ void store4(void* out, bool f32, int64_t at, float4 v) {
@@ -318,8 +329,10 @@ __device__ __forceinline__ bool arrive(unsigned* ticket, int pieces, int* flag, 
   if (leader) {
     __threadfence();
     const bool last = atomicAdd(ticket, 1u) == (unsigned)(pieces - 1);
-    if (last) *ticket = 0u;                      // ready for the next call
-    __threadfence();
+    if (last) {
+      *ticket = 0u;                              // ready for the next call
+      __threadfence();
+    }
     *flag = last;
   }
   sync();
@@ -360,28 +373,38 @@ __device__ __forceinline__ void combine(const AttnParams& P, const float* pieces
       if (32 * k + lane < np) weights[(32 * k + lane) * ROWS + r] = m[k] * inv;
   }
   sync();
-  for (int e = t; e < rows * (D / 4); e += 32 * WARPS) {
-    const int r = e / (D / 4), d = (e - r * (D / 4)) * 4;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    int c = 0;
-    constexpr int B = 8;                       // loads in flight
-    for (; c + B <= np; c += B) {
-      float4 v[B];
+  // two outputs' loads of up to eight pieces in flight
+  constexpr int B = 8, E = 2;
+  for (int e0 = t; e0 < rows * (D / 4); e0 += 32 * WARPS * E) {
+    float4 a[E];
 #pragma unroll
-      for (int k = 0; k < B; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(piece(c0 + c + k) + r * D + d));
+    for (int i = 0; i < E; ++i) a[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < np; c += B) {
+      float4 v[E][B];
 #pragma unroll
-      for (int k = 0; k < B; ++k) {
-        const float w = weights[(c + k) * ROWS + r];
-        a.x = fmaf(w, v[k].x, a.x), a.y = fmaf(w, v[k].y, a.y), a.z = fmaf(w, v[k].z, a.z), a.w = fmaf(w, v[k].w, a.w);
+      for (int i = 0; i < E; ++i) {
+        const int e = e0 + 32 * WARPS * i;
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+          if (c + k < np && e < rows * (D / 4)) v[i][k] = __ldcg(reinterpret_cast<const float4*>(piece(c0 + c + k)) + e);
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int e = e0 + 32 * WARPS * i;
+#pragma unroll
+        for (int k = 0; k < B; ++k)
+          if (c + k < np && e < rows * (D / 4)) {
+            const float w = weights[(c + k) * ROWS + e / (D / 4)];
+            a[i].x = fmaf(w, v[i][k].x, a[i].x), a[i].y = fmaf(w, v[i][k].y, a[i].y);
+            a[i].z = fmaf(w, v[i][k].z, a[i].z), a[i].w = fmaf(w, v[i][k].w, a[i].w);
+          }
       }
     }
-#pragma unroll 4
-    for (; c < np; ++c) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(c0 + c) + r * D + d));
-      const float w = weights[c * ROWS + r];
-      a.x = fmaf(w, v.x, a.x), a.y = fmaf(w, v.y, a.y), a.z = fmaf(w, v.z, a.z), a.w = fmaf(w, v.w, a.w);
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      const int e = e0 + 32 * WARPS * i, r = e / (D / 4);
+      if (e < rows * (D / 4)) store4<BF16>(P.out, P.out_f32, out_row(P, s, head, group, row0 + r) * D + e % (D / 4) * 4, a[i]);
     }
-    store4<BF16>(P.out, P.out_f32, out_row(P, s, head, group, row0 + r) * D + d, a);
   }
   sync();
 }

@@ -10,15 +10,19 @@
 // output of the softmax, and put them together once per item.  So no warp
 // ever waits for another while keys stream.
 //
-// Products run on mma.sync m16n8k16 (fp32 accumulate): S = Q K^T with the 16
-// rows of a warp as M, then O += P V.  The weights P keep fp32's precision
-// through 16-bit operands: P = hi + lo (binary16, 22 bits) or hi + mid + lo
-// (bfloat16, 24 bits), scaled by 2^14 so that weights down to 2^-14 of the
-// largest keep all their bits in binary16's normal range.  With at most 8
-// rows to a tile (PACK) hi and lo share one product: hi in rows 0-7, lo in
-// rows 8-15, their results added.  A slot's products start from zero and
-// are added to O in fp32 registers: the tensor core's own running sum
-// truncates, and over thousands of steps that would show in the 1e-6s.
+// Products run on mma.sync m16n8k16 (fp32 accumulate).  The weights P keep
+// fp32's precision through 16-bit operands: P = hi + lo (binary16, 22 bits)
+// or hi + mid + lo (bfloat16, 24 bits), scaled by 2^14 so that weights down
+// to 2^-14 of the largest keep all their bits in binary16's normal range.  A
+// slot's products start from zero and are added to O in fp32 registers: the
+// tensor core's own running sum truncates, and over thousands of steps that
+// would show in the 1e-6s.
+//
+// Up to 8 rows (Rows8) are the N of the products, with 16 keys or 16 values
+// as M: S^T = K Q^T, O^T += V^T P^T, half of the products that rows as M
+// would take.  Up to 4 of them stand twice, in columns 0-3 and 4-7, and the
+// one P V product has hi in the first and lo in the second.  More rows
+// (Rows16) are the M: S = Q K^T, O += P V, 16 to a warp.
 #pragma once
 
 #include "mma_sync.cuh"
@@ -31,8 +35,6 @@ namespace q4k {
 namespace attn {
 
 constexpr int kUnit = 32;               // keys of a slot
-constexpr int kConsumers = 8;           // consumer warps
-constexpr int kFewThreads = 32 * (kConsumers + 4);   // the producer's warpgroup: one warp works
 constexpr float kLift = 14.0f;          // weights are held times 2^14
 
 template <int D>
@@ -41,11 +43,17 @@ struct FewLayout {
   static constexpr int kSlot = 2 * kTile;
 };
 
-// WR: warps that share a slot, 16 rows each (1, 2, 4); PACK: at most 8 rows, WR 1.
-template <int D, int WR, bool PACK>
+// KIND 0: up to 4 rows, 1: up to 8, else 16 rows in each of WR = KIND / 16
+// warps that share a slot (16, 32, 64).
+template <int D, int KIND>
 struct FewConfig {
-  static constexpr int kRows = PACK ? 8 : 16 * WR;
-  static constexpr int kGroups = kConsumers / WR;          // slots consumed at once
+  static constexpr int kWR = KIND < 16 ? 1 : KIND / 16;
+  static constexpr int kRows = KIND == 0 ? 4 : KIND == 1 ? 8 : KIND;
+  // Consumer warps.  Up to 8 rows a slot is little work: four warps keep up, and leave room for three slots each
+  // (eight with one each read 5.4 TB/s of 64 x 8192 keys, four 5.6).
+  static constexpr int kWarps = KIND < 16 ? 4 : 8;
+  static constexpr int kThreads = 32 * (kWarps + 4);       // and the producer's warpgroup, of which one warp works
+  static constexpr int kGroups = kWarps / kWR;             // slots consumed at once
   // bytes where the groups' outputs meet, and later the pieces' weights
   static constexpr int kOutputs = kGroups * kRows * D * 4, kWeights = kMaxCtas * kRows * 4;
   static constexpr int kSum = kOutputs > kWeights ? kOutputs : kWeights;
@@ -67,20 +75,376 @@ __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// The item as a warp sees it.
+struct Item {
+  const uint16_t* q;
+  int64_t key0;                // position 0 of the item's keys
+  int lo, hi;                  // positions that some row of the tile sees
+  int row0, rows, group, head;
+  Shape s;
+  int window;
+  float to_log2;
+
+  __device__ __forceinline__ const uint16_t* q_row(const AttnParams& P, int row, int dim) const {
+    return q + out_row(P, s, head, group, row0 + row) * dim;
+  }
+  // the positions lo .. hi-1 that row `row` of the tile sees
+  __device__ __forceinline__ void bounds(int row, bool has, int& from, int& to) const {
+    const int64_t pos = s.kv - s.n + (row0 + row) / group;
+    const int64_t first = window ? pos - window + 1 : 0;
+    to = has && pos + 1 > key0 ? (int)(pos + 1 - key0) : 0;
+    from = first > key0 ? (int)(first - key0) : 0;
+  }
+};
+
+// Which values of the 16 keys from position `at` on some row sees, as masks of
+// a V operand's registers (pairs of keys 2 c, 2 c + 1, and 8 more).
+__device__ __forceinline__ void keep_masks(uint32_t (&keep)[2], int at, int c, const Item& it) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int j = at + 8 * e + 2 * c;
+    keep[e] = (j >= it.lo && j < it.hi ? 0xffffu : 0u) | (j + 1 >= it.lo && j + 1 < it.hi ? 0xffff0000u : 0u);
+  }
+}
+
+// A new maximum for a row: what to subtract from its scores (a row that has
+// seen nothing yet keeps weights of zero) and the factor of its sums.
+__device__ __forceinline__ void raise(float& m, float top, float& sub, float& f) {
+  sub = top == -INFINITY ? 0.f : top - kLift;
+  f = m == -INFINITY ? 0.f : ex2(m - top);
+  m = top;
+}
+
+// Up to 8 rows as the N of the products; lane (g, c) = (lane / 4, lane % 4)
+// has the scores of keys g and g + 8 and rows 2 c, 2 c + 1, and of O^T values
+// g and g + 8 of every 16.  TWICE: up to 4 rows, in columns 0-3 and again in
+// 4-7.
+template <int D, bool BF16, bool TWICE>
+struct Rows8 {
+  static constexpr int PARTS = BF16 ? 3 : 2, PRODUCTS = TWICE ? 1 + (PARTS > 2) : PARTS;
+  uint32_t q[D / 16][2];
+  float o[D / 16][4];
+  float m[2], l[2];
+  int lo[2], hi[2], lo_all, hi_all;
+
+  __device__ __forceinline__ static int row(int column) { return TWICE ? column & 3 : column; }
+
+  __device__ __forceinline__ bool begin(const AttnParams& P, const Item& it, int lane) {
+    const int g = lane >> 2, c = lane & 3, r = row(g);
+    const bool has = r < it.rows;
+    const uint16_t* from = it.q_row(P, has ? r : 0, D) + 2 * c;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) q[k][e] = has ? *reinterpret_cast<const uint32_t*>(from + 16 * k + 8 * e) : 0u;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[e] = -INFINITY, l[e] = 0.f;
+      it.bounds(row(2 * c + e), row(2 * c + e) < it.rows, lo[e], hi[e]);
+    }
+    int x;
+    it.bounds(0, true, x, hi_all);
+    it.bounds(it.rows - 1, true, lo_all, x);
+    return true;
+  }
+
+  // the slot of the keys from position `at` on; ks, vs: its keys and values
+  __device__ __forceinline__ void slot(const Item& it, uint32_t ks, uint32_t vs, int at, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    // two sums each, of the even and the odd k steps, for shorter chains
+    float s[2][2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[t][0][e] = s[t][1][e] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; k += 2) {
+      uint32_t a[2][2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          ldsm4(a[i][t], ks + Cells<D>::at(16 * t + (lane & 15), (k + i) >> 2, 2 * ((k + i) & 3) + (lane >> 4)));
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) mma16816<BF16>(s[t][i], a[i][t], q[k + i][0], q[k + i][1]);
+    }
+    float top[2] = {m[0], m[1]};
+    const bool inside = at >= lo_all && at + kUnit <= hi_all;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = (s[t][0][e] + s[t][1][e]) * it.to_log2;
+        if (!inside) {
+          const int p = at + 16 * t + g + 8 * (e >> 1);
+          if (p < lo[e & 1] || p >= hi[e & 1]) v = -INFINITY;
+        }
+        s[t][0][e] = v;
+        top[e & 1] = fmaxf(top[e & 1], v);
+      }
+    float sub[2], f[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], x));
+      raise(m[e], top[e], sub[e], f[e]);
+      l[e] *= f[e];
+    }
+    // weights of (key, row pair), split and turned into operands of (row, key pair)
+    uint32_t p[PRODUCTS][2][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float x = ex2(s[t][0][2 * h] - sub[0]), y = ex2(s[t][0][2 * h + 1] - sub[1]);
+        l[0] += x, l[1] += y;
+        uint32_t part[PARTS + 1];
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+          part[i] = pack2<BF16>(x, y);
+          const float2 r = unpack2<BF16>(part[i]);
+          x -= r.x, y -= r.y;
+        }
+        part[PARTS] = 0u;
+#pragma unroll
+        for (int i = 0; i < PRODUCTS; ++i)
+          p[i][t][h] = transpose8x8(!TWICE ? part[i] : c < 2 ? part[2 * i] : part[2 * i + 1]);
+      }
+    const bool edge = at < it.lo || at + kUnit > it.hi;
+    uint32_t keep[2][2];
+    if (edge) {
+      keep_masks(keep[0], at, c, it);
+      keep_masks(keep[1], at + 16, c, it);
+    }
+#pragma unroll
+    for (int n = 0; n < D / 16; n += 4) {
+      uint32_t a[4][2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          ldsm4t(a[i][t], vs + Cells<D>::at(16 * t + (lane & 7) + 8 * (lane >> 4), (n + i) >> 2,
+                                            2 * ((n + i) & 3) + ((lane >> 3) & 1)));
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) a[i][t][e] &= keep[t][e >> 1];
+          }
+        }
+      float acc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < PRODUCTS; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma16816<BF16>(acc[i], a[i][t], p[j][t][0], p[j][t][1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n + i][e] = fmaf(o[n + i][e], f[e & 1], acc[i][e]);
+    }
+  }
+
+  // this group's statistics and outputs [row], [row][D]
+  __device__ __forceinline__ void end(float* stat_m, float* stat_l, float* sum, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int x = 4; x < 32; x <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], x);
+    if (TWICE) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] += __shfl_xor_sync(0xffffffffu, o[i][e], 2);
+      if (c >= 2) return;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (g == 0) stat_m[2 * c + e] = m[e], stat_l[2 * c + e] = l[e];
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        sum[(2 * c + e) * D + 16 * i + g] = o[i][e];
+        sum[(2 * c + e) * D + 16 * i + g + 8] = o[i][2 + e];
+      }
+    }
+  }
+};
+
+// 16 rows, from row `my0` of the tile on, as the M of the products; lane
+// (g, c) has rows g and g + 8, keys or values 2 c, 2 c + 1 of every 8.
+template <int D, bool BF16>
+struct Rows16 {
+  static constexpr int PARTS = BF16 ? 3 : 2;
+  uint32_t q[D / 16][4];
+  float o[D / 8][4];
+  float m[2], l[2];
+  int lo[2], hi[2], lo_all, hi_all, my0;
+
+  // false: the tile has no such rows
+  __device__ __forceinline__ bool begin(const AttnParams& P, const Item& it, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = my0 + g + 8 * r;
+      const bool has = row < it.rows;
+      const uint16_t* from = it.q_row(P, has ? row : 0, D) + 2 * c;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        q[k][r] = has ? *reinterpret_cast<const uint32_t*>(from + 16 * k) : 0u;
+        q[k][2 + r] = has ? *reinterpret_cast<const uint32_t*>(from + 16 * k + 8) : 0u;
+      }
+      m[r] = -INFINITY, l[r] = 0.f;
+      it.bounds(row, has, lo[r], hi[r]);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    if (my0 >= it.rows) return false;
+    int x;
+    it.bounds(my0, true, x, hi_all);
+    it.bounds(min(my0 + 15, it.rows - 1), true, lo_all, x);
+    return true;
+  }
+
+  __device__ __forceinline__ void slot(const Item& it, uint32_t ks, uint32_t vs, int at, int lane) {
+    const int c = lane & 3;
+    float s[4][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) {              // 32 values: chunks 4k .. 4k+3
+      uint32_t b[4][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ldsm4(b[t], ks + Cells<D>::at(8 * t + (lane & 7), k >> 1, 4 * (k & 1) + (lane >> 3)));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) mma16816<BF16>(s[t], q[2 * k], b[t][0], b[t][1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) mma16816<BF16>(s[t], q[2 * k + 1], b[t][2], b[t][3]);
+    }
+    const bool inside = at >= lo_all && at + kUnit <= hi_all;
+    float top[2] = {m[0], m[1]}, sub[2], f[2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[t][e] *= it.to_log2;
+        if (!inside) {
+          const int p = at + 8 * t + 2 * c + (e & 1);
+          if (p < lo[e >> 1] || p >= hi[e >> 1]) s[t][e] = -INFINITY;
+        }
+        top[e >> 1] = fmaxf(top[e >> 1], s[t][e]);
+      }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+      raise(m[r], top[r], sub[r], f[r]);
+      l[r] *= f[r];
+    }
+    // weights, their sums, and their 16-bit parts as A operands of two k steps of 16 keys
+    uint32_t p[PARTS][2][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float x = ex2(s[t][2 * r] - sub[r]), y = ex2(s[t][2 * r + 1] - sub[r]);
+        l[r] += x + y;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) {
+          const uint32_t h = pack2<BF16>(x, y);
+          const float2 v = unpack2<BF16>(h);
+          x -= v.x, y -= v.y;
+          p[i][t >> 1][(t & 1) * 2 + r] = h;
+        }
+      }
+    const bool edge = at < it.lo || at + kUnit > it.hi;
+    uint32_t keep[2][2];
+    if (edge) {
+      keep_masks(keep[0], at, c, it);
+      keep_masks(keep[1], at + 16, c, it);
+    }
+#pragma unroll
+    for (int n = 0; n < D / 32; ++n) {              // 32 values: four tiles of 8
+      uint32_t b[2][2][4];   // [16 values][16 keys]: (keys 0-7, values 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          ldsm4t(b[j][k], vs + Cells<D>::at(16 * k + (lane & 15), n >> 1, 4 * (n & 1) + 2 * j + (lane >> 4)));
+          if (edge) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[j][k][e] &= keep[k][e & 1];
+          }
+        }
+      float acc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma16816<BF16>(acc[j], p[i][k], b[j >> 1][k][2 * (j & 1)], b[j >> 1][k][2 * (j & 1) + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[4 * n + i][e] = fmaf(o[4 * n + i][e], f[e >> 1], acc[i][e]);
+    }
+  }
+
+  __device__ __forceinline__ void end(float* stat_m, float* stat_l, float* sum, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      const int row = my0 + g + 8 * r;
+      if (c == 0) stat_m[row] = m[r], stat_l[row] = l[r];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        *reinterpret_cast<float2*>(sum + (size_t)row * D + 8 * i + 2 * c) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+    }
+  }
+};
+
+template <int D, bool BF16, int KIND>
+struct RowsOf {
+  using type = Rows16<D, BF16>;
+};
+template <int D, bool BF16>
+struct RowsOf<D, BF16, 0> {
+  using type = Rows8<D, BF16, true>;
+};
+template <int D, bool BF16>
+struct RowsOf<D, BF16, 1> {
+  using type = Rows8<D, BF16, false>;
+};
+
 struct FewParams {
   AttnParams a;
   int page_shift, box;           // box: keys of one copy, min(page size, 32)
   int min_units;
 };
 
-template <int D, bool BF16, int WR, bool PACK>
-__global__ void __launch_bounds__(kFewThreads, 1)
+template <int D, bool BF16, int KIND>
+__global__ void __launch_bounds__((FewConfig<D, KIND>::kThreads), 1)
 paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                       const __grid_constant__ FewParams F) {
   using L = FewLayout<D>;
-  using C = FewConfig<D, WR, PACK>;
-  constexpr int ROWS = C::kRows;
-  constexpr int PARTS = BF16 ? 3 : 2;               // 16-bit parts of a weight
+  using C = FewConfig<D, KIND>;
+  constexpr int ROWS = C::kRows, WR = C::kWR;
   extern __shared__ uint8_t raw[];
   const AttnParams& P = F.a;
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -90,8 +454,8 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   uint64_t* empty = full + C::kSlots;
   int64_t* scratch = reinterpret_cast<int64_t*>(empty + C::kSlots);   // 16 words
   float* stat_m = reinterpret_cast<float*>(scratch + 16);             // [group][row]
-  float* stat_l = stat_m + kConsumers * 16;
-  volatile int* gave_up = reinterpret_cast<volatile int*>(stat_l + kConsumers * 16);
+  float* stat_l = stat_m + 128;
+  volatile int* gave_up = reinterpret_cast<volatile int*>(stat_l + 128);
   int* last = const_cast<int*>(gave_up) + 1;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -104,7 +468,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const Range R = share_out<ROWS, kUnit, kFewThreads>(P, group, F.min_units, scratch);
+  const Range R = share_out<ROWS, kUnit, C::kThreads>(P, group, F.min_units, scratch);
   if ((int)blockIdx.x >= R.ctas) return;
   __syncthreads();                                   // the barriers are there
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -118,11 +482,11 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   w.first(P, R, group);
   uint32_t issued = 0;                               // slots before this item, the same count in every warp
 
-  // 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
-  if (warp >= kConsumers) {
+  // KIND >= 16: 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+  if (warp >= C::kWarps) {
     // ---------------------------------------------------------- producer
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-    if (warp > kConsumers) return;
+    if constexpr (KIND >= 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp > C::kWarps) return;
     const int pages_slot = F.box < kUnit ? kUnit / F.box : 1;
     const int none = P.num_pages > 0 ? (int)P.num_pages : 1;    // a page past the end reads as zeros
     do {
@@ -169,229 +533,30 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   }
 
   // ------------------------------------------------------------ consumers
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  constexpr int kThreads = 32 * kConsumers;
+  if constexpr (KIND >= 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  constexpr int kThreads = 32 * C::kWarps;
   auto sync = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   const uint32_t grp = warp / WR;
-  const int wr = warp % WR;
-  const int g = lane >> 2, c2 = (lane & 3) * 2;
-  const float to_log2 = P.scale * 1.4426950408889634f;
   float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
+  typename RowsOf<D, BF16, KIND>::type part;
+  if constexpr (KIND >= 16) part.my0 = warp % WR * 16;
 
   do {
-    const int rows_all = w.s.n * group, row0 = w.tile * ROWS;
-    const int rows = min(ROWS, rows_all - row0);
-    const int my0 = wr * 16;                          // first of this warp's rows within the tile
-    const bool active = my0 < rows;
-    // Q fragments: rows g and g + 8 (PACK: row g only)
-    uint32_t q[D / 16][4];
-    const int ra = my0 + g, rb = my0 + g + 8;
-    const bool has_a = ra < rows, has_b = !PACK && rb < rows;
-    {
-      const uint16_t* qa = static_cast<const uint16_t*>(P.q);
-      const uint16_t* pa = qa + (has_a ? out_row(P, w.s, w.head, group, row0 + ra) * D : 0);
-      const uint16_t* pb = qa + (has_b ? out_row(P, w.s, w.head, group, row0 + rb) * D : 0);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        q[k][0] = has_a ? *reinterpret_cast<const uint32_t*>(pa + 16 * k + c2) : 0u;
-        q[k][1] = has_b ? *reinterpret_cast<const uint32_t*>(pb + 16 * k + c2) : 0u;
-        q[k][2] = has_a ? *reinterpret_cast<const uint32_t*>(pa + 16 * k + 8 + c2) : 0u;
-        q[k][3] = has_b ? *reinterpret_cast<const uint32_t*>(pb + 16 * k + 8 + c2) : 0u;
-      }
-    }
-    // the keys each row sees, as positions within the item: [lo_x, hi_x)
+    const int row0 = w.tile * ROWS, rows = min(ROWS, w.s.n * group - row0);
     const int64_t key0 = (w.lo / kUnit) * kUnit;
-    auto bounds = [&](int row, bool has, int& lo, int& hi) {
-      const int64_t pos = w.s.kv - w.s.n + (row0 + row) / group;
-      const int64_t from = P.window ? pos - P.window + 1 : 0;
-      hi = has && pos + 1 > key0 ? (int)(pos + 1 - key0) : 0;
-      lo = from > key0 ? (int)(from - key0) : 0;
-    };
-    int lo_a, hi_a, lo_b, hi_b;
-    bounds(ra, has_a, lo_a, hi_a);
-    bounds(rb, has_b, lo_b, hi_b);
-    // positions that every row of the warp sees need no mask
-    int lo_all = 0, hi_all = 0;
-    if (active) {
-      int x;
-      bounds(my0, true, x, hi_all);
-      bounds(min(my0 + 15, rows - 1), true, lo_all, x);
-    }
-    const int lo_item = (int)(w.lo - key0), hi_item = (int)(w.hi - key0);
-
-    constexpr int NT = D / 8;
-    float o[NT][PACK ? 2 : 4];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < (PACK ? 2 : 4); ++e) o[i][e] = 0.f;
-    float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
-
+    const Item it{static_cast<const uint16_t*>(P.q), key0, (int)(w.lo - key0), (int)(w.hi - key0), row0, rows, group,
+                  w.head, w.s, P.window, P.scale * 1.4426950408889634f};
+    const bool active = part.begin(P, it, lane);
     for (int u = w.u0; u < w.u1; ++u, ++issued) {
       if (issued % C::kGroups != grp) continue;
       const int slot = issued % C::kSlots;
       wait(&full[slot], (issued / C::kSlots) & 1);
-      if (active) {
-        const uint32_t ks = ring + slot * L::kSlot, vs = ks + L::kTile;
-        // S: 4 tiles of 8 keys
-        float s[4][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s[t][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {              // 32 values: chunks 4k .. 4k+3
-          uint32_t b[4][4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) ldsm4(b[t], ks + Cells<D>::at(8 * t + (lane & 7), k >> 1, 4 * (k & 1) + (lane >> 3)));
-#pragma unroll
-          for (int t = 0; t < 4; ++t) mma16816<BF16>(s[t], q[2 * k], b[t][0], b[t][1]);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) mma16816<BF16>(s[t], q[2 * k + 1], b[t][2], b[t][3]);
-        }
-        // scores in units of log 2, masked where a row does not see the key
-        const int at = u * kUnit;
-        const bool inside = at >= lo_all && at + kUnit <= hi_all;
-        float top_a = m_a, top_b = m_b;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            s[t][e] *= to_log2;
-            if (!inside) {
-              const int p = at + 8 * t + c2 + (e & 1);
-              const bool seen = e < 2 ? (p >= lo_a && p < hi_a) : (p >= lo_b && p < hi_b);
-              if (!seen) s[t][e] = -INFINITY;
-            }
-          }
-          top_a = fmaxf(top_a, fmaxf(s[t][0], s[t][1]));
-          top_b = fmaxf(top_b, fmaxf(s[t][2], s[t][3]));
-        }
-        top_a = fmaxf(top_a, __shfl_xor_sync(0xffffffffu, top_a, 1));
-        top_a = fmaxf(top_a, __shfl_xor_sync(0xffffffffu, top_a, 2));
-        if (!PACK) {
-          top_b = fmaxf(top_b, __shfl_xor_sync(0xffffffffu, top_b, 1));
-          top_b = fmaxf(top_b, __shfl_xor_sync(0xffffffffu, top_b, 2));
-        }
-        // a row that has seen nothing yet keeps weights of zero
-        const float sub_a = top_a == -INFINITY ? 0.f : top_a - kLift, sub_b = top_b == -INFINITY ? 0.f : top_b - kLift;
-        const float f_a = m_a == -INFINITY ? 0.f : exp2f(m_a - top_a);
-        const float f_b = m_b == -INFINITY ? 0.f : exp2f(m_b - top_b);
-        m_a = top_a, m_b = top_b;
-        // weights, their sums, and their 16-bit parts as A fragments of two k steps of 16 keys
-        uint32_t p[PARTS][2][4];
-        float add_a = 0.f, add_b = 0.f;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float e0 = exp2f(s[t][0] - sub_a), e1 = exp2f(s[t][1] - sub_a);
-          float e2 = 0.f, e3 = 0.f;
-          add_a += e0 + e1;
-          if (!PACK) {
-            e2 = exp2f(s[t][2] - sub_b), e3 = exp2f(s[t][3] - sub_b);
-            add_b += e2 + e3;
-          }
-#pragma unroll
-          for (int i = 0; i < PARTS; ++i) {
-            const uint32_t h = pack2<BF16>(e0, e1);
-            const float2 f = unpack2<BF16>(h);
-            e0 -= f.x, e1 -= f.y;
-            p[i][t >> 1][(t & 1) * 2] = h;
-            if (!PACK) {
-              const uint32_t h2 = pack2<BF16>(e2, e3);
-              const float2 f2 = unpack2<BF16>(h2);
-              e2 -= f2.x, e3 -= f2.y;
-              p[i][t >> 1][(t & 1) * 2 + 1] = h2;
-            }
-          }
-        }
-        l_a = l_a * f_a + add_a;
-        l_b = l_b * f_b + add_b;
-        // values that no row of the tile sees may be anything: they become zeros
-        uint32_t keep[2][2];
-        const bool edge = at < lo_item || at + kUnit > hi_item;
-        if (edge) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int j = at + 16 * k + 8 * e + c2;
-              keep[k][e] = (j >= lo_item && j < hi_item ? 0xffffu : 0u) |
-                           (j + 1 >= lo_item && j + 1 < hi_item ? 0xffff0000u : 0u);
-            }
-        }
-        // O += P V, 32 values (four tiles of 8) at a time
-#pragma unroll
-        for (int n = 0; n < D / 32; ++n) {
-          float acc[4][4];
-          uint32_t b[2][2][4];   // [16 values][16 keys]: (keys 0-7, values 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              ldsm4t(b[j][k], vs + Cells<D>::at(16 * k + (lane & 15), n >> 1, 4 * (n & 1) + 2 * j + (lane >> 4)));
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) b[j][k][e] &= keep[k][e & 1];
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            constexpr int STEP = PACK ? 2 : 1;
-#pragma unroll
-            for (int i = 0; i < PARTS; i += STEP) {
-              uint32_t a[4];
-              if constexpr (PACK) {
-                const int lo = i + 1 < PARTS ? i + 1 : i;
-                a[0] = p[i][k][0], a[2] = p[i][k][2];
-                a[1] = i + 1 < PARTS ? p[lo][k][0] : 0u, a[3] = i + 1 < PARTS ? p[lo][k][2] : 0u;
-              } else {
-                a[0] = p[i][k][0], a[1] = p[i][k][1], a[2] = p[i][k][2], a[3] = p[i][k][3];
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma16816<BF16>(acc[j], a, b[j >> 1][k][2 * (j & 1)], b[j >> 1][k][2 * (j & 1) + 1]);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float(&x)[PACK ? 2 : 4] = o[4 * n + i];
-            if constexpr (PACK) {
-              x[0] = fmaf(x[0], f_a, acc[i][0] + acc[i][2]);
-              x[1] = fmaf(x[1], f_a, acc[i][1] + acc[i][3]);
-            } else {
-              x[0] = fmaf(x[0], f_a, acc[i][0]), x[1] = fmaf(x[1], f_a, acc[i][1]);
-              x[2] = fmaf(x[2], f_b, acc[i][2]), x[3] = fmaf(x[3], f_b, acc[i][3]);
-            }
-          }
-        }
-      }
+      if (active) part.slot(it, ring + slot * L::kSlot, ring + slot * L::kSlot + L::kTile, u * kUnit, lane);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty[slot]);
     }
-
-    // ---- the groups' statistics and outputs meet: sum[group][row][D]
-    l_a += __shfl_xor_sync(0xffffffffu, l_a, 1);
-    l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
-    l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
-    l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-    if ((lane & 3) == 0) {
-      stat_m[grp * ROWS + my0 + g] = m_a;
-      stat_l[grp * ROWS + my0 + g] = l_a;
-      if (!PACK) {
-        stat_m[grp * ROWS + my0 + g + 8] = m_b;
-        stat_l[grp * ROWS + my0 + g + 8] = l_b;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      float* at = sum + (size_t)(grp * ROWS + my0 + g) * D + 8 * i + c2;
-      *reinterpret_cast<float2*>(at) = make_float2(o[i][0], o[i][1]);
-      if constexpr (!PACK) *reinterpret_cast<float2*>(at + 8 * D) = make_float2(o[i][2], o[i][3]);
-    }
+    // the groups' statistics and outputs meet: sum[group][row][D]
+    part.end(stat_m + grp * ROWS, stat_l + grp * ROWS, sum + (size_t)grp * ROWS * D, lane);
     sync();
     const bool whole = w.u0 == 0 && w.u1 == w.units;
     float* mine = pieces + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * piece_floats<ROWS, D>();
@@ -428,24 +593,24 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     } else {
       const int c0 = owner(w.at, R), c1 = owner(w.at + w.units - 1, R);
       if (arrive(static_cast<unsigned*>(P.workspace) + c0, c1 - c0 + 1, last, tid == 0, sync))
-        combine<ROWS, D, BF16, kConsumers>(P, pieces, c0, c1, w.s, w.head, group, row0, rows, sum, tid, sync);
+        combine<ROWS, D, BF16, C::kWarps>(P, pieces, c0, c1, w.s, w.head, group, row0, rows, sum, tid, sync);
     }
   } while (w.next(P, R, group));
 }
 
 // Launch the variant; defined in one translation unit per head size and type.
 template <int D, bool BF16>
-cudaError_t launch_few(const CUtensorMap& kmap, const CUtensorMap& vmap, const FewParams& f, int variant, int ctas,
+cudaError_t launch_few(const CUtensorMap& kmap, const CUtensorMap& vmap, const FewParams& f, int kind, int ctas,
                        cudaStream_t s);
 
-template <int D, bool BF16, int WR, bool PACK>
+template <int D, bool BF16, int KIND>
 cudaError_t launch_few_variant(const CUtensorMap& kmap, const CUtensorMap& vmap, const FewParams& f, int ctas,
                                cudaStream_t s) {
-  auto kernel = paged_attn_few_kernel<D, BF16, WR, PACK>;
-  constexpr int smem = FewConfig<D, WR, PACK>::kSmem;
+  auto kernel = paged_attn_few_kernel<D, BF16, KIND>;
+  constexpr int smem = FewConfig<D, KIND>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kFewThreads, smem, s>>>(kmap, vmap, f);
+  kernel<<<ctas, FewConfig<D, KIND>::kThreads, smem, s>>>(kmap, vmap, f);
   return cudaGetLastError();
 }
 

@@ -4,13 +4,14 @@
 namespace q4k {
 namespace attn {
 template <>
-cudaError_t launch_few<128, false>(const CUtensorMap& kmap, const CUtensorMap& vmap, const FewParams& f, int variant,
+cudaError_t launch_few<128, false>(const CUtensorMap& kmap, const CUtensorMap& vmap, const FewParams& f, int kind,
                                 int ctas, cudaStream_t s) {
-  switch (variant) {
-    case 0: return launch_few_variant<128, false, 1, true>(kmap, vmap, f, ctas, s);
-    case 1: return launch_few_variant<128, false, 1, false>(kmap, vmap, f, ctas, s);
-    case 2: return launch_few_variant<128, false, 2, false>(kmap, vmap, f, ctas, s);
-    default: return launch_few_variant<128, false, 4, false>(kmap, vmap, f, ctas, s);
+  switch (kind) {
+    case 0: return launch_few_variant<128, false, 0>(kmap, vmap, f, ctas, s);
+    case 1: return launch_few_variant<128, false, 1>(kmap, vmap, f, ctas, s);
+    case 16: return launch_few_variant<128, false, 16>(kmap, vmap, f, ctas, s);
+    case 32: return launch_few_variant<128, false, 32>(kmap, vmap, f, ctas, s);
+    default: return launch_few_variant<128, false, 64>(kmap, vmap, f, ctas, s);
   }
 }
 }  // namespace attn
