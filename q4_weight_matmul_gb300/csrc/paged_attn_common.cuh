@@ -347,6 +347,27 @@ __device__ __forceinline__ void combine(const AttnParams& P, const float* pieces
   // piece of CTA c: slot 1 (the item starts in its range) for the first, slot 0 for the others
   auto piece = [&](int c) { return pieces + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * piece_floats<ROWS, D>(); };
   const int np = c1 - c0 + 1, lane = t & 31;
+  if (np <= 8) {
+    // few pieces: a thread per row
+    for (int r = t; r < rows; r += 32 * WARPS) {
+      float m[8], l[8], top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        m[k] = k < np ? __ldcg(piece(c0 + k) + ROWS * D + r) : -INFINITY;
+        l[k] = k < np ? __ldcg(piece(c0 + k) + ROWS * D + ROWS + r) : 0.f;
+        top = fmaxf(top, m[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        m[k] = m[k] == -INFINITY ? 0.f : ex2(m[k] - top);
+        sum += m[k] * l[k];
+      }
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < np) weights[k * ROWS + r] = m[k] * inv;
+    }
+  } else
   // a warp per row: the lanes have its pieces' statistics
   for (int r = t >> 5; r < rows; r += WARPS) {
     constexpr int K = kMaxCtas / 32;

@@ -482,10 +482,10 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   w.first(P, R, group);
   uint32_t issued = 0;                               // slots before this item, the same count in every warp
 
-  // KIND >= 16: 384 threads x 168 registers at launch = 256 x 208 + 128 x 88
+  // KIND >= 16: 384 threads x 168 registers at launch = 256 x 232 + 128 x 40
   if (warp >= C::kWarps) {
     // ---------------------------------------------------------- producer
-    if constexpr (KIND >= 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if constexpr (KIND >= 16) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp > C::kWarps) return;
     const int pages_slot = F.box < kUnit ? kUnit / F.box : 1;
     const int none = P.num_pages > 0 ? (int)P.num_pages : 1;    // a page past the end reads as zeros
@@ -533,7 +533,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   }
 
   // ------------------------------------------------------------ consumers
-  if constexpr (KIND >= 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  if constexpr (KIND >= 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
   constexpr int kThreads = 32 * C::kWarps;
   auto sync = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   const uint32_t grp = warp / WR;
