@@ -9,10 +9,10 @@
 //
 //   warp 8   streams key and value tiles (64 x D, tensor copies of pages or
 //            page parts, 128-byte swizzled) into a ring of ten
-//   warps 9, 10   issue a half's products: S = Q K^T (both operands from
-//            shared memory, S in tensor memory), O += P V (P from tensor
-//            memory, V read with its keys as the K dimension, O in tensor
-//            memory); one warp polling for both halves was the bottleneck
+//   warps 9, 10     issue a half's S = Q K^T (both operands from shared
+//            memory, S in tensor memory)
+//   warps 12, 13    issue a half's O += P V (P from tensor memory, V read with
+//            its keys as the K dimension, O in tensor memory)
 //   warps 0-3, 4-7   load Q, turn S into P = exp2(S c - m) in place, rescale
 //            O when a row's maximum grows, write the results
 //
@@ -21,6 +21,9 @@
 // (tiles of 128 keys with one S per half spent half of the time in that
 // chain: 4400 cycles per 128 keys against 2048 of tensor work).  64 keys is
 // what tensor memory has room for: 2 (halves) x (2 x 64 + D) columns of 512.
+// Each kind of product of each half has a warp of its own, whose waits hold
+// up nothing else (one warp for both kinds of a half took 1830 cycles per 64
+// keys, one polling for both halves 3800; the tensor work is 1280).
 //
 // P is rounded to the cache's type for the second product (16 bits: 2^-11 or
 // 2^-8 of each weight, as the result itself is); its sum is taken in fp32
@@ -40,7 +43,7 @@ namespace attn {
 
 constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 64;
-constexpr int kChunkThreads = 352;
+constexpr int kChunkThreads = 512;
 constexpr float kChunkLift = 8.0f, kChunkGrow = 6.0f;
 
 template <int D>
@@ -124,7 +127,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
       tc::mbar_init(&p_full[i], 4);
       tc::mbar_init(&pv_done[i], 1);
     }
-    tc::mbar_init(drained, 2);
+    tc::mbar_init(drained, 4);
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -150,136 +153,173 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     }
   };
 
-  Walk<kChunkRows, kChunkKeys> w;
-  w.first(P, R, group);
-
-  if (warp == 8) {
-    // ------------------------------------------------ key and value tiles
-    const int none = P.num_pages > 0 ? (int)P.num_pages : 1;        // a page past the end reads as zeros
-    const int parts = kChunkKeys / F.box;                            // of one tile
-    uint32_t n = 0;                                                  // tiles issued
-    do {
-      const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
-      const int32_t* table = P.page_table + (int64_t)w.req * P.max_pages;
-      for (int u = w.u0; u < w.u1; ++u) {
-        // lane i has part i's page (parts <= 8)
-        const int64_t key = key0 + (int64_t)u * kChunkKeys;
-        int page = none;
-        if (lane < parts) {
-          const int64_t p = (key + (int64_t)lane * F.box) >> F.page_shift, from = p << F.page_shift;
-          if (from < w.hi && from + P.page_size > w.lo) {
-            page = table[p];
-            if (page < 0 || page >= P.num_pages) {
-              atomicOr(P.err, kErrIndex);
-              page = none;
-            }
-          }
-        }
-        const int cell = (int)((key + (int64_t)lane * F.box) & (P.page_size - 1));
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++n) {
-          const uint32_t slot = n % L::kRing, use = n / L::kRing;
-          if (use > 0) wait(&empty[slot], use - 1);
-          const bool go = !*gave_up;
-          if (lane == 0 && go) tc::mbar_arrive_expect_tx(&full[slot], L::kTile);
-          __syncwarp();
-          if (lane < parts && go)
-            load_cells(ring + slot * L::kTile + lane * F.box * D * 2, kv ? &vmap : &kmap, cell >> 3, page, P.kv_heads,
-                       w.head, &full[slot]);
-        }
-      }
-    } while (w.next(P, R, group));
-    // after a wait gave up, the copies still in flight end before the block does
-    if (lane == 0 && *gave_up) {
-      for (uint32_t j = n < L::kRing ? 0 : n - L::kRing; j < n; ++j)
-        if (!tc::mbar_wait_sleep(&full[j % L::kRing], (j / L::kRing) & 1)) break;
-    }
-  } else if (warp >= 9) {
-    // ------------------------------------------------------------ products
-    // S = Q K^T of a unit when its S tile is free (the P V of two units before is done), O += P V when its P is
-    // there.  Each half goes at its own pace; a ring tile is free when both have let it go.
-    constexpr uint32_t kQK = tc::idesc_f16(128, kChunkKeys, BF16);
-    constexpr uint32_t kPV = tc::idesc_f16(128, D, BF16) | (1u << 16);        // B: K is its slow dimension
-    const int h = warp - 9;
-    const uint32_t q_at = (q_smem + h * L::kQTile) >> 4;
-    uint32_t n0 = 0, item = 0;            // ring tiles before this item: K of unit u is n0 + 2 u, V the next
-    uint32_t uses0 = 0, uses1 = 0;        // of this half's S tiles, before this item
-    auto landed = [&](uint32_t n) { wait(&full[n % L::kRing], n / L::kRing); };
-    auto release = [&](uint32_t n) {
-      if (lane == 0) tc::mbar_arrive(&empty[n % L::kRing]);
-    };
-    auto qk = [&](int u) {
-      const int b = u & 1;
-      const uint32_t n = n0 + 2 * u, k_at = (ring + n % L::kRing * L::kTile) >> 4;
-      landed(n);
-      if (elect()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          tc::mma_f16_ss(s_at(h, b), desc(q_at + (((k >> 2) * L::kQHalf + (k & 3) * 32) >> 4), 16, 1024),
-                         desc(k_at + (((k >> 2) * C::kNext + (k & 3) * 32) >> 4), 16, C::kGroup), kQK, k > 0);
-        tc::mma_commit(&s_full[2 * h + b]);
-      }
-      __syncwarp();
-    };
-    do {
-      const int halves = w.s.n * group - w.tile * kChunkRows > 128 ? 2 : 1, units = w.u1 - w.u0;
-      if (h >= halves) {                  // no rows: only let the tiles go
-        for (int i = 0; i < 2 * units; ++i) {
-          landed(n0 + i);
-          release(n0 + i);
-        }
-        n0 += 2 * units;
-        continue;
-      }
-      const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
-      wait(&q_full[h], item++);
-      tc::fence_after_sync();
-      qk(0);
-      if (units > 1) qk(1);
-      for (int u = 0; u < units && !*gave_up; ++u) {
-        const int b = u & 1;
-        const uint32_t n = n0 + 2 * u, use = (b ? uses1 : uses0) + (u >> 1);
-        landed(n + 1);
-        const int64_t key = key0 + (int64_t)(w.u0 + u) * kChunkKeys;
-        if (key < w.lo || key + kChunkKeys > w.hi) {
-          // values that no row of the tile sees may be anything: they become zeros (both halves write them)
-          const int first = w.lo > key ? (int)min(w.lo - key, (int64_t)kChunkKeys) : 0;
-          const int end = w.hi > key ? (int)min(w.hi - key, (int64_t)kChunkKeys) : 0;
-          uint8_t* v = smem + L::kQ + (n + 1) % L::kRing * L::kTile;
-          for (int i = lane; i < kChunkKeys * (D / 8); i += 32) {
-            const int r = i / (D / 8), c = i % (D / 8);
-            if (r < first || r >= end)
-              *reinterpret_cast<uint4*>(v + C::at(r, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
-          }
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-        }
-        wait(&p_full[2 * h + b], use);
-        tc::fence_after_sync();
-        const uint32_t v_at = (ring + (n + 1) % L::kRing * L::kTile) >> 4;
-        if (elect()) {
-          mma_f16_ts(o_at(h), s_at(h, b), desc(v_at, C::kNext, C::kGroup), kPV, u > 0);
-#pragma unroll
-          for (int k = 1; k < kChunkKeys / 16; ++k)
-            mma_f16_ts(o_at(h), s_at(h, b) + 8 * k, desc(v_at + (k * 2 * C::kGroup >> 4), C::kNext, C::kGroup), kPV, 1);
-          tc::mma_commit(&pv_done[2 * h + b]);
-        }
-        __syncwarp();
-        release(n);                       // P is there, so S is done
-        wait(&pv_done[2 * h + b], use);
-        tc::fence_after_sync();
-        release(n + 1);
-        if (u + 2 < units) qk(u + 2);
-      }
-      n0 += 2 * units;
-      uses0 += (units + 1) >> 1;
-      uses1 += units >> 1;
-      if (__any_sync(0xffffffffu, *gave_up)) break;
-    } while (w.next(P, R, group));
+  auto landed = [&](uint32_t n) { wait(&full[n % L::kRing], n / L::kRing); };
+  auto release = [&](uint32_t n) {
+    if (lane == 0) tc::mbar_arrive(&empty[n % L::kRing]);
+  };
+  // the end of a product-issuing warp: its products are done
+  auto drain = [&] {
     if (elect()) tc::mma_commit(drained);
     __syncwarp();
     if (!tc::mbar_wait_sleep(drained, 0)) atomicOr(P.err, 1);
+  };
+
+  Walk<kChunkRows, kChunkKeys> w;
+  w.first(P, R, group);
+  // 512 threads x 128 registers at launch = 256 x 176 + 256 x 80
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == 8) {
+      // ------------------------------------------------ key and value tiles
+      const int none = P.num_pages > 0 ? (int)P.num_pages : 1;        // a page past the end reads as zeros
+      const int parts = kChunkKeys / F.box;                            // of one tile
+      uint32_t n = 0;                                                  // tiles issued
+      do {
+        const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
+        const int32_t* table = P.page_table + (int64_t)w.req * P.max_pages;
+        // lane i has part i's page (parts <= 4), read one unit ahead
+        auto page_of = [&](int u, int& page) {                       // false: no row needs it
+          const int64_t p = (key0 + (int64_t)u * kChunkKeys + (int64_t)lane * F.box) >> F.page_shift;
+          const int64_t from = p << F.page_shift;
+          const bool need = u < w.u1 && lane < parts && from < w.hi && from + P.page_size > w.lo;
+          page = need ? table[p] : none;
+          return need;
+        };
+        int next;
+        bool needed = page_of(w.u0, next);
+        for (int u = w.u0; u < w.u1; ++u) {
+          const int64_t key = key0 + (int64_t)u * kChunkKeys;
+          int page = next;
+          const bool bad = needed && (page < 0 || page >= P.num_pages);
+          needed = page_of(u + 1, next);
+          if (bad) {
+            atomicOr(P.err, kErrIndex);
+            page = none;
+          }
+          const int cell = (int)((key + (int64_t)lane * F.box) & (P.page_size - 1));
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++n) {
+            const uint32_t slot = n % L::kRing, use = n / L::kRing;
+            if (use > 0) wait(&empty[slot], use - 1);
+            const bool go = !*gave_up;
+            if (lane == 0 && go) tc::mbar_arrive_expect_tx(&full[slot], L::kTile);
+            __syncwarp();
+            if (lane < parts && go)
+              load_cells(ring + slot * L::kTile + lane * F.box * D * 2, kv ? &vmap : &kmap, cell >> 3, page, P.kv_heads,
+                         w.head, &full[slot]);
+          }
+        }
+      } while (w.next(P, R, group));
+      // after a wait gave up, the copies still in flight end before the block does
+      if (lane == 0 && *gave_up) {
+        for (uint32_t j = n < L::kRing ? 0 : n - L::kRing; j < n; ++j)
+          if (!tc::mbar_wait_sleep(&full[j % L::kRing], (j / L::kRing) & 1)) break;
+      }
+    } else if (warp == 9 || warp == 10) {
+      // ----------------------------------------------------------- S = Q K^T
+      // of a unit when its S tile is free: the P V of two units before is done (which also frees that unit's values).
+      // Each half goes at its own pace; a ring tile is free when both have let it go.
+      constexpr uint32_t kQK = tc::idesc_f16(128, kChunkKeys, BF16);
+      const int h = warp - 9;
+      const uint32_t q_at = (q_smem + h * L::kQTile) >> 4;
+      uint32_t n0 = 0, item = 0;            // ring tiles before this item: K of unit u is n0 + 2 u, V the next
+      uint32_t uses0 = 0, uses1 = 0;        // of this half's S tiles, before this item
+      do {
+        const int units = w.u1 - w.u0;
+        if (h * 128 >= w.s.n * group - w.tile * kChunkRows) {      // no rows: only let the values go
+          for (int u = 0; u < units; ++u) {
+            landed(n0 + 2 * u + 1);
+            release(n0 + 2 * u + 1);
+          }
+          n0 += 2 * units;
+          continue;
+        }
+        wait(&q_full[h], item++);
+        tc::fence_after_sync();
+        for (int u = 0; u < units + 2 && !*gave_up; ++u) {
+          const int b = u & 1;
+          if (u >= 2) {
+            wait(&pv_done[2 * h + b], (b ? uses1 : uses0) + (u >> 1) - 1);
+            tc::fence_after_sync();
+            release(n0 + 2 * (u - 2) + 1);
+          }
+          if (u < units) {
+            const uint32_t n = n0 + 2 * u, k_at = (ring + n % L::kRing * L::kTile) >> 4;
+            landed(n);
+            if (elect()) {
+#pragma unroll
+              for (int k = 0; k < D / 16; ++k)
+                tc::mma_f16_ss(s_at(h, b), desc(q_at + (((k >> 2) * L::kQHalf + (k & 3) * 32) >> 4), 16, 1024),
+                               desc(k_at + (((k >> 2) * C::kNext + (k & 3) * 32) >> 4), 16, C::kGroup), kQK, k > 0);
+              tc::mma_commit(&s_full[2 * h + b]);
+            }
+            __syncwarp();
+          }
+        }
+        n0 += 2 * units;
+        uses0 += (units + 1) >> 1;
+        uses1 += units >> 1;
+        if (__any_sync(0xffffffffu, *gave_up)) break;
+      } while (w.next(P, R, group));
+      drain();
+    } else if (warp == 12 || warp == 13) {
+      // ------------------------------------------------------------ O += P V
+      // of a unit when its P is there (so its S is done, and its keys may go)
+      constexpr uint32_t kPV = tc::idesc_f16(128, D, BF16) | (1u << 16);        // B: K is its slow dimension
+      const int h = warp - 12;
+      uint32_t n0 = 0, uses0 = 0, uses1 = 0;
+      do {
+        const int units = w.u1 - w.u0;
+        if (h * 128 >= w.s.n * group - w.tile * kChunkRows) {      // no rows: only let the keys go
+          for (int u = 0; u < units; ++u) {
+            landed(n0 + 2 * u);
+            release(n0 + 2 * u);
+          }
+          n0 += 2 * units;
+          continue;
+        }
+        const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
+        for (int u = 0; u < units && !*gave_up; ++u) {
+          const int b = u & 1;
+          const uint32_t n = n0 + 2 * u;
+          landed(n + 1);
+          const int64_t key = key0 + (int64_t)(w.u0 + u) * kChunkKeys;
+          if (key < w.lo || key + kChunkKeys > w.hi) {
+            // values that no row of the tile sees may be anything: they become zeros (both halves write them)
+            const int first = w.lo > key ? (int)min(w.lo - key, (int64_t)kChunkKeys) : 0;
+            const int end = w.hi > key ? (int)min(w.hi - key, (int64_t)kChunkKeys) : 0;
+            uint8_t* v = smem + L::kQ + (n + 1) % L::kRing * L::kTile;
+            for (int i = lane; i < kChunkKeys * (D / 8); i += 32) {
+              const int r = i / (D / 8), c = i % (D / 8);
+              if (r < first || r >= end)
+                *reinterpret_cast<uint4*>(v + C::at(r, c >> 3, c & 7)) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+          }
+          wait(&p_full[2 * h + b], (b ? uses1 : uses0) + (u >> 1));
+          tc::fence_after_sync();
+          const uint32_t v_at = (ring + (n + 1) % L::kRing * L::kTile) >> 4;
+          if (elect()) {
+            mma_f16_ts(o_at(h), s_at(h, b), desc(v_at, C::kNext, C::kGroup), kPV, u > 0);
+#pragma unroll
+            for (int k = 1; k < kChunkKeys / 16; ++k)
+              mma_f16_ts(o_at(h), s_at(h, b) + 8 * k, desc(v_at + (k * 2 * C::kGroup >> 4), C::kNext, C::kGroup), kPV, 1);
+            tc::mma_commit(&pv_done[2 * h + b]);
+          }
+          __syncwarp();
+          release(n);
+        }
+        n0 += 2 * units;
+        uses0 += (units + 1) >> 1;
+        uses1 += units >> 1;
+        if (__any_sync(0xffffffffu, *gave_up)) break;
+      } while (w.next(P, R, group));
+      drain();
+    }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     // ------------------------------------------------------------- softmax
     const int h = warp >> 2, row = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
