@@ -697,22 +697,19 @@ def q4k_lora_add(x, a, b, base, order, seg_start, seg_adapter, scale, y=None, wo
         raise TypeError("a must be float16 or bfloat16")
     if y is None:
         y = [torch.empty((tokens, w.shape[1]), dtype=f32, device=x.device) for w in b]
-    mats = (LoraMat * n)()
-    for mat, am, bm, basem, ym in zip(mats, a, b, base, y):
+    mats = []                                # the fields of a q4k_lora_mat each, all 8 bytes wide
+    for am, bm, basem, ym in zip(a, b, base, y):
         rows = bm.shape[1]
         if am.shape != (adapters, rank, cols) or bm.shape != (adapters, rows, rank):
             raise ValueError(f"every a must be [{adapters}][{rank}][{cols}] and every b [{adapters}][rows][{rank}]")
-        mat.a = _arg(am, dtype, adapters * rank * cols, "a")
-        mat.b = _arg(bm, dtype, adapters * rows * rank, "b")
-        mat.base = None if basem is None else _arg(basem, f32, tokens * rows, "base")
-        mat.y = _arg(ym, f32, tokens * rows, "y")
-        mat.rows = rows
+        mats += (_arg(am, dtype, adapters * rank * cols, "a"), _arg(bm, dtype, adapters * rows * rank, "b"),
+                 0 if basem is None else _arg(basem, f32, tokens * rows, "base"), _arg(ym, f32, tokens * rows, "y"), rows)
     n_seg = seg_adapter.numel()
     if workspace is None:
         workspace = q4k_lora_workspace(tokens, rank, n, x.device)
     size = workspace.numel()
     status = lib().q4k_lora_add(
-        n, mats, adapters, rank, _CACHE_TYPES[dtype], cols, _arg(x, f32, tokens * cols, "x"), tokens,
+        n, (ctypes.c_int64 * (5 * n))(*mats), adapters, rank, _CACHE_TYPES[dtype], cols, _arg(x, f32, tokens * cols, "x"), tokens,
         _arg(order, i32, tokens, "order"), _arg(seg_start, i32, n_seg + 1, "seg_start"),
         _arg(seg_adapter, i32, n_seg, "seg_adapter"), n_seg, _arg(scale, f32, adapters, "scale"),
         _arg(workspace, torch.uint8, size, "workspace"), size, _stream(stream))

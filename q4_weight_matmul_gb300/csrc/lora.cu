@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int PARTS = BF16 ? 3 : 2;
   const Tile T = find_tile(P, blockIdx.x);
-  if (T.n <= 0) return;
+  if (T.n <= 0) {                                        // as the others, not before the first kernel has ended
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   const int all = P.n * P.rank, rank_blocks_m = (P.rank + 31) / 32, kblocks = T.adapter >= 0 ? rank_blocks_m : 1;
   uint8_t* ring = smem + P.n * rank_blocks_m * block_bytes<BF16>();
@@ -529,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
 template <bool BF16, int NT>
 cudaError_t shrink(const LoraParams& p, unsigned tiles, int parts, cudaStream_t s) {
   auto kernel = lora_shrink_kernel<BF16, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shrink<NT>::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kernel, Shrink<NT>::kSmem, done);
   if (e != cudaSuccess) return e;
   const int groups = (p.n * p.rank / 8 + NT - 1) / NT;
   kernel<<<dim3(tiles, parts, groups), kThreads, Shrink<NT>::kSmem, s>>>(p);
@@ -559,8 +563,8 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
   // three slots if two CTAs fit an SM with them, else two
   const int parts_bytes = rank_blocks(p.n, p.rank) * block_bytes<BF16>();
   const int slots = parts_bytes + 3 * kSlot <= 112 * 1024 ? 3 : 2, smem = parts_bytes + slots * kSlot;
-  e = cudaFuncSetAttribute(lora_expand_kernel<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           rank_blocks(kLoraMaxMats, 128) * block_bytes<BF16>() + 3 * kSlot);
+  static std::atomic<uint64_t> done{0};
+  e = allow_smem(lora_expand_kernel<BF16>, rank_blocks(kLoraMaxMats, 128) * block_bytes<BF16>() + 3 * kSlot, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(tiles, std::min(chunks, want));

@@ -46,7 +46,7 @@ size_t paged_attn_workspace(const AttnParams& p) {
   int rows;
   few_kind(p, &rows);
   if (many_rows(p)) rows = kChunkRows;
-  return kTicketBytes + (size_t)cta_count() * 2 * rows * (p.dim + 2) * sizeof(float);
+  return kPieceBytes + (size_t)cta_count() * 2 * rows * (p.dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_attn(const AttnParams& p, cudaStream_t s) {

@@ -111,7 +111,6 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
   uint64_t* drained = pv_done + 4;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_at + 1);
-  int* last = reinterpret_cast<int*>(tmem_at + 2);
   int64_t* scratch = reinterpret_cast<int64_t*>(smem + L::kQ + L::kRing * L::kTile + 320);   // 16 words
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -131,6 +130,9 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Split* split = reinterpret_cast<Split*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes) + blockIdx.x;
+  if (tid == 0) split->last_cta = -1;                // until this thread finds one
   const Range R = share_out<kChunkRows, kChunkKeys, kChunkThreads>(P, group, F.min_units, scratch);
   if ((int)blockIdx.x >= R.ctas) return;
   if (warp == 9) {
@@ -325,8 +327,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const float c = fmaxf(fabsf(P.scale) * 1.4426950408889634f, 1e-30f);   // a scale of 0 must not meet -inf
     const uint32_t flip = P.scale < 0.f ? 0x80008000u : 0u;
-    float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
-    auto sync = [&] { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+    float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kPieceBytes);
     uint32_t uses0 = 0, uses1 = 0;              // of this half's S tiles, before this item
     // This thread's row of the item's Q, negated where the scale is, so that the largest score has the largest weight
     auto load_q = [&](const Walk<kChunkRows, kChunkKeys>& x) {
@@ -460,6 +461,10 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           tc::fence_before_sync();
         }
       } else {
+        if (tid == 0 && w.u0 == 0) {
+          split->q0 = w.s.q0, split->head = w.head, split->row0 = row0, split->rows = rows;
+          split->last_cta = owner(w.at + w.units - 1, R);
+        }
         float* piece = pieces + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * piece_floats<kChunkRows, D>();
         if (h < halves) {
 #pragma unroll
@@ -480,9 +485,6 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
             __stcg(piece + kChunkRows * D + kChunkRows + r, l);
           }
         }
-        const int c0 = owner(w.at, R), c1 = owner(w.at + w.units - 1, R);
-        if (arrive(static_cast<unsigned*>(P.workspace) + c0, c1 - c0 + 1, last, tid == 0, sync))
-          combine_rows<kChunkRows, D, BF16>(P, pieces, c0, c1, mine, r, out_at);
       }
       w = x;
     } while (more);
@@ -495,6 +497,52 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
   }
 }
 
+// Puts the items together that several CTAs have pieces of: blocks (c, i) the
+// one that begins in CTA c's range and goes on past it, rows 32 i .., a lane
+// per row, D / 8 values a warp.  All SMs share this; the last CTA of an item
+// doing it alone, as the few-row kernel's does, took 10 us of a 55 us call.
+// Its pieces are laid out [D/4][rows][4], so that a warp reads whole lines.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) paged_attn_join_kernel(const AttnParams P) {
+  // every block waits for the kernel before, so that this one does not end before it
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int group = P.heads / P.kv_heads, c0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4* at_split = reinterpret_cast<const int4*>(static_cast<const uint8_t*>(P.workspace) + kTicketBytes) + 2 * c0;
+  const int4 first = __ldcg(at_split);
+  const int c1 = first.x, row0 = first.w, r = blockIdx.y * 32 + lane, rows = __ldcg(at_split + 1).x;
+  if (c1 < 0 || r >= rows) return;
+  const Shape s{first.y, 0, 0};
+  const float* pieces = reinterpret_cast<const float*>(static_cast<const uint8_t*>(P.workspace) + kPieceBytes);
+  auto piece = [&](int c) { return pieces + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * piece_floats<kChunkRows, D>(); };
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(piece(c) + kChunkRows * D + r));
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float mc = __ldcg(piece(c) + kChunkRows * D + r), lc = __ldcg(piece(c) + kChunkRows * D + kChunkRows + r);
+    l += mc == -INFINITY ? 0.f : ex2(mc - m) * lc;
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  constexpr int N = D / 32;                                   // float4 of a lane
+  float4 a[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float mc = __ldcg(piece(c) + kChunkRows * D + r), f = mc == -INFINITY ? 0.f : ex2(mc - m) * inv;
+    const float* from = piece(c) + ((size_t)(warp * N) * kChunkRows + r) * 4;
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(from + q * kChunkRows * 4));
+      a[q].x = fmaf(f, v.x, a[q].x), a[q].y = fmaf(f, v.y, a[q].y);
+      a[q].z = fmaf(f, v.z, a[q].z), a[q].w = fmaf(f, v.w, a[q].w);
+    }
+  }
+  const int64_t at = out_row(P, s, first.z, group, row0 + r) * D + warp * N * 4;
+#pragma unroll
+  for (int q = 0; q < N; ++q) store4<BF16>(P.out, false, at + 4 * q, a[q]);
+}
+
 template <int D, bool BF16>
 cudaError_t launch_chunk(const CUtensorMap& kmap, const CUtensorMap& vmap, const ChunkParams& f, int ctas,
                          cudaStream_t s);
@@ -504,10 +552,21 @@ cudaError_t launch_chunk_kernel(const CUtensorMap& kmap, const CUtensorMap& vmap
                                 cudaStream_t s) {
   auto kernel = paged_attn_chunk_kernel<D, BF16>;
   constexpr int smem = ChunkLayout<D>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
   kernel<<<ctas, kChunkThreads, smem, s>>>(kmap, vmap, f);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, kChunkRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, BF16>, f.a);
 }
 
 }  // namespace attn

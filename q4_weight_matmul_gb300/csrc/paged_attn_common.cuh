@@ -22,7 +22,15 @@ namespace q4k {
 namespace attn {
 
 constexpr int kMaxCtas = 160;           // of a launch
-constexpr int kTicketBytes = 1024;      // leading workspace bytes: one counter per CTA
+// The workspace: a counter per CTA (few rows), a Split per CTA (many rows), the pieces.
+constexpr int kTicketBytes = 1024, kSplitBytes = kMaxCtas * 32, kPieceBytes = kTicketBytes + kSplitBytes;
+
+// The item that begins in a CTA's range and goes on past it.
+struct Split {
+  int last_cta;            // -1: there is none
+  int q0, head, row0, rows;
+  int unused[3];
+};
 
 // Keys (or values) in shared memory: groups of 8 cells, per group the first
 // 64 values of its cells, then the next 64; a cell's 64 values are 128 bytes,
@@ -428,45 +436,6 @@ __device__ __forceinline__ void combine(const AttnParams& P, const float* pieces
     }
   }
   sync();
-}
-
-// The same with one thread per row (row r, its output at out_at) and pieces
-// laid out [D/4][ROWS][4], so that the threads of a warp read whole lines.
-template <int ROWS, int D, bool BF16>
-__device__ __forceinline__ void combine_rows(const AttnParams& P, const float* pieces, int c0, int c1, bool mine,
-                                             int r, int64_t out_at) {
-  if (!mine) return;
-  auto piece = [&](int c) { return pieces + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * piece_floats<ROWS, D>(); };
-  float m = -INFINITY, l = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(piece(c) + ROWS * D + r));
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float mc = __ldcg(piece(c) + ROWS * D + r);
-    if (mc != -INFINITY) l += exp2f(mc - m) * __ldcg(piece(c) + ROWS * D + ROWS + r);
-  }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
-  for (int d = 0; d < D; d += 32) {
-    float4 a[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int c = c0; c <= c1; ++c) {
-      const float* from = piece(c) + (d / 4 * ROWS + r) * 4;
-      float4 v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = __ldcg(reinterpret_cast<const float4*>(from + q * ROWS * 4));
-      const float mc = __ldcg(piece(c) + ROWS * D + r), w = mc == -INFINITY ? 0.f : exp2f(mc - m) * inv;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        a[q].x = fmaf(w, v[q].x, a[q].x), a[q].y = fmaf(w, v[q].y, a[q].y);
-        a[q].z = fmaf(w, v[q].z, a[q].z), a[q].w = fmaf(w, v[q].w, a[q].w);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) store4<BF16>(P.out, P.out_f32, out_at + d + 4 * q, a[q]);
-  }
 }
 
 }  // namespace attn

@@ -537,7 +537,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
   constexpr int kThreads = 32 * C::kWarps;
   auto sync = [&] { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); };
   const uint32_t grp = warp / WR;
-  float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kTicketBytes);
+  float* pieces = reinterpret_cast<float*>(static_cast<uint8_t*>(P.workspace) + kPieceBytes);
   typename RowsOf<D, BF16, KIND>::type part;
   if constexpr (KIND >= 16) part.my0 = warp % WR * 16;
 
@@ -608,7 +608,8 @@ cudaError_t launch_few_variant(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                cudaStream_t s) {
   auto kernel = paged_attn_few_kernel<D, BF16, KIND>;
   constexpr int smem = FewConfig<D, KIND>::kSmem;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
   kernel<<<ctas, FewConfig<D, KIND>::kThreads, smem, s>>>(kmap, vmap, f);
   return cudaGetLastError();

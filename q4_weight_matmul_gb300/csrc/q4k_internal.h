@@ -3,6 +3,7 @@
 // before it calls one.  Each returns the cudaError_t of its launch.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -23,6 +24,21 @@ struct DeviceInfo {
   int l2_bytes;
 };
 const DeviceInfo& device_info(int device);
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// `done` (one per kernel, bit per device) says where that has been set
+// already (setting it again takes a microsecond of every call).
+template <class K>
+inline cudaError_t allow_smem(K* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Library-owned device error word of the current device (see abi.cu).
 int* device_error_word();
