@@ -19,8 +19,16 @@ int few_kind(const AttnParams& p, int* rows) {
   return kind;
 }
 
-// The many-row kernel keeps its weights at 16 bits, so it gives 16-bit results.
-bool many_rows(const AttnParams& p) { return !p.out_f32 && p.max_q * (p.heads / p.kv_heads) > 64; }
+// The many-row kernel keeps its weights at 16 bits, so it gives 16-bit
+// results.  It pays 128 rows per half whatever their number, the few-row
+// kernel one pass over the keys' operands per 16 rows.  Few | many rows, us,
+// 8 key heads of 128:
+//   rows per key head       12            16            32            36            128
+//   1 request,    512 keys  11.3 | 13.2   11.7 | 13.3   13.6 | 14.1   14.5 | 14.2   19.4 | 15.4
+//   1 request,  32768 keys  43.6 | 58.8   44.1 | 53.9   53.6 | 51.5   72.3 | 59.2   120  | 53.3
+//   8 requests,  4096 keys  41.3 | 43.9   42.4 | 43.5   47.6 | 42.6   64.2 | 43.9   114  | 45.5
+//   8 requests, 32768 keys  202  | 205    202  | 205    227  | 188    371  | 195    730  | 179
+bool many_rows(const AttnParams& p) { return !p.out_f32 && p.max_q * (p.heads / p.kv_heads) > 16; }
 
 int cta_count() {
   int dev = 0;
