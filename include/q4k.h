@@ -4,7 +4,9 @@
  * The library computes the Q4_K-quantised weight matmul of an LLM inference
  * engine in its two halves (genie-ai-runtime: a Jetson edge LLM inference
  * engine, §2 "the roofline that dictates strategy"): the bandwidth-bound
- * decode GEMV and the compute-bound prefill GEMM over q8_1 activations.
+ * decode GEMV and the compute-bound prefill GEMM over q8_1 activations; and
+ * what stands between a layer's projections: head norms with rotation,
+ * attention over a paged key/value cache, low-rank adapters.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -23,8 +25,8 @@
  *  - Device pointers must be 16-byte aligned (Q4K_ERR_ALIGNMENT otherwise).
  *  - Sizes of zero (rows, tokens, batch) are valid and enqueue nothing.
  *  - A call whose work takes more than one kernel launch (a q4k_gemv_seq
- *    list of more than 96 jobs, or 48 Q6_K jobs) validates and plans all of
- *    it first; only a
+ *    list of more than 96 jobs, or 48 Q6_K jobs; q4k_lora_add;
+ *    q4k_paged_attn of many rows) validates and plans all of it first; only a
  *    CUDA launch failure of a later launch can leave the earlier ones
  *    enqueued (the status is then Q4K_ERR_CUDA).
  *

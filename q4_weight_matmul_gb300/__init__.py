@@ -1,4 +1,5 @@
-"""Python binding of libq4k.so, the GB300 Q4_K weight-matmul library.
+"""Python binding of libq4k.so, the GB300 Q4_K weight-matmul library with the
+attention block beside it.
 
 Argument marshalling only: every function checks that its torch tensors are
 contiguous CUDA tensors of the expected dtype, passes their device pointers

