@@ -15,7 +15,7 @@ import os
 
 import torch
 
-from .build import LIB_PATH, build
+from .build import BINDING_LIB, LIB_PATH, build
 
 BLOCK144 = 0
 LAYOUT_GPU = 1          # declared by the C ABI; every call refuses it (Q4K_ERR_UNSUPPORTED)
@@ -123,6 +123,24 @@ def lib() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = handle
     return _lib
+
+
+_bound = None
+
+
+def _native():
+    """The module ``_calls`` (``csrc/binding.cpp``), bound to the library: the
+    attention block's calls without interpreted checks of every tensor."""
+    global _bound
+    if _bound is None:
+        lib()
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise RuntimeError(f"{BINDING_LIB} is not built: run q4_weight_matmul_gb300.build.build()") from e
+        module.bind(LIB_PATH)
+        _bound = module
+    return _bound
 
 
 def _stream(stream) -> int:
@@ -592,20 +610,14 @@ def q4k_qk_norm_rope(q, k, v, k_cache, v_cache, pos, slot, cos_sin, q_weight=Non
     at the int32 ``pos`` [tokens], or None for no rotation; the weights
     [head_dim] float32, or both None for no norm.  Returns the queries
     [tokens][heads][head_dim] in the cache's type."""
-    f32, cache = torch.float32, _kv_cache(k_cache, v_cache)
-    dim, shape = cache.head_dim, q.shape
-    tokens, heads = shape[0], shape[1] if len(shape) == 3 else shape[1] // dim
-    nq, nk = tokens * heads * dim, tokens * cache.kv_heads * dim
-    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
     if q_out is None:
-        q_out = torch.empty((tokens, heads, dim), dtype=k_cache.dtype, device=q.device)
-    status = lib().q4k_qk_norm_rope(
-        _arg(q, f32, nq, "q"), _arg(k, f32, nk, "k"), _arg(v, f32, nk, "v"), tokens, heads, ctypes.byref(cache),
-        None if q_weight is None else _arg(q_weight, f32, dim, "q_weight"),
-        None if k_weight is None else _arg(k_weight, f32, dim, "k_weight"), eps,
-        _arg(cos_sin, f32, max_pos * rot, "cos_sin") if rot else None, max_pos, rot, interleaved,
-        _arg(pos, torch.int32, tokens, "pos") if rot else None, _arg(slot, torch.int32, tokens, "slot"),
-        _arg(q_out, k_cache.dtype, nq, "q_out"), _stream(stream))
+        if len(k_cache.shape) != 4:
+            raise TypeError("k_cache must be [num_pages][kv_heads][page_size][head_dim]")
+        dim = k_cache.shape[3]
+        q_out = torch.empty((q.shape[0], q.shape[1] if len(q.shape) == 3 else q.shape[1] // dim, dim),
+                            dtype=k_cache.dtype, device=k_cache.device)
+    status = (_bound or _native()).qk_norm_rope(q, k, v, k_cache, v_cache, pos, slot, cos_sin, q_weight, k_weight, eps,
+                                                interleaved, q_out, stream)
     if status:
         raise Q4KError(status, "q4k_qk_norm_rope")
     return q_out
@@ -634,28 +646,12 @@ def q4k_paged_attn(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int, sc
     tokens.  ``scale`` is head_dim ** -0.5 by default; ``window`` > 0 limits a
     token to its last ``window`` keys.  Keep a ``workspace``
     (``q4k_paged_attn_workspace``) for repeated calls."""
-    cache, i32 = _kv_cache(k_cache, v_cache), torch.int32
-    dim, shape, dtype = cache.head_dim, q.shape, k_cache.dtype
-    if len(shape) != 3 or shape[2] != dim:
-        raise ValueError(f"q must be [tokens][heads][{dim}]")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [n_req][max_pages]")
-    tokens, heads, n = shape[0], shape[1], q.numel()
-    n_req, max_pages = page_table.shape
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=q.device)
-    elif out.shape != shape or out.dtype not in _TYPES:
-        raise ValueError("out must have q's shape and be float32 or of the cache's type")
-    out_dtype = out.dtype
+        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
     if workspace is None:
-        workspace = q4k_paged_attn_workspace(q, k_cache, page_table, max_q, out_dtype)
-    size = workspace.numel()
-    status = lib().q4k_paged_attn(
-        _arg(q, dtype, n, "q"), tokens, heads, ctypes.byref(cache),
-        _arg(page_table, i32, n_req * max_pages, "page_table"), max_pages, _arg(cu_q, i32, n_req + 1, "cu_q"),
-        _arg(kv_len, i32, n_req, "kv_len"), n_req, max_q, dim ** -0.5 if scale is None else scale, window,
-        _arg(out, out_dtype, n, "out"), _TYPES[out_dtype], _arg(workspace, torch.uint8, size, "workspace"), size,
-        _stream(stream))
+        workspace = q4k_paged_attn_workspace(q, k_cache, page_table, max_q, out.dtype)
+    status = (_bound or _native()).paged_attn(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q, scale, window, out,
+                                              workspace, stream)
     if status:
         raise Q4KError(status, "q4k_paged_attn")
     return out
@@ -690,30 +686,11 @@ def q4k_lora_add(x, a, b, base, order, seg_start, seg_adapter, scale, y=None, wo
     here when ``y`` is None).  ``order``, ``seg_start``, ``seg_adapter``: the
     tokens grouped by adapter (``q4k_lora_segments``); ``scale`` [n_adapters]
     float32.  Returns the list ``y``."""
-    n, (tokens, cols), f32, i32 = len(a), x.shape, torch.float32, torch.int32
-    if not (len(b) == len(base) == n and (y is None or len(y) == n)) or n == 0:
-        raise ValueError("a, b, base and y must be lists of one length")
-    (adapters, rank, _), dtype = a[0].shape, a[0].dtype
-    if dtype not in _CACHE_TYPES:
-        raise TypeError("a must be float16 or bfloat16")
     if y is None:
-        y = [torch.empty((tokens, w.shape[1]), dtype=f32, device=x.device) for w in b]
-    mats = []                                # the fields of a q4k_lora_mat each, all 8 bytes wide
-    for am, bm, basem, ym in zip(a, b, base, y):
-        rows = bm.shape[1]
-        if am.shape != (adapters, rank, cols) or bm.shape != (adapters, rows, rank):
-            raise ValueError(f"every a must be [{adapters}][{rank}][{cols}] and every b [{adapters}][rows][{rank}]")
-        mats += (_arg(am, dtype, adapters * rank * cols, "a"), _arg(bm, dtype, adapters * rows * rank, "b"),
-                 0 if basem is None else _arg(basem, f32, tokens * rows, "base"), _arg(ym, f32, tokens * rows, "y"), rows)
-    n_seg = seg_adapter.numel()
+        y = [torch.empty((x.shape[0], w.shape[1]), dtype=torch.float32, device=x.device) for w in b]
     if workspace is None:
-        workspace = q4k_lora_workspace(tokens, rank, n, x.device)
-    size = workspace.numel()
-    status = lib().q4k_lora_add(
-        n, (ctypes.c_int64 * (5 * n))(*mats), adapters, rank, _CACHE_TYPES[dtype], cols, _arg(x, f32, tokens * cols, "x"), tokens,
-        _arg(order, i32, tokens, "order"), _arg(seg_start, i32, n_seg + 1, "seg_start"),
-        _arg(seg_adapter, i32, n_seg, "seg_adapter"), n_seg, _arg(scale, f32, adapters, "scale"),
-        _arg(workspace, torch.uint8, size, "workspace"), size, _stream(stream))
+        workspace = q4k_lora_workspace(x.shape[0], a[0].shape[1], len(a), x.device)
+    status = (_bound or _native()).lora_add(x, a, b, base, order, seg_start, seg_adapter, scale, y, workspace, stream)
     if status:
         raise Q4KError(status, "q4k_lora_add")
     return y

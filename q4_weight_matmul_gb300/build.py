@@ -3,6 +3,8 @@
 Each ``csrc/*.cu`` file is compiled on its own (in parallel) with
 ``-gencode arch=compute_103a,code=sm_103a``; the objects are linked into
 ``q4_weight_matmul_gb300/libq4k.so`` (CUDA runtime linked statically).
+``csrc/binding.cpp`` becomes the Python module ``_calls`` beside it (g++,
+against the headers of the torch that imports it).
 A build is skipped when the library is newer than every source file.
 
     python -m q4_weight_matmul_gb300.build [--force] [--verbose]
@@ -15,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +27,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(PKG, "libq4k.so")
 PEAKS_SRC = os.path.join(CSRC, "peaks", "peaks.cu")
 PEAKS_LIB = os.path.join(PKG, "libq4k_peaks.so")
+BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_LIB = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -42,11 +47,12 @@ def sources() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(PEAKS_LIB):
+    made = (LIB_PATH, PEAKS_LIB, BINDING_LIB)
+    if not all(map(os.path.exists, made)):
         return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(PEAKS_LIB))
+    t = min(map(os.path.getmtime, made))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h")) + [PEAKS_SRC, os.path.abspath(__file__)]
+        + glob.glob(os.path.join(INCLUDE, "*.h")) + [PEAKS_SRC, BINDING_SRC, os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
@@ -65,6 +71,23 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = BINDING_LIB + ".tmp"
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           *(f for d in (INCLUDE, sysconfig.get_paths()["include"], os.path.join(at, "include"),
+                         os.path.join(at, "include", "torch", "csrc", "api", "include"), cuda) for f in ("-I", d)),
+           BINDING_SRC, "-o", tmp, "-L", os.path.join(at, "lib"), "-Wl,-rpath," + os.path.join(at, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {os.path.basename(BINDING_SRC)} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA source and link libq4k.so (and the benchmark's
     tensor-rate probe, libq4k_peaks.so); return the library's path."""
@@ -72,8 +95,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sources() + [PEAKS_SRC]
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding.result()
     for path, members in ((LIB_PATH, objs[:-1]), (PEAKS_LIB, objs[-1:])):
         tmp = path + ".tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *members]
