@@ -98,6 +98,33 @@ __device__ __forceinline__ bool elect() {
   return e != 0;
 }
 
+__device__ __forceinline__ float max3(uint32_t a, uint32_t b, uint32_t c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+  return d;
+}
+// Two fp32 values as one operand, their product-sum and sum.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -372,7 +399,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           const uint32_t use = (b ? uses1 : uses0) + (i >> 1);
           wait(&s_full[2 * h + b], use);
           tc::fence_after_sync();
-          float s[kChunkKeys];
+          uint32_t s[kChunkKeys];
 #pragma unroll
           for (int k = 0; k < kChunkKeys / 32; ++k)
             tc::tmem_ld32(s_at(h, b) + lanes + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * k));
@@ -381,14 +408,11 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           if (lo > at || hi < at + kChunkKeys) {
             const int x = lo - at, y = hi - at;
 #pragma unroll
-            for (int k = 0; k < kChunkKeys; ++k) s[k] = k >= x && k < y ? s[k] : -INFINITY;
+            for (int k = 0; k < kChunkKeys; ++k) s[k] = k >= x && k < y ? s[k] : 0xff800000u;      // -infinity
           }
-          float t[4] = {s[0], s[1], s[2], s[3]};
+          float t[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
 #pragma unroll
-          for (int k = 4; k < kChunkKeys; k += 4) {
-            t[0] = fmaxf(t[0], s[k]), t[1] = fmaxf(t[1], s[k + 1]);
-            t[2] = fmaxf(t[2], s[k + 2]), t[3] = fmaxf(t[3], s[k + 3]);
-          }
+          for (int k = 12; k + 1 < kChunkKeys; k += 2) t[(k >> 1) & 3] = max3(__float_as_uint(t[(k >> 1) & 3]), s[k], s[k + 1]);
           const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;     // c >= 0
           float f = 1.f;
           bool grow = false;
@@ -415,16 +439,19 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
             }
           }
           const float sub = m == -INFINITY ? 0.f : m - kChunkLift;
-          float add[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t c2 = pair(c, c), sub2 = pair(-sub, -sub);
+          uint64_t add[2] = {0, 0};
           uint32_t p[kChunkKeys / 2];
 #pragma unroll
           for (int e = 0; e < kChunkKeys / 2; ++e) {
-            const float x = ex2(fmaf(s[2 * e], c, -sub)), y = ex2(fmaf(s[2 * e + 1], c, -sub));
-            add[(2 * e) & 3] += x, add[(2 * e + 1) & 3] += y;
+            const float2 z = unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, sub2));
+            const float x = ex2(z.x), y = ex2(z.y);
+            add[e & 1] = add2(add[e & 1], pair(x, y));
             p[e] = pack2<BF16>(x, y);
           }
           tc::tmem_st32(s_at(h, b) + lanes, p);
-          l += (add[0] + add[1]) + (add[2] + add[3]);
+          const float2 sum = unpair(add2(add[0], add[1]));
+          l += sum.x + sum.y;
           tc::tmem_wait_st();
           tc::fence_before_sync();
           __syncwarp();
