@@ -75,7 +75,7 @@ def _compile_binding() -> str:
     import torch
     at = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    tmp = BINDING_LIB + ".tmp"
+    tmp = f"{BINDING_LIB}.{os.getpid()}.tmp"
     cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            *(f for d in (INCLUDE, sysconfig.get_paths()["include"], os.path.join(at, "include"),
                          os.path.join(at, "include", "torch", "csrc", "api", "include"), cuda) for f in ("-I", d)),
