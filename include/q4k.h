@@ -638,6 +638,9 @@ int q4k_qk_norm_rope(const float* q, const float* k, const float* v, int64_t tok
  * scores of large z are themselves that far off); with 16-bit out the weights may be rounded to that type
  * before they meet the values, as the result is after.
  * Deterministic on one device: the same inputs give the same bits.
+ * Errors: Q4K_ERR_INVALID_ARG, Q4K_ERR_ALIGNMENT, Q4K_ERR_UNSUPPORTED
+ * (head_dim; tokens * heads / kv_heads of 2^31 or more).  tokens == 0
+ * enqueues nothing.
  */
 size_t q4k_paged_attn_workspace_bytes(const q4k_kv_cache* cache, int heads, int64_t tokens,
                                       int64_t n_req, int64_t max_q, int64_t max_pages,

@@ -69,6 +69,7 @@ int check_attn(const q4k_kv_cache* c, int heads, int64_t tokens, int64_t n_req, 
     return Q4K_ERR_INVALID_ARG;
   if (max_pages < 0 || max_pages > (int64_t(1) << 31) / c->page_size - 1) return Q4K_ERR_INVALID_ARG;
   if (out_type != c->type && out_type != Q4K_F32) return Q4K_ERR_INVALID_ARG;
+  if (tokens * (heads / c->kv_heads) >= (int64_t(1) << 31) - 1024) return Q4K_ERR_UNSUPPORTED;   // rows of a key head
   p->tokens = tokens;
   p->num_pages = c->num_pages;
   p->n_req = n_req;

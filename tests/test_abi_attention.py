@@ -71,6 +71,7 @@ def test_paged_attn_refusals(lib):
                         (dict(out=None), INVALID), (dict(ws=None), INVALID), (dict(ws_bytes=8), INVALID),
                         (dict(q=ODD16), ALIGN), (dict(out=ODD16), ALIGN), (dict(ws=ODD16), ALIGN),
                         (dict(table=ODD4), ALIGN), (dict(cu=ODD4), ALIGN), (dict(kv=ODD4), ALIGN),
+                        (dict(tokens=2 ** 22, heads=2048, max_q=2 ** 22), UNSUPPORTED),
                         (dict(tokens=0, q=None, out=None, ws=None), OK)]:
         assert attn(lib, **bad) == status, bad
     ws = lib.q4k_paged_attn_workspace_bytes

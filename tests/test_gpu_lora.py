@@ -53,6 +53,7 @@ CASES = [  # tokens, adapters, rank, cols, rows
     (129, 2, 32, 9728, [250]),
     (300, 3, 120, 512, [323]),
     (700, 6, 16, 1280, [1000, 999]),
+    (400, 300, 8, 256, [33]),                       # more segments than one warp looks at
 ]
 
 

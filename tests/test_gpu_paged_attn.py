@@ -106,6 +106,21 @@ def test_long_contexts(new, kv, dtype):
     assert q4k.q4k_device_error() == 0
 
 
+@pytest.mark.parametrize("requests,new,kv", [(129, 1, 40), (700, 1, 20), (9, 40, 70), (40, 19, 60), (200, 3, 30),
+                                             (1100, 2, 3)])
+def test_many_requests(requests, new, kv):
+    """More requests than one warp looks at, with and without several row tiles each, some of them without tokens."""
+    q4k.build()
+    r = np.random.default_rng(requests)
+    news = [int(v) for v in r.integers(0, new + 1, requests)]
+    kvs = [int(v) for v in r.integers(0, kv + 1, requests)]
+    news[0], kvs[0] = new, kv
+    d = make(requests, news, kvs, 8, 2, 64, 16, torch.float16)
+    for out_dtype in (torch.float32, torch.float16):
+        check(run(d, new, out_dtype), d, news, kvs)
+    assert q4k.q4k_device_error() == 0
+
+
 @pytest.mark.parametrize("new", [1, 6, 130])
 def test_peaked_and_flat_scores(new):
     """Scores of several hundred (one key takes all, at the far end or the near one), and equal scores."""
