@@ -668,7 +668,8 @@ int q4k_paged_attn(const void* q, int64_t tokens, int heads, const q4k_kv_cache*
  *   seg_adapter : int32 [n_seg], 0..n_adapters-1, or negative for tokens
  *               without an adapter
  *   scale     : float [n_adapters]
- *   workspace : device memory of at least q4k_lora_workspace_bytes() bytes,
+ *   workspace : device memory of at least q4k_lora_workspace_bytes() bytes
+ *               (enough for fewer tokens, projections and ranks as well),
  *               16-byte aligned; it needs no clearing.  Calls that share a
  *               workspace must not overlap on the GPU.
  * fp32 sums, A and B entries exact: |y - exact| <= 1e-5 * (|base| + |scale|

@@ -34,11 +34,16 @@ constexpr int kTile = 16;        // tokens of a tile
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
-// Parts of the columns that the shrink's CTAs split among them: more for few
-// tokens, which have few tiles.
+// Parts of the columns that the shrink's CTAs split among them: as many as
+// give its tiles of 16 tokens a CTA per SM, 2 at least (us with 8, 4, 2 for up
+// to 64, 512 and more tokens | this: 80 tokens, rank 48 of 5632 columns 12.9 |
+// 11.3; 278, rank 64 of 6912 23.9 | 20.4; 513, 2 x rank 24 of 7424 35.7 | 29.2;
+// 1600 the same; twice as many parts: 28.1 for the 513, but 19.4 -> 22.0 for
+// 3 x rank 32 of 2560, whose second launch adds them up).
 constexpr int kMaxParts = 8;
+constexpr int64_t kSplitTokens = 152 * kTile;
 int column_parts(int64_t tokens, int64_t cols) {
-  const int64_t want = tokens <= 64 ? kMaxParts : tokens <= 512 ? 4 : 2;
+  const int64_t want = std::max<int64_t>(2, std::min<int64_t>(kMaxParts, kSplitTokens / tokens));
   return (int)std::max<int64_t>(1, std::min(want, cols / 256));
 }
 
@@ -607,8 +612,10 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// Rows of h for any number of tokens up to this one.
 size_t lora_workspace(int n, int rank, int64_t tokens) {
-  return sizeof(float) * (size_t)n * (size_t)rank * (size_t)tokens * (size_t)column_parts(tokens, int64_t(1) << 24);
+  const int64_t rows = std::min(kMaxParts * tokens, std::max(kSplitTokens, 2 * tokens));
+  return sizeof(float) * (size_t)n * (size_t)rank * (size_t)rows;
 }
 
 cudaError_t launch_lora_add(const LoraParams& p, cudaStream_t s) {

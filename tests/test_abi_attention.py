@@ -110,6 +110,8 @@ def test_lora_add_refusals(lib):
         assert lora(lib, mats=[{}, bad]) == status, bad
     assert lora(lib, mats=[dict(rows=0, y=None)]) == OK and lora(lib, mats=[]) == OK
     assert lib.q4k_lora_workspace_bytes(1, 16, 5) > 0 and lib.q4k_lora_workspace_bytes(1, 12, 5) == 0
+    need = [lib.q4k_lora_workspace_bytes(2, 16, t) for t in range(1, 6000)]
+    assert need == sorted(need)                              # serves fewer tokens as well
     assert lib.q4k_lora_workspace_bytes(0, 16, 5) == 0 and lib.q4k_lora_workspace_bytes(5, 16, 5) == 0
 
 
