@@ -19,7 +19,7 @@
 // registers (the tensor core's own running sum truncates).
 //
 // Measured: 2049 tokens of 4 adapters of rank 32 beside 2560 x 9728: 39 us (3.2
-// TB/s); 64 tokens of 17 adapters of rank 64 beside 2 x 9728 x 2560: 27 us; one
+// TB/s); 64 tokens of 17 adapters of rank 64 beside 2 x 9728 x 2560: 26.6 us; one
 // token beside q, k and v: 6.2 us.
 #include "mma_sync.cuh"
 #include "q4k_internal.h"

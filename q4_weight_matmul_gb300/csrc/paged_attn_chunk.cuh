@@ -33,10 +33,12 @@
 // largest value and above its subnormals down to 2^-22 of the largest weight.
 //
 // Measured (8 key heads of 128, groups of 4): chunks of 2048 and 1705 tokens
-// over 16384 and 16086 keys 723 us with pages of 16, 1300 TFLOP/s (68 % of the
-// bf16 rate); 512 tokens over 4096 keys 51 us.  About 1650 cycles per 64 keys:
+// over 16384 and 16086 keys 701 us with pages of 16, 1340 TFLOP/s (70 % of the
+// bf16 rate); 512 tokens over 4096 keys 50 us.  About 1600 cycles per 64 keys:
 // the tensor pipe needs 1280 (S = Q K^T with 64 keys to an instruction is fed
-// by shared memory at two thirds of its rate), the softmax 830 beside it.
+// by shared memory at two thirds of its rate), the softmax runs beside it
+// (two weights to a packed operation and three values to a maximum: 717 ->
+// 701 us).
 #pragma once
 
 #include "paged_attn_common.cuh"
@@ -144,7 +146,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
   uint64_t* drained = pv_done + 4;
   uint32_t* tmem_at = reinterpret_cast<uint32_t*>(drained + 1);
   volatile int* gave_up = reinterpret_cast<volatile int*>(tmem_at + 1);
-  int64_t* scratch = reinterpret_cast<int64_t*>(smem + L::kQ + L::kRing * L::kTile + 320);   // 16 words
+  int64_t* scratch = reinterpret_cast<int64_t*>(smem + L::kQ + L::kRing * L::kTile + 320);   // 19 words
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int group = P.heads / P.kv_heads;
