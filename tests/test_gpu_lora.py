@@ -53,6 +53,9 @@ CASES = [  # tokens, adapters, rank, cols, rows
     (129, 2, 32, 9728, [250]),
     (300, 3, 120, 512, [323]),
     (700, 6, 16, 1280, [1000, 999]),
+    (1100, 3, 32, 512, [97]),
+    (1301, 5, 64, 768, [130, 33]),
+    (1025, 14, 8, 1024, [70]),
     (400, 300, 8, 256, [33]),                       # more segments than one warp looks at
 ]
 
