@@ -10,6 +10,7 @@ loads), but every compute call needs the CUDA device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -147,6 +148,35 @@ def _stream(stream) -> int:
     if stream is None:                       # the current stream's handle, without a Stream object (2.7 us less)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+@contextlib.contextmanager
+def _stream_scope(stream):
+    """What is allocated or filled inside belongs to the call's ``stream``: it
+    is ordered before the launch, and its memory goes back to that stream's
+    pool, so that nothing else gets it while the launch still runs."""
+    handle = _stream(stream)
+    if handle == _stream(None):
+        yield
+        return
+    if not isinstance(stream, torch.cuda.Stream):      # a handle of 0 is the default stream
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        yield
+
+
+def _made_on(stream, make):
+    """The tensors that ``make`` allocates for a call on ``stream``; the
+    caller may use and drop them on torch's current stream."""
+    if stream is None:
+        return make()
+    with _stream_scope(stream):
+        made = make()
+    current = torch.cuda.current_stream()
+    for t in made if isinstance(made, list) else [made]:
+        if t.is_cuda:
+            t.record_stream(current)
+    return made
 
 
 def _ptr(t, dtype, name):
@@ -614,8 +644,8 @@ def q4k_qk_norm_rope(q, k, v, k_cache, v_cache, pos, slot, cos_sin, q_weight=Non
         if len(k_cache.shape) != 4:
             raise TypeError("k_cache must be [num_pages][kv_heads][page_size][head_dim]")
         dim = k_cache.shape[3]
-        q_out = torch.empty((q.shape[0], q.shape[1] if len(q.shape) == 3 else q.shape[1] // dim, dim),
-                            dtype=k_cache.dtype, device=k_cache.device)
+        shape = (q.shape[0], q.shape[1] if len(q.shape) == 3 else q.shape[1] // dim, dim)
+        q_out = _made_on(stream, lambda: torch.empty(shape, dtype=k_cache.dtype, device=k_cache.device))
     status = (_bound or _native()).qk_norm_rope(q, k, v, k_cache, v_cache, pos, slot, cos_sin, q_weight, k_weight, eps,
                                                 interleaved, q_out, stream)
     if status:
@@ -624,8 +654,9 @@ def q4k_qk_norm_rope(q, k, v, k_cache, v_cache, pos, slot, cos_sin, q_weight=Non
 
 
 def q4k_paged_attn_workspace(q, k_cache, page_table, max_q: int, out_dtype=torch.float32, tokens=None):
-    """A zeroed workspace for ``q4k_paged_attn`` calls of these shapes (``tokens``: in
-    place of ``q``'s, for the most tokens of any step)."""
+    """A workspace for ``q4k_paged_attn`` calls of these shapes (``tokens``: in
+    place of ``q``'s, for the most tokens of any step), zeroed on torch's
+    current stream: calls on another stream have to wait for that."""
     cache = _kv_cache(k_cache, k_cache)
     n_req, max_pages = page_table.shape
     need = int(lib().q4k_paged_attn_workspace_bytes(ctypes.byref(cache), q.shape[1],
@@ -645,11 +676,13 @@ def q4k_paged_attn(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q: int, sc
     ``page_table[r]`` (int32 [n_req][max_pages]), and at most ``max_q`` new
     tokens.  ``scale`` is head_dim ** -0.5 by default; ``window`` > 0 limits a
     token to its last ``window`` keys.  Keep a ``workspace``
-    (``q4k_paged_attn_workspace``) for repeated calls."""
+    (``q4k_paged_attn_workspace``) for repeated calls on one stream; without
+    one the call makes its own on ``stream``."""
     if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype, device=q.device)
+        out = _made_on(stream, lambda: torch.empty(q.shape, dtype=out_dtype, device=q.device))
     if workspace is None:
-        workspace = q4k_paged_attn_workspace(q, k_cache, page_table, max_q, out.dtype)
+        with _stream_scope(stream):
+            workspace = q4k_paged_attn_workspace(q, k_cache, page_table, max_q, out.dtype)
     status = (_bound or _native()).paged_attn(q, k_cache, v_cache, page_table, cu_q, kv_len, max_q, scale, window, out,
                                               workspace, stream)
     if status:
@@ -687,9 +720,11 @@ def q4k_lora_add(x, a, b, base, order, seg_start, seg_adapter, scale, y=None, wo
     tokens grouped by adapter (``q4k_lora_segments``); ``scale`` [n_adapters]
     float32.  Returns the list ``y``."""
     if y is None:
-        y = [torch.empty((x.shape[0], w.shape[1]), dtype=torch.float32, device=x.device) for w in b]
+        y = _made_on(stream, lambda: [torch.empty((x.shape[0], w.shape[1]), dtype=torch.float32, device=x.device)
+                                      for w in b])
     if workspace is None:
-        workspace = q4k_lora_workspace(x.shape[0], a[0].shape[1], len(a), x.device)
+        with _stream_scope(stream):
+            workspace = q4k_lora_workspace(x.shape[0], a[0].shape[1], len(a), x.device)
     status = (_bound or _native()).lora_add(x, a, b, base, order, seg_start, seg_adapter, scale, y, workspace, stream)
     if status:
         raise Q4KError(status, "q4k_lora_add")

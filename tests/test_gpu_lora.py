@@ -140,6 +140,28 @@ def test_repeats_streams_and_graphs(tokens):
         assert torch.equal(ref[m], again[m]) and torch.equal(ref[m], other[m]) and torch.equal(ref[m], y[m])
 
 
+@pytest.mark.parametrize("tokens", [3, 200])
+def test_stream_argument_while_the_current_stream_is_busy(tokens):
+    """Workspace and outputs made by the call belong to ``stream``: the current stream's next allocation gets neither."""
+    q4k.build()
+    d = make(47, ids_of(47, tokens, 4), 4, 32, 1024, [300, 300], torch.float16)
+    c = {k: ([t.cuda() for t in v] if isinstance(v, list) else v.cuda()) for k, v in d.items() if k != "ids"}
+    seg = q4k.q4k_lora_segments(d["ids"])
+    need = q4k.q4k_lora_workspace(tokens, 32, 2).numel()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    outs = []
+    torch.cuda._sleep(2_000_000)
+    s.wait_stream(torch.cuda.current_stream())         # both streams start when every call has returned
+    for _ in range(8):
+        outs.append(q4k.q4k_lora_add(c["x"], c["a"], c["b"], c["base"], *seg, c["scale"], stream=s))
+        torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    s.synchronize()
+    for y in outs:
+        check(y, d)
+    assert q4k.q4k_device_error() == 0
+
+
 def test_no_tokens_and_refusals():
     q4k.build()
     d = make(45, [], 2, 16, 512, [70], torch.float16)

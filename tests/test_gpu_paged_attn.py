@@ -254,6 +254,34 @@ def test_on_another_stream_and_in_a_graph(new):
         check(out, d, [new], [new + 100])
 
 
+@pytest.mark.parametrize("by_handle", [False, True])
+@pytest.mark.parametrize("new,kv", [([1], [9000]), ([4, 1], [5000, 700]), ([300], [4000])])
+def test_stream_argument_while_the_current_stream_is_busy(new, kv, by_handle):
+    """The call makes its workspace and output for ``stream``: neither a fill that waits behind the current stream's work
+    nor memory given back to that stream may reach the kernels."""
+    q4k.build()
+    d = make(34, new, kv, 16, 4, 128, 16, torch.float16)
+    c = {k: v.cuda() for k, v in d.items()}
+    for t in (torch.float32, torch.float16):
+        need = q4k.q4k_paged_attn_workspace(c["q"], c["kc"], c["table"], max(new), t).numel()
+        torch.cuda.empty_cache()
+        dirty = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")     # what a fresh workspace would be made of
+        torch.cuda.synchronize()
+        del dirty
+        s = torch.cuda.Stream()
+        outs = []
+        torch.cuda._sleep(20_000_000)                                           # some 10 ms on the current stream
+        for _ in range(3):
+            outs.append(q4k.q4k_paged_attn(c["q"], c["kc"], c["vc"], c["table"], c["cu"], c["kv"], max(new),
+                                           out_dtype=t, stream=s.cuda_stream if by_handle else s))
+            torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")          # takes what the call gave back
+        s.synchronize()
+        for got in outs:
+            check(got, d, new, kv)
+        torch.cuda.synchronize()
+    assert q4k.q4k_device_error() == 0
+
+
 @pytest.mark.parametrize("new", [1, 100])
 def test_offsets_past_32_bits(new):
     q4k.build()
