@@ -451,10 +451,10 @@ def _job_array(jobs):
     return arr, n, dev
 
 
-def _workspace(arr, n, batch, dev, workspace):
+def _workspace(arr, n, batch, dev, workspace, stream=None):
     need = int(lib().q4k_gemv_seq_workspace_bytes(arr, n, batch)) if n else 0
     if workspace is None:
-        workspace = torch.zeros(max(need, 16), dtype=torch.uint8, device=dev)
+        workspace = _made_on(stream, lambda: torch.zeros(max(need, 16), dtype=torch.uint8, device=dev))
     elif workspace.numel() < need:
         raise ValueError(f"workspace holds {workspace.numel()} bytes, the job list needs {need}")
     return workspace, need
@@ -469,6 +469,8 @@ class GemvSeq:
     ``cols``, ``x`` ([batch][cols] float32), ``y`` ([batch][rows] float32),
     optional ``residual`` and ``wait`` (read x only after every earlier job
     has stored its y).  The tensors must stay alive while the list is used.
+    A workspace made here is zeroed on the stream current at that time: calls
+    on another stream have to wait for it.
     """
 
     def __init__(self, jobs, batch: int, layout: int = BLOCK144, workspace=None):
@@ -536,7 +538,7 @@ def q4k_gemv_seq(jobs, batch: int, layout: int = BLOCK144, workspace=None, strea
     """One call of ``q4k_gemv_seq`` (plan and launch in one) over an ordered
     GEMV job list (see ``GemvSeq``); returns the workspace it used."""
     arr, n, dev = _job_array(jobs)
-    workspace, _ = _workspace(arr, n, int(batch), dev, workspace)
+    workspace, _ = _workspace(arr, n, int(batch), dev, workspace, stream)
     _check(lib().q4k_gemv_seq(arr, n, layout, int(batch), _ptr(workspace, torch.uint8, "workspace"),
                               workspace.numel(), _stream(stream)), "q4k_gemv_seq")
     return workspace

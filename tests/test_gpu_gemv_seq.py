@@ -429,3 +429,28 @@ def test_q4km_stack_across_launches_and_entry_points():
     for i in (0, 47, 48, 50, 59):
         assert_close(host(ys6[i]), *O6.gemv_q6k(fs[i], x), f"q6k job {i}")
     assert q4k.q4k_device_error() == 0
+
+
+def test_stream_argument_while_the_current_stream_is_busy():
+    """The call zeroes its workspace on ``stream``, not behind the current stream's work, and keeps the memory there."""
+    batch = 2
+    fields, xs = synth.decode_layer(synth.WL_DECODE_4B, 6, batch)
+    w = {n: pack_dev(fields[n]) for n in SHAPES}
+    xd = {k: dev(v) for k, v in xs.items()}
+    ys = [{n: torch.empty((batch, SHAPES[n][0]), device="cuda") for n in SHAPES} for _ in range(3)]
+    need = q4k.q4k_gemv_seq(layer_jobs(w, xd, ys[0], batch), batch).numel()
+    want = {n: host(ys[0][n]).copy() for n in SHAPES}
+    torch.cuda.empty_cache()
+    dirty = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")      # what a fresh workspace would be made of
+    torch.cuda.synchronize()
+    del dirty
+    s = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)                                            # some 10 ms on the current stream
+    for y in ys:
+        q4k.q4k_gemv_seq(layer_jobs(w, xd, y, batch), batch, stream=s)       # its workspace is dropped at once
+        torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    s.synchronize()
+    for y in ys:
+        for n in SHAPES:
+            assert np.array_equal(y[n].cpu().numpy(), want[n]), n
+    assert q4k.q4k_device_error() == 0
