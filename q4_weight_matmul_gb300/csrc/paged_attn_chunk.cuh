@@ -212,6 +212,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
       const int none = P.num_pages > 0 ? (int)P.num_pages : 1;        // a page past the end reads as zeros
       const int parts = kChunkKeys / F.box;                            // of one tile
       uint32_t n = 0;                                                  // tiles issued
+      bool stop = false;                                               // a wait of the block gave up: nothing more is
       do {
         const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
         const int32_t* table = P.page_table + (int64_t)w.req * P.max_pages;
@@ -225,7 +226,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         };
         int next;
         bool needed = page_of(w.u0, next);
-        for (int u = w.u0; u < w.u1; ++u) {
+        for (int u = w.u0; u < w.u1 && !stop; ++u) {
           const int64_t key = key0 + (int64_t)u * kChunkKeys;
           int page = next;
           const bool bad = needed && (page < 0 || page >= P.num_pages);
@@ -239,17 +240,17 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           for (int kv = 0; kv < 2; ++kv, ++n) {
             const uint32_t slot = n % L::kRing, use = n / L::kRing;
             if (use > 0) wait(&empty[slot], use - 1);
-            const bool go = !*gave_up;
-            if (lane == 0 && go) tc::mbar_arrive_expect_tx(&full[slot], L::kTile);
+            if ((stop = given_up(gave_up))) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(&full[slot], L::kTile);
             __syncwarp();
-            if (lane < parts && go)
+            if (lane < parts)
               load_cells(ring + slot * L::kTile + lane * F.box * D * 2, kv ? &vmap : &kmap, cell >> 3, page, P.kv_heads,
                          w.head, &full[slot]);
           }
         }
-      } while (w.next(P, R, group));
-      // after a wait gave up, the copies still in flight end before the block does
-      if (lane == 0 && *gave_up) {
+      } while (!stop && w.next(P, R, group));
+      // copies end before the block does, whoever gives up and when: the last ones to each place of the ring
+      if (lane == 0) {
         for (uint32_t j = n < L::kRing ? 0 : n - L::kRing; j < n; ++j)
           if (!tc::mbar_wait_sleep(&full[j % L::kRing], (j / L::kRing) & 1)) break;
       }
@@ -274,7 +275,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         }
         wait(&q_full[h], item++);
         tc::fence_after_sync();
-        for (int u = 0; u < units + 2 && !*gave_up; ++u) {
+        for (int u = 0; u < units + 2 && !given_up(gave_up); ++u) {
           const int b = u & 1;
           if (u >= 2) {
             wait(&pv_done[2 * h + b], (b ? uses1 : uses0) + (u >> 1) - 1);
@@ -297,7 +298,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         n0 += 2 * units;
         uses0 += (units + 1) >> 1;
         uses1 += units >> 1;
-        if (__any_sync(0xffffffffu, *gave_up)) break;
+        if (given_up(gave_up)) break;
       } while (w.next(P, R, group));
       drain();
     } else if (warp == 12 || warp == 13) {
@@ -317,7 +318,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           continue;
         }
         const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
-        for (int u = 0; u < units && !*gave_up; ++u) {
+        for (int u = 0; u < units && !given_up(gave_up); ++u) {
           const int b = u & 1;
           const uint32_t n = n0 + 2 * u;
           landed(n + 1);
@@ -351,7 +352,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         n0 += 2 * units;
         uses0 += (units + 1) >> 1;
         uses1 += units >> 1;
-        if (__any_sync(0xffffffffu, *gave_up)) break;
+        if (given_up(gave_up)) break;
       } while (w.next(P, R, group));
       drain();
     }

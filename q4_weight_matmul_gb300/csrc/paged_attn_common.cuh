@@ -57,6 +57,11 @@ __device__ __forceinline__ void load_cells(uint32_t dst, const void* map, int gr
       ::"r"(dst), "l"(map), "r"(0), "r"(group), "r"(page * kv_heads + head), "r"(tc::smem_u32(bar)) : "memory");
 }
 
+// Whether some wait of the block has given up: one answer for the (converged)
+// warp.  Lanes that read the flag at different times would part ways around
+// the votes, elections and copies that the whole warp takes part in.
+__device__ __forceinline__ bool given_up(volatile int* gave_up) { return __any_sync(0xffffffffu, *gave_up != 0); }
+
 struct Shape {             // of one request
   int q0, n;               // first token, new tokens
   int kv;                  // keys

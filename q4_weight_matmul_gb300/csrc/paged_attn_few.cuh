@@ -495,12 +495,13 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
     if (warp > C::kWarps) return;
     const int pages_slot = F.box < kUnit ? kUnit / F.box : 1;
     const int none = P.num_pages > 0 ? (int)P.num_pages : 1;    // a page past the end reads as zeros
+    bool stop = false;                               // a wait of the block gave up: no more copies
     do {
       const int64_t key0 = (w.lo / kUnit) * kUnit;
       const int32_t* table = P.page_table + (int64_t)w.req * P.max_pages;
       int64_t cached = -1;                           // page index that lane 0's entry is for
       int entry = none;
-      for (int u = w.u0; u < w.u1; ++u, ++issued) {
+      for (int u = w.u0; u < w.u1; ++u, ++issued) {  // `issued`: slots that got their copies
         const int slot = issued % C::kSlots;
         const int64_t key = key0 + (int64_t)u * kUnit;
         const int64_t p0 = key >> F.page_shift;
@@ -517,11 +518,12 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
           }
         }
         if (issued >= C::kSlots) wait(&empty[slot], (issued / C::kSlots - 1) & 1);
-        if (lane == 0 && !*gave_up) tc::mbar_arrive_expect_tx(&full[slot], L::kSlot);
+        if ((stop = given_up(gave_up))) break;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&full[slot], L::kSlot);
         for (int i = 0; i < pages_slot; ++i) {
           const int page = __shfl_sync(0xffffffffu, entry, (int)(p0 + i - cached));
           const int cell = (int)(key & (P.page_size - 1));
-          if (lane == 0 && !*gave_up) {
+          if (lane == 0) {
             const uint32_t dst = ring + slot * L::kSlot + i * F.box * D * 2;
             const int from = F.box < kUnit ? 0 : cell >> 3;
             load_cells(dst, &kmap, from, page, P.kv_heads, w.head, &full[slot]);
@@ -529,9 +531,9 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
           }
         }
       }
-    } while (w.next(P, R, group));
-    // after a wait gave up, the copies still in flight end before the block does
-    if (lane == 0 && *gave_up) {
+    } while (!stop && w.next(P, R, group));
+    // copies end before the block does, whoever gives up and when: the last ones to each slot
+    if (lane == 0) {
       for (uint32_t j = issued < C::kSlots ? 0 : issued - C::kSlots; j < issued; ++j)
         if (!tc::mbar_wait_sleep(&full[j % C::kSlots], (j / C::kSlots) & 1)) break;
     }
