@@ -28,13 +28,19 @@ class Pages:
 
     def step(self, new):
         """``new``: {request: new tokens} in batch order.  Takes the pages that
-        the new tokens need and returns the step's arrays (int32, host)."""
+        the new tokens need and returns the step's arrays (int32, host).  Where
+        pages are missing it raises RuntimeError and changes nothing."""
+        need = {r: -(-(self.length.get(r, 0) + n) // self.page_size) for r, n in new.items()}
+        for r, n in need.items():
+            if n > self.max_pages:
+                raise RuntimeError(f"request {r} needs {n} pages of the {self.max_pages} that one may have")
+        missing = sum(max(0, n - len(self.of.get(r, ()))) for r, n in need.items()) - len(self.free)
+        if missing > 0:
+            raise RuntimeError(f"{missing} pages too few are left")
         pos, slot, cu, kv, table = [], [], [0], [], []
         for r, n in new.items():
             pages, start = self.of.setdefault(r, []), self.length.get(r, 0)
             while len(pages) * self.page_size < start + n:
-                if len(pages) == self.max_pages or not self.free:
-                    raise RuntimeError(f"no page left for request {r}")
                 pages.append(self.free.pop())
             for p in range(start, start + n):
                 pos.append(p)

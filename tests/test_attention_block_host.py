@@ -1,0 +1,29 @@
+"""The attention block's host side: the bookkeeping of pages (no GPU)."""
+import copy
+
+import pytest
+
+from q4_weight_matmul_gb300.attention_block import Pages
+
+
+def state(p):
+    return copy.deepcopy((p.free, p.of, p.length))
+
+
+def lists(step):
+    return {k: v.tolist() for k, v in step.items()}
+
+
+@pytest.mark.parametrize("new", [{0: 5, 1: 30, 2: 1}, {0: 5, 1: 4, 2: 60}, {2: 1, 1: 4, 0: 17}])
+def test_a_refused_step_changes_nothing(new):
+    """Six pages of 4 cells, four for a request at most: too many pages in all, or for one request, after earlier requests
+    of the batch would have had theirs."""
+    pages = Pages(6, 4, 4)
+    pages.step({0: 3, 1: 9})
+    before = state(pages)
+    with pytest.raises(RuntimeError):
+        pages.step(new)
+    assert state(pages) == before
+    step = lists(pages.step({0: 5, 2: 1}))                     # and the next step goes on from there
+    assert step["pos"] == [3, 4, 5, 6, 7, 0] and step["kv_len"] == [8, 1]
+    assert len({s // 4 for s in step["slot"]} | set(pages.of[1])) == 6
