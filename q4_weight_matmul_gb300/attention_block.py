@@ -52,6 +52,12 @@ class Pages:
         make = lambda v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
         return {"pos": make(pos), "slot": make(slot), "cu_q": make(cu), "kv_len": make(kv), "table": make(table)}
 
+    def release(self, request):
+        """Give the pages of a finished request back (its launches need not
+        have ended: the next owner's come after them on their stream)."""
+        self.free.extend(reversed(self.of.pop(request)))
+        del self.length[request]
+
 
 class AttentionBlock:
     """One layer's attention block.  ``weights``: packed Q4_K ``q``, ``k``,

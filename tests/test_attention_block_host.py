@@ -27,3 +27,17 @@ def test_a_refused_step_changes_nothing(new):
     step = lists(pages.step({0: 5, 2: 1}))                     # and the next step goes on from there
     assert step["pos"] == [3, 4, 5, 6, 7, 0] and step["kv_len"] == [8, 1]
     assert len({s // 4 for s in step["slot"]} | set(pages.of[1])) == 6
+
+
+def test_released_pages_are_used_again():
+    pages = Pages(5, 4, 4)
+    for i in range(40):
+        step = lists(pages.step({i: 13, "kept": 0 if i else 3}))
+        assert step["kv_len"] == [13, 3] and all(0 <= p < 5 for p in step["table"][0])
+        assert set(step["table"][0]) & set(pages.of["kept"]) == set()
+        with pytest.raises(RuntimeError):
+            pages.step({"other": 1})
+        pages.release(i)
+    assert pages.length == {"kept": 3} and sorted(pages.free + pages.of["kept"]) == list(range(5))
+    with pytest.raises(KeyError):
+        pages.release(0)
