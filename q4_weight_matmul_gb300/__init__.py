@@ -655,15 +655,20 @@ def q4k_qk_norm_rope(q, k, v, k_cache, v_cache, pos, slot, cos_sin, q_weight=Non
     return q_out
 
 
+def q4k_paged_attn_workspace_bytes(q, k_cache, page_table, max_q: int, out_dtype=torch.float32, tokens=None) -> int:
+    """The bytes of ``q4k_paged_attn_workspace``."""
+    cache = _kv_cache(k_cache, k_cache)
+    n_req, max_pages = page_table.shape
+    return int(lib().q4k_paged_attn_workspace_bytes(ctypes.byref(cache), q.shape[1],
+                                                    q.shape[0] if tokens is None else tokens, n_req, max_q, max_pages,
+                                                    _TYPES[out_dtype]))
+
+
 def q4k_paged_attn_workspace(q, k_cache, page_table, max_q: int, out_dtype=torch.float32, tokens=None):
     """A workspace for ``q4k_paged_attn`` calls of these shapes (``tokens``: in
     place of ``q``'s, for the most tokens of any step), zeroed on torch's
     current stream: calls on another stream have to wait for that."""
-    cache = _kv_cache(k_cache, k_cache)
-    n_req, max_pages = page_table.shape
-    need = int(lib().q4k_paged_attn_workspace_bytes(ctypes.byref(cache), q.shape[1],
-                                                    q.shape[0] if tokens is None else tokens, n_req, max_q, max_pages,
-                                                    _TYPES[out_dtype]))
+    need = q4k_paged_attn_workspace_bytes(q, k_cache, page_table, max_q, out_dtype, tokens)
     return torch.zeros(max(need, 16), dtype=torch.uint8, device=k_cache.device)
 
 
@@ -703,9 +708,14 @@ def q4k_lora_segments(adapters, device="cuda"):
     return make(order), make(starts + [len(ids)]), make([ids[order[i]] for i in starts])
 
 
+def q4k_lora_workspace_bytes(tokens: int, rank: int, n_mats: int = 1) -> int:
+    """The bytes of ``q4k_lora_workspace``."""
+    return int(lib().q4k_lora_workspace_bytes(n_mats, rank, tokens))
+
+
 def q4k_lora_workspace(tokens: int, rank: int, n_mats: int = 1, device="cuda"):
     """A workspace for ``q4k_lora_add`` calls of up to these sizes."""
-    need = int(lib().q4k_lora_workspace_bytes(n_mats, rank, tokens))
+    need = q4k_lora_workspace_bytes(tokens, rank, n_mats)
     return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
 
 
@@ -753,7 +763,7 @@ __all__ = ["build", "lib", "Q4KError", "BLOCK144", "LAYOUT_GPU", "q4k_packed_byt
            "q8_1_bytes", "q8_quantize", "q8_quantize_h16", "q4k_gemm_h16", "q4k_gemm_blockdots_h16",
            "q4k_gemv", "q4k_gemv_multi", "GemvJob", "GemvSeq", "q4k_gemv_seq", "q4k_gemv_seq_static", "q4k_gemm",
            "q4k_gemm_blockdots", "q4k_device_error",
-           "KvCache", "LoraMat", "q4k_qk_norm_rope", "q4k_paged_attn_workspace", "q4k_paged_attn",
-           "q4k_lora_segments", "q4k_lora_workspace", "q4k_lora_add",
+           "KvCache", "LoraMat", "q4k_qk_norm_rope", "q4k_paged_attn_workspace_bytes", "q4k_paged_attn_workspace",
+           "q4k_paged_attn", "q4k_lora_segments", "q4k_lora_workspace_bytes", "q4k_lora_workspace", "q4k_lora_add",
            "q4k_selftest_wait_timeout", "q4k_version",
            "SIGNATURES"]

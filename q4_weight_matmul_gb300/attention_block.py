@@ -59,6 +59,28 @@ class Pages:
         del self.length[request]
 
 
+class Workspaces:
+    """Scratch memory for the calls of one stream, or of one captured graph:
+    one tensor for the attention and one for the adapters, as large as the
+    largest step so far.  Steps that share it must not overlap on the GPU, so
+    one object serves all layers of a model that runs on one stream."""
+
+    def __init__(self):
+        self.held, self.in_graphs = {}, []
+
+    def get(self, name, need, make, for_graph=False):
+        """The tensor ``name`` of ``need`` bytes or more.  One that a graph
+        was captured with stays where it is as long as this object does."""
+        t = self.held.get(name)
+        if t is None or t.numel() < need:
+            if for_graph:
+                raise RuntimeError("a step is captured with `work` only after it, or a larger one, has run with it")
+            t = self.held[name] = make()
+        if for_graph and not any(t is kept for kept in self.in_graphs):
+            self.in_graphs.append(t)
+        return t
+
+
 class AttentionBlock:
     """One layer's attention block.  ``weights``: packed Q4_K ``q``, ``k``,
     ``v``, ``o``; ``norms``: head norm weights (q, k); ``adapters``: None or
@@ -68,7 +90,7 @@ class AttentionBlock:
         self.w, self.hidden, self.heads, self.kv_heads, self.dim = weights, hidden, heads, kv_heads, head_dim
         self.norms, self.cos_sin, (self.k_cache, self.v_cache) = norms, cos_sin, cache
         self.adapters, self.scale = adapters, scale
-        self.work = {}
+        self.work = {}                      # stream handle -> its Workspaces
 
     def _project(self, names, rows, x, residual=None):
         """The projections of ``x``: a weight pass per step for a few tokens, tensor-core products for many."""
@@ -79,33 +101,43 @@ class AttentionBlock:
         ys = [q4k.q4k_gemm_f16(self.w[n], r, x.shape[1], *split) for n, r in zip(names, rows)]
         return ys if residual is None else [ys[0] + residual]
 
-    def _adapt(self, names, x, ys, segments):
+    def _adapt(self, names, x, ys, segments, scratch):
         if self.adapters is None or segments is None:
             return
         a, b = [self.adapters[n][0] for n in names], [self.adapters[n][1] for n in names]
-        key = ("lora", x.shape[0], len(names))
-        if key not in self.work:
-            self.work[key] = q4k.q4k_lora_workspace(x.shape[0], a[0].shape[1], len(names))
-        q4k.q4k_lora_add(x, a, b, ys, *segments, self.scale, y=ys, workspace=self.work[key])
+        size = x.shape[0], a[0].shape[1], len(names)
+        work = scratch("lora", q4k.q4k_lora_workspace_bytes(*size), lambda: q4k.q4k_lora_workspace(*size))
+        q4k.q4k_lora_add(x, a, b, ys, *segments, self.scale, y=ys, workspace=work)
 
-    def __call__(self, x, step, max_q, segments=None):
+    def __call__(self, x, step, max_q, segments=None, work=None):
         """``x`` [tokens][hidden] float32 (normed input, also the residual
         here); ``step``: ``Pages.step`` arrays on the device; ``segments``:
-        ``q4k_lora_segments`` of the tokens' adapters."""
+        ``q4k_lora_segments`` of the tokens' adapters; ``work``: the
+        ``Workspaces`` to use.  Without it every stream has its own, and a
+        call that is captured makes some for itself, which the graph keeps
+        (its replays zero the attention's: a pass over some 0.6 to 40 MB)."""
+        capturing = torch.cuda.is_current_stream_capturing()
+        for_graph = capturing and work is not None
+        if work is None:
+            key = torch.cuda.current_stream().cuda_stream
+            work = Workspaces() if capturing else self.work.setdefault(key, Workspaces())
+
+        def scratch(name, need, make):
+            return work.get(name, need, make, for_graph)
+
         rows = [self.heads * self.dim, self.kv_heads * self.dim, self.kv_heads * self.dim]
         q, k, v = qkv = self._project("qkv", rows, x)
-        self._adapt("qkv", x, qkv, segments)
+        self._adapt("qkv", x, qkv, segments, scratch)
         q = q4k.q4k_qk_norm_rope(q, k, v, self.k_cache, self.v_cache, step["pos"], step["slot"], self.cos_sin,
                                  *self.norms)
         # a few tokens: fp32 results cost nothing; a chunk: 16-bit ones, from the tensor cores
         dtype = torch.float32 if max_q <= 8 else self.k_cache.dtype
-        key = ("attn", x.shape[0], max_q)
-        if key not in self.work:
-            self.work[key] = q4k.q4k_paged_attn_workspace(q, self.k_cache, step["table"], max_q, dtype)
+        size = q, self.k_cache, step["table"], max_q, dtype
+        space = scratch("attn", q4k.q4k_paged_attn_workspace_bytes(*size), lambda: q4k.q4k_paged_attn_workspace(*size))
         o = q4k.q4k_paged_attn(q, self.k_cache, self.v_cache, step["table"], step["cu_q"], step["kv_len"], max_q,
-                               out_dtype=dtype, workspace=self.work[key]).float().flatten(1)
+                               out_dtype=dtype, workspace=space).float().flatten(1)
         y = self._project("o", [self.hidden], o, residual=x)
-        self._adapt("o", o, y, segments)
+        self._adapt("o", o, y, segments, scratch)
         return y[0]
 
 
@@ -176,16 +208,16 @@ def main():
     new = {r: 1 for r in range(a.requests)}
     x = torch.randn((a.requests, a.hidden), device="cuda")
     segments = q4k.q4k_lora_segments(adapter)
-    buffers, graph = None, None
+    buffers, graph, work = None, None, Workspaces()
     for i in range(a.steps):
         host = pages.step(new)
         if buffers is None:
             buffers = {k: v.cuda() for k, v in host.items()}
-            y = block(x, buffers, 1, segments)                     # makes the workspaces
+            y = block(x, buffers, 1, segments, work)               # makes the workspaces
             torch.cuda.synchronize()
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph):
-                y = block(x, buffers, 1, segments)
+                y = block(x, buffers, 1, segments, work)
         else:
             for k, v in host.items():
                 buffers[k].copy_(v)

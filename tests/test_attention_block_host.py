@@ -1,9 +1,10 @@
-"""The attention block's host side: the bookkeeping of pages (no GPU)."""
+"""The attention block's host side: the bookkeeping of pages and workspaces (no GPU)."""
 import copy
 
 import pytest
+import torch
 
-from q4_weight_matmul_gb300.attention_block import Pages
+from q4_weight_matmul_gb300.attention_block import Pages, Workspaces
 
 
 def state(p):
@@ -41,3 +42,18 @@ def test_released_pages_are_used_again():
     assert pages.length == {"kept": 3} and sorted(pages.free + pages.of["kept"]) == list(range(5))
     with pytest.raises(KeyError):
         pages.release(0)
+
+
+def test_workspaces_grow_and_stay_for_graphs():
+    made = lambda n: lambda: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    w = Workspaces()
+    with pytest.raises(RuntimeError):                                   # a capture makes none
+        w.get("attn", 10, made(10), for_graph=True)
+    small = w.get("attn", 10, made(10))
+    assert w.get("attn", 7, made(7)) is small and w.get("attn", 10, made(10), for_graph=True) is small
+    large = w.get("attn", 100, made(100))
+    assert large.numel() == 100 and w.get("attn", 10, made(10)) is large
+    assert any(t is small for t in w.in_graphs)                         # what the graph writes to is still there
+    for n in range(50):
+        assert w.get("attn", 50 + n, made(50 + n), for_graph=True) is large
+    assert len(w.held) == 1 and len(w.in_graphs) == 2

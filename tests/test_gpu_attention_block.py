@@ -13,7 +13,7 @@ import torch
 
 import q4_weight_matmul_gb300 as q4k
 from oracle import attention as A
-from q4_weight_matmul_gb300.attention_block import AttentionBlock, Pages
+from q4_weight_matmul_gb300.attention_block import AttentionBlock, Pages, Workspaces
 import synth
 from _gpu import pack_dev
 
@@ -92,6 +92,59 @@ def test_prompts_and_decode_steps():
             start[q] += n
         err = np.linalg.norm(y.cpu().double().numpy() - want, axis=1) / np.linalg.norm(want, axis=1)
         assert err.max() < 16 * 2.0 ** -11, (new, err.max())
+    assert q4k.q4k_device_error() == 0
+
+
+def run_step(block, pages, new, seed, **kw):
+    """One step of the requests ``new``; what the block gave, and the call's arguments."""
+    x = torch.randn((sum(new.values()), HIDDEN), generator=torch.Generator().manual_seed(seed)).cuda()
+    step = {k: v.cuda() for k, v in pages.step(new).items()}
+    segments = q4k.q4k_lora_segments([r % 3 - 1 for r, n in new.items() for _ in range(n)])
+    return block(x, step, max(new.values()), segments, **kw), (x, step, max(new.values()), segments)
+
+
+def test_workspaces_do_not_add_up():
+    """Steps of many sizes keep the workspaces of the largest, not one for every size."""
+    block, pages, *_ = make()
+    sizes = []
+    for n in (60, 3, 1, 41, 57, 1, 2, 22, 50, 9):
+        run_step(block, pages, {n * 100: n, n * 100 + 1: 1}, n)
+        pages.release(n * 100), pages.release(n * 100 + 1)
+        assert len(block.work) == 1
+        held = next(iter(block.work.values())).held
+        sizes.append({k: t.numel() for k, t in held.items()})
+    assert set(sizes[-1]) == {"attn", "lora"} and all(s == sizes[0] for s in sizes)       # the first step was the largest
+    assert q4k.q4k_device_error() == 0
+
+
+def test_streams_and_graphs_have_their_own_workspaces():
+    """A first call inside a capture, the same step called directly on two streams, and the graph replayed beside them."""
+    block, pages, *_ = make()
+    run_step(block, pages, {0: 90, 1: 70, 2: 1}, 1)                       # something in the cache
+    mine = next(iter(block.work.values())).held["attn"].data_ptr()
+    for new, work in (({0: 1, 1: 1, 2: 1}, None), ({0: 40, 1: 1, 2: 2}, None), ({1: 1, 2: 1}, Workspaces())):
+        want, args = run_step(block, pages, new, 2, **({"work": work} if work else {}))
+        want = want.clone()
+        torch.cuda.synchronize()
+        graph, kept = torch.cuda.CUDAGraph(), dict(block.work)
+        with torch.cuda.graph(graph):
+            got = block(*args, work=work)
+        assert block.work == kept                                        # nothing of the capture stays behind
+        side = torch.cuda.Stream()
+        for _ in range(3):
+            got.zero_()
+            side.wait_stream(torch.cuda.current_stream())
+            graph.replay()
+            with torch.cuda.stream(side):
+                other = block(*args)
+            direct = block(*args)
+            torch.cuda.synchronize()
+            assert torch.equal(got, want) and torch.equal(direct, want) and torch.equal(other, want)
+        assert block.work[side.cuda_stream].held["attn"].data_ptr() != mine
+    with pytest.raises(RuntimeError):                                    # a graph never makes the workspaces it is given
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            block(*args, work=Workspaces())
+    torch.cuda.synchronize()
     assert q4k.q4k_device_error() == 0
 
 
