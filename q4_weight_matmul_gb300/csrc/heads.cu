@@ -94,9 +94,11 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const HeadsParams 
   }
   const int page = slot >> page_shift, cell = slot & (P.page_size - 1);
 
-  // factors of the lane's values (c) and of their partners (s), lower and upper half
-  const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 c0 = one, s0 = zero, c1 = one, s1 = zero;
+  // factors of the lane's values (c) and of their partners (s), lower and upper half, where those are rotated (the
+  // others are left alone, not multiplied by 1 and 0: an infinity would make its neighbour, or itself, NaN)
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 c0 = zero, s0 = zero, c1 = zero, s1 = zero;
+  const bool turn0 = MODE == kWhole ? P.rot != 0 : 4 * l < P.rot, turn1 = 4 * l + D / 2 < P.rot;
   const float* cs = P.cos_sin + (int64_t)pos * P.rot;
   const int half = P.rot / 2;
   int from0 = lane, from1 = lane;           // kPart: the lanes of the partners,
@@ -165,14 +167,16 @@ __global__ void __launch_bounds__(256, 3) qk_norm_rope_kernel(const HeadsParams 
     uint16_t* dst;
     if (rv < 0) {
       if constexpr (MODE == kWhole) {
-        px = mul2(x, c0, mul(y, -1.f), s0);
-        y = mul2(y, c0, x, s0);
-        x = px;
+        if (turn0) {
+          px = mul2(x, c0, mul(y, -1.f), s0);
+          y = mul2(y, c0, x, s0);
+          x = px;
+        }
       } else {
         if constexpr (MODE == kNeighbours)
           px = make_float4(x.y, x.x, x.w, x.z), py = make_float4(y.y, y.x, y.w, y.z);
-        x = mul2(x, c0, px, s0);
-        y = mul2(y, c1, py, s1);
+        if (turn0) x = mul2(x, c0, px, s0);
+        if (turn1) y = mul2(y, c1, py, s1);
       }
       dst = rk < 0 ? q_out + r * D : static_cast<uint16_t*>(P.k_cache) + cell_at + (int64_t)rk * head_step;
     } else {

@@ -96,6 +96,33 @@ def test_rows_of_zeros_large_values_and_nan():
     check(out[3], want[3], mag[3], torch.float16)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim,rot,interleaved", [(128, 0, False), (128, 0, True), (64, 0, False), (128, 64, False),
+                                                 (128, 64, True), (64, 24, False), (128, 104, False), (64, 40, True)])
+def test_infinities_and_nan_outside_the_rotation(dim, rot, interleaved, dtype):
+    """Without norm, values that are not rotated are only rounded: one that is not finite changes no other."""
+    q4k.build()
+    d, _ = make(11, 5, 6, 2, dim, 16, dtype, rot=rot)
+    r = np.random.default_rng(rot)
+    for n in "qk":
+        for value in (np.inf, -np.inf, np.nan):
+            at = r.random(d[n].shape) < 0.1
+            at[..., :rot] = False
+            d[n][at] = value
+        assert not np.all(np.isfinite(d[n]))
+    out, kc, _ = run(d, rot, False, interleaved)
+    cells = [(int(s) // 16, int(s) % 16) for s in d["slot"]]
+    keys = torch.stack([kc[p, :, c] for p, c in cells])
+    for n, got in (("q", out), ("k", keys)):
+        want = torch.from_numpy(d[n][..., rot:]).to(dtype)
+        assert torch.equal(got[..., rot:].cpu().view(torch.int16)[~want.isnan()], want.view(torch.int16)[~want.isnan()])
+        assert torch.equal(got[..., rot:].cpu().isnan(), want.isnan())
+        if rot:
+            turned, mag = O.norm_rope(d[n][..., :rot], None, 0.0, d["cs"], d["pos"], rot, interleaved)
+            check(got[..., :rot], turned, mag, dtype)
+    assert q4k.q4k_device_error() == 0
+
+
 def test_no_tokens_and_indices_out_of_range():
     q4k.build()
     d, rot = make(6, 0, 4, 2, 128, 16, torch.bfloat16)
