@@ -673,7 +673,9 @@ int q4k_paged_attn(const void* q, int64_t tokens, int heads, const q4k_kv_cache*
  *               16-byte aligned; it needs no clearing.  Calls that share a
  *               workspace must not overlap on the GPU.
  * fp32 sums, A and B entries exact: |y - exact| <= 1e-5 * (|base| + |scale|
- * sum |B||A||x|).  Deterministic on one device.  An index out of range is
+ * sum |B||A||x|) for activations and A x of any magnitude beside one another
+ * (those below 2^-97, where fp32 itself begins to run out, aside).
+ * Deterministic on one device.  An index out of range is
  * skipped and reported by q4k_device_error (Q4K_ERR_DEVICE_INDEX): a token
  * out of range gets no output, an adapter out of range counts as none.
  * order, seg_start and seg_adapter need 4-byte alignment.

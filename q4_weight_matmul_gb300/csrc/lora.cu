@@ -11,8 +11,11 @@
 // Products run on mma.sync m16n8k16 with the adapters' 16-bit values as they
 // are; a fp32 activation enters as a sum of values of their type: three
 // bfloat16 (24 bits), or two binary16 (22 bits) of the activations scaled by
-// a power of two, the same for 32 of a row, that puts the largest near 2^14
-// (smaller ones lose nothing until 2^-38 of it).  The k index of an
+// a power of two, the same for 32 of a row, that puts the largest near 2^14,
+// the second part times 2^11.  So binary16 keeps 22 bits down to 2^-29 of the
+// largest and 20 down to 2^-31; where a value but zero is smaller, the warp
+// makes its sums again with tf32 instructions (22 bits for any value).  Looking
+// for such values costs 5 % of the first launch.  The k index of an
 // instruction is free to permute, so every lane loads 8 consecutive k of its
 // row (16 bytes of an adapter, 32 of x) and feeds them to two instructions
 // without a transpose.  Sums of 32 k start from zero and are added up in fp32
@@ -99,17 +102,27 @@ __device__ __forceinline__ int token_at(const LoraParams& P, int i) {
   return -1;
 }
 
+constexpr float kLow = 2048.f;   // the second part of a binary16 operand is held times 2^11
+
 // The 16-bit parts of the two rows' 8 values each: p[part][i] is the A operand
-// of instruction i; `back`: what the products are to be multiplied by.
+// of instruction i; `back`: what the products are to be multiplied by.  Bit r
+// of the result: a value of this lane in row r is so far below the row's
+// largest that the parts do not hold it, and the products are to be made apart
+// (below).
 template <bool BF16>
-__device__ __forceinline__ void split(const float (&a)[8], const float (&b)[8], uint32_t (&p)[BF16 ? 3 : 2][2][4],
+__device__ __forceinline__ uint32_t split(const float (&a)[8], const float (&b)[8], uint32_t (&p)[BF16 ? 3 : 2][2][4],
                                       float (&back)[2]) {
   float s[2] = {1.f, 1.f};
   back[0] = back[1] = 1.f;
+  uint32_t apart = 0;
   if constexpr (!BF16) {
     float top[2] = {0.f, 0.f};
+    uint32_t low[2] = {0xffffffffu, 0xffffffffu};                           // twice the least magnitude but zero, less one
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top[0] = fmaxf(top[0], fabsf(a[e])), top[1] = fmaxf(top[1], fabsf(b[e]));
+    for (int e = 0; e < 8; ++e) {
+      top[0] = fmaxf(top[0], fabsf(a[e])), top[1] = fmaxf(top[1], fabsf(b[e]));
+      low[0] = min(low[0], 2u * __float_as_uint(a[e]) - 1u), low[1] = min(low[1], 2u * __float_as_uint(b[e]) - 1u);
+    }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));      // the row's other 24 values
@@ -117,6 +130,7 @@ __device__ __forceinline__ void split(const float (&a)[8], const float (&b)[8], 
       const uint32_t e = max(__float_as_uint(top[r]) >> 23, 15u);           // biased exponent
       s[r] = __uint_as_float((268u - e) << 23);                             // 2^(14 - exponent)
       back[r] = __uint_as_float((e - 14u) << 23);
+      if (e > 30u && low[r] < (e - 30u) << 24) apart |= 1u << r;            // below 2^-16 when scaled
     }
   }
 #pragma unroll
@@ -124,6 +138,7 @@ __device__ __forceinline__ void split(const float (&a)[8], const float (&b)[8], 
     float x0 = a[2 * i] * s[0], x1 = a[2 * i + 1] * s[0], y0 = b[2 * i] * s[1], y1 = b[2 * i + 1] * s[1];
 #pragma unroll
     for (int k = 0; k < (BF16 ? 3 : 2); ++k) {
+      if (!BF16 && k == 1) x0 *= kLow, x1 *= kLow, y0 *= kLow, y1 *= kLow;
       const uint32_t x = pack2<BF16>(x0, x1), y = pack2<BF16>(y0, y1);
       const float2 fx = unpack2<BF16>(x), fy = unpack2<BF16>(y);
       x0 -= fx.x, x1 -= fx.y, y0 -= fy.x, y1 -= fy.y;
@@ -131,6 +146,7 @@ __device__ __forceinline__ void split(const float (&a)[8], const float (&b)[8], 
       p[k][i >> 1][2 * (i & 1) + 1] = y;
     }
   }
+  return apart;
 }
 
 // c += X W^T over 32 k: X as split() made it, W row g of each tile as 8
@@ -143,9 +159,15 @@ __device__ __forceinline__ void products(float (&c)[NT][4], const uint32_t (&p)[
     if (q < tiles) {
       float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < (BF16 ? 3 : 2); ++k) {
+      for (int k = BF16 ? 0 : 1; k < (BF16 ? 3 : 2); ++k) {
         mma16816<BF16>(t, p[k][0], w[q].x, w[q].y);
         mma16816<BF16>(t, p[k][1], w[q].z, w[q].w);
+      }
+      if constexpr (!BF16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] *= 1.f / kLow;
+        mma16816<BF16>(t, p[0][0], w[q].x, w[q].y);
+        mma16816<BF16>(t, p[0][1], w[q].z, w[q].w);
       }
       c[q][0] = fmaf(t[0], back[0], c[q][0]), c[q][1] = fmaf(t[1], back[0], c[q][1]);
       c[q][2] = fmaf(t[2], back[1], c[q][2]), c[q][3] = fmaf(t[3], back[1], c[q][3]);
@@ -153,16 +175,59 @@ __device__ __forceinline__ void products(float (&c)[NT][4], const uint32_t (&p)[
   }
 }
 
-// The same with X rows g and g + 8 as 8 consecutive k each (xa, xb).
+// The same with X rows g and g + 8 as 8 consecutive k each (xa, xb); result as split()'s.
 template <bool BF16, int NT>
-__device__ __forceinline__ void step32(float (&c)[NT][4], const float4 (&xa)[2], const float4 (&xb)[2],
+__device__ __forceinline__ uint32_t step32(float (&c)[NT][4], const float4 (&xa)[2], const float4 (&xb)[2],
                                        const uint4 (&w)[NT], int tiles) {
   const float a[8] = {xa[0].x, xa[0].y, xa[0].z, xa[0].w, xa[1].x, xa[1].y, xa[1].z, xa[1].w};
   const float b[8] = {xb[0].x, xb[0].y, xb[0].z, xb[0].w, xb[1].x, xb[1].y, xb[1].z, xb[1].w};
   uint32_t p[BF16 ? 3 : 2][2][4];
   float back[2];
-  split<BF16>(a, b, p, back);
+  const uint32_t apart = split<BF16>(a, b, p, back);
   products<BF16, NT>(c, p, back, w, tiles);
+  return apart;
+}
+
+// Products of binary16 adapters with activations that are too far apart for
+// one scale: tf32 instructions, whose operands have fp32's exponents and hold
+// binary16 exactly (twice as many: 45.7 against 38.6 us for the 2049-token
+// case if all products were made so).
+__device__ __forceinline__ uint32_t to_tf32(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+// C += A B, 16 x 8 x 8: A holds rows g (a[0], a[2]) and g + 8 (a[1], a[3]) at
+// k = c and c + 4, B column g at the same k, C as mma16816's.
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], float b0, float b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
+}
+// c += X W^T over 32 k for one tile of W's rows, a and b rows g and g + 8 of X.
+__device__ __forceinline__ void step32_apart(float (&c)[4], const float (&a)[8], const float (&b)[8], const uint4& w) {
+  const float2 f[4] = {unpack2<false>(w.x), unpack2<false>(w.y), unpack2<false>(w.z), unpack2<false>(w.w)};
+  float t[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x[4] = {a[2 * i], b[2 * i], a[2 * i + 1], b[2 * i + 1]};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      uint32_t p[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[e] = to_tf32(x[e]), x[e] -= __uint_as_float(p[e]);
+      mma1688(t, p, f[i].x, f[i].y);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] += t[e];
+}
+__device__ __forceinline__ void load8(float (&x)[8], const float* from) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float4 v = from ? reinterpret_cast<const float4*>(from)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+    x[4 * e] = v.x, x[4 * e + 1] = v.y, x[4 * e + 2] = v.z, x[4 * e + 3] = v.w;
+  }
 }
 
 // h[part][place][m * rank + j], scaled.  Grid: tiles x column parts x groups
@@ -195,10 +260,49 @@ __device__ __forceinline__ const uint16_t* a_row(const LoraParams& P, int adapte
   return static_cast<const uint16_t*>(P.mat[m].a) + ((int64_t)adapter * P.rank + j) * P.cols;
 }
 
+// A warp's sums again, all products made apart; its steps of 32 columns are
+// every (parts * kWarps)-th in both kernels.
+template <int NT>
+struct Sums {
+  float v[NT][4];
+};
+template <int NT>
+__device__ __noinline__ Sums<NT> sums_apart(const LoraParams& P, int adapter, int ta, int tb, int q0, int tiles) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const float* xa = ta >= 0 ? P.x + (int64_t)ta * P.cols + 8 * c : nullptr;
+  const float* xb = tb >= 0 ? P.x + (int64_t)tb * P.cols + 8 * c : nullptr;
+  const int64_t stride = (int64_t)gridDim.y * kWarps;
+  Sums<NT> sum{};
+  for (int64_t s = blockIdx.y * kWarps + warp; s < P.cols / 32; s += stride) {
+    float a[8], b[8];
+    load8(a, xa ? xa + s * 32 : nullptr);
+    load8(b, xb ? xb + s * 32 : nullptr);
+#pragma unroll
+    for (int q = 0; q < NT; ++q)
+      if (q < tiles)
+        step32_apart(sum.v[q], a, b,
+                     __ldg(reinterpret_cast<const uint4*>(a_row(P, adapter, (q0 + q) * 8 + g) + 8 * c + s * 32)));
+  }
+  return sum;
+}
+template <bool BF16, int NT>
+__device__ __forceinline__ void replace_apart(const LoraParams& P, const Tile& T, float (&acc)[NT][4], int q0, int tiles,
+                                              uint32_t apart) {
+  const int g = (threadIdx.x & 31) >> 2;
+  const uint32_t there = (g < T.n ? 1u : 0u) | (g + 8 < T.n ? 2u : 0u);      // other rows hold anything
+  if (BF16 || !__any_sync(0xffffffffu, apart & there)) return;
+  const int ta = g < T.n ? token_at(P, T.first + g) : -1, tb = g + 8 < T.n ? token_at(P, T.first + g + 8) : -1;
+  const Sums<NT> sum = sums_apart<NT>(P, T.adapter, ta, tb, q0, tiles);
+#pragma unroll
+  for (int q = 0; q < NT; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[q][e] = sum.v[q][e];
+}
+
 // Few tokens: latency counts.  Operands straight into registers, one rank
 // tile per CTA.
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const LoraParams P) {
+__global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const __grid_constant__ LoraParams P) {
   __shared__ float part[kWarps][8][kTile + 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Tile T = find_tile(P, blockIdx.x);
@@ -226,15 +330,17 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const LoraPar
     w[i][0] = in ? __ldg(reinterpret_cast<const uint4*>(wp + k)) : make_uint4(0, 0, 0, 0);
   };
   int s = blockIdx.y * kWarps + warp;
+  uint32_t apart = 0;
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) load(i, s + i * stride);
   for (; s < steps; s += kAhead * stride) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      step32<BF16, 1>(acc, a[i], b[i], w[i], 1);
+      apart |= step32<BF16, 1>(acc, a[i], b[i], w[i], 1);
       load(i, s + (i + kAhead) * stride);
     }
   }
+  replace_apart<BF16, 1>(P, T, acc, blockIdx.z, 1, apart);
   store_h<1>(P, T, part, acc, blockIdx.z, 1);
 }
 
@@ -264,7 +370,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
 }
 
 template <bool BF16, int NT>
-__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraParams P) {
+__global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const __grid_constant__ LoraParams P) {
   using S = Shrink<NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -304,6 +410,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraPara
 #pragma unroll
   for (int i = 0; i < S::kStages - 1; ++i) copy(i);
 
+  uint32_t apart = 0;
   float acc[NT][4];
 #pragma unroll
   for (int q = 0; q < NT; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.f;
@@ -323,8 +430,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_shrink_kernel(const LoraPara
     }
 #pragma unroll
     for (int q = 0; q < NT; ++q) w[q] = *reinterpret_cast<const uint4*>(a + q * 8 * kARow);
-    step32<BF16, NT>(acc, xa, xb, w, tiles);
+    apart |= step32<BF16, NT>(acc, xa, xb, w, tiles);
   }
+  replace_apart<BF16, NT>(P, T, acc, q0, tiles, apart);
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();
   store_h<NT>(P, T, reinterpret_cast<float(*)[NT * 8][kTile + 1]>(smem), acc, q0, tiles);
@@ -351,8 +459,59 @@ __host__ __device__ constexpr int block_bytes() { return (BF16 ? 3 : 2) * 2 * 32
 constexpr int kBRow = 64;
 constexpr int kSlot = kTile * kXRow + kChunk * kBRow;
 
+// A CTA's outputs with all products made apart, operands straight from global
+// memory; output 8 q + 2 c + e of a warp's 32 is column 2 c + e of tile q.
+__device__ __noinline__ void expand_apart(const LoraParams& P, const Tile& T, int ta, int tb, int parts, int chunks) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3, all = P.n * P.rank;
+  const int token[2] = {ta, tb};
+  int m = 0, first = 0;
+  for (int chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
+    for (;; ++m) {
+      const int n = (int)((P.mat[m].rows + kChunk - 1) / kChunk);
+      if (chunk < first + n) break;
+      first += n;
+    }
+    const LoraMat& w = P.mat[m];
+    const int64_t o0 = (int64_t)(chunk - first) * kChunk + warp * kOuts;
+    float y[4][4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t o = o0 + 8 * q + 2 * c + (e & 1), t = token[e >> 1];
+        y[q][e] = w.base && t >= 0 && o < w.rows ? w.base[t * w.rows + o] : 0.f;
+      }
+    for (int j0 = 0; j0 < P.rank; j0 += 32) {
+      const int j = j0 + 8 * c;
+      float x[2][8] = {};
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (g + 8 * r >= T.n || j >= P.rank) continue;
+        const float* from = P.work + ((int64_t)T.first + g + 8 * r) * all + m * P.rank + j;
+        for (int k = 0; k < parts; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[r][e] += __ldcg(from + (int64_t)k * P.tokens * all + e);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t o = o0 + 8 * q + g;
+        const uint16_t* from = static_cast<const uint16_t*>(w.b) + ((int64_t)T.adapter * w.rows + o) * P.rank + j;
+        const uint4 b = o < w.rows && j < P.rank ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0, 0, 0, 0);
+        step32_apart(y[q], x[0], x[1], b);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t o = o0 + 8 * q + 2 * c + (e & 1), t = token[e >> 1];
+        if (t >= 0 && o < w.rows) w.y[t * w.rows + o] = y[q][e];
+      }
+  }
+}
+
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraParams P, int parts, int chunks, int slots) {
+__global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const __grid_constant__ LoraParams P, int parts, int chunks, int slots) {
   // [block]: parts [part][instruction][lane], back [row][lane]; then the ring
   extern __shared__ __align__(128) uint8_t smem[];
   constexpr int PARTS = BF16 ? 3 : 2;
@@ -434,6 +593,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
   for (int i = 0; i < slots - 1; ++i) copy(put++);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (T.adapter >= 0) {
+    uint32_t apart = 0;
     // a warp per block: lane (g, c) has 8 ranks of places g and g + 8
     for (int i = warp; i < P.n * kblocks; i += kWarps) {
       const int j = 32 * (i % kblocks) + 8 * c;
@@ -459,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
       }
       uint32_t p[PARTS][2][4];
       float back[2];
-      split<BF16>(x[0], x[1], p, back);
+      apart |= split<BF16>(x[0], x[1], p, back);
       uint8_t* at = smem + i * block_bytes<BF16>();
 #pragma unroll
       for (int k = 0; k < PARTS; ++k)
@@ -469,6 +629,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_expand_kernel(const LoraPara
       float* scale = reinterpret_cast<float*>(at + PARTS * 2 * 32 * 16);
       scale[lane] = back[0];
       scale[32 + lane] = back[1];
+    }
+    if (!BF16 && __syncthreads_or(apart)) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      expand_apart(P, T, token[0], token[1], parts, chunks);
+      return;
     }
   }
 

@@ -96,6 +96,43 @@ def test_large_and_small_activations():
     check(run(d), d)
 
 
+def banded(seed, tokens, dtype):
+    """Activations over 110 binades, by columns; one adapter sees only the small ones, one all, and one has ranks that
+    see a band of columns each, so that its products spread as far, beside outputs that take only some of the ranks."""
+    d = make(seed, ids_of(seed, tokens, 3), 3, 32, 512, [200, 61], dtype)
+    r = np.random.default_rng(seed)
+    e = r.integers(-60, 51, 512)
+    d["x"] *= torch.from_numpy(2.0 ** e).float()
+    d["ids"][0] = 0
+    for a, b in zip(d["a"], d["b"]):
+        a[0, :, torch.from_numpy(e > -35)] = 0
+        low = torch.from_numpy(-60 + 100 * np.arange(32) // 32)[:, None]
+        band = torch.from_numpy(e)[None]
+        a[2][(band < low) | (band > low + 12)] = 0
+        b[2][torch.from_numpy(r.random(b[2].shape) < 0.9)] = 0
+    return d
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens", [1, 4, 16, 60, 300])
+def test_small_activations_beside_large_ones(tokens, dtype):
+    """The bound is against sum |B||A||x|: where A, or B, is zero at the large values, the small ones still count in full."""
+    q4k.build()
+    d = banded(48 + tokens, tokens, dtype)
+    check(run(d, None), d, None)
+    assert q4k.q4k_device_error() == 0
+
+
+def test_one_large_value_in_front():
+    q4k.build()
+    for dtype in (torch.float16, torch.bfloat16):
+        for tokens in (1, 20):
+            d = make(49, [0] * tokens, 1, 8, 256, [8], dtype)
+            d["x"][:, 0], d["x"][:, 1:] = 2.0 ** 30, 1.2345678
+            d["a"][0][:, :, 0], d["a"][0][:, :, 2:] = 0, 0
+            check(run(d, None), d, None)
+
+
 def test_indices_out_of_range_are_reported():
     q4k.build()
     d = make(43, [0, 0, 1, 1, 2, 2], 3, 16, 512, [70], torch.float16)
