@@ -104,6 +104,31 @@ __device__ __forceinline__ int token_at(const LoraParams& P, int i) {
 
 constexpr float kLow = 2048.f;   // the second part of a binary16 operand is held times 2^11
 
+// The parts of a s[0] and b s[1] (s = 1: bfloat16).  CUT: the first part of a
+// value is cut off, not rounded, so that it is finite where the value is; of an
+// infinity it is all, and the others are zero (not its difference from itself).
+template <bool BF16, bool CUT>
+__device__ __forceinline__ void split_rows(const float (&a)[8], const float (&b)[8], const float (&s)[2],
+                                           uint32_t (&p)[BF16 ? 3 : 2][2][4]) {
+  auto pack = [](float v, float w, bool cut) {
+    return cut ? __float_as_uint(v) >> 16 | (__float_as_uint(w) & 0xffff0000u) : pack2<BF16>(v, w);
+  };
+  auto rest = [](float v, float part) { return CUT && fabsf(v) == INFINITY ? 0.f : v - part; };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0 = a[2 * i] * s[0], x1 = a[2 * i + 1] * s[0], y0 = b[2 * i] * s[1], y1 = b[2 * i + 1] * s[1];
+#pragma unroll
+    for (int k = 0; k < (BF16 ? 3 : 2); ++k) {
+      if (!BF16 && k == 1) x0 *= kLow, x1 *= kLow, y0 *= kLow, y1 *= kLow;
+      const uint32_t x = pack(x0, x1, CUT && k == 0), y = pack(y0, y1, CUT && k == 0);
+      const float2 fx = unpack2<BF16>(x), fy = unpack2<BF16>(y);
+      x0 = rest(x0, fx.x), x1 = rest(x1, fx.y), y0 = rest(y0, fy.x), y1 = rest(y1, fy.y);
+      p[k][i >> 1][2 * (i & 1)] = x;
+      p[k][i >> 1][2 * (i & 1) + 1] = y;
+    }
+  }
+}
+
 // The 16-bit parts of the two rows' 8 values each: p[part][i] is the A operand
 // of instruction i; `back`: what the products are to be multiplied by.  Bit r
 // of the result: a value of this lane in row r is so far below the row's
@@ -115,7 +140,11 @@ __device__ __forceinline__ uint32_t split(const float (&a)[8], const float (&b)[
   float s[2] = {1.f, 1.f};
   back[0] = back[1] = 1.f;
   uint32_t apart = 0;
-  if constexpr (!BF16) {
+  float top = 0.f;
+  if constexpr (BF16) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
+  } else {
     float top[2] = {0.f, 0.f};
     uint32_t low[2] = {0xffffffffu, 0xffffffffu};                           // twice the least magnitude but zero, less one
 #pragma unroll
@@ -130,22 +159,11 @@ __device__ __forceinline__ uint32_t split(const float (&a)[8], const float (&b)[
       const uint32_t e = max(__float_as_uint(top[r]) >> 23, 15u);           // biased exponent
       s[r] = __uint_as_float((268u - e) << 23);                             // 2^(14 - exponent)
       back[r] = __uint_as_float((e - 14u) << 23);
-      if (e > 30u && low[r] < (e - 30u) << 24) apart |= 1u << r;            // below 2^-16 when scaled
+      if (e > 30u && (low[r] < (e - 30u) << 24 || e == 255u)) apart |= 1u << r;      // below 2^-16 when scaled; infinite
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x0 = a[2 * i] * s[0], x1 = a[2 * i + 1] * s[0], y0 = b[2 * i] * s[1], y1 = b[2 * i + 1] * s[1];
-#pragma unroll
-    for (int k = 0; k < (BF16 ? 3 : 2); ++k) {
-      if (!BF16 && k == 1) x0 *= kLow, x1 *= kLow, y0 *= kLow, y1 *= kLow;
-      const uint32_t x = pack2<BF16>(x0, x1), y = pack2<BF16>(y0, y1);
-      const float2 fx = unpack2<BF16>(x), fy = unpack2<BF16>(y);
-      x0 -= fx.x, x1 -= fx.y, y0 -= fy.x, y1 -= fy.y;
-      p[k][i >> 1][2 * (i & 1)] = x;
-      p[k][i >> 1][2 * (i & 1) + 1] = y;
-    }
-  }
+  if (BF16 && top > 0x1.fep127f) split_rows<BF16, true>(a, b, s, p);
+  else split_rows<BF16, false>(a, b, s, p);
   return apart;
 }
 
@@ -215,7 +233,11 @@ __device__ __forceinline__ void step32_apart(float (&c)[4], const float (&a)[8],
     for (int k = 0; k < 2; ++k) {
       uint32_t p[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] = to_tf32(x[e]), x[e] -= __uint_as_float(p[e]);
+      for (int e = 0; e < 4; ++e) {
+        const float size = fabsf(x[e]);                  // past tf32's largest value: cut off; infinite: this part is all
+        p[e] = size > 0x1.ffcp127f ? __float_as_uint(x[e]) & 0xffffe000u : to_tf32(x[e]);
+        x[e] = size == INFINITY ? 0.f : x[e] - __uint_as_float(p[e]);
+      }
       mma1688(t, p, f[i].x, f[i].y);
     }
   }

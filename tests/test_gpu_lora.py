@@ -133,6 +133,35 @@ def test_one_large_value_in_front():
             check(run(d, None), d, None)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens", [1, 3, 70])
+def test_infinite_and_largest_activations(tokens, dtype):
+    """An infinite activation gives what the definition gives, an infinity where all products agree; the largest finite
+    ones (beyond what bfloat16 and tf32 round to) count as what they are; other tokens take nothing from either."""
+    q4k.build()
+    r = np.random.default_rng(tokens)
+    d = make(50, [0] * tokens, 1, 16, 512, [67, 40], dtype)
+    for a, b in zip(d["a"], d["b"]):
+        a[:] = (a.abs().clamp(2.0 ** -6, 2.0 ** -2) * 2.0 ** -3).to(dtype)      # positive: A x has x's sign
+        side = torch.from_numpy(np.where(r.random(b.shape[1]) < 0.5, -1.0, 1.0))[None, :, None]
+        b[:] = ((b.abs() + 0.05) * side).to(dtype)                              # of one sign in a row: so have its terms
+    value = {0: np.inf, 1: -np.inf, 2: float(np.finfo(np.float32).max), 3: float.fromhex("-0x1.fffep127")}
+    for t in range(tokens):
+        if t % 7 in value:
+            d["x"][t, (97 * t + 5) % 512] = value[t % 7]
+    y = run(d)
+    f = lambda t: t.float().numpy()  # noqa: E731
+    for m in range(2):
+        with np.errstate(invalid="ignore"):
+            want, mag = O.lora_add(f(d["x"]), f(d["a"][m]), f(d["b"][m]), f(d["base"][m]), d["ids"], f(d["scale"]))
+        got = y[m].cpu().double().numpy()
+        assert np.all(np.isinf(want[0])) and not np.any(np.isnan(want))
+        far = np.isinf(want)
+        assert np.array_equal(got[far], want[far])
+        assert np.all(np.abs(got[~far] - want[~far]) <= 1e-5 * mag[~far])
+    assert q4k.q4k_device_error() == 0
+
+
 def test_indices_out_of_range_are_reported():
     q4k.build()
     d = make(43, [0, 0, 1, 1, 2, 2], 3, 16, 512, [70], torch.float16)
