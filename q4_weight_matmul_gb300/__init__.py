@@ -138,7 +138,7 @@ def _native():
         try:
             from . import _calls as module
         except ImportError as e:
-            raise RuntimeError(f"{BINDING_LIB} is not built: run q4_weight_matmul_gb300.build.build()") from e
+            raise RuntimeError(f"{BINDING_LIB} cannot be imported ({e}): run q4_weight_matmul_gb300.build.build()") from e
         module.bind(LIB_PATH)
         _bound = module
     return _bound

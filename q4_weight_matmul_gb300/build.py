@@ -5,7 +5,8 @@ Each ``csrc/*.cu`` file is compiled on its own (in parallel) with
 ``q4_weight_matmul_gb300/libq4k.so`` (CUDA runtime linked statically).
 ``csrc/binding.cpp`` becomes the Python module ``_calls`` beside it (g++,
 against the headers of the torch that imports it).
-A build is skipped when the library is newer than every source file.
+Each is made again only when a source file is newer, the module also when it
+was made for another Python or torch.
 
     python -m q4_weight_matmul_gb300.build [--force] [--verbose]
 """
@@ -29,6 +30,7 @@ PEAKS_SRC = os.path.join(CSRC, "peaks", "peaks.cu")
 PEAKS_LIB = os.path.join(PKG, "libq4k_peaks.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 BINDING_LIB = os.path.join(PKG, "_calls.so")
+BINDING_STAMP = os.path.join(BUILD_DIR, "calls_made_for.txt")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
@@ -46,14 +48,31 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _stale() -> bool:
-    made = (LIB_PATH, PEAKS_LIB, BINDING_LIB)
+def _older(made, deps) -> bool:
     if not all(map(os.path.exists, made)):
         return True
     t = min(map(os.path.getmtime, made))
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
-        + glob.glob(os.path.join(INCLUDE, "*.h")) + [PEAKS_SRC, BINDING_SRC, os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def _stale_lib() -> bool:
+    return _older((LIB_PATH, PEAKS_LIB),
+                  sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(INCLUDE, "*.h")) + [PEAKS_SRC, os.path.abspath(__file__)])
+
+
+def _made_for() -> str:
+    """The Python and the torch that the binding's module is compiled against."""
+    import torch
+    return f"python {sys.version}\ntorch {torch.__version__} in {os.path.dirname(torch.__file__)}\n"
+
+
+def _stale_binding() -> bool:
+    if _older((BINDING_LIB, BINDING_STAMP),
+              glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC, os.path.abspath(__file__)]):
+        return True
+    with open(BINDING_STAMP) as f:
+        return f.read() != _made_for()
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -71,7 +90,7 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_binding() -> str:
+def _compile_binding() -> None:
     import torch
     at = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
@@ -85,20 +104,26 @@ def _compile_binding() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"compiling {os.path.basename(BINDING_SRC)} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING_LIB)
-    return BINDING_LIB
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_made_for())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA source and link libq4k.so (and the benchmark's
-    tensor-rate probe, libq4k_peaks.so); return the library's path."""
-    if not force and not _stale():
+    tensor-rate probe, libq4k_peaks.so), and the binding's module; return the
+    library's path."""
+    lib, binding = force or _stale_lib(), force or _stale_binding()
+    if not lib and not binding:
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sources() + [PEAKS_SRC]
+    srcs = sources() + [PEAKS_SRC] if lib else []
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        binding = ex.submit(_compile_binding)
+        made = ex.submit(_compile_binding) if binding else None
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding.result()
+        if made:
+            made.result()
+    if not lib:
+        return LIB_PATH
     for path, members in ((LIB_PATH, objs[:-1]), (PEAKS_LIB, objs[-1:])):
         tmp = path + ".tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *members]
