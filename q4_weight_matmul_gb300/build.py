@@ -13,6 +13,7 @@ was made for another Python or torch.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import fcntl
 import glob
 import os
 import shutil
@@ -112,10 +113,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
     """Compile every CUDA source and link libq4k.so (and the benchmark's
     tensor-rate probe, libq4k_peaks.so), and the binding's module; return the
     library's path."""
-    lib, binding = force or _stale_lib(), force or _stale_binding()
-    if not lib and not binding:
+    def stale():
+        return force or _stale_lib(), force or _stale_binding()
+
+    if not any(stale()):
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
+    # one process at a time: the others wait, and find what it made
+    with open(os.path.join(BUILD_DIR, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)
+        _make(*stale(), verbose)
+    return LIB_PATH
+
+
+def _make(lib: bool, binding: bool, verbose: bool) -> None:
     srcs = sources() + [PEAKS_SRC] if lib else []
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         made = ex.submit(_compile_binding) if binding else None
@@ -123,7 +134,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if made:
             made.result()
     if not lib:
-        return LIB_PATH
+        return
     for path, members in ((LIB_PATH, objs[:-1]), (PEAKS_LIB, objs[-1:])):
         tmp = path + ".tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *members]
@@ -131,7 +142,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link of {os.path.basename(path)} failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, path)
-    return LIB_PATH
 
 
 if __name__ == "__main__":

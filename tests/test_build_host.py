@@ -59,3 +59,15 @@ def test_a_binding_that_cannot_be_imported_says_why(tree):
     code = ("import q4_weight_matmul_gb300 as q\nq.lib = lambda: None\ntry:\n    q._native()\nexcept RuntimeError as e:\n"
             "    assert '_calls.so' in str(e) and str(e.__cause__) in str(e), e\nelse:\n    raise SystemExit(1)")
     assert run(code) == []
+
+
+def test_builds_at_the_same_time_do_not_write_the_same_files(tree):
+    at, log, start, run = tree
+    builds = [start() for _ in range(3)]
+    for p in builds:
+        out = p.communicate(timeout=300)[0]
+        assert p.returncode == 0, out
+    made = [line for line in log.read_text().split()]
+    assert len(made) == len(set(made)) and not list((at / "q4_weight_matmul_gb300").rglob("*.busy"))
+    log.write_text("")
+    assert run() == []
