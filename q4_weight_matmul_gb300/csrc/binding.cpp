@@ -64,6 +64,12 @@ double number(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused{};
+  return v != 0;
+}
+
 // A stream argument: None (torch's current one), an object with cuda_stream, or a handle.
 void* stream_of(PyObject* o) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
@@ -122,7 +128,7 @@ int qk_norm_rope(PyObject* const* a) {
       pointer<const float>(a[2], at::kFloat, nk, "v"), tokens, (int)heads, &c.c,
       a[8] == Py_None ? nullptr : pointer<const float>(a[8], at::kFloat, dim, "q_weight"),
       a[9] == Py_None ? nullptr : pointer<const float>(a[9], at::kFloat, dim, "k_weight"), (float)number(a[10]), cos_sin,
-      max_pos, (int)rot, PyObject_IsTrue(a[11]) == 1,
+      max_pos, (int)rot, truth(a[11]),
       rot ? pointer<const int32_t>(a[5], at::kInt, tokens, "pos") : nullptr,
       pointer<const int32_t>(a[6], at::kInt, tokens, "slot"), address(a[12], c.type, nq, "q_out"), stream_of(a[13]));
 }

@@ -202,3 +202,19 @@ def test_binding_refuses():
                      (dict(cs=c["cs"][:, :100].contiguous()), q4k.Q4KError)):
         with pytest.raises(err):
             call(**bad)
+
+
+def test_an_argument_without_a_truth_value_is_refused():
+    """Its own exception comes out, before any launch."""
+    class Neither:
+        def __bool__(self):
+            raise ZeroDivisionError("neither")
+
+    q4k.build()
+    d, rot = make(12, 4, 4, 2, 128, 16, torch.float16)
+    fill = torch.full((4, 4, 128), 7.0, dtype=torch.float16, device="cuda")
+    with pytest.raises(ZeroDivisionError):
+        run(d, rot, interleaved=Neither(), q_out=fill)
+    with pytest.raises(RuntimeError):                                        # of more values than one: torch's own
+        run(d, rot, interleaved=torch.ones(2), q_out=fill)
+    assert torch.all(fill == 7)
