@@ -32,6 +32,12 @@
 // after a row's first tiles, and P, lifted by 2^8, stays below binary16's
 // largest value and above its subnormals down to 2^-22 of the largest weight.
 //
+// The tensor core's running sum O truncates at every product, some 2^-23 of
+// itself a time and always the same way (the mean of 2^28 keys' values came out
+// 1.2 % low; 131072 keys cost as much as binary16's rounding).  So after 256
+// units (1024 products: 2^-13) O is added to sums in the workspace, in fp32,
+// and starts again from zero.
+//
 // Measured (8 key heads of 128, groups of 4): chunks of 2048 and 1705 tokens
 // over 16384 and 16086 keys 701 us with pages of 16, 1340 TFLOP/s (70 % of the
 // bf16 rate); 512 tokens over 4096 keys 50 us.  About 1600 cycles per 64 keys:
@@ -53,6 +59,7 @@ constexpr int kChunkRows = 256;
 constexpr int kChunkKeys = 64;
 constexpr int kChunkThreads = 512;
 constexpr float kChunkLift = 8.0f, kChunkGrow = 6.0f;
+constexpr int kChunkFold = 256;         // units after which O starts again from zero
 
 template <int D>
 struct ChunkLayout {
@@ -125,6 +132,20 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// o += g times the four sums at `at`, where g is not 0; `store`: kept there again.
+__device__ __forceinline__ void add_held(float* at, uint32_t* o, float g, bool store) {
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(o[e]);
+  if (g != 0.f) {
+    const float4 was = __ldcg(reinterpret_cast<const float4*>(at));
+    v[0] = fmaf(g, was.x, v[0]), v[1] = fmaf(g, was.y, v[1]), v[2] = fmaf(g, was.z, v[2]), v[3] = fmaf(g, was.w, v[3]);
+  }
+  if (store) __stcg(reinterpret_cast<float4*>(at), make_float4(v[0], v[1], v[2], v[3]));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(v[e]);
 }
 
 template <int D, bool BF16>
@@ -340,7 +361,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           tc::fence_after_sync();
           const uint32_t v_at = (ring + (n + 1) % L::kRing * L::kTile) >> 4;
           if (elect()) {
-            mma_f16_ts(o_at(h), s_at(h, b), desc(v_at, C::kNext, C::kGroup), kPV, u > 0);
+            mma_f16_ts(o_at(h), s_at(h, b), desc(v_at, C::kNext, C::kGroup), kPV, u % kChunkFold != 0);
 #pragma unroll
             for (int k = 1; k < kChunkKeys / 16; ++k)
               mma_f16_ts(o_at(h), s_at(h, b) + 8 * k, desc(v_at + (k * 2 * C::kGroup >> 4), C::kNext, C::kGroup), kPV, 1);
@@ -391,74 +412,97 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
       const int halves = rows > 128 ? 2 : 1, r = h * 128 + row, units = w.u1 - w.u0;
       const bool mine = r < rows;
       float m = -INFINITY, l = 0.f;
+      // where the item's piece goes; until then, and for a whole item too, what O held before it started again
+      auto piece = [&] { return pieces + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * piece_floats<kChunkRows, D>(); };
+      float held = -INFINITY;                  // the maximum that those sums are relative to
       const int64_t out_at = mine ? out_row(P, w.s, w.head, group, row0 + r) * D : 0;
       if (h < halves) {
         // the keys this row sees, as positions within the item
         const int64_t key0 = (w.lo / kChunkKeys) * kChunkKeys;
         const int64_t pos = w.s.kv - w.s.n + (row0 + r) / group, from = P.window ? pos - P.window + 1 : 0;
         const int hi = mine && pos + 1 > key0 ? (int)(pos + 1 - key0) : 0, lo = from > key0 ? (int)(from - key0) : 0;
-        for (int i = 0; i < units; ++i) {
-          const int b = i & 1;
-          const uint32_t use = (b ? uses1 : uses0) + (i >> 1);
-          wait(&s_full[2 * h + b], use);
-          tc::fence_after_sync();
-          uint32_t s[kChunkKeys];
-#pragma unroll
-          for (int k = 0; k < kChunkKeys / 32; ++k)
-            tc::tmem_ld32(s_at(h, b) + lanes + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * k));
-          tc::tmem_wait_ld();
-          const int at = (w.u0 + i) * kChunkKeys;
-          if (lo > at || hi < at + kChunkKeys) {
-            const int x = lo - at, y = hi - at;
-#pragma unroll
-            for (int k = 0; k < kChunkKeys; ++k) s[k] = k >= x && k < y ? s[k] : 0xff800000u;      // -infinity
-          }
-          float t[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
-#pragma unroll
-          for (int k = 12; k + 1 < kChunkKeys; k += 2) t[(k >> 1) & 3] = max3(__float_as_uint(t[(k >> 1) & 3]), s[k], s[k + 1]);
-          const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;     // c >= 0
-          float f = 1.f;
-          bool grow = false;
-          if (m == -INFINITY) {
-            m = top;                       // nothing seen so far: O and l are zero
-          } else if (top > m + kChunkGrow) {
-            f = ex2(m - top);
-            m = top;
-            grow = true;
-          }
-          l *= f;
-          if (__any_sync(0xffffffffu, grow) && i > 0) {
-            // O holds every unit before this one: wait for the last of their products
-            wait(&pv_done[2 * h + 1 - b], (b ? uses0 : uses1) + ((i - 1) >> 1));
+        for (int begin = 0; begin < units;) {
+          const int end = min(begin + kChunkFold, units);
+          for (int i = begin; i < end; ++i) {
+            const int b = i & 1;
+            const uint32_t use = (b ? uses1 : uses0) + (i >> 1);
+            wait(&s_full[2 * h + b], use);
             tc::fence_after_sync();
-#pragma unroll 1
-            for (int k = 0; k < D / 16; ++k) {
-              uint32_t o[16];
-              tc::tmem_ld16(o_at(h) + lanes + 16 * k, o);
-              tc::tmem_wait_ld();
+            uint32_t s[kChunkKeys];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tc::tmem_st16(o_at(h) + lanes + 16 * k, o);
+            for (int k = 0; k < kChunkKeys / 32; ++k)
+              tc::tmem_ld32(s_at(h, b) + lanes + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * k));
+            tc::tmem_wait_ld();
+            const int at = (w.u0 + i) * kChunkKeys;
+            if (lo > at || hi < at + kChunkKeys) {
+              const int x = lo - at, y = hi - at;
+#pragma unroll
+              for (int k = 0; k < kChunkKeys; ++k) s[k] = k >= x && k < y ? s[k] : 0xff800000u;      // -infinity
+            }
+            float t[4] = {max3(s[0], s[1], s[2]), max3(s[3], s[4], s[5]), max3(s[6], s[7], s[8]), max3(s[9], s[10], s[11])};
+#pragma unroll
+            for (int k = 12; k + 1 < kChunkKeys; k += 2) t[(k >> 1) & 3] = max3(__float_as_uint(t[(k >> 1) & 3]), s[k], s[k + 1]);
+            const float top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * c;     // c >= 0
+            float f = 1.f;
+            bool grow = false;
+            if (m == -INFINITY) {
+              m = top;                       // nothing seen so far: O and l are zero
+            } else if (top > m + kChunkGrow) {
+              f = ex2(m - top);
+              m = top;
+              grow = true;
+            }
+            l *= f;
+            if (__any_sync(0xffffffffu, grow) && i > begin) {
+              // O holds every unit before this one: wait for the last of their products
+              wait(&pv_done[2 * h + 1 - b], (b ? uses0 : uses1) + ((i - 1) >> 1));
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int k = 0; k < D / 16; ++k) {
+                uint32_t o[16];
+                tc::tmem_ld16(o_at(h) + lanes + 16 * k, o);
+                tc::tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tc::tmem_st16(o_at(h) + lanes + 16 * k, o);
+              }
+            }
+            const float sub = m == -INFINITY ? 0.f : m - kChunkLift;
+            const uint64_t c2 = pair(c, c), sub2 = pair(-sub, -sub);
+            uint64_t add[2] = {0, 0};
+            uint32_t p[kChunkKeys / 2];
+#pragma unroll
+            for (int e = 0; e < kChunkKeys / 2; ++e) {
+              const float2 z = unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, sub2));
+              const float x = ex2(z.x), y = ex2(z.y);
+              add[e & 1] = add2(add[e & 1], pair(x, y));
+              p[e] = pack2<BF16>(x, y);
+            }
+            tc::tmem_st32(s_at(h, b) + lanes, p);
+            const float2 sum = unpair(add2(add[0], add[1]));
+            l += sum.x + sum.y;
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&p_full[2 * h + b]);
+          }
+          begin = end;
+          if (end == units) break;
+          // O up to here, to the sums held
+          wait(&pv_done[2 * h + ((end - 1) & 1)], ((end - 1) & 1 ? uses1 : uses0) + ((end - 1) >> 1));
+          tc::fence_after_sync();
+          const float g = held == -INFINITY ? 0.f : ex2(held - m);
+          held = m;
+#pragma unroll 1
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t o[16];
+            tc::tmem_ld16(o_at(h) + lanes + 16 * k, o);
+            tc::tmem_wait_ld();
+            if (mine) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) add_held(piece() + ((4 * k + e) * kChunkRows + r) * 4, o + 4 * e, g, true);
             }
           }
-          const float sub = m == -INFINITY ? 0.f : m - kChunkLift;
-          const uint64_t c2 = pair(c, c), sub2 = pair(-sub, -sub);
-          uint64_t add[2] = {0, 0};
-          uint32_t p[kChunkKeys / 2];
-#pragma unroll
-          for (int e = 0; e < kChunkKeys / 2; ++e) {
-            const float2 z = unpair(fma2(pair(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), c2, sub2));
-            const float x = ex2(z.x), y = ex2(z.y);
-            add[e & 1] = add2(add[e & 1], pair(x, y));
-            p[e] = pack2<BF16>(x, y);
-          }
-          tc::tmem_st32(s_at(h, b) + lanes, p);
-          const float2 sum = unpair(add2(add[0], add[1]));
-          l += sum.x + sum.y;
-          tc::tmem_wait_st();
-          tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&p_full[2 * h + b]);
         }
       }
       // every score of this item is there, so Q's place is free: the next item's first scores are made while this
@@ -474,6 +518,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
         uses1 += units >> 1;
       }
       const bool whole = w.u0 == 0 && w.u1 == w.units;
+      const float g = held == -INFINITY ? 0.f : ex2(held - m);
       if (whole) {
         if (h < halves) {
           const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -484,6 +529,10 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
             tc::tmem_ld32(o_at(h) + lanes + 32 * i, o);
             tc::tmem_wait_ld();
             if (mine) {
+              if (g != 0.f) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) add_held(piece() + ((8 * i + e) * kChunkRows + r) * 4, o + 4 * e, g, false);
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 uint32_t v[4];
@@ -501,7 +550,6 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
           split->q0 = w.s.q0, split->head = w.head, split->row0 = row0, split->rows = rows;
           split->last_cta = owner(w.at + w.units - 1, R);
         }
-        float* piece = pieces + ((size_t)blockIdx.x * 2 + (w.u0 == 0 ? 1 : 0)) * piece_floats<kChunkRows, D>();
         if (h < halves) {
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
@@ -510,15 +558,13 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
             tc::tmem_wait_ld();
             if (mine) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                __stcg(reinterpret_cast<uint4*>(piece + ((8 * i + e) * kChunkRows + r) * 4),
-                       make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+              for (int e = 0; e < 8; ++e) add_held(piece() + ((8 * i + e) * kChunkRows + r) * 4, o + 4 * e, g, true);
             }
           }
           tc::fence_before_sync();
           if (mine) {
-            __stcg(piece + kChunkRows * D + r, m);
-            __stcg(piece + kChunkRows * D + kChunkRows + r, l);
+            __stcg(piece() + kChunkRows * D + r, m);
+            __stcg(piece() + kChunkRows * D + kChunkRows + r, l);
           }
         }
       }

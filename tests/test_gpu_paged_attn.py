@@ -300,6 +300,40 @@ def test_offsets_past_32_bits(new):
     assert q4k.q4k_device_error() == 0
 
 
+@pytest.mark.parametrize("dim,dtype", [(64, torch.float16), (128, torch.float16), (128, torch.bfloat16)])
+def test_sums_over_very_many_keys(dim, dtype):
+    """2^28 keys, two pages again and again, with values that do not cancel: a sum that loses some 2^-23 of itself in one
+    direction at every step is off by more than the result's rounding then.  The second page's scores are higher by 8; it
+    comes last, near the end, or after a third of the keys, so that what was summed before has to be scaled."""
+    q4k.build()
+    g = torch.Generator().manual_seed(35)
+    pages, new = 2 ** 28 // 256, 20
+    kc, vc = torch.zeros((2, 1, 256, dim), dtype=dtype), (1 + 0.2 * torch.randn((2, 1, 256, dim), generator=g)).to(dtype)
+    kc[:, 0, :, 0] = torch.randn((2, 256), generator=g).to(dtype)
+    kc[1, :, :, 1] = 16.0
+    q = torch.zeros((new, 1, dim), dtype=dtype)
+    q[:, :, :2] = 1.0
+    score = 0.5 * kc[:, 0, :, :2].double().sum(-1)                           # [page][cell]
+    weight, values = score.exp(), vc[:, 0].double()
+    cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    kv = torch.tensor([pages * 256], dtype=torch.int32, device="cuda")
+    q, kc, vc = q.cuda(), kc.cuda(), vc.cuda()
+    for turn in (pages, pages - 1, pages - 150, pages // 3):                 # pages from `turn` on are the second
+        table = (torch.arange(pages, device="cuda") >= turn).to(torch.int32)[None]
+        got = q4k.q4k_paged_attn(q, kc, vc, table, cu, kv, new, scale=0.5, out_dtype=dtype)
+        times = torch.tensor([turn, pages - turn]).double()
+        for i in (0, 7, new - 1):                                            # token i misses the last new - 1 - i cells
+            gone = slice(256 - (new - 1 - i), 256)
+            last = 0 if turn == pages else 1
+            num = (times[:, None] * (weight[:, :, None] * values).sum(1)).sum(0) - (weight[last, gone, None] * values[last, gone]).sum(0)
+            den = (times * weight.sum(1)).sum() - weight[last, gone].sum()
+            want, most = num / den, values.abs().max()
+            tol = U[dtype] * 2 * want.abs() + 1e-5 * most + (2.0 ** -24 if dtype == torch.float16 else 0.0)
+            far = (got[i, 0].cpu().double() - want).abs()
+            assert bool((far <= tol).all()), (turn, i, float((far / tol).max()))
+    assert q4k.q4k_device_error() == 0
+
+
 def test_no_tokens_and_refusals():
     q4k.build()
     d = make(32, [0, 0], [5, 7], 8, 2, 128, 16, torch.float16)
