@@ -434,7 +434,7 @@ paged_attn_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_c
               tc::tmem_ld32(s_at(h, b) + lanes + 32 * k, *reinterpret_cast<uint32_t(*)[32]>(s + 32 * k));
             tc::tmem_wait_ld();
             const int at = (w.u0 + i) * kChunkKeys;
-            if (lo > at || hi < at + kChunkKeys) {
+            if (lo > at || hi - at < kChunkKeys) {
               const int x = lo - at, y = hi - at;
 #pragma unroll
               for (int k = 0; k < kChunkKeys; ++k) s[k] = k >= x && k < y ? s[k] : 0xff800000u;      // -infinity

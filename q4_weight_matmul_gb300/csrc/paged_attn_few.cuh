@@ -185,7 +185,7 @@ struct Rows8 {
         for (int t = 0; t < 2; ++t) mma16816<BF16>(s[t][i], a[i][t], q[k + i][0], q[k + i][1]);
     }
     float top[2] = {m[0], m[1]};
-    const bool inside = at >= lo_all && at + kUnit <= hi_all;
+    const bool inside = at >= lo_all && hi_all - at >= kUnit;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -226,7 +226,7 @@ struct Rows8 {
         for (int i = 0; i < PRODUCTS; ++i)
           p[i][t][h] = transpose8x8(!TWICE ? part[i] : c < 2 ? part[2 * i] : part[2 * i + 1]);
       }
-    const bool edge = at < it.lo || at + kUnit > it.hi;
+    const bool edge = at < it.lo || it.hi - at < kUnit;
     uint32_t keep[2][2];
     if (edge) {
       keep_masks(keep[0], at, c, it);
@@ -338,7 +338,7 @@ struct Rows16 {
 #pragma unroll
       for (int t = 0; t < 4; ++t) mma16816<BF16>(s[t], q[2 * k + 1], b[t][2], b[t][3]);
     }
-    const bool inside = at >= lo_all && at + kUnit <= hi_all;
+    const bool inside = at >= lo_all && hi_all - at >= kUnit;
     float top[2] = {m[0], m[1]}, sub[2], f[2];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -374,7 +374,7 @@ struct Rows16 {
           p[i][t >> 1][(t & 1) * 2 + r] = h;
         }
       }
-    const bool edge = at < it.lo || at + kUnit > it.hi;
+    const bool edge = at < it.lo || it.hi - at < kUnit;
     uint32_t keep[2][2];
     if (edge) {
       keep_masks(keep[0], at, c, it);

@@ -334,6 +334,27 @@ def test_sums_over_very_many_keys(dim, dtype):
     assert q4k.q4k_device_error() == 0
 
 
+@pytest.mark.parametrize("new,out_dtype", [(1, torch.float32), (9, torch.float32), (20, torch.float16)])
+def test_the_longest_context(new, out_dtype):
+    """As many keys as a table of pages of 16 can name: the last unit ends past 2^31.  All keys are one page, scored far
+    below zero, so that a cell past the last one, which reads as zeros, would outweigh them all."""
+    q4k.build()
+    pages = 2 ** 31 // 16 - 1
+    kv = pages * 16
+    kc = torch.full((1, 1, 16, 64), -1.0, dtype=torch.float16, device="cuda")
+    vc = torch.arange(16, dtype=torch.float16, device="cuda")[None, None, :, None].expand(1, 1, 16, 64).contiguous()
+    q = torch.ones((new, 1, 64), dtype=torch.float16, device="cuda")
+    table = torch.zeros((1, pages), dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    got = q4k.q4k_paged_attn(q, kc, vc, table, cu, torch.tensor([kv], dtype=torch.int32, device="cuda"), new, scale=1.0,
+                             out_dtype=out_dtype)
+    assert q4k.q4k_device_error() == 0
+    # equal weights: the mean of 0..15; token i misses the last new - 1 - i cells, nothing beside 2^31.  Sums of 2^31
+    # equal weights in fp32: each lane's are exact up to 2^24 of them, then the lanes' and pieces' are added up
+    tol = 15 * 1e-5 + (2.0 ** -11 * 2 * 7.5 if out_dtype == torch.float16 else 0.0)
+    assert float((got.double() - 7.5).abs().max()) <= tol
+
+
 def test_no_tokens_and_refusals():
     q4k.build()
     d = make(32, [0, 0], [5, 7], 8, 2, 128, 16, torch.float16)
