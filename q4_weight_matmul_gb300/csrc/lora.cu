@@ -14,16 +14,18 @@
 // a power of two, the same for 32 of a row, that puts the largest near 2^14,
 // the second part times 2^11.  So binary16 keeps 22 bits down to 2^-29 of the
 // largest and 20 down to 2^-31; where a value but zero is smaller, the warp
-// makes its sums again with tf32 instructions (22 bits for any value).  Looking
-// for such values costs 5 % of the first launch.  The k index of an
+// makes its sums again with tf32 instructions (22 bits for any value).  That
+// and the second scale cost 7 % (2049 tokens, below: 38.6 us without; 45.7 with
+// tf32 throughout).  A value that rounding to its type would make infinite is
+// cut off instead, and an infinity is its first part alone.  The k index of an
 // instruction is free to permute, so every lane loads 8 consecutive k of its
 // row (16 bytes of an adapter, 32 of x) and feeds them to two instructions
 // without a transpose.  Sums of 32 k start from zero and are added up in fp32
 // registers (the tensor core's own running sum truncates).
 //
-// Measured: 2049 tokens of 4 adapters of rank 32 beside 2560 x 9728: 39 us (3.2
-// TB/s); 64 tokens of 17 adapters of rank 64 beside 2 x 9728 x 2560: 26.6 us; one
-// token beside q, k and v: 6.2 us.
+// Measured, binary16 | bfloat16: 2049 tokens of 4 adapters of rank 32 beside
+// 2560 x 9728: 41.2 | 40.3 us (3.0 TB/s); 64 tokens of 17 adapters of rank 64
+// beside 2 x 9728 x 2560: 25.5 | 26.1 us; one token beside q, k and v: 6.1 | 5.9 us.
 #include "mma_sync.cuh"
 #include "q4k_internal.h"
 #include "tc_ptx.cuh"
@@ -176,16 +178,20 @@ __device__ __forceinline__ void products(float (&c)[NT][4], const uint32_t (&p)[
   for (int q = 0; q < NT; ++q) {
     if (q < tiles) {
       float t[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (BF16) {
 #pragma unroll
-      for (int k = BF16 ? 0 : 1; k < (BF16 ? 3 : 2); ++k) {
-        mma16816<BF16>(t, p[k][0], w[q].x, w[q].y);
-        mma16816<BF16>(t, p[k][1], w[q].z, w[q].w);
-      }
-      if constexpr (!BF16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] *= 1.f / kLow;
+        for (int k = 0; k < 3; ++k) {
+          mma16816<BF16>(t, p[k][0], w[q].x, w[q].y);
+          mma16816<BF16>(t, p[k][1], w[q].z, w[q].w);
+        }
+      } else {
+        float u[4] = {0.f, 0.f, 0.f, 0.f};
         mma16816<BF16>(t, p[0][0], w[q].x, w[q].y);
+        mma16816<BF16>(u, p[1][0], w[q].x, w[q].y);
         mma16816<BF16>(t, p[0][1], w[q].z, w[q].w);
+        mma16816<BF16>(u, p[1][1], w[q].z, w[q].w);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = fmaf(u[e], 1.f / kLow, t[e]);
       }
       c[q][0] = fmaf(t[0], back[0], c[q][0]), c[q][1] = fmaf(t[1], back[0], c[q][1]);
       c[q][2] = fmaf(t[2], back[1], c[q][2]), c[q][3] = fmaf(t[3], back[1], c[q][3]);
@@ -207,9 +213,8 @@ __device__ __forceinline__ uint32_t step32(float (&c)[NT][4], const float4 (&xa)
 }
 
 // Products of binary16 adapters with activations that are too far apart for
-// one scale: tf32 instructions, whose operands have fp32's exponents and hold
-// binary16 exactly (twice as many: 45.7 against 38.6 us for the 2049-token
-// case if all products were made so).
+// one scale: tf32 instructions, twice as many, whose operands have fp32's
+// exponents and hold binary16 exactly.
 __device__ __forceinline__ uint32_t to_tf32(float x) {
   uint32_t r;
   asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
@@ -322,7 +327,11 @@ __device__ __forceinline__ void replace_apart(const LoraParams& P, const Tile& T
 }
 
 // Few tokens: latency counts.  Operands straight into registers, one rank
-// tile per CTA.
+// tile per CTA.  Up to 16 tokens; both sides, us for the whole call, this |
+// the kernel below:
+//   tokens                                 1          4          8           16          32          64
+//   rank 16, (4096 + 2 x 1024) x 2560   6.1 | 7.9  7.7 | 7.9  7.7 | 8.1   7.7 | 8.6   8.8 | 9.6   11.0 | 11.2
+//   rank 64, 2 x 9728 x 2560            8.6 | 9.0             13.2 | 10.8 14.4 | 11.8 15.5 | 13.4 19.9 | 16.8
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) lora_shrink_few_kernel(const __grid_constant__ LoraParams P) {
   __shared__ float part[kWarps][8][kTile + 1];
@@ -767,6 +776,9 @@ cudaError_t launch(const LoraParams& p, cudaStream_t s) {
     lora_shrink_few_kernel<BF16><<<dim3(tiles, parts, p.n * p.rank / 8), kThreads, 0, s>>>(p);
     e = cudaGetLastError();
   } else if (p.n * p.rank <= 32) {
+    // groups of 32 ranks | of 64, us, beside 2560 x 2560: 64 tokens, 8 to 32 ranks 7.5-8.6 | 8.3-9.4; 2048 tokens
+    // 24.0-25.6 | 26.1-27.3; 40, 64, 3 x 16 ranks: 64 tokens 9.2-10.0 | 10.1-11.4, 512 15.0-19.5 | 15.3-19.8, 2048
+    // 36.4-53.1 | 33.1-49.6
     e = shrink<BF16, 4>(p, tiles, parts, s);
   } else {
     e = shrink<BF16, 8>(p, tiles, parts, s);             // x is read once for 64 ranks
