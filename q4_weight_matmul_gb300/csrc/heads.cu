@@ -12,10 +12,10 @@
 // lanes, all of one token, with their loads in flight at once, and reads the
 // token's cosines and sines once for all of them.
 //
-// Measured: 8192 tokens of 32 + 8 + 8 heads of 128, bfloat16: 54.7 us, 5.6
-// TB/s (84 % of the copy rate; two rows' worth of lanes per row, so that the
+// Measured: 8192 tokens of 32 + 8 + 8 heads of 128, bfloat16: 54.2 us, 5.6
+// TB/s (85 % of the copy rate; two rows' worth of lanes per row, so that the
 // pairs of a rotation by halves met across lanes, took 97 us: 67 % of the
-// issue slots).  One token: 3.1 us.
+// issue slots).  One token: 2.7 us.
 #include "q4k_internal.h"
 
 #include <cuda_bf16.h>

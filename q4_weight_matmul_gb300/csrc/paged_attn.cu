@@ -22,12 +22,13 @@ int few_kind(const AttnParams& p, int* rows) {
 // The many-row kernel keeps its weights at 16 bits, so it gives 16-bit
 // results.  It pays 128 rows per half whatever their number, the few-row
 // kernel one pass over the keys' operands per 16 rows.  Few | many rows, us,
-// 8 key heads of 128:
+// 8 key heads of 128, pages of 16:
 //   rows per key head       12            16            32            36            128
-//   1 request,    512 keys  11.3 | 13.2   11.7 | 13.3   13.6 | 14.1   14.5 | 14.2   19.4 | 15.4
-//   1 request,  32768 keys  43.6 | 58.8   44.1 | 53.9   53.6 | 51.5   72.3 | 59.2   120  | 53.3
-//   8 requests,  4096 keys  41.3 | 43.9   42.4 | 43.5   47.6 | 42.6   64.2 | 43.9   114  | 45.5
-//   8 requests, 32768 keys  202  | 205    202  | 205    227  | 188    371  | 195    730  | 179
+//   1 request,    512 keys  11.3 | 12.1   11.7 | 12.2   13.9 | 13.0   15.3 | 12.9   18.6 | 14.1
+//   1 request,  32768 keys  47.6 | 56.6   48.5 | 51.7   58.3 | 49.5   82.4 | 56.2   140  | 52.5
+//   8 requests,  4096 keys  45.5 | 41.6   46.3 | 41.2   52.8 | 40.7   74.4 | 41.9   135  | 43.3
+//   8 requests, 32768 keys  245  | 196    246  | 196    272  | 180    455  | 185    898  | 180
+// (16 rows and fewer keep the weights' bits, whatever the number of requests.)
 bool many_rows(const AttnParams& p) { return !p.out_f32 && p.max_q * (p.heads / p.kv_heads) > 16; }
 
 int cta_count() {

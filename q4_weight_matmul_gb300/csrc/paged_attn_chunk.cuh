@@ -39,12 +39,19 @@
 // and starts again from zero.
 //
 // Measured (8 key heads of 128, groups of 4): chunks of 2048 and 1705 tokens
-// over 16384 and 16086 keys 701 us with pages of 16, 1340 TFLOP/s (70 % of the
-// bf16 rate); 512 tokens over 4096 keys 50 us.  About 1600 cycles per 64 keys:
-// the tensor pipe needs 1280 (S = Q K^T with 64 keys to an instruction is fed
-// by shared memory at two thirds of its rate), the softmax runs beside it
-// (two weights to a packed operation and three values to a maximum: 717 ->
-// 701 us).
+// over 16384 and 16086 keys, pages of 16: 667 us at the full clock, 1410
+// TFLOP/s (74 % of the bf16 rate); back to back 711-735 us, as the GPU's power
+// cap takes the clock from 2070 to some 1830 MHz after a tenth of a second.
+// 512 tokens over 4096 keys 49 us.
+//
+// What bounds it: 667 us are 1850 cycles per 64 keys of 256 rows.  The products
+// take 1024 of them at the tensor pipe's full rate (its counter says 58 %
+// active, the issue slots' 41 %) and 1280 as far as S = Q K^T with 64 keys to
+// an instruction is fed by shared memory at two thirds of that; the softmax
+// runs beside them (two weights to a packed operation and three values to a
+// maximum: 717 -> 701 us).  Where the other 570 cycles go is not known: waits
+// between the roles, or the kernel's spills (384 bytes a thread, of the share
+// of the work and the walk over it).
 #pragma once
 
 #include "paged_attn_common.cuh"

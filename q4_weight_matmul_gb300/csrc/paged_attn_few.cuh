@@ -25,10 +25,14 @@
 // (Rows16) are the M: S = Q K^T, O += P V, 16 to a warp.
 //
 // Measured (8 key heads of 128, groups of 4, fp32 results): 64 requests of up
-// to 8192 keys 217 us, 5.9 TB/s (88 % of the copy rate; 206 us with the
-// products skipped); 131072 keys of one request 94 us; 1021 keys 9.8 us, of
-// which the launch 2, the share of the work 1.5, the first copy 1, a slot 1,
-// putting warps and pieces together 3.
+// to 8192 keys 200 us, 6.4 TB/s (96 % of the copy rate; 218 us while the
+// producer read the shared give-up flag before every copy instead of once a
+// slot); 131072 keys of one request 86 us; 1021 keys 8.9 us, of which the
+// launch 2, the share of the work 1.5, the first copy 1, a slot 1, putting
+// warps and pieces together 3.  The variants for 16, 32 and 64 rows spill some
+// 300 bytes a thread (the share of the work and the walk over it, in 64-bit
+// numbers; the producer's 40 registers), those for up to 8 none; what that
+// costs has not been measured.
 #pragma once
 
 #include "mma_sync.cuh"
@@ -56,7 +60,7 @@ struct FewConfig {
   static constexpr int kWR = KIND < 16 ? 1 : KIND / 16;
   static constexpr int kRows = KIND == 0 ? 4 : KIND == 1 ? 8 : KIND;
   // Consumer warps.  Up to 8 rows a slot is little work: four warps keep up, and leave room for three slots each
-  // (eight with one each read 5.4 TB/s of 64 x 8192 keys, four 5.6).
+  // (eight with one each read 5.4 TB/s of 64 x 8192 keys where four read 5.6).
   static constexpr int kWarps = KIND < 16 ? 4 : 8;
   static constexpr int kThreads = 32 * (kWarps + 4);       // and the producer's warpgroup, of which one warp works
   static constexpr int kGroups = kWarps / kWR;             // slots consumed at once
