@@ -164,8 +164,13 @@ __device__ __forceinline__ uint32_t split(const float (&a)[8], const float (&b)[
       if (e > 30u && (low[r] < (e - 30u) << 24 || e == 255u)) apart |= 1u << r;      // below 2^-16 when scaled; infinite
     }
   }
-  if (BF16 && top > 0x1.fep127f) split_rows<BF16, true>(a, b, s, p);
-  else split_rows<BF16, false>(a, b, s, p);
+  if constexpr (BF16) {
+    if (top > 0x1.fep127f) split_rows<true, true>(a, b, s, p);       // bfloat16's largest value
+    else split_rows<true, false>(a, b, s, p);
+    __syncwarp();                                                    // the products are the whole warp's
+  } else {
+    split_rows<false, false>(a, b, s, p);
+  }
   return apart;
 }
 

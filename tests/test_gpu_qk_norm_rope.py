@@ -165,6 +165,30 @@ def test_on_another_stream_and_in_a_graph():
     assert torch.equal(out, ref) and torch.equal(kc, rk)
 
 
+def test_stream_argument_while_the_current_stream_is_busy():
+    """The queries that the call makes belong to ``stream``: what the current stream still reads is not written over."""
+    q4k.build()
+    d, rot = make(13, 40, 32, 8, 128, 16, torch.float16)
+    ref, rk, _ = run(d, rot)
+    torch.cuda.synchronize()
+    for by_handle in (False, True):
+        s = torch.cuda.Stream()
+        old = torch.full_like(ref, 3.0)
+        torch.cuda._sleep(20_000_000)                                        # some 10 ms on the current stream
+        kept = old + 1                                                       # reads `old` after that
+        del old
+        c = {k: torch.from_numpy(v).pin_memory() for k, v in d.items() if isinstance(v, np.ndarray)}
+        with torch.cuda.stream(s):
+            c = {k: v.cuda(non_blocking=True) for k, v in c.items()}
+            kc, vc = d["kc"].cuda(), d["vc"].cuda()
+        out = q4k.q4k_qk_norm_rope(c["q"], c["k"], c["v"], kc, vc, c["pos"], c["slot"], c["cs"], c["qw"], c["kw"],
+                                   stream=s.cuda_stream if by_handle else s)
+        s.synchronize()
+        assert torch.equal(out.cpu(), ref.cpu()) and torch.equal(kc.cpu(), rk.cpu())
+        torch.cuda.synchronize()
+        assert torch.all(kept == 4.0)
+
+
 def test_offsets_past_32_bits():
     """A cache of 2^31 + elements: the last page's cells lie past a 32-bit offset."""
     q4k.build()
