@@ -693,6 +693,101 @@ int q4k_lora_add(int n, const q4k_lora_mat* mats, int64_t n_adapters, int rank, 
                  const int32_t* seg_start, const int32_t* seg_adapter, int64_t n_seg,
                  const float* scale, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * A layer with routed experts: the router's choice, and the products of the
+ * experts' quantised matrices over the ragged numbers of tokens that chose
+ * them.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * q4k_moe_plan - which experts the tokens of a step go to (HOST struct of
+ * device arrays, read during the call only; 4-byte alignment).  Pair
+ * p = t * top_k + j is token t's j-th choice.  q4k_moe_route writes all of
+ * it; q4k_moe_gate_up and q4k_moe_down read it.
+ */
+typedef struct q4k_moe_plan {
+  int32_t* expert;            /* [tokens][top_k], the best first; -1: none     */
+  float* weight;              /* [tokens][top_k], 0 where there is none        */
+  int32_t* place;             /* [tokens][top_k]: the pair's position in order;
+                                 -1: no expert; -2: a token behind the last    */
+  int32_t* order;             /* [tokens * top_k]: the pairs grouped by expert,
+                                 ascending in a group; -1 behind the last      */
+  int32_t* offsets;           /* [experts + 1]: expert e's pairs are order[
+                                 offsets[e]] .. order[offsets[e + 1] - 1]      */
+  int64_t tokens;
+  int32_t top_k;              /* 1..32, at most experts                        */
+  int32_t experts;            /* 1..512                                        */
+} q4k_moe_plan;
+
+/*
+ * q4k_moe_workspace_bytes - workspace of the three calls below for layers
+ * with experts of hidden -> width -> hidden (gate and up: width x hidden,
+ * down: hidden x width; 0, 0 for q4k_moe_route alone); it serves fewer tokens too.  0 for an invalid request.  16-byte aligned,
+ * no clearing; calls that share a workspace must not overlap on the GPU.
+ */
+size_t q4k_moe_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t hidden,
+                               int64_t width);
+
+/*
+ * q4k_moe_route - the router's choice from its logits, and the pairs grouped
+ * by expert.  Token t's experts are those with the top_k largest logits; the
+ * lower index comes first where logits are equal; an expert whose logit is
+ * -inf or NaN is never chosen, so a token may have fewer (or none).
+ *   weight[t][j] = scale * exp(l_j - max) / sum exp(l - max),
+ * the sum over the chosen experts (`renormalize`) or over all of the token's
+ * logits (not NaN); logits of +inf share the weight equally.
+ *   logits   : float [tokens][experts]
+ *   n_tokens : int32 on the device, or NULL for `tokens`: tokens from
+ *              *n_tokens on get no experts (expert -1, place -2): the rows
+ *              behind the last request of a padded batch
+ * *n_tokens out of 0..tokens is cut to that and reported by q4k_device_error
+ * (Q4K_ERR_DEVICE_INDEX).  Weights are fp32, within 3e-6 |scale| of the exact value.
+ * Errors: Q4K_ERR_INVALID_ARG, Q4K_ERR_ALIGNMENT.  tokens == 0 enqueues
+ * nothing and leaves the arrays as they are.
+ */
+int q4k_moe_route(const float* logits, const q4k_moe_plan* plan, int renormalize, float scale,
+                  const int32_t* n_tokens, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * q4k_moe_gate_up - the gated first half of every pair's expert:
+ *   h[i] = silu(Wg_e x[t]) * (Wu_e x[t]),   silu(g) = g / (1 + exp(-g)),
+ * for i < offsets[experts], e the expert whose pairs position i lies among,
+ * t = order[i] / top_k; the rows of h from offsets[experts] on are left as
+ * they are.
+ *   gate, up : Q4_K (BLOCK144), [experts][rows][cols/256] superblocks
+ *   x        : float [tokens][cols]
+ *   h        : float [tokens * top_k][rows]
+ * Both products are within the bound at the top of this header (x held to 22
+ * bits beside the largest value of its row).
+ */
+int q4k_moe_gate_up(const q4k_moe_plan* plan, const void* gate, const void* up, int64_t rows,
+                    int64_t cols, const float* x, float* h, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/*
+ * q4k_moe_down - the second half, and the experts' results put together:
+ *   y[t] = residual[t] + sum_j weight[t][j] * Wd_e h[place[t][j]]
+ * over token t's experts; y[t] = residual[t] (0 without one) for a token that
+ * has none, and left as it is where place[t][0] == -2.
+ *   w        : [experts][rows] rows of `cols` weights, Q4_K (BLOCK144;
+ *              format 0) or Q6_K (Q6K_LAYOUT_GPU; format 1)
+ *   h        : float [tokens * top_k][cols], in the order of the positions
+ *   residual : float [tokens][rows] or NULL; may be y
+ *   y        : float [tokens][rows]
+ * Accuracy: |y - exact| <= 1e-4 * (|residual| + sum_j |weight_j| (M_j +
+ * 2^-16 max|h_j| W1)) with M_j as at the top of this header and W1 the same
+ * sum for activations of 1.
+ * In both calls offsets out of range or descending are cut, an order or place
+ * out of range is skipped (its row counts as zeros), and each is reported by
+ * q4k_device_error (Q4K_ERR_DEVICE_INDEX).  Deterministic on one device.
+ * Errors: Q4K_ERR_INVALID_ARG, Q4K_ERR_ALIGNMENT, Q4K_ERR_UNSUPPORTED (rows *
+ * experts or tokens * top_k of 2^31 or more).  tokens == 0 or rows == 0
+ * enqueues nothing.
+ */
+int q4k_moe_down(const q4k_moe_plan* plan, const void* w, int format, int64_t rows, int64_t cols,
+                 const float* h, const float* residual, float* y, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
 /*
  * q4k_device_error - synchronise `stream` and read (then clear) the
  * library's device-side error word on the current device.  Returns Q4K_OK,

@@ -1,5 +1,5 @@
 """Python binding of libq4k.so, the GB300 Q4_K weight-matmul library with the
-attention block beside it.
+attention block and routed experts beside it.
 
 Argument marshalling only: every function checks that its torch tensors are
 contiguous CUDA tensors of the expected dtype, passes their device pointers
@@ -13,6 +13,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -49,6 +50,12 @@ class KvCache(ctypes.Structure):
 class LoraMat(ctypes.Structure):
     """``q4k_lora_mat`` of the C ABI (one projection of a ``q4k_lora_add`` call)."""
     _fields_ = [("a", _P), ("b", _P), ("base", _P), ("y", _P), ("rows", _I64)]
+
+
+class MoePlan(ctypes.Structure):
+    """``q4k_moe_plan`` of the C ABI (which experts the tokens of a step go to)."""
+    _fields_ = [("expert", _P), ("weight", _P), ("place", _P), ("order", _P), ("offsets", _P), ("tokens", _I64),
+                ("top_k", ctypes.c_int32), ("experts", ctypes.c_int32)]
 
 
 # Every symbol the header declares, with its ctypes signature.
@@ -91,6 +98,10 @@ SIGNATURES = {
                             ctypes.c_size_t, _P]),
     "q4k_lora_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I64]),
     "q4k_lora_add": (_I, [_I, _P, _I64, _I, _I, _I64, _P, _I64, _P, _P, _P, _I64, _P, _P, ctypes.c_size_t, _P]),
+    "q4k_moe_workspace_bytes": (ctypes.c_size_t, [_I64, _I, _I, _I64, _I64]),
+    "q4k_moe_route": (_I, [_P, _P, _I, ctypes.c_float, _P, _P, ctypes.c_size_t, _P]),
+    "q4k_moe_gate_up": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    "q4k_moe_down": (_I, [_P, _P, _I, _I64, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "q4k_device_error": (_I, [_P]),
     "q4k_selftest_wait_timeout": (_I, [_P]),
     "q4k_status_string": (ctypes.c_char_p, [_I]),
@@ -743,6 +754,103 @@ def q4k_lora_add(x, a, b, base, order, seg_start, seg_adapter, scale, y=None, wo
     return y
 
 
+class MoeRoute(NamedTuple):
+    """Which experts the tokens of a step go to (``q4k_moe_route``).  Pair p =
+    t * top_k + j is token t's j-th choice."""
+    expert: torch.Tensor      # int32 [tokens][top_k], the best first; -1: none
+    weight: torch.Tensor      # float32 [tokens][top_k]
+    place: torch.Tensor       # int32 [tokens][top_k]: the pair's position; -1: no expert, -2: a token behind the last
+    order: torch.Tensor       # int32 [tokens * top_k]: the pairs grouped by expert; -1 behind the last
+    offsets: torch.Tensor     # int32 [experts + 1]: where each expert's pairs start in order
+
+
+def q4k_moe_route_out(tokens: int, top_k: int, experts: int, device="cuda") -> MoeRoute:
+    """Arrays for ``q4k_moe_route`` to write (``out``), for calls that are captured or repeated."""
+    i = lambda *s: torch.empty(s, dtype=torch.int32, device=device)  # noqa: E731
+    return MoeRoute(i(tokens, top_k), torch.empty((tokens, top_k), dtype=torch.float32, device=device),
+                    i(tokens, top_k), i(tokens * top_k), i(experts + 1))
+
+
+def q4k_moe_workspace_bytes(tokens: int, top_k: int, experts: int, hidden: int = 0, width: int = 0) -> int:
+    """The bytes of ``q4k_moe_workspace``."""
+    return int(lib().q4k_moe_workspace_bytes(tokens, top_k, experts, hidden, width))
+
+
+def q4k_moe_workspace(tokens: int, top_k: int, experts: int, hidden: int = 0, width: int = 0, device="cuda"):
+    """A workspace for ``q4k_moe_route``, ``q4k_moe_gate_up`` (``hidden`` columns,
+    ``width`` rows) and ``q4k_moe_down`` (``width`` columns, ``hidden`` rows) of
+    up to so many tokens; hidden and width may be left out for the first alone."""
+    need = q4k_moe_workspace_bytes(tokens, top_k, experts, hidden, width)
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+
+
+def q4k_moe_route(logits, top_k: int, renormalize: bool = True, scale: float = 1.0, n_tokens=None, out=None,
+                  workspace=None, stream=None) -> MoeRoute:
+    """The ``top_k`` experts of each token with the largest ``logits``
+    [tokens][experts] float32, their weights, and the pairs grouped by expert.
+
+    Weights are ``scale`` * softmax, over the chosen experts (``renormalize``)
+    or over all.  An expert whose logit is -inf or NaN is not chosen.
+    ``n_tokens``: None, or int32 [1] on the device: tokens from there on (the
+    padding of a batch) get none.  ``out``: a ``MoeRoute`` to write."""
+    if out is None:
+        tokens, experts = logits.shape
+        with _stream_scope(stream):
+            out = q4k_moe_route_out(tokens, top_k, experts, logits.device)
+        if stream is not None:
+            for t in out:
+                t.record_stream(torch.cuda.current_stream())
+    elif out.expert.shape[1] != top_k:
+        raise ValueError(f"out holds {out.expert.shape[1]} experts a token, not {top_k}")
+    if workspace is None:
+        with _stream_scope(stream):
+            workspace = q4k_moe_workspace(logits.shape[0], top_k, logits.shape[1], device=logits.device)
+    status = (_bound or _native()).moe_route(logits, *out, renormalize, scale, n_tokens, workspace, stream)
+    if status:
+        raise Q4KError(status, "q4k_moe_route")
+    return out
+
+
+def q4k_moe_gate_up(x, gate, up, rows: int, route: MoeRoute, out=None, workspace=None, stream=None):
+    """silu(gate x) * (up x) of every pair of ``route``, for the experts' Q4_K
+    matrices ``gate`` and ``up`` (packed, [experts][rows][cols/256]
+    superblocks) and ``x`` [tokens][cols] float32.  Returns ``out`` [tokens *
+    top_k][rows] float32 in the order of the positions; rows behind the last
+    pair are left as they are."""
+    tokens, top_k = route.expert.shape
+    if out is None:
+        out = _made_on(stream, lambda: torch.empty((tokens * top_k, rows), dtype=torch.float32, device=x.device))
+    if workspace is None:
+        with _stream_scope(stream):
+            workspace = q4k_moe_workspace(tokens, top_k, route.offsets.numel() - 1, x.shape[1], rows, x.device)
+    status = (_bound or _native()).moe_gate_up(x, gate, up, *route, rows, out, workspace, stream)
+    if status:
+        raise Q4KError(status, "q4k_moe_gate_up")
+    return out
+
+
+def q4k_moe_down(h, w, rows: int, route: MoeRoute, residual=None, q6k: bool = False, out=None, workspace=None,
+                 stream=None):
+    """Each token's weighted sum of its experts' down projections:
+    ``out[t] = residual[t] + sum_j weight[t][j] * W_e h[place[t][j]]``.
+
+    ``h`` [tokens * top_k][cols] float32 (``q4k_moe_gate_up``); ``w``: the
+    experts' matrices, packed Q4_K, or with ``q6k`` Q6_K in the GPU layout, an
+    expert's ``rows`` after the other's; ``residual`` [tokens][rows] float32 or
+    None (it may be ``out``).  Rows of tokens behind the last (place -2) are
+    left as they are."""
+    tokens, top_k = route.expert.shape
+    if out is None:
+        out = _made_on(stream, lambda: torch.empty((tokens, rows), dtype=torch.float32, device=h.device))
+    if workspace is None:
+        with _stream_scope(stream):
+            workspace = q4k_moe_workspace(tokens, top_k, route.offsets.numel() - 1, rows, h.shape[1], h.device)
+    status = (_bound or _native()).moe_down(h, w, q6k, *route, rows, residual, out, workspace, stream)
+    if status:
+        raise Q4KError(status, "q4k_moe_down")
+    return out
+
+
 def q4k_device_error(stream=None) -> int:
     """Synchronise ``stream`` and return (and clear) the device error status."""
     return int(lib().q4k_device_error(_stream(stream)))
@@ -765,5 +873,7 @@ __all__ = ["build", "lib", "Q4KError", "BLOCK144", "LAYOUT_GPU", "q4k_packed_byt
            "q4k_gemm_blockdots", "q4k_device_error",
            "KvCache", "LoraMat", "q4k_qk_norm_rope", "q4k_paged_attn_workspace_bytes", "q4k_paged_attn_workspace",
            "q4k_paged_attn", "q4k_lora_segments", "q4k_lora_workspace_bytes", "q4k_lora_workspace", "q4k_lora_add",
+           "MoePlan", "MoeRoute", "q4k_moe_route_out", "q4k_moe_workspace_bytes", "q4k_moe_workspace", "q4k_moe_route",
+           "q4k_moe_gate_up", "q4k_moe_down",
            "q4k_selftest_wait_timeout", "q4k_version",
            "SIGNATURES"]

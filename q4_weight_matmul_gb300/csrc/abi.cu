@@ -805,6 +805,95 @@ int q4k_lora_add(int n, const q4k_lora_mat* mats, int64_t n_adapters, int rank, 
   return e == cudaSuccess ? Q4K_OK : record_cuda(e);
 }
 
+static int check_moe(int64_t tokens, int top_k, int experts) {
+  if (tokens < 0 || tokens > kMaxTokens || experts < 1 || experts > kMoeMaxExperts || top_k < 1 ||
+      top_k > kMoeMaxTopK || top_k > experts)
+    return Q4K_ERR_INVALID_ARG;
+  return tokens * top_k >= (int64_t(1) << 31) ? Q4K_ERR_UNSUPPORTED : Q4K_OK;
+}
+
+static int check_moe_plan(const q4k_moe_plan* plan, MoePlan* p) {
+  if (!plan) return Q4K_ERR_INVALID_ARG;
+  if (int e = check_moe(plan->tokens, plan->top_k, plan->experts)) return e;
+  if (plan->tokens) {
+    if (!plan->expert || !plan->weight || !plan->place || !plan->order || !plan->offsets) return Q4K_ERR_INVALID_ARG;
+    for (const void* a : {(const void*)plan->expert, (const void*)plan->weight, (const void*)plan->place,
+                          (const void*)plan->order, (const void*)plan->offsets})
+      if (!aligned4(a)) return Q4K_ERR_ALIGNMENT;
+  }
+  *p = {plan->expert, plan->place, plan->order, plan->offsets, plan->weight, plan->tokens, plan->top_k, plan->experts};
+  return Q4K_OK;
+}
+
+static int check_moe_matrix(int experts, int64_t rows, int64_t cols) {
+  if (int e = check_rows(rows)) return e;
+  if (int e = check_cols(cols)) return e;
+  return rows * experts >= (int64_t(1) << 31) - 1024 ? Q4K_ERR_UNSUPPORTED : Q4K_OK;
+}
+
+size_t q4k_moe_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t hidden, int64_t width) {
+  if (check_moe(tokens, top_k, experts) || check_rows(hidden) || check_rows(width)) return 0;
+  size_t need = std::max<size_t>(16, moe_route_workspace(tokens, experts));
+  if (hidden && width) {
+    if (hidden % kQK == 0) need = std::max(need, moe_gate_up_workspace(tokens, top_k, experts, width, hidden));
+    if (width % kQK == 0) need = std::max(need, moe_down_workspace(tokens, top_k, experts, hidden, width));
+  }
+  return need;
+}
+
+int q4k_moe_route(const float* logits, const q4k_moe_plan* plan, int renormalize, float scale,
+                  const int32_t* n_tokens, void* workspace, size_t workspace_bytes, void* stream) {
+  MoePlan p{};
+  if (int e = check_moe_plan(plan, &p)) return e;
+  if (!(scale > -3.0e38f && scale < 3.0e38f)) return Q4K_ERR_INVALID_ARG;
+  if (p.tokens == 0) return Q4K_OK;
+  if (!logits || !workspace) return Q4K_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(workspace) || !aligned4(n_tokens)) return Q4K_ERR_ALIGNMENT;
+  if (workspace_bytes < moe_route_workspace(p.tokens, p.experts)) return Q4K_ERR_INVALID_ARG;
+  int* err = device_error_word();
+  if (!err) return record_cuda(cudaGetLastError());
+  cudaError_t e = launch_moe_route(p, logits, n_tokens, renormalize != 0, scale, workspace, err,
+                                   static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? Q4K_OK : record_cuda(e);
+}
+
+int q4k_moe_gate_up(const q4k_moe_plan* plan, const void* gate, const void* up, int64_t rows, int64_t cols,
+                    const float* x, float* h, void* workspace, size_t workspace_bytes, void* stream) {
+  MoeProduct p{};
+  if (int e = check_moe_plan(plan, &p.plan)) return e;
+  if (int e = check_moe_matrix(p.plan.experts, rows, cols)) return e;
+  if (p.plan.tokens == 0 || rows == 0) return Q4K_OK;
+  if (!gate || !up || !x || !h || !workspace) return Q4K_ERR_INVALID_ARG;
+  for (const void* a : {gate, up, (const void*)x, (const void*)h, (const void*)workspace})
+    if (!aligned16(a)) return Q4K_ERR_ALIGNMENT;
+  if (workspace_bytes < moe_gate_up_workspace(p.plan.tokens, p.plan.top_k, p.plan.experts, rows, cols))
+    return Q4K_ERR_INVALID_ARG;
+  p.w = static_cast<const uint8_t*>(gate), p.up = static_cast<const uint8_t*>(up);
+  p.x = x, p.out = h, p.workspace = workspace, p.rows = rows, p.cols = cols;
+  if (!(p.err = device_error_word())) return record_cuda(cudaGetLastError());
+  cudaError_t e = launch_moe_gate_up(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? Q4K_OK : record_cuda(e);
+}
+
+int q4k_moe_down(const q4k_moe_plan* plan, const void* w, int format, int64_t rows, int64_t cols, const float* h,
+                 const float* residual, float* y, void* workspace, size_t workspace_bytes, void* stream) {
+  MoeProduct p{};
+  if (int e = check_moe_plan(plan, &p.plan)) return e;
+  if (int e = check_moe_matrix(p.plan.experts, rows, cols)) return e;
+  if (format != 0 && format != 1) return Q4K_ERR_INVALID_ARG;
+  if (p.plan.tokens == 0 || rows == 0) return Q4K_OK;
+  if (!w || !h || !y || !workspace) return Q4K_ERR_INVALID_ARG;
+  for (const void* a : {w, (const void*)h, (const void*)residual, (const void*)y, (const void*)workspace})
+    if (!aligned16(a)) return Q4K_ERR_ALIGNMENT;
+  if (workspace_bytes < moe_down_workspace(p.plan.tokens, p.plan.top_k, p.plan.experts, rows, cols))
+    return Q4K_ERR_INVALID_ARG;
+  p.w = static_cast<const uint8_t*>(w), p.x = h, p.residual = residual, p.out = y;
+  p.workspace = workspace, p.rows = rows, p.cols = cols, p.q6k = format == 1;
+  if (!(p.err = device_error_word())) return record_cuda(cudaGetLastError());
+  cudaError_t e = launch_moe_down(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? Q4K_OK : record_cuda(e);
+}
+
 int q4k_selftest_wait_timeout(void* stream) {
   int* err = device_error_word();
   if (!err) return record_cuda(cudaGetLastError());

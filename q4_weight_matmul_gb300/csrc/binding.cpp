@@ -1,4 +1,4 @@
-// The Python module _calls: the attention block's calls from torch tensors to
+// The Python module _calls: the attention block's and the routed experts' calls from torch tensors to
 // the C ABI (include/q4k.h).  Checking ten tensors and passing twenty
 // arguments took some 6 us of interpreted code, twice the kernel of a single
 // token's heads; here it takes a few hundred nanoseconds.  Every function
@@ -19,6 +19,9 @@ namespace {
 decltype(&q4k_qk_norm_rope) g_qk_norm_rope;
 decltype(&q4k_paged_attn) g_paged_attn;
 decltype(&q4k_lora_add) g_lora_add;
+decltype(&q4k_moe_route) g_moe_route;
+decltype(&q4k_moe_gate_up) g_moe_gate_up;
+decltype(&q4k_moe_down) g_moe_down;
 
 struct Refused {};      // a Python exception is set
 
@@ -197,6 +200,69 @@ int lora_add(PyObject* const* a) {
                     address(work, at::kByte, work.numel(), "workspace"), (size_t)work.numel(), stream_of(a[10]));
 }
 
+// (expert, weight, place, order, offsets)
+q4k_moe_plan plan_of(PyObject* const* a) {
+  const at::Tensor &expert = tensor(a[0], "route.expert"), &offsets = tensor(a[4], "route.offsets");
+  if (expert.dim() != 2) refuse(PyExc_ValueError, "%s must be [tokens][top_k]", "route.expert");
+  const int64_t pairs = expert.numel(), n = offsets.numel();
+  q4k_moe_plan p{};
+  p.expert = static_cast<int32_t*>(address(expert, at::kInt, pairs, "route.expert"));
+  p.weight = pointer<float>(a[1], at::kFloat, pairs, "route.weight");
+  p.place = pointer<int32_t>(a[2], at::kInt, pairs, "route.place");
+  p.order = pointer<int32_t>(a[3], at::kInt, pairs, "route.order");
+  p.offsets = static_cast<int32_t*>(address(offsets, at::kInt, n, "route.offsets"));
+  p.tokens = expert.size(0);
+  p.top_k = (int32_t)std::min<int64_t>(expert.size(1), INT32_MAX);
+  p.experts = (int32_t)std::min<int64_t>(n - 1, INT32_MAX);
+  return p;
+}
+
+const float* floats_or_null(PyObject* o, int64_t n, const char* name) {
+  return o == Py_None ? nullptr : pointer<const float>(o, at::kFloat, n, name);
+}
+
+// (logits, expert, weight, place, order, offsets, renormalize, scale, n_tokens, workspace, stream)
+int moe_route(PyObject* const* a) {
+  const q4k_moe_plan p = plan_of(a + 1);
+  const at::Tensor &logits = tensor(a[0], "logits"), &work = tensor(a[9], "workspace");
+  if (logits.dim() != 2 || logits.size(0) != p.tokens || logits.size(1) != p.experts)
+    refuse(PyExc_ValueError, "%s must be [tokens][experts], as many as the route's arrays hold", "logits");
+  const bool renormalize = truth(a[6]);
+  return g_moe_route(static_cast<const float*>(address(logits, at::kFloat, logits.numel(), "logits")), &p, renormalize,
+                     (float)number(a[7]), a[8] == Py_None ? nullptr : pointer<const int32_t>(a[8], at::kInt, 1, "n_tokens"),
+                     address(work, at::kByte, work.numel(), "workspace"), (size_t)work.numel(), stream_of(a[10]));
+}
+
+// (x, gate, up, expert, weight, place, order, offsets, rows, h, workspace, stream)
+int moe_gate_up(PyObject* const* a) {
+  const q4k_moe_plan p = plan_of(a + 3);
+  const at::Tensor &x = tensor(a[0], "x"), &work = tensor(a[10], "workspace");
+  if (x.dim() != 2 || x.size(0) != p.tokens) refuse(PyExc_ValueError, "%s must be [tokens][cols]", "x");
+  const int64_t rows = integer(a[8]), cols = x.size(1), pairs = p.tokens * p.top_k;
+  if (rows < 0 || rows > (int64_t(1) << 24) || cols > (int64_t(1) << 24)) return Q4K_ERR_INVALID_ARG;
+  const int64_t bytes = rows * p.experts * (cols / 256) * 144;
+  return g_moe_gate_up(&p, address(a[1], at::kByte, bytes, "gate"), address(a[2], at::kByte, bytes, "up"), rows, cols,
+                       static_cast<const float*>(address(x, at::kFloat, x.numel(), "x")),
+                       pointer<float>(a[9], at::kFloat, pairs * rows, "out"),
+                       address(work, at::kByte, work.numel(), "workspace"), (size_t)work.numel(), stream_of(a[11]));
+}
+
+// (h, w, q6k, expert, weight, place, order, offsets, rows, residual, y, workspace, stream)
+int moe_down(PyObject* const* a) {
+  const q4k_moe_plan p = plan_of(a + 3);
+  const at::Tensor &h = tensor(a[0], "h"), &work = tensor(a[11], "workspace");
+  if (h.dim() != 2 || h.size(0) != p.tokens * p.top_k)
+    refuse(PyExc_ValueError, "%s must be [tokens * top_k][cols]", "h");
+  const int64_t rows = integer(a[8]), cols = h.size(1);
+  if (rows < 0 || rows > (int64_t(1) << 24) || cols > (int64_t(1) << 24)) return Q4K_ERR_INVALID_ARG;
+  const bool q6k = truth(a[2]);
+  const int64_t nb = cols / 256, bytes = rows * p.experts * (q6k ? (nb * 210 + 15) / 16 * 16 : nb * 144);
+  return g_moe_down(&p, address(a[1], at::kByte, bytes, "w"), q6k, rows, cols,
+                    static_cast<const float*>(address(h, at::kFloat, h.numel(), "h")),
+                    floats_or_null(a[9], p.tokens * rows, "residual"), pointer<float>(a[10], at::kFloat, p.tokens * rows, "out"),
+                    address(work, at::kByte, work.numel(), "workspace"), (size_t)work.numel(), stream_of(a[12]));
+}
+
 template <int (*F)(PyObject* const*), int N>
 PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) return PyErr_Format(PyExc_TypeError, "%d arguments expected, got %zd", N, n);
@@ -219,7 +285,10 @@ PyObject* bind(PyObject*, PyObject* path) {
   g_qk_norm_rope = reinterpret_cast<decltype(g_qk_norm_rope)>(dlsym(lib, "q4k_qk_norm_rope"));
   g_paged_attn = reinterpret_cast<decltype(g_paged_attn)>(dlsym(lib, "q4k_paged_attn"));
   g_lora_add = reinterpret_cast<decltype(g_lora_add)>(dlsym(lib, "q4k_lora_add"));
-  if (!g_qk_norm_rope || !g_paged_attn || !g_lora_add) {
+  g_moe_route = reinterpret_cast<decltype(g_moe_route)>(dlsym(lib, "q4k_moe_route"));
+  g_moe_gate_up = reinterpret_cast<decltype(g_moe_gate_up)>(dlsym(lib, "q4k_moe_gate_up"));
+  g_moe_down = reinterpret_cast<decltype(g_moe_down)>(dlsym(lib, "q4k_moe_down"));
+  if (!g_qk_norm_rope || !g_paged_attn || !g_lora_add || !g_moe_route || !g_moe_gate_up || !g_moe_down) {
     g_qk_norm_rope = nullptr;
     return PyErr_Format(PyExc_RuntimeError, "%s lacks a function", p);
   }
@@ -235,6 +304,9 @@ PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
                          {"qk_norm_rope", fast<qk_norm_rope, 14>(), METH_FASTCALL, nullptr},
                          {"paged_attn", fast<paged_attn, 12>(), METH_FASTCALL, nullptr},
                          {"lora_add", fast<lora_add, 11>(), METH_FASTCALL, nullptr},
+                         {"moe_route", fast<moe_route, 11>(), METH_FASTCALL, nullptr},
+                         {"moe_gate_up", fast<moe_gate_up, 12>(), METH_FASTCALL, nullptr},
+                         {"moe_down", fast<moe_down, 13>(), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -188,6 +188,35 @@ struct LoraParams {
 size_t lora_workspace(int n, int rank, int64_t tokens);
 cudaError_t launch_lora_add(const LoraParams& p, cudaStream_t s);
 
+// A layer with routed experts (q4k_moe_*).
+constexpr int kMoeMaxExperts = 512, kMoeMaxTopK = 32;
+struct MoePlan {
+  int32_t *expert, *place, *order, *offsets;
+  float* weight;
+  int64_t tokens;
+  int top_k, experts;
+};
+size_t moe_route_workspace(int64_t tokens, int experts);
+cudaError_t launch_moe_route(const MoePlan& plan, const float* logits, const int32_t* n_tokens, bool renormalize,
+                             float scale, void* workspace, int* err, cudaStream_t s);
+// Products of the pairs' rows with their experts' matrices: gate and up
+// (`up` set; h = silu(gate x) * (up x), x [tokens][cols]) or down (x
+// [pairs][cols], y [tokens][rows] = residual + the weighted sum).
+struct MoeProduct {
+  MoePlan plan;
+  const uint8_t *w, *up;
+  const float *x, *residual;
+  float* out;
+  void* workspace;
+  int* err;
+  int64_t rows, cols;
+  bool q6k;
+};
+size_t moe_gate_up_workspace(int64_t tokens, int top_k, int experts, int64_t rows, int64_t cols);
+size_t moe_down_workspace(int64_t tokens, int top_k, int experts, int64_t rows, int64_t cols);
+cudaError_t launch_moe_gate_up(const MoeProduct& p, cudaStream_t s);
+cudaError_t launch_moe_down(const MoeProduct& p, cudaStream_t s);
+
 // One-thread kernel whose only (bounded) wait can never complete: after the
 // library's wait limit it records a timeout in `err` and returns.
 cudaError_t launch_wait_timeout_selftest(int* err, cudaStream_t s);
