@@ -1,0 +1,10 @@
+// The products of few rows an expert: an instantiation of its own, so that they compile in parallel.
+#include "moe_few.cuh"
+
+namespace q4k {
+
+cudaError_t launch_moe_few_down_q4(const MoeProduct& p, float* out, cudaStream_t s) {
+  return few::launch_mode<few::kDownQ4>(p, out, s);
+}
+
+}  // namespace q4k

@@ -216,6 +216,10 @@ size_t moe_gate_up_workspace(int64_t tokens, int top_k, int experts, int64_t row
 size_t moe_down_workspace(int64_t tokens, int top_k, int experts, int64_t rows, int64_t cols);
 cudaError_t launch_moe_gate_up(const MoeProduct& p, cudaStream_t s);
 cudaError_t launch_moe_down(const MoeProduct& p, cudaStream_t s);
+// The products alone, [pairs][rows], for few rows an expert (moe_few.cuh).
+cudaError_t launch_moe_few_gate_up(const MoeProduct& p, float* out, cudaStream_t s);
+cudaError_t launch_moe_few_down_q4(const MoeProduct& p, float* out, cudaStream_t s);
+cudaError_t launch_moe_few_down_q6(const MoeProduct& p, float* out, cudaStream_t s);
 
 // One-thread kernel whose only (bounded) wait can never complete: after the
 // library's wait limit it records a timeout in `err` and returns.
