@@ -872,6 +872,7 @@ int q4k_moe_gate_up(const q4k_moe_plan* plan, const void* gate, const void* up, 
   p.x = x, p.out = h, p.workspace = workspace, p.rows = rows, p.cols = cols;
   if (!(p.err = device_error_word())) return record_cuda(cudaGetLastError());
   cudaError_t e = launch_moe_gate_up(p, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return Q4K_ERR_UNSUPPORTED;
   return e == cudaSuccess ? Q4K_OK : record_cuda(e);
 }
 
@@ -891,6 +892,7 @@ int q4k_moe_down(const q4k_moe_plan* plan, const void* w, int format, int64_t ro
   p.workspace = workspace, p.rows = rows, p.cols = cols, p.q6k = format == 1;
   if (!(p.err = device_error_word())) return record_cuda(cudaGetLastError());
   cudaError_t e = launch_moe_down(p, static_cast<cudaStream_t>(stream));
+  if (e == cudaErrorNotSupported) return Q4K_ERR_UNSUPPORTED;
   return e == cudaSuccess ? Q4K_OK : record_cuda(e);
 }
 

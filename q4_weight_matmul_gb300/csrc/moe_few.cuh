@@ -17,26 +17,28 @@
 // Which k an instruction's operands hold is free, so a lane feeds the 4 or 8
 // consecutive bytes that it loads without a transpose.
 //
-// A CTA's warps: 8 consumers, a producer that fills the ring (tensor copies of
-// a stage's weights: kTileRows rows of one superblock, 256-value pieces of the
-// pairs' activations), and kCvt warps that turn a stage's activations into
-// operands in place, in the order in which the consumers' lanes read them.
-// Consumers: 8 / KS warps take 32 rows each of every KS-th superblock (KS = 8
-// where there are few rows of weights in all, so that every SM gets some), and
-// add up their parts at an item's end.  An item is one tile of pairs times
-// kOutRows outputs; CTAs take items in turn, tiles of one expert side by side
-// so that they share the weights in L2.
+// The activations' operands depend on neither the rows nor the matrix, so a
+// first launch makes them once, in the order in which the lanes read them, and
+// the products copy them beside the weights (made in every CTA by warps of its
+// own they held the products up: 64 users x 8 of 128 experts 107 us).
 //
-// Waits are bounded; a warp agrees on a wait's outcome by a vote, and the
-// producer waits for its copies before it leaves.  A warp that skips stages
-// first waits until its stage has been issued (`issued`), since a parity alone
-// could be that of the slot's phase before the last.
+// A CTA's warps: 12 consumers, three that copy weights into the ring (a stage:
+// kTileRows rows of one superblock; 16 bytes a lane, since tensor copies of
+// 144-byte rows take longer than memory: 64 users 79 us) and one that draws
+// the items and copies the pairs' operands.  Consumers: four
+// groups of 32 rows; the three warps of a group take every third superblock
+// and add up their parts at an item's end.  An item is one tile of pairs times
+// kOutRows outputs.  CTAs draw items from a counter, experts with many pairs
+// first, so that the last to end are short; tiles of one expert lie side by
+// side and share the weights in L2.
+//
+// Waits are bounded; a warp agrees on a wait's outcome by a vote, and who
+// copies waits for its copies before it leaves.
 #pragma once
 
 #include "mma_sync.cuh"
 #include "moe.cuh"
 #include "tc_ptx.cuh"
-#include "tmap.h"
 
 #include <algorithm>
 
@@ -45,52 +47,71 @@ namespace few {
 
 enum Mode { kGateUp, kDownQ4, kDownQ6 };
 
-constexpr int kConsumers = 8;
-constexpr int kCvt = 3;                      // 12 warps in all: 168 registers a thread (13: 128)
-constexpr int kThreads = 32 * (kConsumers + 1 + kCvt);
-constexpr int kStep = 576;                   // bytes of an instruction's activations: 32 lanes x 16 bytes, 64 to spare
-constexpr int kSums = 16 * kStep;            // the sub-blocks' sums of a tile of 8 pairs: 32 lanes x 8 bytes
-constexpr int kInv = kSums + 256;            // the powers of two to take off: 8 floats
-constexpr int kTileX = 9600;                 // bytes of a tile's activations (before: 8 rows of 1024)
-constexpr int kMaxSmem = 232448 - 1024;
+constexpr int kGroups = 4, kShares = 3;      // consumer warps: four groups of 32 rows, each shared by three
+constexpr int kConsumers = kGroups * kShares;
+constexpr int kCopiers = 3, kLead = kConsumers + kCopiers;     // warps that copy weights; the one that leads
+constexpr int kThreads = 32 * (kLead + 1);
+constexpr int kTileRows = 32 * kGroups;
+constexpr int kMaxSmem = 232448 - 1024, kHeadBytes = 8064;
+// The operands of 8 pairs and a superblock: 16 instructions x 32 lanes x 16
+// bytes (of up to four pairs: x 8), the sub-blocks' sums of x (32 lanes x 8
+// bytes), the powers of two to take off (8 floats).
+constexpr int kTileX = 16 * 512 + 256 + 32, kHalfX = 16 * 256 + 256 + 32;
+constexpr int kQueue = 4;                    // items on their way from the producer to the consumers
 
-template <int MODE, int NT, int KS>
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+// An arrival on `bar` once this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
+}
+
+template <int MODE, int NT>
 struct Cfg {
   static constexpr bool kUp = MODE == kGateUp, kQ6 = MODE == kDownQ6;
   static constexpr int kPairs = 8 * NT;
-  static constexpr int kGroups = kConsumers / KS;
-  static constexpr int kTileRows = 32 * kGroups;
   static constexpr int kOutRows = kUp ? kTileRows / 2 : kTileRows;
   static constexpr int kSb = kQ6 ? kQ6GpuBytes : kBlockBytes;
   static constexpr int kWeights = kTileRows * kSb;
-  static constexpr int kScales = kQ6 ? kTileRows * 16 : 0;
-  static constexpr int kSlot = kWeights + kScales + NT * kTileX;
-  static constexpr int kPart = kGroups * (KS - 1) * 2 * NT * 4 * 32 * (int)sizeof(float);
-  static constexpr int kFixed = 8192 + kPart;
-  static constexpr int kSlots = (kMaxSmem - kFixed) / kSlot < 16 ? (kMaxSmem - kFixed) / kSlot : 16;
+  static constexpr int kScales = kQ6 ? kTileRows * 4 : 0;            // the rows' d of two superblocks
+  static constexpr int kSlot = (kWeights + kScales + NT * kTileX + 127) / 128 * 128;
+  static constexpr int kValues = 2 * NT * 4;                        // sums of a lane
+  static constexpr int kFixed = kHeadBytes + kGroups * kValues * 32 * (int)sizeof(float);
+  // Where a slot serves one share alone, a warp sees every phase of the slots
+  // it waits for.  Elsewhere it waits first until its stage has been issued: a
+  // parity alone could be that of the slot's phase before the last.
+  static constexpr int kRoom = (kMaxSmem - kFixed) / kSlot;
+  static constexpr int kSlots = kRoom >= 2 * kShares ? kRoom / kShares * kShares : kRoom;
+  static constexpr bool kOwnSlots = kSlots % kShares == 0;
   static constexpr int kSmem = 1024 + kFixed + kSlots * kSlot;
-  static_assert(kSlots >= 3 && kSlot % 128 == 0 && kWeights % 128 == 0);
+  static_assert(kSlots >= 3 && kSlots <= 12 && kWeights % 128 == 0 && kFixed % 128 == 0);
 };
 
 struct Params {
-  CUtensorMap w;              // rows of the experts' superblocks
-  CUtensorMap w2;             // of the up matrices, or the rows' d (Q6_K)
-  const float* x;
-  const int32_t *order, *offsets;
+  const uint8_t *w, *up;      // the experts' matrices, rows of `pitch` bytes
+  const uint8_t* x;           // operands [eighths of tiles][nb][kTileX]
+  const int32_t* offsets;
+  int32_t* counter;
   float* out;
   int* err;
-  int64_t pairs, cols, blocks;   // blocks of kOutRows rows of a matrix
-  int rows, nb, experts, top_k;
+  int64_t pairs, pitch;
+  uint32_t blocks;            // of kOutRows rows of a matrix
+  int rows, nb, experts;
 };
 
-struct Head {                 // at the start of shared memory
-  uint64_t full[16], ready[16], empty[16], part_full[8], part_empty[8];
-  uint32_t mask[16];          // pairs of a stage that have activations
-  uint32_t issued;            // stages whose copies are on their way
-  int gave_up;
-  int off[kMoeMaxExperts + 1], tiles[kMoeMaxExperts + 33];
+struct SplitParams {
+  const float* x;
+  const int32_t *order, *offsets;
+  uint8_t* out;
+  int32_t* counter;
+  int* err;
+  int64_t pairs, cols;
+  int nb, experts, top_k;     // top_k 0: x has a row for every pair
 };
-static_assert(sizeof(Head) <= 8192);
 
 __device__ __forceinline__ bool agreed(bool ok, volatile int* gave_up, int* err) {
   if (__all_sync(~0u, ok)) return true;
@@ -104,6 +125,7 @@ __device__ __forceinline__ bool agreed(bool ok, volatile int* gave_up, int* err)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up, int* err) {
   return agreed(tc::mbar_wait(bar, parity, gave_up), gave_up, err);
 }
+
 // Until stage n has been issued.
 __device__ __forceinline__ bool warp_wait_issued(const uint32_t* issued, uint32_t n, volatile int* gave_up, int* err) {
   bool ok = true;
@@ -116,89 +138,164 @@ __device__ __forceinline__ bool warp_wait_issued(const uint32_t* issued, uint32_
       ok = false;
       break;
     }
+    __nanosleep(40);
   }
   return agreed(ok, gave_up, err);
 }
 
+// Which pairs each expert has, and the tiles of up to `per_tile` of them that
+// they make: experts in `perm`'s order (those with more than 8 pairs, with
+// more than 4, the rest), position i's tiles from first[i] on.
+struct Tiles {
+  int off[kMoeMaxExperts + 1], eighth[kMoeMaxExperts];   // an expert's first pair, its first group of 8 pairs
+  int first[kMoeMaxExperts + 33];
+  uint16_t perm[kMoeMaxExperts];
+  int warps[16];
+};
+struct Head {                 // at the start of shared memory
+  uint64_t full[12], empty[12], part[kGroups][kShares], item_full[kQueue], item_empty[kQueue];
+  int4 item[kQueue];          // expert, block, first pair, pairs; no pairs: the end
+  uint32_t issued;            // stages whose copies are on their way
+  int gave_up;
+  Tiles tiles;
+};
+static_assert(sizeof(Head) <= kHeadBytes);
+
 struct Item {
-  int expert, first, n;       // pairs order[first] .. first + n - 1
-  int64_t block;
+  int expert, block;
+  int first, n;               // pairs order[first] .. first + n - 1
 };
 
-// The table of tiles; one warp.  Offsets are cut to ascending values of 0..pairs.
-__device__ inline void make_tiles(const Params& P, Head& H, int per_tile) {
-  const int lane = threadIdx.x & 31, E = P.experts;
-  int last = 0, run = 0;
-  bool bad = false;
-  for (int e0 = 0; e0 <= E; e0 += 32) {
-    const int e = e0 + lane, raw = e <= E ? P.offsets[e] : 0;
-    int v = raw < 0 ? 0 : raw > P.pairs ? (int)P.pairs : raw;
+// Exclusive sum of `v` over the block's threads before this one (`most`:
+// maximum in place of a sum); every thread gets the whole block's in `all`.
+template <int THREADS, bool MOST>
+__device__ __forceinline__ int scan_block(int v, int* warps, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int u = __shfl_up_sync(~0u, v, o);
-      if (lane >= o) v = max(v, u);
-    }
-    v = max(v, last);
-    if (e <= E) {
-      bad |= v != raw;
-      H.off[e] = v;
-    }
-    last = __shfl_sync(~0u, v, 31);
+  for (int o = 1; o < 32; o *= 2) {
+    const int u = __shfl_up_sync(~0u, s, o);
+    if (lane >= o) s = MOST ? max(s, u) : s + u;
   }
-  __syncwarp();
-  for (int e0 = 0; e0 <= E; e0 += 32) {
-    const int e = e0 + lane, n = e < E ? (H.off[e + 1] - H.off[e] + per_tile - 1) / per_tile : 0;
-    int s = n;
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  int before = 0;
+  all = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int u = __shfl_up_sync(~0u, s, o);
-      if (lane >= o) s += u;
-    }
-    H.tiles[e] = e <= E ? run + s - n : INT32_MAX;
-    run += __shfl_sync(~0u, s, 31);
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const int u = warps[w];
+    if (w < warp) before = MOST ? max(before, u) : before + u;
+    all = MOST ? max(all, u) : all + u;
   }
-  for (int e = (E / 32 + 1) * 32 + lane; e < kMoeMaxExperts + 33; e += 32) H.tiles[e] = INT32_MAX;
-  if (bad && blockIdx.x == 0) atomicOr(P.err, kErrIndex);
+  const int u = __shfl_up_sync(~0u, s, 1);
+  if (lane > 0) before = MOST ? max(before, u) : before + u;
+  __syncthreads();
+  return before;
 }
 
-// Item i; the whole warp.
-__device__ __forceinline__ Item find_item(const Params& P, const Head& H, int64_t i, int per_tile) {
+// The tables; a whole block, each thread for kMoeMaxExperts / THREADS
+// experts.  Offsets are cut to ascending values of 0..pairs.  Returns the
+// number of tiles.
+template <int THREADS, int PER_TILE>
+__device__ __forceinline__ int make_tiles(Tiles& T, const int32_t* offsets, int E, int pairs, int* err) {
+  constexpr int J = kMoeMaxExperts / THREADS;
+  const int e0 = threadIdx.x * J;
+  int raw[J + 1], v[J + 1], all;
+#pragma unroll
+  for (int j = 0; j <= J; ++j) raw[j] = e0 + j <= E ? offsets[e0 + j] : INT32_MAX;
+  for (int i = threadIdx.x; i < kMoeMaxExperts + 33; i += THREADS) T.first[i] = INT32_MAX;
+  int top = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) top = max(top, min(raw[j], pairs));             // beyond E: pairs, past every expert
+  int last = scan_block<THREADS, true>(top, T.warps, all);
+  bool bad = false;
+  int classes = 0, eighths = 0;                                               // three counts of ten bits
+#pragma unroll
+  for (int j = 0; j <= J; ++j) {
+    last = v[j] = max(last, min(raw[j], pairs));
+    bad |= e0 + j <= E && v[j] != raw[j];
+    if (j > 0 && e0 + j <= E) {
+      const int n = v[j] - v[j - 1];
+      eighths += (n + 7) / 8;
+      classes += n > 8 ? 1 : n > 4 ? 1 << 10 : 1 << 20;
+    }
+  }
+  int count;
+  int at = scan_block<THREADS, false>(classes, T.warps, count);
+  eighths = scan_block<THREADS, false>(eighths, T.warps, all);
+  int p0 = at & 1023, p1 = (count & 1023) + (at >> 10 & 1023), p2 = (count & 1023) + (count >> 10 & 1023) + (at >> 20);
+#pragma unroll
+  for (int j = 0; j <= J; ++j) {
+    if (e0 + j <= E && (j < J || e0 + j == kMoeMaxExperts)) T.off[e0 + j] = v[j];
+    if (j < J && e0 + j < E) {
+      const int n = v[j + 1] - v[j];
+      T.eighth[e0 + j] = eighths;
+      eighths += (n + 7) / 8;
+      T.perm[n > 8 ? p0++ : n > 4 ? p1++ : p2++] = (uint16_t)(e0 + j);
+    }
+  }
+  if (bad && blockIdx.x == 0) atomicOr(err, kErrIndex);
+  __syncthreads();
+  int tiles[J], sum = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    tiles[j] = 0;
+    if (e0 + j < E) {
+      const int e = T.perm[e0 + j];
+      tiles[j] = (T.off[e + 1] - T.off[e] + PER_TILE - 1) / PER_TILE;
+    }
+    sum += tiles[j];
+  }
+  int first = scan_block<THREADS, false>(sum, T.warps, all);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    if (e0 + j <= E) T.first[e0 + j] = first;
+    first += tiles[j];
+  }
+  if (E == kMoeMaxExperts && threadIdx.x == 0) T.first[E] = all;
+  __syncthreads();
+  return all;
+}
+
+// Item i of items of `blocks` blocks a tile; the whole warp.
+__device__ __forceinline__ Item find_item(const Tiles& T, uint32_t i, uint32_t blocks, int per_tile) {
   const int lane = threadIdx.x & 31;
-  const int64_t t = i / P.blocks;
-  // the last expert whose first tile is t or before: among every 17th, then among those behind it
-  const int a = __popc(__ballot_sync(~0u, lane * 17 <= P.experts && H.tiles[lane * 17] <= t)) - 1;
-  const int b = __popc(__ballot_sync(~0u, lane < 17 && H.tiles[a * 17 + lane] <= t)) - 1;
-  const int e = a * 17 + b;
-  const int tiles = H.tiles[e + 1] - H.tiles[e];
-  const int64_t in = i - H.tiles[e] * P.blocks;
+  const int t = (int)(i / blocks);
+  // the last position whose first tile is t or before: among every 17th, then among those behind it
+  const int a = __popc(__ballot_sync(~0u, T.first[lane * 17] <= t)) - 1;
+  const int b = __popc(__ballot_sync(~0u, lane < 17 && T.first[a * 17 + lane] <= t)) - 1;
+  const int k = a * 17 + b;
+  const uint32_t tiles = T.first[k + 1] - T.first[k], in = i - T.first[k] * blocks;
   Item r;
-  r.expert = e;
-  r.block = in / tiles;
-  const int k = (int)(in - r.block * tiles);
-  r.first = H.off[e] + k * per_tile;
-  r.n = min(per_tile, H.off[e + 1] - r.first);
+  r.expert = T.perm[k];
+  r.block = (int)(in / tiles);
+  r.first = T.off[r.expert] + (int)(in - r.block * tiles) * per_tile;
+  r.n = min(per_tile, T.off[r.expert + 1] - r.first);
   return r;
 }
 
 // ------------------------------------------------------------- activations
-// A stage's pieces of 256 activations become operands in place; one warp.
-// Two pairs at a time, 16 lanes each; a lane's four consecutive values are one
-// lane's operand of one instruction: (0, 2), (1, 3), hi then lo.
-template <bool Q6>
-__device__ __forceinline__ void convert_tile(uint8_t* tile, uint32_t mask, int lane) {
+// The operands of 8 pairs and a superblock; one warp.  Two pairs at a time, 16
+// lanes each; a lane's four consecutive values are one lane's operand of one
+// instruction: (0, 2), (1, 3), hi then lo.  With up to four pairs (HALF) the
+// hi parts are the columns 0..3 and the lo parts the columns 4..7 of one
+// product.  `row`: lane i's pair's activations, NULL for zeros.  The columns
+// behind the n pairs stay as they are: no result is stored from them.
+template <bool Q6, bool HALF>
+__device__ __forceinline__ void make_operands(uint8_t* tile, const float* row, int n, int lane) {
   const int l = lane & 15, side = lane >> 4;
-  float4 v[4][4];
+  constexpr int kRounds = HALF ? 2 : 4, kSums = HALF ? 16 * 256 : 16 * 512, kInv = kSums + 256;
+  float4 v[kRounds][4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    const int pair = 2 * r + side;
-    const bool have = (mask >> pair) & 1;
+  for (int r = 0; r < kRounds; ++r) {
+    const float* from = reinterpret_cast<const float*>(__shfl_sync(~0u, (unsigned long long)row, 2 * r + side));
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      v[r][j] = have ? *reinterpret_cast<const float4*>(tile + 1024 * pair + 16 * l + 256 * j) : make_float4(0, 0, 0, 0);
+      v[r][j] = from ? reinterpret_cast<const float4*>(from)[l + 16 * j] : make_float4(0, 0, 0, 0);
   }
-  __syncwarp();
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < kRounds; ++r) {
+    if (2 * r >= n) break;
     const int pair = 2 * r + side;
     float top = 0.0f;
 #pragma unroll
@@ -209,7 +306,7 @@ __device__ __forceinline__ void convert_tile(uint8_t* tile, uint32_t mask, int l
     // 2^(141 - E) for the biased exponent E of the largest; 1/s stays a normal float
     const int E = (int)((__float_as_uint(top) >> 23) & 0xFFu), es = top == 0.0f ? 127 : min(253, max(1, 268 - E));
     const float s = __uint_as_float((uint32_t)es << 23);
-    if (l == 0) reinterpret_cast<float*>(tile + kInv)[pair] = __uint_as_float((uint32_t)(254 - es) << 23);
+    if (l < (HALF ? 2 : 1)) reinterpret_cast<float*>(tile + kInv)[pair + 4 * l] = __uint_as_float((uint32_t)(254 - es) << 23);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float x0 = v[r][j].x * s, x1 = v[r][j].y * s, x2 = v[r][j].z * s, x3 = v[r][j].w * s;
@@ -219,7 +316,12 @@ __device__ __forceinline__ void convert_tile(uint8_t* tile, uint32_t mask, int l
       // Q4_K: sub-block 2 j + l / 8, bytes 4 (l % 8) ..: a lane's word l % 2 of the 8 bytes from 8 c on, c = l % 8 / 2
       // Q6_K: group 4 j + l / 4, lane c = l % 4
       const int step = Q6 ? 4 * j + (l >> 2) : 2 * (2 * j + (l >> 3)) + (l & 1), c = Q6 ? l & 3 : (l & 7) >> 1;
-      *reinterpret_cast<uint4*>(tile + step * kStep + 16 * (4 * pair + c)) = make_uint4(h02, h13, l02, l13);
+      if constexpr (HALF) {
+        *reinterpret_cast<uint2*>(tile + step * 256 + 8 * (4 * pair + c)) = make_uint2(h02, h13);
+        *reinterpret_cast<uint2*>(tile + step * 256 + 8 * (4 * pair + 16 + c)) = make_uint2(l02, l13);
+      } else {
+        *reinterpret_cast<uint4*>(tile + step * 512 + 16 * (4 * pair + c)) = make_uint4(h02, h13, l02, l13);
+      }
       if constexpr (!Q6) {
         const float2 e = unpack2<false>(l02), f = unpack2<false>(l13);
         float sum = ((f02.x + f02.y) + (f13.x + f13.y)) + ((e.x + e.y) + (f.x + f.y));
@@ -235,11 +337,56 @@ __device__ __forceinline__ void convert_tile(uint8_t* tile, uint32_t mask, int l
       }
     }
   }
+  if constexpr (HALF && !Q6)
+    if (side) *reinterpret_cast<uint2*>(tile + kSums + 128 + 8 * l) = make_uint2(0, 0);   // columns 4..7
+}
+
+constexpr int kSplitWarps = 4;
+
+// A CTA for each group of 8 pairs, its warps for the superblocks.
+template <bool Q6>
+__global__ void __launch_bounds__(32 * kSplitWarps) moe_few_split_kernel(const SplitParams P, int per_tile) {
+  __shared__ Tiles T;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 32) *P.counter = 0;
+  if ((int)blockIdx.x >= make_tiles<32 * kSplitWarps, 8>(T, P.offsets, P.experts, (int)P.pairs, P.err)) return;
+  const Item it = find_item(T, blockIdx.x, 1, 8);
+  const int k = (it.first - T.off[it.expert]) / per_tile;                    // the tile that the group is part of
+  const bool half = min(per_tile, T.off[it.expert + 1] - T.off[it.expert] - k * per_tile) <= 4;
+  const float* row = nullptr;
+  if (lane < it.n) {
+    int64_t r = it.first + lane;
+    if (P.top_k) {
+      const int p = P.order[r];
+      r = p >= 0 && p < P.pairs ? p / P.top_k : -1;
+      if (r < 0 && warp == 0) atomicOr(P.err, kErrIndex);
+    }
+    if (r >= 0) row = P.x + r * P.cols;
+  }
+  const int64_t eighth = T.eighth[it.expert] + (it.first - T.off[it.expert]) / 8;
+  for (int sb = blockIdx.y * kSplitWarps + warp; sb < P.nb; sb += gridDim.y * kSplitWarps) {
+    uint8_t* tile = P.out + (eighth * P.nb + sb) * kTileX;
+    const float* at = row ? row + sb * kQK : nullptr;
+    if (half) make_operands<Q6, true>(tile, at, it.n, lane);
+    else make_operands<Q6, false>(tile, at, it.n, lane);
+  }
 }
 
 // ----------------------------------------------------------------- products
 // 2^23 + byte i of w as a float, to become that byte times d by one exact FMA
 __device__ __forceinline__ float magic(uint32_t w, int i) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + i)); }
+
+// A lane's activations of one instruction: hi in x, y, lo in z, w (HALF: x, y alone).
+template <bool HALF>
+__device__ __forceinline__ uint4 operand(const uint8_t* x, int step, int lane) {
+  if constexpr (HALF) {
+    const uint2 v = *reinterpret_cast<const uint2*>(x + step * 256 + 8 * lane);
+    return make_uint4(v.x, v.y, 0, 0);
+  } else {
+    return *reinterpret_cast<const uint4*>(x + step * 512 + 16 * lane);
+  }
+}
 
 __device__ __forceinline__ void add_scaled(float (&t)[4], const float (&a)[4], float low, float high) {
   t[0] = fmaf(low, a[0], t[0]), t[1] = fmaf(low, a[1], t[1]);
@@ -250,8 +397,9 @@ __device__ __forceinline__ void add_scaled(float (&t)[4], const float (&a)[4], f
 // first; the second `apart` bytes on) times the stage's activations.  A lane
 // has rows r and r + 8 with r = 2 (g % 4) + g / 4, so that the 8-byte loads of
 // a half-warp (rows 0, 2, 4, 6 x 32 bytes, 144 apart) touch every bank once.
-template <int NT>
+template <int NT, bool HALF>
 __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint8_t* x, int lane, float (&total)[2][NT][4]) {
+  constexpr int kSums = HALF ? 16 * 256 : 16 * 512;
   const int c = lane & 3;
   uint32_t sc[2][2][2];
   float d[2][2], dmin[2][2];
@@ -286,7 +434,7 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-          b[i][n] = *reinterpret_cast<const uint4*>(x + n * kTileX + (2 * s + i) * kStep + 16 * lane);
+          b[i][n] = operand<HALF>(x + n * kTileX, 2 * s + i, lane);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         float acc[NT][4] = {};
@@ -296,8 +444,9 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
           const uint32_t a[4] = {u & bits, v & bits, (u >> 8) & bits, (v >> 8) & bits};
 #pragma unroll
           for (int n = 0; n < NT; ++n) mma16816<false>(acc[n], a, b[i][n].x, b[i][n].y);
+          if constexpr (!HALF)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<false>(acc[n], a, b[i][n].z, b[i][n].w);
+            for (int n = 0; n < NT; ++n) mma16816<false>(acc[n], a, b[i][n].z, b[i][n].w);
         }
         const float d0 = half ? d[t][0] * 0.0625f : d[t][0], d1 = half ? d[t][1] * 0.0625f : d[t][1];
         const float s0 = fmaf(magic(sc[t][0][s >> 2], s & 3), d0, -8388608.0f * d0),
@@ -310,7 +459,7 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const uint2 b = *reinterpret_cast<const uint2*>(x + n * kTileX + kSums + 8 * lane);
-    const float2 inv = *reinterpret_cast<const float2*>(x + n * kTileX + kInv + 8 * c);
+    const float2 inv = *reinterpret_cast<const float2*>(x + n * kTileX + kSums + 256 + 8 * c);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       float acc[4] = {};
@@ -324,13 +473,14 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
 }
 
 // The same of Q6_K superblocks (GPU layout); `dr`: this lane's first row's
-// scale of the superblock, rows 16 bytes apart.  q - 32 is made exactly: the
+// scale of the superblock, rows 4 bytes apart.  q - 32 is made exactly: the
 // nibble and the bit pair (upper bit inverted) under the exponent of 1024 with
 // that bit turned back, minus 1056.  A lane has rows g and g + 8: 4-byte loads
 // of 8 rows 208 bytes apart touch every bank once.
-template <int NT>
+template <int NT, bool HALF>
 __device__ __forceinline__ void stage_q6(const uint8_t* w, const uint8_t* dr, const uint8_t* x, int lane,
                                          float (&total)[2][NT][4]) {
+  constexpr int kSums = HALF ? 16 * 256 : 16 * 512;
   const int c = lane & 3;
   float d[2][2];
   uint4 sc[2][2];
@@ -338,7 +488,7 @@ __device__ __forceinline__ void stage_q6(const uint8_t* w, const uint8_t* dr, co
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      d[t][r] = __half2float(*reinterpret_cast<const __half*>(dr + (16 * t + 8 * r) * 16));
+      d[t][r] = __half2float(*reinterpret_cast<const __half*>(dr + (16 * t + 8 * r) * 4));
       sc[t][r] = *reinterpret_cast<const uint4*>(w + (16 * t + 8 * r) * kQ6GpuBytes);
     }
   float sum[2][NT][4] = {};
@@ -359,7 +509,7 @@ __device__ __forceinline__ void stage_q6(const uint8_t* w, const uint8_t* dr, co
       uint4 b[NT];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        b[n] = *reinterpret_cast<const uint4*>(x + n * kTileX + (4 * ch + f) * kStep + 16 * lane);
+        b[n] = operand<HALF>(x + n * kTileX, 4 * ch + f, lane);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         uint32_t a[4];
@@ -382,7 +532,7 @@ __device__ __forceinline__ void stage_q6(const uint8_t* w, const uint8_t* dr, co
         for (int n = 0; n < NT; ++n) {
           float acc[4] = {};
           mma16816<false>(acc, a, b[n].x, b[n].y);
-          mma16816<false>(acc, a, b[n].z, b[n].w);
+          if constexpr (!HALF) mma16816<false>(acc, a, b[n].z, b[n].w);
           add_scaled(sum[t][n], acc, s0, s1);
         }
       }
@@ -390,7 +540,7 @@ __device__ __forceinline__ void stage_q6(const uint8_t* w, const uint8_t* dr, co
   }
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const float2 inv = *reinterpret_cast<const float2*>(x + n * kTileX + kInv + 8 * c);
+    const float2 inv = *reinterpret_cast<const float2*>(x + n * kTileX + kSums + 256 + 8 * c);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       total[t][n][0] = fmaf(inv.x, sum[t][n][0], total[t][n][0]), total[t][n][1] = fmaf(inv.y, sum[t][n][1], total[t][n][1]);
@@ -400,206 +550,247 @@ __device__ __forceinline__ void stage_q6(const uint8_t* w, const uint8_t* dr, co
 }
 
 // -------------------------------------------------------------------- kernel
-template <int MODE, int NT, int KS>
+// A consumer warp's part of an item of up to 8 N pairs: its superblocks, the
+// sums of its group's warps put together, the results stored.  False: a wait
+// gave up.
+template <class C, int N, bool HALF>
+__device__ __forceinline__ bool consume(const Params& P, Head& H, float* part, const uint8_t* ring, const Item& it,
+                                        uint32_t first, uint32_t turn) {
+  volatile int* gave_up = &H.gave_up;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp % kGroups;
+  // (the stages' shares go on from item to item, so that a slot stays one share's)
+  const int share = warp / kGroups;
+  const int c = lane & 3, r0 = C::kQ6 ? lane >> 2 : 2 * ((lane >> 2) & 3) + (lane >> 4);
+  // the warp's first row in a stage; gate and up: 16 rows of both halves
+  const int base = C::kUp ? 16 * group : 32 * group;
+  float total[2][N][4] = {};
+  for (uint32_t n = first + (share + kShares - first % kShares) % kShares; n < first + P.nb; n += kShares) {
+    const uint32_t slot = n % C::kSlots, sb = n - first;
+    if (!C::kOwnSlots && !warp_wait_issued(&H.issued, n, gave_up, P.err)) return false;
+    if (!warp_wait(&H.full[slot], (n / C::kSlots) & 1, gave_up, P.err)) return false;
+    const uint8_t* at = ring + slot * C::kSlot;
+    const uint8_t* x = at + C::kWeights + C::kScales;
+    if constexpr (C::kQ6)
+      stage_q6<N, HALF>(at + (base + r0) * C::kSb, at + C::kWeights + (base + r0) * 4 + 2 * (sb & 1), x, lane, total);
+    else
+      stage_q4<N, HALF>(at + (base + r0) * C::kSb, (C::kUp ? kTileRows / 2 : 16) * C::kSb, x, lane, total);
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&H.empty[slot]);
+  }
+  // the shares' sums, one after the other through the group's place: share 2, 1, 0
+  constexpr int kSums = 8 * N;
+  float* place = part + group * C::kValues * 32 + lane;
+  if (share < kShares - 1) {
+    if (!warp_wait(&H.part[group][share + 1], turn & 1, gave_up, P.err)) return false;
+#pragma unroll
+    for (int j = 0; j < kSums; ++j) total[j / (4 * N)][(j / 4) % N][j % 4] += place[32 * j];
+  } else if (!warp_wait(&H.part[group][0], (turn & 1) ^ 1, gave_up, P.err)) {
+    return false;
+  }
+  if (share > 0) {
+#pragma unroll
+    for (int j = 0; j < kSums; ++j) place[32 * j] = total[j / (4 * N)][(j / 4) % N][j % 4];
+  }
+  __syncwarp();
+  if (lane == 0) tc::mbar_arrive(&H.part[group][share]);
+  if (share > 0) return true;
+  if constexpr (HALF) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) total[t][0][j] += __shfl_xor_sync(~0u, total[t][0][j], 2);     // lo to hi
+  }
+#pragma unroll
+  for (int t = 0; t < (C::kUp ? 1 : 2); ++t)
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int row = it.block * C::kOutRows + base + 16 * t + r0 + 8 * (j >> 1);
+        const int col = 8 * n + 2 * c + (j & 1);
+        if (row < P.rows && col < it.n) {
+          float v = total[t][n][j];
+          if constexpr (C::kUp) v = v / (1.0f + expf(-v)) * total[1][n][j];
+          P.out[(int64_t)(it.first + col) * P.rows + row] = v;
+        }
+      }
+  return true;
+}
+
+template <int MODE, int NT>
 __global__ void __launch_bounds__(kThreads, 1) moe_few_kernel(const __grid_constant__ Params P) {
-  using C = Cfg<MODE, NT, KS>;
+  using C = Cfg<MODE, NT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u);
   Head& H = *reinterpret_cast<Head*>(smem);
-  float* part = reinterpret_cast<float*>(smem + 8192);
+  float* part = reinterpret_cast<float*>(smem + kHeadBytes);
   uint8_t* ring = smem + C::kFixed;
   volatile int* gave_up = &H.gave_up;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = P.nb;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kSlots; ++i) {
-      tc::mbar_init(&H.full[i], 1);
-      tc::mbar_init(&H.ready[i], 1);
-      tc::mbar_init(&H.empty[i], C::kGroups);
+      tc::mbar_init(&H.full[i], 32 * kCopiers + 1);
+      tc::mbar_init(&H.empty[i], kGroups);
     }
-    for (int i = 0; i < C::kGroups; ++i) {
-      tc::mbar_init(&H.part_full[i], KS - 1);
-      tc::mbar_init(&H.part_empty[i], 1);
+    for (int i = 0; i < kGroups * kShares; ++i) tc::mbar_init(&H.part[0][i], 1);
+    for (int i = 0; i < kQueue; ++i) {
+      tc::mbar_init(&H.item_full[i], 1);
+      tc::mbar_init(&H.item_empty[i], kConsumers + kCopiers);
     }
     H.issued = 0;
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kConsumers) make_tiles(P, H, C::kPairs);
-  __syncthreads();
-  const int64_t items = H.tiles[P.experts] * P.blocks;
-  const int nb = P.nb;
+  const uint32_t items = make_tiles<kThreads, C::kPairs>(H.tiles, P.offsets, P.experts, (int)P.pairs, P.err) * P.blocks;
 
-  if (warp == kConsumers) {
-    // ------------------------------------------------------------ producer
-    uint32_t n = 0;
+  if (warp == kLead) {
+    // ------------------------------------------------- items, and the operands
+    uint32_t n = 0, i = blockIdx.x;
+    int ticket = 0;
     bool stop = false;
-    for (int64_t i = blockIdx.x; i < items && !stop; i += gridDim.x) {
-      const Item it = find_item(P, H, i, C::kPairs);
-      int64_t row = -1;
-      if (lane < it.n) {
-        row = it.first + lane;
-        if constexpr (C::kUp) {
-          const int p = P.order[row];
-          row = p >= 0 && p < P.pairs ? p / P.top_k : -1;
-          if (row < 0) atomicOr(P.err, kErrIndex);
-        }
+    for (uint32_t turn = 0; !stop; ++turn) {
+      const Item it = i < items ? find_item(H.tiles, i, P.blocks, C::kPairs) : Item{0, 0, 0, 0};
+      const uint32_t q = turn % kQueue;
+      if (!warp_wait(&H.item_empty[q], ((turn / kQueue) & 1) ^ 1, gave_up, P.err)) break;
+      if (lane == 0) {
+        H.item[q] = make_int4(it.expert, it.block, it.first, it.n);
+        tc::mbar_arrive(&H.item_full[q]);
       }
       __syncwarp();
-      const uint32_t mask = __ballot_sync(~0u, row >= 0);
-      const float* src = P.x + row * P.cols;
-      const int w0 = (int)(it.expert * (int64_t)P.rows + it.block * C::kOutRows);
+      if (turn == 0) asm volatile("griddepcontrol.wait;" ::: "memory");       // the operands; the weights need no wait
+      if (it.n == 0) break;
+      const int eighths = (it.n + 7) / 8;
+      const uint32_t bytes = it.n <= 4 ? kHalfX : kTileX;
+      const uint8_t* x = P.x + (int64_t)(H.tiles.eighth[it.expert] + (it.first - H.tiles.off[it.expert]) / 8) * nb * kTileX;
+      if (lane == 0) ticket = (int)gridDim.x + atomicAdd(P.counter, 1);
       for (int sb = 0; sb < nb; ++sb, ++n) {
         const uint32_t slot = n % C::kSlots;
         if (!warp_wait(&H.empty[slot], ((n / C::kSlots) & 1) ^ 1, gave_up, P.err)) {
           stop = true;
           break;
         }
-        uint8_t* at = ring + slot * C::kSlot;
-        tc::fence_proxy_async_smem();                            // the activations were rewritten in place
         if (lane == 0) {
-          H.mask[slot] = mask;
-          tc::mbar_arrive_expect_tx(&H.full[slot], C::kWeights + C::kScales + 1024 * __popc(mask));
-          tc::tma_load_3d(at, &P.w, 0, w0, sb, &H.full[slot]);
-          if constexpr (C::kUp) tc::tma_load_3d(at + C::kWeights / 2, &P.w2, 0, w0, sb, &H.full[slot]);
-          if constexpr (C::kQ6) tc::tma_load_2d(at + C::kWeights, &P.w2, sb & ~7, w0, &H.full[slot]);
+          tc::mbar_arrive_expect_tx(&H.full[slot], eighths * bytes);
+          uint8_t* at = ring + slot * C::kSlot + C::kWeights + C::kScales;
+          for (int k = 0; k < eighths; ++k)
+            tc::bulk_g2s(at + k * kTileX, x + ((int64_t)k * nb + sb) * kTileX, bytes, &H.full[slot]);
+          if constexpr (!C::kOwnSlots)
+            asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(tc::smem_u32(&H.issued)), "r"(n + 1) : "memory");
         }
         __syncwarp();
-        if (row >= 0)
-          tc::bulk_g2s(at + C::kWeights + C::kScales + (lane >> 3) * kTileX + (lane & 7) * 1024, src + sb * kQK, 1024,
-                       &H.full[slot]);
-        __syncwarp();
-        if (lane == 0)
-          asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(tc::smem_u32(&H.issued)), "r"(n + 1) : "memory");
       }
+      i = __shfl_sync(~0u, ticket, 0);
     }
     // its copies land before the CTA ends
     if (lane == 0)
       for (uint32_t j = n < C::kSlots ? 0 : n - C::kSlots; j < n; ++j)
         if (!tc::mbar_wait_sleep(&H.full[j % C::kSlots], (j / C::kSlots) & 1)) break;
-  } else if (warp > kConsumers) {
-    // ---------------------------------------------------------- activations
-    const int64_t mine = items > blockIdx.x ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
-    const uint32_t stages = (uint32_t)(mine * nb);
-    for (uint32_t n = warp - kConsumers - 1; n < stages; n += kCvt) {
-      const uint32_t slot = n % C::kSlots;
-      if (!warp_wait_issued(&H.issued, n, gave_up, P.err) ||
-          !warp_wait(&H.full[slot], (n / C::kSlots) & 1, gave_up, P.err))
-        break;
-      const uint32_t mask = *reinterpret_cast<volatile uint32_t*>(&H.mask[slot]);
-      uint8_t* at = ring + slot * C::kSlot + C::kWeights + C::kScales;
-#pragma unroll 1
-      for (int t = 0; t < NT; ++t) convert_tile<C::kQ6>(at + t * kTileX, (mask >> (8 * t)) & 0xFFu, lane);
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&H.ready[slot]);
+  } else if (warp >= kConsumers) {
+    // -------------------------------------------------------------- weights
+    const int tid = threadIdx.x - 32 * kConsumers;
+    constexpr int kPieces = C::kSb / 16, kMatrixRows = C::kOutRows, kEach = kMatrixRows * kPieces / (32 * kCopiers),
+                  kRest = kMatrixRows * kPieces % (32 * kCopiers);
+    int row[kEach + (kRest > 0)], col[kEach + (kRest > 0)];
+#pragma unroll
+    for (int j = 0; j < kEach + (kRest > 0); ++j) {
+      const int q = tid + 32 * kCopiers * j;
+      row[j] = q / kPieces, col[j] = 16 * (q % kPieces);
     }
-  } else {
-    // ------------------------------------------------------------- products
-    const int group = warp % C::kGroups, share = warp / C::kGroups;
-    const int g = lane >> 2, c = lane & 3;
-    const int r0 = C::kQ6 ? g : 2 * (g & 3) + (g >> 2);
-    // the warp's first row in a stage; gate and up: 16 rows of both halves
-    const int base = C::kUp ? 16 * group : 32 * group;
-    const int apart = (C::kUp ? C::kTileRows / 2 : 16) * C::kSb;
-    uint32_t first = 0, turn = 0;
+    const int last = P.experts * P.rows - 1;
+    uint32_t n = 0;
     bool stop = false;
-    for (int64_t i = blockIdx.x; i < items && !stop; i += gridDim.x, first += nb, ++turn) {
-      float total[2][NT][4] = {};
-      for (int sb = share; sb < nb; sb += KS) {
-        const uint32_t n = first + sb, slot = n % C::kSlots, parity = (n / C::kSlots) & 1;
-        if (!warp_wait_issued(&H.issued, n, gave_up, P.err) || !warp_wait(&H.full[slot], parity, gave_up, P.err) ||
-            !warp_wait(&H.ready[slot], parity, gave_up, P.err)) {
+    for (uint32_t turn = 0; !stop; ++turn) {
+      const uint32_t q = turn % kQueue;
+      if (!warp_wait(&H.item_full[q], (turn / kQueue) & 1, gave_up, P.err)) break;
+      const int4 it = H.item[q];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&H.item_empty[q]);
+      if (it.w == 0) break;
+      const int w0 = it.x * P.rows + it.y * C::kOutRows;
+      uint32_t off[kEach + (kRest > 0)];                         // (128 rows are less than 2^32 bytes)
+#pragma unroll
+      for (int j = 0; j < kEach + (kRest > 0); ++j) off[j] = (uint32_t)(min(row[j], last - w0) * P.pitch) + col[j];
+      const uint8_t *from = P.w + w0 * P.pitch, *from2 = C::kUp ? P.up + w0 * P.pitch : nullptr;
+      for (int sb = 0; sb < nb; ++sb, ++n) {
+        const uint32_t slot = n % C::kSlots;
+        if (!warp_wait(&H.empty[slot], ((n / C::kSlots) & 1) ^ 1, gave_up, P.err)) {
           stop = true;
           break;
         }
-        const uint8_t* at = ring + slot * C::kSlot;
-        const uint8_t* x = at + C::kWeights + C::kScales;
+        const uint32_t at = tc::smem_u32(ring + slot * C::kSlot) + 16 * tid;
+#pragma unroll
+        for (int j = 0; j < kEach + (kRest > 0); ++j) {
+          if (j == kEach && tid >= kRest) break;
+          copy16(at + 16 * 32 * kCopiers * j, from + off[j]);
+          if constexpr (C::kUp) copy16(at + C::kWeights / 2 + 16 * 32 * kCopiers * j, from2 + off[j]);
+        }
         if constexpr (C::kQ6)
-          stage_q6<NT>(at + (base + r0) * C::kSb, at + C::kWeights + (base + r0) * 16 + 2 * (sb & 7), x, lane, total);
-        else
-          stage_q4<NT>(at + (base + r0) * C::kSb, apart, x, lane, total);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&H.empty[slot]);
+          for (int r = tid; r < kTileRows; r += 32 * kCopiers)
+            copy4(tc::smem_u32(ring + slot * C::kSlot + C::kWeights) + 4 * r,
+                  P.w + (int64_t)min(w0 + r, last) * P.pitch + (int64_t)kQ6GpuBytes * nb + 2 * (sb & ~1));
+        copies_arrive(&H.full[slot]);
+        from += C::kSb;
+        if constexpr (C::kUp) from2 += C::kSb;
       }
-      if (stop) break;
-      if constexpr (KS > 1) {
-        constexpr int kValues = 2 * NT * 4;
-        if (share > 0) {
-          float* mine = part + (group * (KS - 1) + share - 1) * kValues * 32 + lane;
-          if (!warp_wait(&H.part_empty[group], (turn & 1) ^ 1, gave_up, P.err)) break;
-#pragma unroll
-          for (int j = 0; j < kValues; ++j) mine[32 * j] = total[j / (4 * NT)][(j / 4) % NT][j % 4];
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&H.part_full[group]);
-          continue;
-        }
-        if (!warp_wait(&H.part_full[group], turn & 1, gave_up, P.err)) break;
-        for (int s = 0; s < KS - 1; ++s) {
-          const float* other = part + (group * (KS - 1) + s) * kValues * 32 + lane;
-#pragma unroll
-          for (int j = 0; j < kValues; ++j) total[j / (4 * NT)][(j / 4) % NT][j % 4] += other[32 * j];
-        }
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&H.part_empty[group]);
-      }
-      const Item it = find_item(P, H, i, C::kPairs);
-#pragma unroll
-      for (int t = 0; t < (C::kUp ? 1 : 2); ++t)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t row = it.block * C::kOutRows + base + 16 * t + r0 + 8 * (j >> 1);
-            const int col = 8 * n + 2 * c + (j & 1);
-            if (row < P.rows && col < it.n) {
-              float v = total[t][n][j];
-              if constexpr (C::kUp) v = v / (1.0f + expf(-v)) * total[1][n][j];
-              P.out[(int64_t)(it.first + col) * P.rows + row] = v;
-            }
-          }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // ------------------------------------------------------------- products
+    uint32_t first = 0;
+    for (uint32_t turn = 0;; ++turn, first += nb) {
+      const uint32_t q = turn % kQueue;
+      if (!warp_wait(&H.item_full[q], (turn / kQueue) & 1, gave_up, P.err)) break;
+      const int4 v = H.item[q];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&H.item_empty[q]);
+      const Item it{v.x, v.y, v.z, v.w};
+      bool ok;
+      if (it.n == 0) break;
+      if (it.n <= 4) ok = consume<C, 1, true>(P, H, part, ring, it, first, turn);
+      else if (NT == 1 || it.n <= 8) ok = consume<C, 1, false>(P, H, part, ring, it, first, turn);
+      else ok = consume<C, NT, false>(P, H, part, ring, it, first, turn);
+      if (!ok) break;
     }
   }
 }
 
-template <int MODE, int NT, int KS>
-cudaError_t launch(const MoeProduct& p, float* out, cudaStream_t s) {
-  using C = Cfg<MODE, NT, KS>;
+inline int64_t most_eighths(int64_t pairs, int experts) { return std::min(pairs, pairs / 8 + experts); }
+
+template <int MODE, int NT>
+cudaError_t launch(const MoeProduct& p, void* work, float* out, cudaStream_t s) {
+  using C = Cfg<MODE, NT>;
   static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(moe_few_kernel<MODE, NT, KS>, C::kSmem, done);
+  cudaError_t e = allow_smem(moe_few_kernel<MODE, NT>, C::kSmem, done);
   if (e != cudaSuccess) return e;
   Params P{};
-  const int64_t rows = p.rows * p.plan.experts, nb = p.cols / kQK;
+  const int64_t nb = p.cols / kQK, pairs = p.plan.tokens * p.plan.top_k;
   const int64_t pitch = C::kQ6 ? q6k_gpu_row_bytes(nb) : nb * kBlockBytes;
-  const uint64_t dims[3] = {(uint64_t)C::kSb, (uint64_t)rows, (uint64_t)nb};
-  const uint64_t strides[2] = {(uint64_t)pitch, (uint64_t)C::kSb};
-  const uint32_t box[3] = {(uint32_t)C::kSb, (uint32_t)(C::kUp ? C::kTileRows / 2 : C::kTileRows), 1};
-  if (!encode_tmap_u8_3d(&P.w, p.w, dims, strides, box)) return cudaErrorInvalidValue;
-  if (C::kUp && !encode_tmap_u8_3d(&P.w2, p.up, dims, strides, box)) return cudaErrorInvalidValue;
-  if (C::kQ6 && !encode_tmap_2d(&P.w2, CU_TENSOR_MAP_DATA_TYPE_UINT16, p.w + nb * kQ6GpuBytes, (uint64_t)nb,
-                                (uint64_t)rows, (uint64_t)pitch, 8, C::kTileRows, CU_TENSOR_MAP_SWIZZLE_NONE))
-    return cudaErrorInvalidValue;
-  P.x = p.x, P.order = p.plan.order, P.offsets = p.plan.offsets, P.out = out, P.err = p.err;
-  P.pairs = p.plan.tokens * p.plan.top_k, P.cols = p.cols, P.blocks = (p.rows + C::kOutRows - 1) / C::kOutRows;
-  P.rows = (int)p.rows, P.nb = (int)nb, P.experts = p.plan.experts, P.top_k = p.plan.top_k;
+  P.counter = static_cast<int32_t*>(work), P.x = static_cast<uint8_t*>(work) + 128;
+  P.w = p.w, P.up = p.up, P.pitch = pitch;
+  P.offsets = p.plan.offsets, P.out = out, P.err = p.err, P.pairs = pairs;
+  P.blocks = (uint32_t)((p.rows + C::kOutRows - 1) / C::kOutRows);
+  P.rows = (int)p.rows, P.nb = (int)nb, P.experts = p.plan.experts;
+  const int64_t most = std::min(pairs, pairs / C::kPairs + P.experts) * P.blocks;
+  if (most * nb >= (int64_t(1) << 31)) return cudaErrorNotSupported;           // 32-bit counters of items and stages
+  SplitParams S{p.x, p.plan.order, p.plan.offsets, static_cast<uint8_t*>(work) + 128, P.counter, p.err, pairs, p.cols,
+                (int)nb, p.plan.experts, C::kUp ? p.plan.top_k : 0};
+  const int64_t eighths = most_eighths(pairs, p.plan.experts);
+  // few groups of pairs: a warp for each superblock
+  const unsigned parts = (unsigned)std::max<int64_t>(1, std::min<int64_t>((nb + kSplitWarps - 1) / kSplitWarps, 4 * 152 / eighths));
+  moe_few_split_kernel<C::kQ6><<<dim3((unsigned)eighths, parts), 32 * kSplitWarps, 0, s>>>(S, C::kPairs);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   int dev = 0;
   cudaGetDevice(&dev);
-  const int64_t most = std::min(P.pairs, P.pairs / C::kPairs + P.experts) * P.blocks;
-  moe_few_kernel<MODE, NT, KS><<<(unsigned)std::min<int64_t>(most, device_info(dev).sm_count), kThreads, C::kSmem, s>>>(P);
-  return cudaGetLastError();
+  return launch_after(moe_few_kernel<MODE, NT>, dim3((unsigned)std::min<int64_t>(most, device_info(dev).sm_count)), kThreads,
+                      C::kSmem, s, P);
 }
 
-// The variant for a product of `rows` outputs.
+// Tiles of 16 pairs as soon as some expert can have more than 8.
 template <int MODE>
-cudaError_t launch_mode(const MoeProduct& p, float* out, cudaStream_t s) {
-  const int64_t pairs = p.plan.tokens * p.plan.top_k, used = std::min<int64_t>(pairs, p.plan.experts);
-  if (pairs <= 8 * used) {
-    // a block of rows for each of four groups of warps, unless that leaves SMs without one
-    if (used * ((p.rows + 63) / 64) >= 2 * 152) return launch<MODE, 1, 2>(p, out, s);
-    return launch<MODE, 1, 8>(p, out, s);
-  }
-  if (pairs <= 16 * used) return launch<MODE, 2, 2>(p, out, s);
-  return launch<MODE, 4, 2>(p, out, s);
+cudaError_t launch_mode(const MoeProduct& p, void* work, float* out, cudaStream_t s) {
+  return p.plan.tokens <= 8 ? launch<MODE, 1>(p, work, out, s) : launch<MODE, 2>(p, work, out, s);
 }
 
 }  // namespace few

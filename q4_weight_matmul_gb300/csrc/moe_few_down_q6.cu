@@ -3,8 +3,8 @@
 
 namespace q4k {
 
-cudaError_t launch_moe_few_down_q6(const MoeProduct& p, float* out, cudaStream_t s) {
-  return few::launch_mode<few::kDownQ6>(p, out, s);
+cudaError_t launch_moe_few_down_q6(const MoeProduct& p, void* work, float* out, cudaStream_t s) {
+  return few::launch_mode<few::kDownQ6>(p, work, out, s);
 }
 
 }  // namespace q4k

@@ -3,8 +3,8 @@
 
 namespace q4k {
 
-cudaError_t launch_moe_few_gate_up(const MoeProduct& p, float* out, cudaStream_t s) {
-  return few::launch_mode<few::kGateUp>(p, out, s);
+cudaError_t launch_moe_few_gate_up(const MoeProduct& p, void* work, float* out, cudaStream_t s) {
+  return few::launch_mode<few::kGateUp>(p, work, out, s);
 }
 
 }  // namespace q4k

@@ -3,43 +3,83 @@
 //
 #include "moe.cuh"
 
+#include <type_traits>
+
 namespace q4k {
 namespace {
 
 constexpr int kThreads = 256;
 
-// y = residual + the weighted rows of z.
+// y = residual + the weighted rows of z: a thread adds up V neighbouring
+// outputs of one token, its loads of up to kBatch rows in flight at once.
+constexpr int kBatch = 8;
+
+template <int V>
 __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const MoeProduct P, const float* z) {
+  using F = std::conditional_t<V == 4, float4, float>;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const MoePlan& L = P.plan;
-  const int64_t t = blockIdx.x, pairs = L.tokens * L.top_k;
+  const int64_t per = P.rows / V, at = (int64_t)blockIdx.x * kThreads + threadIdx.x, t = at / per, pairs = L.tokens * L.top_k;
+  if (t >= L.tokens) return;
+  const int64_t r = (at - t * per) * V;
   const int32_t* place = L.place + t * L.top_k;
+  const float* weight = L.weight + t * L.top_k;
   if (place[0] == -2) return;
-  for (int64_t r = threadIdx.x; r < P.rows; r += kThreads) {
-    float y = P.residual ? P.residual[t * P.rows + r] : 0.0f;
-    for (int j = 0; j < L.top_k; ++j) {
-      const int at = place[j];
-      if (at >= 0 && at < pairs) y = fmaf(L.weight[t * L.top_k + j], z[at * P.rows + r], y);
-      else if ((at >= pairs || at < -1) && threadIdx.x == 0) atomicOr(P.err, kErrIndex);
+  alignas(16) float y[V] = {};
+  if (P.residual) *reinterpret_cast<F*>(y) = *reinterpret_cast<const F*>(P.residual + t * P.rows + r);
+  for (int j0 = 0; j0 < L.top_k; j0 += kBatch) {
+    alignas(16) float v[kBatch][V];
+    float w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int p = j0 + j < L.top_k ? place[j0 + j] : -1;
+      const bool have = p >= 0 && p < pairs;
+      if (!have && p != -1 && r == 0) atomicOr(P.err, kErrIndex);
+      w[j] = have ? weight[j0 + j] : 0.0f;
+      if (have) {
+        *reinterpret_cast<F*>(v[j]) = *reinterpret_cast<const F*>(z + p * P.rows + r);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j][i] = 0.0f;
+      }
     }
-    P.out[t * P.rows + r] = y;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] = fmaf(w[j], v[j][i], y[i]);
   }
+  *reinterpret_cast<F*>(P.out + t * P.rows + r) = *reinterpret_cast<const F*>(y);
+}
+
+cudaError_t combine(const MoeProduct& p, const float* z, cudaStream_t s) {
+  const int64_t n = p.plan.tokens * p.rows;
+  if (p.rows % 4 == 0)
+    return launch_after(moe_combine_kernel<4>, dim3((unsigned)((n / 4 + kThreads - 1) / kThreads)), kThreads, 0, s, p, z);
+  return launch_after(moe_combine_kernel<1>, dim3((unsigned)((n + kThreads - 1) / kThreads)), kThreads, 0, s, p, z);
 }
 
 }  // namespace
 
-size_t moe_gate_up_workspace(int64_t, int, int, int64_t, int64_t) { return 0; }
-size_t moe_down_workspace(int64_t tokens, int top_k, int, int64_t rows, int64_t) {
-  return sizeof(float) * (size_t)(tokens * top_k) * (size_t)rows;
+// The down products' rows, before they are put together, lie behind the operands.
+static size_t rows_at(size_t operands) { return (operands + 255) / 256 * 256; }
+
+size_t moe_gate_up_workspace(int64_t tokens, int top_k, int experts, int64_t, int64_t cols) {
+  return moe_few_workspace(tokens * top_k, experts, cols);
+}
+size_t moe_down_workspace(int64_t tokens, int top_k, int experts, int64_t rows, int64_t cols) {
+  return rows_at(moe_few_workspace(tokens * top_k, experts, cols)) + sizeof(float) * (size_t)(tokens * top_k) * (size_t)rows;
 }
 
-cudaError_t launch_moe_gate_up(const MoeProduct& p, cudaStream_t s) { return launch_moe_few_gate_up(p, p.out, s); }
+cudaError_t launch_moe_gate_up(const MoeProduct& p, cudaStream_t s) {
+  return launch_moe_few_gate_up(p, p.workspace, p.out, s);
+}
 
 cudaError_t launch_moe_down(const MoeProduct& p, cudaStream_t s) {
-  float* z = static_cast<float*>(p.workspace);
-  cudaError_t e = p.q6k ? launch_moe_few_down_q6(p, z, s) : launch_moe_few_down_q4(p, z, s);
+  float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) +
+                                      rows_at(moe_few_workspace(p.plan.tokens * p.plan.top_k, p.plan.experts, p.cols)));
+  cudaError_t e = p.q6k ? launch_moe_few_down_q6(p, p.workspace, z, s) : launch_moe_few_down_q4(p, p.workspace, z, s);
   if (e != cudaSuccess) return e;
-  return launch_after(moe_combine_kernel, dim3((unsigned)p.plan.tokens), kThreads, 0, s, p, (const float*)z);
+  return combine(p, z, s);
 }
 
 }  // namespace q4k

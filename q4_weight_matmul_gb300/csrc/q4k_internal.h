@@ -216,10 +216,14 @@ size_t moe_gate_up_workspace(int64_t tokens, int top_k, int experts, int64_t row
 size_t moe_down_workspace(int64_t tokens, int top_k, int experts, int64_t rows, int64_t cols);
 cudaError_t launch_moe_gate_up(const MoeProduct& p, cudaStream_t s);
 cudaError_t launch_moe_down(const MoeProduct& p, cudaStream_t s);
-// The products alone, [pairs][rows], for few rows an expert (moe_few.cuh).
-cudaError_t launch_moe_few_gate_up(const MoeProduct& p, float* out, cudaStream_t s);
-cudaError_t launch_moe_few_down_q4(const MoeProduct& p, float* out, cudaStream_t s);
-cudaError_t launch_moe_few_down_q6(const MoeProduct& p, float* out, cudaStream_t s);
+// The products alone, [pairs][rows], for few pairs an expert (moe_few.cuh); `work`: moe_few_workspace() bytes.
+constexpr int64_t kMoeFewTile = 16 * 512 + 256 + 32;   // operands of 8 pairs and 256 columns
+inline size_t moe_few_workspace(int64_t pairs, int experts, int64_t cols) {
+  return (size_t)(128 + (pairs < pairs / 8 + experts ? pairs : pairs / 8 + experts) * (cols / kQK) * kMoeFewTile);
+}
+cudaError_t launch_moe_few_gate_up(const MoeProduct& p, void* work, float* out, cudaStream_t s);
+cudaError_t launch_moe_few_down_q4(const MoeProduct& p, void* work, float* out, cudaStream_t s);
+cudaError_t launch_moe_few_down_q6(const MoeProduct& p, void* work, float* out, cudaStream_t s);
 
 // One-thread kernel whose only (bounded) wait can never complete: after the
 // library's wait limit it records a timeout in `err` and returns.
