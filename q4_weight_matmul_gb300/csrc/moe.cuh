@@ -1,9 +1,9 @@
-// What the kernels of a layer with routed experts share: the plan, the tiles
-// of pairs that share an expert, and launches that overlap the end of the one
-// before.
+// What the kernels of a layer with routed experts share: launches that overlap
+// the end of the one before, waits, sums over a block.
 #pragma once
 
 #include "q4k_internal.h"
+#include "tc_ptx.cuh"
 
 #include <cstdint>
 
@@ -24,6 +24,48 @@ inline cudaError_t launch_after(K* kernel, dim3 grid, int threads, size_t smem, 
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A warp agrees on a wait's outcome, so that its lanes stay together; one that
+// gives up raises the block's flag and the device error word.
+__device__ __forceinline__ bool agreed(bool ok, volatile int* gave_up, int* err) {
+  if (__all_sync(~0u, ok)) return true;
+  if ((threadIdx.x & 31) == 0) {
+    if (!*gave_up) atomicOr(err, 1);
+    *gave_up = 1;
+  }
+  __syncwarp();
+  return false;
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up, int* err) {
+  return agreed(tc::mbar_wait(bar, parity, gave_up), gave_up, err);
+}
+
+// Exclusive sum of `v` over the block's threads before this one (`most`:
+// maximum in place of a sum); every thread gets the whole block's in `all`.
+template <int THREADS, bool MOST>
+__device__ __forceinline__ int scan_block(int v, int* warps, int& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int u = __shfl_up_sync(~0u, s, o);
+    if (lane >= o) s = MOST ? max(s, u) : s + u;
+  }
+  if (lane == 31) warps[warp] = s;
+  __syncthreads();
+  int before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const int u = warps[w];
+    if (w < warp) before = MOST ? max(before, u) : before + u;
+    all = MOST ? max(all, u) : all + u;
+  }
+  const int u = __shfl_up_sync(~0u, s, 1);
+  if (lane > 0) before = MOST ? max(before, u) : before + u;
+  __syncthreads();
+  return before;
 }
 
 }  // namespace q4k

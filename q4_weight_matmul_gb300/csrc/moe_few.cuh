@@ -113,19 +113,6 @@ struct SplitParams {
   int nb, experts, top_k;     // top_k 0: x has a row for every pair
 };
 
-__device__ __forceinline__ bool agreed(bool ok, volatile int* gave_up, int* err) {
-  if (__all_sync(~0u, ok)) return true;
-  if ((threadIdx.x & 31) == 0) {
-    if (!*gave_up) atomicOr(err, 1);
-    *gave_up = 1;
-  }
-  __syncwarp();
-  return false;
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up, int* err) {
-  return agreed(tc::mbar_wait(bar, parity, gave_up), gave_up, err);
-}
-
 // Until stage n has been issued.
 __device__ __forceinline__ bool warp_wait_issued(const uint32_t* issued, uint32_t n, volatile int* gave_up, int* err) {
   bool ok = true;
@@ -165,33 +152,6 @@ struct Item {
   int expert, block;
   int first, n;               // pairs order[first] .. first + n - 1
 };
-
-// Exclusive sum of `v` over the block's threads before this one (`most`:
-// maximum in place of a sum); every thread gets the whole block's in `all`.
-template <int THREADS, bool MOST>
-__device__ __forceinline__ int scan_block(int v, int* warps, int& all) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const int u = __shfl_up_sync(~0u, s, o);
-    if (lane >= o) s = MOST ? max(s, u) : s + u;
-  }
-  if (lane == 31) warps[warp] = s;
-  __syncthreads();
-  int before = 0;
-  all = 0;
-#pragma unroll
-  for (int w = 0; w < THREADS / 32; ++w) {
-    const int u = warps[w];
-    if (w < warp) before = MOST ? max(before, u) : before + u;
-    all = MOST ? max(all, u) : all + u;
-  }
-  const int u = __shfl_up_sync(~0u, s, 1);
-  if (lane > 0) before = MOST ? max(before, u) : before + u;
-  __syncthreads();
-  return before;
-}
 
 // The tables; a whole block, each thread for kMoeMaxExperts / THREADS
 // experts.  Offsets are cut to ascending values of 0..pairs.  Returns the

@@ -1,0 +1,790 @@
+// Products of the experts' matrices with many rows each (prompts), on the
+// tensor cores (tcgen05): 128 or 256 weight rows times up to 128 pairs of one
+// expert, fp32 sums of exact 16-bit products as in moe_few.cuh.
+//
+// Four launches.  (1) One CTA lays the pairs out in tiles: an expert's n pairs
+// become ceil(n / 128) tiles of equal size, a multiple of 16.  (2) Each pair's
+// activations, times a power of two that puts the row's largest in
+// [2^14, 2^15), become two binary16 parts, stored tile by tile as the products
+// read them (64 k of hi, then of lo, in the 128-byte-swizzled layout), with
+// the sums of every 32 of them (hi and lo, times 2^-6).  (3) The products.
+// (4) For down: the weighted rows of a token are added up (moe_product.cu).
+//
+// The weights are the products' A and lie in tensor memory: a converter thread
+// owns a weight row, which is a lane there, and writes sc q as binary16, exact.
+// So shared memory feeds the tensor core with B alone (with both operands
+// there, 128 columns an instruction would take all of its bandwidth).  The min
+// term dmin m sums(x) is part of the same sum: with r = dmin / d the sum over a
+// superblock is d (sum sc q x - sum r m sums(x)), r m as two binary16 parts (22
+// bits) beside the sums' parts, so a superblock takes one FMA per row and
+// column in the epilogue.  Where |r| > 16, all of it is taken 2^-e times, e =
+// floor(log2 |r|) - 3, so that r m fits binary16; sc q 2^-e stays exact up to
+// e = 20, and beyond (dmin > 2^24 d) d counts as 0.
+// Q6_K: sc (q - 32) needs up to 13 bits: hi = binary16 of it and lo = the rest
+// (-1, 0, 1), two tiles that meet the hi and lo, and the hi parts of x.
+//
+// A CTA's warps: 0 copies activations, 2 weights, 3 draws items (a tile of
+// pairs times a block of rows; large tiles first), 1 issues the products, 4-7
+// convert, 8-15 run the epilogue (64 columns a thread; totals in registers).
+// Tensor memory: three sums of 128 columns in turn, four tiles of A (128 rows x
+// 64 k) in turn.  Every wait is bounded.
+#pragma once
+
+#include "mma_sync.cuh"
+#include "mmq_cvt.cuh"
+#include "moe.cuh"
+#include "tmap.h"
+
+#include <algorithm>
+
+namespace q4k {
+namespace many {
+
+enum Mode { kGateUp, kDownQ4, kDownQ6 };
+
+constexpr int kThreads = 512;
+constexpr int kRows = 128, kCols = 128;       // of a product: weight rows, pairs
+constexpr int kStages = 4, kStageBytes = 2 * kCols * 128;   // 64 k of the activations, hi and lo
+constexpr int kSumBytes = kCols * 128;        // the sums of four superblocks, 32 bytes a pair each
+constexpr int kATiles = 4, kUnits = 3, kScaleSlots = 4, kQueue = 4;
+constexpr uint32_t kAColumn = kUnits * kCols; // of the first A tile in tensor memory
+constexpr int kConverters = 4, kEpilogue = 8; // warps
+constexpr uint32_t kProduct = (1u << 4) | ((uint32_t)(kRows >> 4) << 24);      // f16 operands, f32 sums, 128 rows
+
+struct Tile {                 // pairs first .. first + n - 1 of an expert; their padded rows from `row` on
+  int expert, first, n, row;
+};
+struct Control {
+  int tiles, counter, pad[30];
+};
+
+template <int MODE>
+struct Cfg {
+  static constexpr bool kUp = MODE == kGateUp, kQ6 = MODE == kDownQ6;
+  static constexpr int kSb = kQ6 ? kQ6GpuBytes : kBlockBytes;
+  static constexpr int kRaw = kQ6 ? 2 : 3;                   // weight tiles (128 rows of a superblock) in flight
+  static constexpr int kTilesM = kQ6 ? 1 : 2;                // of 128 rows each
+  static constexpr int kOutRows = MODE == kDownQ4 ? 2 * kRows : kRows;
+};
+
+struct Params {
+  CUtensorMap w, up;          // rows of the experts' superblocks
+  const Control* control;
+  const Tile* tiles;
+  const float* inv;
+  const uint8_t *x, *sums, *scales;    // scales: the rows' d (Q6_K), rows of `pitch` bytes
+  float* out;
+  int* counter;
+  int* err;
+  int64_t pitch;
+  int rows, nb, blocks;
+};
+
+template <int MODE>
+struct __align__(1024) Smem {
+  uint8_t x[kStages][kStageBytes];
+  uint8_t sums[2][kSumBytes];
+  uint8_t raw[Cfg<MODE>::kRaw][kRows * Cfg<MODE>::kSb];
+  float scale[kScaleSlots][kRows];
+  uint64_t xfull[kStages], xempty[kStages], sfull[2], sempty[2], rfull[3], rempty[3], afull[kATiles], aempty[kATiles],
+      tfull[kUnits], tempty[kUnits], dfull[kScaleSlots], dempty[kScaleSlots], qfull[kQueue], qempty[kQueue], drain;
+  Tile item[kQueue];
+  int block[kQueue];
+  uint32_t tmem;
+  int gave_up;
+};
+static_assert(sizeof(Smem<kGateUp>) + 1024 <= 232448 && sizeof(Smem<kDownQ6>) + 1024 <= 232448);
+
+// One lane of a converged warp; what it issues takes its operands from uniform
+// registers.
+__device__ __forceinline__ bool elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+// D[tmem] (+)= A[tmem] B[smem]^T
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t what, uint32_t add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(what), "r"(add) : "memory");
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_of(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// ---------------------------------------------------------------- the tiles
+// One CTA, a thread per expert.  Tiles of equal size lie in any order: each
+// result is the same wherever its tile comes.
+struct LayoutParams {
+  const int32_t* offsets;
+  Control* control;
+  Tile* tiles;
+  int* err;
+  int pairs, experts;
+};
+
+static __global__ void __launch_bounds__(kMoeMaxExperts) moe_many_layout_kernel(const LayoutParams P) {
+  __shared__ int warps[16], count[9], start[9];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int e = threadIdx.x, E = P.experts;
+  if (e < 9) count[e] = 0;
+  const int raw0 = e <= E ? P.offsets[e] : INT32_MAX, raw1 = e < E ? P.offsets[e + 1] : INT32_MAX;
+  int all;
+  const int before = scan_block<kMoeMaxExperts, true>(min(raw0, P.pairs), warps, all);
+  const int first = max(max(before, 0), min(raw0, P.pairs)), last = max(first, min(raw1, P.pairs));
+  if (e < E && (first != raw0 || last != raw1)) atomicOr(P.err, kErrIndex);
+  const int n = e < E ? last - first : 0, tiles = (n + kCols - 1) / kCols;
+  const int each = tiles ? ((n + tiles - 1) / tiles + 15) / 16 * 16 : 16;
+  const int used = (n + each - 1) / each;                     // (rounding up can save one)
+  int row = scan_block<kMoeMaxExperts, false>(used ? (used - 1) * each + (n - (used - 1) * each + 15) / 16 * 16 : 0, warps, all);
+  for (int k = 0; k < used; ++k) atomicAdd(&count[(min(each, n - k * each) + 15) / 16], 1);
+  __syncthreads();
+  if (e == 0) {
+    int run = 0;
+    for (int c = 8; c > 0; --c) start[c] = run, run += count[c];
+    P.control->tiles = run;
+    P.control->counter = 0;
+  }
+  __syncthreads();
+  for (int k = 0; k < used; ++k) {
+    const int m = min(each, n - k * each);
+    P.tiles[atomicAdd(&start[(m + 15) / 16], 1)] = Tile{e, first + k * each, m, row + k * each};
+  }
+}
+
+// ----------------------------------------------------------- activations
+struct SplitParams {
+  const float* x;
+  const int32_t* order;
+  const Control* control;
+  const Tile* tiles;
+  uint8_t *out, *sums;
+  float* inv;
+  int* err;
+  int64_t pairs, cols;
+  int nb, top_k;              // top_k 0: x has a row for every pair
+};
+
+// A CTA for 8 pairs of a tile, a warp each; a lane has 8 neighbouring values
+// of a superblock.  PERMUTE: the values of 4 in the order 0, 2, 1, 3, in which
+// Q4_K quants leave their bytes without a transpose.
+template <bool PERMUTE>
+__global__ void __launch_bounds__(256) moe_many_split_kernel(const SplitParams P) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if ((int)blockIdx.x >= P.control->tiles) return;
+  const Tile T = P.tiles[blockIdx.x];
+  const int i = 8 * blockIdx.y + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (i >= T.n) return;
+  const int padded = (T.n + 15) / 16 * 16;
+  int64_t r = T.first + i;
+  if (P.top_k) {
+    const int p = P.order[r];
+    r = p >= 0 && p < P.pairs ? p / P.top_k : -1;
+    if (r < 0 && lane == 0) atomicOr(P.err, kErrIndex);
+  }
+  const float4* from = reinterpret_cast<const float4*>(P.x + max(r, (int64_t)0) * P.cols);
+  float top = 0.0f;
+  if (r >= 0) {
+#pragma unroll 4
+    for (int k = lane; k < P.cols / 4; k += 32) {
+      const float4 v = from[k];
+      top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+  const int E = (int)((__float_as_uint(top) >> 23) & 0xFFu), es = top == 0.0f ? 127 : min(253, max(1, 268 - E));
+  const float s = __uint_as_float((uint32_t)es << 23);
+  if (lane == 0) P.inv[T.row + i] = __uint_as_float((uint32_t)(254 - es) << 23);
+  uint8_t* out = P.out + (int64_t)T.row * P.cols * 4 + i * 128 + (((lane & 7) ^ (i & 7)) << 4);
+  __half* sums = reinterpret_cast<__half*>(P.sums + (int64_t)T.row * ((P.nb + 3) / 4) * 128 + i * 128);
+  for (int sb = 0; sb < P.nb; ++sb) {
+    float4 a = make_float4(0, 0, 0, 0), b = a;
+    if (r >= 0) a = from[64 * sb + 2 * lane], b = from[64 * sb + 2 * lane + 1];
+    const float v[8] = {a.x * s, (PERMUTE ? a.z : a.y) * s, (PERMUTE ? a.y : a.z) * s, a.w * s,
+                        b.x * s, (PERMUTE ? b.z : b.y) * s, (PERMUTE ? b.y : b.z) * s, b.w * s};
+    uint32_t hi[4], lo[4];
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      hi[k] = pack2<false>(v[2 * k], v[2 * k + 1]);
+      const float2 h = unpack2<false>(hi[k]);
+      lo[k] = pack2<false>(v[2 * k] - h.x, v[2 * k + 1] - h.y);
+      const float2 l = unpack2<false>(lo[k]);
+      sum += (h.x + h.y) + (l.x + l.y);
+    }
+    uint8_t* at = out + (int64_t)(4 * sb + (lane >> 3)) * 2 * padded * 128;
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + padded * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    if constexpr (PERMUTE) {                                   // Q4_K: the sub-blocks' sums
+      sum += __shfl_xor_sync(~0u, sum, 1);
+      sum += __shfl_xor_sync(~0u, sum, 2);
+      if ((lane & 3) == 0) {
+        const float x = sum * 0.015625f;
+        const __half h = __float2half_rn(x);
+        // 16-byte chunk 2 (sb % 4) has the hi parts, the next one the lo parts
+        const int c = 2 * (sb & 3), k = lane >> 2;
+        __half* to = sums + (int64_t)(sb >> 2) * padded * 64;
+        to[((c ^ (i & 7)) << 3) + k] = h;
+        to[(((c + 1) ^ (i & 7)) << 3) + k] = __float2half_rn(x - __half2float(h));
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------- converters
+// 64 weights of a Q4_K row (32 quant bytes, sub-blocks 2 c and 2 c + 1) as
+// sc q 2^-e, pairs (0, 2), (1, 3) of every four.
+__device__ __forceinline__ void convert_q4(const uint4& q0, const uint4& q1, uint32_t s_low, uint32_t s_high,
+                                           uint32_t (&a)[32]) {
+  // (1024 + q) s - 1024 s, (1024 + 16 q) s / 16 - 64 s: one exact FMA each
+  const uint32_t b_low = cvt::mul_h2(s_low, 0xE400E400u), m_high = cvt::mul_h2(s_high, 0x2C002C00u),
+                 b_high = cvt::mul_h2(s_high, 0xD400D400u);
+  const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t u = w[i] >> 8;
+    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
+        : "=r"(a[2 * i]) : "r"(w[i]), "r"(s_low), "r"(b_low));
+    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
+        : "=r"(a[2 * i + 1]) : "r"(u), "r"(s_low), "r"(b_low));
+    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
+        : "=r"(a[16 + 2 * i]) : "r"(w[i]), "r"(m_high), "r"(b_high));
+    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
+        : "=r"(a[16 + 2 * i + 1]) : "r"(u), "r"(m_high), "r"(b_high));
+  }
+}
+
+// What a Q4_K row's header says about a superblock.
+struct Header {
+  uint32_t sc[2], m[2];       // 6-bit scales and mins
+  uint32_t down;              // 2^-e twice, or 0 where d counts as 0
+  float scale, r;             // what a sum is to be multiplied with; r m 2^-e as part of it: r times 2^6
+};
+__device__ __forceinline__ Header header_of(const uint4& h) {
+  Header H;
+  cvt::header_sc_m(h, H.sc[0], H.sc[1], H.m[0], H.m[1]);
+  const float2 d = unpack2<false>(h.x);                        // d, dmin
+  H.r = -64.0f * d.y / d.x;
+  H.scale = d.x;
+  H.down = 0x3C003C00u;
+  if (!(fabsf(H.r) <= 1024.0f) && d.y != 0.0f) {               // |r| > 16, or d = 0
+    const int e = (int)(__float_as_uint(H.r) >> 23 & 0xFF) - 127 - 9;
+    if (d.x == 0.0f || e > 20) {
+      H.down = 0, H.r = -512.0f, H.scale = d.y * 0.125f;
+    } else {
+      H.r = __uint_as_float(__float_as_uint(H.r) - ((uint32_t)e << 23));
+      H.scale = __uint_as_float(__float_as_uint(d.x) + ((uint32_t)e << 23));
+      const __half2 t = __float2half2_rn(__uint_as_float((uint32_t)(127 - e) << 23));
+      H.down = *reinterpret_cast<const uint32_t*>(&t);
+    }
+  } else if (d.y == 0.0f) {
+    H.r = 0.0f;
+  }
+  return H;
+}
+
+// The two binary16 parts of r m for the eight mins: [hi | hi], [lo | lo].
+__device__ __forceinline__ void convert_min(const Header& H, uint32_t (&a)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = H.m[i >> 1] >> (16 * (i & 1));
+    const float v0 = H.r * (float)(w & 0xFFu), v1 = H.r * (float)(w >> 8 & 0xFFu);
+    a[i] = a[4 + i] = pack2<false>(v0, v1);
+    const float2 h = unpack2<false>(a[i]);
+    a[8 + i] = a[12 + i] = pack2<false>(v0 - h.x, v1 - h.y);
+  }
+}
+
+// 64 weights of a Q6_K row (chunk c: 32 bytes of low nibbles, 16 of bit pairs)
+// as the parts of sc (q - 32), in order.
+__device__ __forceinline__ void convert_q6(const uint4& l0, const uint4& l1, const uint4& h, uint32_t scales,
+                                           uint32_t (&hi)[32], uint32_t (&lo)[32]) {
+  const uint32_t lw[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w}, hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {                                // group f: sub-block f / 2, half f % 2
+    const float sf = (float)(int8_t)(scales >> (8 * f));
+    const __half2 sc = __float2half2_rn(sf), bias = __float2half2_rn(-1056.0f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // bytes of q with the top bit inverted, then two at a time under the exponent of 1024
+      const uint32_t v = ((lw[4 * (f & 1) + i] >> (4 * (f >> 1))) & 0x0F0F0F0Fu) | (((hw[i] >> (2 * f)) & 0x03030303u) << 4);
+      const uint32_t p0 = __byte_perm(v, 0, 0x4140) ^ 0x64206420u, p1 = __byte_perm(v, 0, 0x4342) ^ 0x64206420u;
+      const __half2 q0 = __hadd2(*reinterpret_cast<const __half2*>(&p0), bias),
+                    q1 = __hadd2(*reinterpret_cast<const __half2*>(&p1), bias);
+      const __half2 h0 = __hmul2(q0, sc), h1 = __hmul2(q1, sc);
+      const __half2 r0 = __hfma2(q0, sc, __hneg2(h0)), r1 = __hfma2(q1, sc, __hneg2(h1));
+      hi[8 * f + 2 * i] = *reinterpret_cast<const uint32_t*>(&h0), hi[8 * f + 2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+      lo[8 * f + 2 * i] = *reinterpret_cast<const uint32_t*>(&r0), lo[8 * f + 2 * i + 1] = *reinterpret_cast<const uint32_t*>(&r1);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ products
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_constant__ Params P) {
+  using C = Cfg<MODE>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem<MODE>& S = *reinterpret_cast<Smem<MODE>*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
+  volatile int* gave_up = &S.gave_up;
+  int* err = P.err;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = P.nb;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&S.xfull[i], 1), tc::mbar_init(&S.xempty[i], 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&S.sfull[i], 1), tc::mbar_init(&S.sempty[i], 1);
+    for (int i = 0; i < C::kRaw; ++i) tc::mbar_init(&S.rfull[i], 1), tc::mbar_init(&S.rempty[i], kConverters);
+    for (int i = 0; i < kATiles; ++i) tc::mbar_init(&S.afull[i], kConverters), tc::mbar_init(&S.aempty[i], 1);
+    for (int i = 0; i < kUnits; ++i) tc::mbar_init(&S.tfull[i], 1), tc::mbar_init(&S.tempty[i], kEpilogue);
+    for (int i = 0; i < kScaleSlots; ++i) tc::mbar_init(&S.dfull[i], kConverters), tc::mbar_init(&S.dempty[i], kEpilogue);
+    for (int i = 0; i < kQueue; ++i) tc::mbar_init(&S.qfull[i], 1), tc::mbar_init(&S.qempty[i], 3 + kConverters + kEpilogue);
+    tc::mbar_init(&S.drain, 1);
+    *gave_up = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&S.tmem, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = S.tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  // The next item of a warp; false: there is none, or a wait gave up.
+  uint32_t turn = 0;
+  Tile T;
+  int block;
+  auto next_item = [&]() -> bool {
+    const uint32_t q = turn % kQueue;
+    if (!warp_wait(&S.qfull[q], (turn / kQueue) & 1, gave_up, err)) return false;
+    T = S.item[q], block = S.block[q];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&S.qempty[q]);
+    ++turn;
+    return T.n > 0;
+  };
+
+  // 512 threads x 128 registers at launch = 128 x 40 + 128 x 104 + 256 x 184
+  if (warp < 4) {
+    registers_down<40>();
+    if (warp == 0) {
+      // ------------------------------------------------------ activations
+      uint32_t j = 0, g = 0;                                   // stages, groups of sums issued
+      bool stop = false;
+      while (!stop && next_item()) {
+        const uint32_t padded = (T.n + 15) / 16 * 16;
+        const uint8_t* x = P.x + (int64_t)T.row * nb * 1024;
+        const uint8_t* sums = P.sums + (int64_t)T.row * ((nb + 3) / 4) * 128;
+        for (int c = 0; c < 4 * nb; ++c, ++j) {
+          if (!C::kQ6 && c % 16 == 0) {
+            stop = !warp_wait(&S.sempty[g & 1], ((g >> 1) & 1) ^ 1, gave_up, err);
+            if (stop) break;
+            if (elect()) {
+              tc::mbar_arrive_expect_tx(&S.sfull[g & 1], padded * 128);
+              tc::bulk_g2s(S.sums[g & 1], sums + (int64_t)(c / 16) * padded * 128, padded * 128, &S.sfull[g & 1]);
+            }
+            __syncwarp();
+            ++g;
+          }
+          const uint32_t slot = j % kStages;
+          stop = !warp_wait(&S.xempty[slot], ((j / kStages) & 1) ^ 1, gave_up, err);
+          if (stop) break;
+          if (elect()) {
+            tc::mbar_arrive_expect_tx(&S.xfull[slot], 2 * padded * 128);
+            tc::bulk_g2s(S.x[slot], x + (int64_t)c * 2 * padded * 128, 2 * padded * 128, &S.xfull[slot]);
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0) {                                         // its copies land before the CTA ends
+        for (uint32_t i = j < kStages ? 0 : j - kStages; i < j; ++i)
+          if (!tc::mbar_wait_sleep(&S.xfull[i % kStages], (i / kStages) & 1)) break;
+        for (uint32_t i = g < 2 ? 0 : g - 2; i < g; ++i)
+          if (!tc::mbar_wait_sleep(&S.sfull[i & 1], (i >> 1) & 1)) break;
+      }
+    } else if (warp == 2) {
+      // ---------------------------------------------------------- weights
+      uint32_t n = 0;
+      bool stop = false;
+      while (!stop && next_item()) {
+        const int w0 = T.expert * P.rows + block * C::kOutRows;
+        for (int i = 0; i < C::kTilesM * nb; ++i, ++n) {
+          const int sb = i / C::kTilesM, mt = i % C::kTilesM;
+          const uint32_t slot = n % C::kRaw;
+          stop = !warp_wait(&S.rempty[slot], ((n / C::kRaw) & 1) ^ 1, gave_up, err);
+          if (stop) break;
+          if (elect()) {
+            tc::mbar_arrive_expect_tx(&S.rfull[slot], kRows * C::kSb);
+            tc::tma_load_3d(S.raw[slot], C::kUp && mt ? &P.up : &P.w, 0, C::kUp ? w0 : w0 + kRows * mt, sb, &S.rfull[slot]);
+          }
+          __syncwarp();
+        }
+      }
+      if (lane == 0)
+        for (uint32_t i = n < C::kRaw ? 0 : n - C::kRaw; i < n; ++i)
+          if (!tc::mbar_wait_sleep(&S.rfull[i % C::kRaw], (i / C::kRaw) & 1)) break;
+    } else if (warp == 3) {
+      // ------------------------------------------------------------ items
+      const int items = P.control->tiles * P.blocks;
+      int i = blockIdx.x;
+      for (uint32_t t = 0;; ++t) {
+        const uint32_t q = t % kQueue;
+        Tile tile{0, 0, 0, 0};
+        int ticket = 0;
+        if (i < items) {
+          tile = P.tiles[i / P.blocks];
+          if (lane == 0) ticket = (int)gridDim.x + atomicAdd(P.counter, 1);
+        }
+        if (!warp_wait(&S.qempty[q], ((t / kQueue) & 1) ^ 1, gave_up, err)) break;
+        if (lane == 0) {
+          S.item[q] = tile, S.block[q] = i < items ? i % P.blocks : 0;
+          tc::mbar_arrive(&S.qfull[q]);
+        }
+        if (i >= items) break;
+        i = __shfl_sync(~0u, ticket, 0);
+      }
+    } else {
+      // --------------------------------------------------------- products
+      uint32_t j = 0, g = 0, a = 0, u = 0;                     // stages, groups of sums, A tiles, sums
+      bool stop = false;
+      while (!stop && next_item()) {
+        const uint32_t padded = (T.n + 15) / 16 * 16, what = kProduct | (padded >> 3) << 17;
+        for (int sb = 0; sb < nb && !stop; ++sb) {
+          for (int c = 0; c < 4 && !stop; ++c, ++j) {
+            const uint32_t slot = j % kStages;
+            stop = !warp_wait(&S.xfull[slot], (j / kStages) & 1, gave_up, err);
+            if (stop) break;
+            const uint32_t x = tc::smem_u32(S.x[slot]);
+            for (int mt = 0; mt < 2; ++mt, ++a) {              // two tiles of rows, or (Q6_K) the two parts of one
+              const uint32_t sum = C::kQ6 ? u : u + mt;
+              if (c == 0 && !(C::kQ6 && mt)) {
+                stop = !warp_wait(&S.tempty[sum % kUnits], ((sum / kUnits) & 1) ^ 1, gave_up, err);
+                if (stop) break;
+              }
+              stop = !warp_wait(&S.afull[a % kATiles], (a / kATiles) & 1, gave_up, err);
+              if (stop) break;
+              tc::fence_after_sync();
+              const uint32_t d = tmem + kCols * (sum % kUnits), at = tmem + kAColumn + 32 * (a % kATiles);
+              if (elect()) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ts(d, at + 8 * k, tc::desc_sw128(x + 32 * k), what, c | k | (C::kQ6 ? mt : 0) ? 1 : 0);
+                if (!C::kQ6 || mt == 0) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) mma_ts(d, at + 8 * k, tc::desc_sw128(x + padded * 128 + 32 * k), what, 1);
+                }
+                tc::mma_commit(&S.aempty[a % kATiles]);
+                if (mt == 1) tc::mma_commit(&S.xempty[slot]);
+                if (C::kQ6 && mt == 1 && c == 3) tc::mma_commit(&S.tfull[u % kUnits]);
+              }
+              __syncwarp();
+            }
+          }
+          if (stop) break;
+          if constexpr (C::kQ6) {
+            ++u;
+            continue;
+          }
+          stop = !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err);
+          if (stop) break;
+          const uint32_t sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
+          for (int mt = 0; mt < 2; ++mt, ++a, ++u) {
+            stop = !warp_wait(&S.afull[a % kATiles], (a / kATiles) & 1, gave_up, err);
+            if (stop) break;
+            tc::fence_after_sync();
+            const uint32_t d = tmem + kCols * (u % kUnits), at = tmem + kAColumn + 32 * (a % kATiles);
+            if (elect()) {
+              mma_ts(d, at, tc::desc_sw128(sums), what, 1);
+              mma_ts(d, at + 8, tc::desc_sw128(sums), what, 1);
+              tc::mma_commit(&S.aempty[a % kATiles]);
+              tc::mma_commit(&S.tfull[u % kUnits]);
+              if (mt == 1 && ((sb & 3) == 3 || sb == nb - 1)) tc::mma_commit(&S.sempty[g & 1]);
+            }
+            __syncwarp();
+          }
+          if ((sb & 3) == 3 || sb == nb - 1) ++g;
+        }
+      }
+      if (elect()) tc::mma_commit(&S.drain);                   // every product is done before tensor memory goes
+      __syncwarp();
+      if (!tc::mbar_wait_sleep(&S.drain, 0)) atomicOr(err, 1);
+    }
+  } else if (warp < 4 + kConverters) {
+    // --------------------------------------------------------------- converters
+    registers_down<104>();
+    const int quarter = warp & 3, row = 32 * quarter + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + kAColumn;
+    uint32_t n = 0, a = 0, u = 0;                              // raw tiles, A tiles, sums
+    // one A tile's turn: its place is free; it has been written
+    auto free_tile = [&] {
+      const bool ok = warp_wait(&S.aempty[a % kATiles], ((a / kATiles) & 1) ^ 1, gave_up, err);
+      tc::fence_after_sync();
+      return ok;
+    };
+    auto done_tile = [&] {
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&S.afull[a % kATiles]);
+      ++a;
+    };
+    auto scale_of = [&](float v) -> bool {                     // of the sum u, for the epilogue
+      const uint32_t s = u % kScaleSlots;
+      if (!warp_wait(&S.dempty[s], ((u / kScaleSlots) & 1) ^ 1, gave_up, err)) return false;
+      S.scale[s][row] = v;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&S.dfull[s]);
+      ++u;
+      return true;
+    };
+    bool stop = false;
+    while (!stop && next_item()) {
+      const uint8_t* d_at = nullptr;
+      if constexpr (C::kQ6)
+        d_at = P.scales + (T.expert * (int64_t)P.rows + min(block * C::kOutRows + row, P.rows - 1)) * P.pitch;
+      for (int sb = 0; sb < nb && !stop; ++sb, n += C::kTilesM) {
+        const uint32_t slot = n % C::kRaw;
+        if constexpr (C::kQ6) {
+          const float d = __half2float(reinterpret_cast<const __half*>(d_at)[sb]);
+          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err);
+          if (stop) break;
+          const uint8_t* w = S.raw[slot] + row * C::kSb;
+          const uint4 sc = *reinterpret_cast<const uint4*>(w);
+          const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+          stop = !scale_of(d);
+          if (stop) break;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const uint4* p = reinterpret_cast<const uint4*>(w + 16 + 48 * c);
+            const uint4 l0 = p[0], l1 = p[1], h = p[2];
+            uint32_t hi[32], lo[32];
+            convert_q6(l0, l1, h, c == 0 ? scw[0] : c == 1 ? scw[1] : c == 2 ? scw[2] : scw[3], hi, lo);
+            __syncwarp();
+            if (c == 3 && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
+            stop = !free_tile();
+            if (stop) break;
+            tc::tmem_st32(lanes + 32 * (a % kATiles), hi);
+            done_tile();
+            stop = !free_tile();
+            if (stop) break;
+            tc::tmem_st32(lanes + 32 * (a % kATiles), lo);
+            done_tile();
+          }
+        } else {
+          const uint32_t slot1 = (n + 1) % C::kRaw;
+          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err);
+          if (stop) break;
+          stop = !warp_wait(&S.rfull[slot1], ((n + 1) / C::kRaw) & 1, gave_up, err);
+          if (stop) break;
+          const uint8_t* w[2] = {S.raw[slot] + row * C::kSb, S.raw[slot1] + row * C::kSb};
+          Header H[2];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            H[mt] = header_of(*reinterpret_cast<const uint4*>(w[mt]));
+            stop = !scale_of(H[mt].scale);
+            if (stop) break;
+          }
+          if (stop) break;
+#pragma unroll 1
+          for (int c = 0; c < 4 && !stop; ++c) {
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const uint4* p = reinterpret_cast<const uint4*>(w[mt] + 16 + 32 * c);
+              const uint4 q0 = p[0], q1 = p[1];
+              const uint32_t s = c < 2 ? H[mt].sc[0] : H[mt].sc[1];
+              uint32_t v[32];
+              convert_q4(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1)), H[mt].down),
+                         cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1) + 1), H[mt].down), v);
+              if (c == 3) {
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&S.rempty[mt ? slot1 : slot]);
+              }
+              stop = !free_tile();
+              if (stop) break;
+              tc::tmem_st32(lanes + 32 * (a % kATiles), v);
+              done_tile();
+            }
+          }
+          if (stop) break;
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            uint32_t v[16];
+            convert_min(H[mt], v);
+            stop = !free_tile();
+            if (stop) break;
+            tc::tmem_st16(lanes + 32 * (a % kATiles), v);
+            done_tile();
+          }
+        }
+      }
+    }
+  } else {
+    // ----------------------------------------------------------------- epilogue
+    registers_up<184>();
+    const int quarter = warp & 3, row = 32 * quarter + lane, half = (warp - 8) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+    uint32_t u = 0;
+    bool stop = false;
+    while (!stop && next_item()) {
+      // 16 columns at a time, half of them each
+      const int sixteens = (T.n + 15) / 16, first = half ? (sixteens + 1) / 2 : 0, mine = half ? sixteens / 2 : (sixteens + 1) / 2;
+      uint64_t total[C::kTilesM][4][8];
+#pragma unroll
+      for (int mt = 0; mt < C::kTilesM; ++mt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) total[mt][k][i] = 0;
+      for (int sb = 0; sb < nb && !stop; ++sb) {
+#pragma unroll
+        for (int mt = 0; mt < C::kTilesM; ++mt, ++u) {
+          const uint32_t s = u % kScaleSlots, t = u % kUnits;
+          stop = !warp_wait(&S.dfull[s], (u / kScaleSlots) & 1, gave_up, err);
+          if (stop) break;
+          const float d = S.scale[s][row];
+          const uint64_t d2 = pair_of(d, d);
+          stop = !warp_wait(&S.tfull[t], (u / kUnits) & 1, gave_up, err);
+          if (stop) break;
+          tc::fence_after_sync();
+          const uint32_t at = lanes + kCols * t + 16 * first;
+#pragma unroll
+          for (int k = 0; k < 4; k += 2) {
+            if (k < mine) {
+              uint32_t v[2][16];
+              tc::tmem_ld16(at + 16 * k, v[0]);
+              if (k + 1 < mine) tc::tmem_ld16(at + 16 * k + 16, v[1]);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) total[mt][k][i] = fma2(d2, pair_of(v[0][2 * i], v[0][2 * i + 1]), total[mt][k][i]);
+              if (k + 1 < mine)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  total[mt][k + 1][i] = fma2(d2, pair_of(v[1][2 * i], v[1][2 * i + 1]), total[mt][k + 1][i]);
+            }
+          }
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            tc::mbar_arrive(&S.tempty[t]);
+            tc::mbar_arrive(&S.dempty[s]);
+          }
+        }
+      }
+      if (stop) break;
+#pragma unroll
+      for (int mt = 0; mt < (C::kUp ? 1 : C::kTilesM); ++mt) {
+        const int r = block * C::kOutRows + kRows * mt + row;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= mine) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int col = 16 * (first + k) + 2 * i;
+            const float2 inv = *reinterpret_cast<const float2*>(P.inv + T.row + col);
+            float2 v = halves(total[mt][k][i]);
+            v.x *= inv.x, v.y *= inv.y;
+            if constexpr (C::kUp) {
+              const float2 w = halves(total[1][k][i]);
+              v.x = v.x / (1.0f + expf(-v.x)) * (w.x * inv.x), v.y = v.y / (1.0f + expf(-v.y)) * (w.y * inv.y);
+            }
+            if (r < P.rows) {
+              float* out = P.out + (int64_t)(T.first + col) * P.rows + r;
+              if (col < T.n) out[0] = v.x;
+              if (col + 1 < T.n) out[P.rows] = v.y;
+            }
+          }
+        }
+      }
+    }
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// -------------------------------------------------------------------- launches
+inline int64_t most_tiles(int64_t pairs, int experts) { return std::min(pairs, pairs / kCols + experts); }
+inline int64_t most_rows(int64_t pairs, int experts) { return (pairs + 15 * most_tiles(pairs, experts) + 15) / 16 * 16; }
+
+struct Places {               // in the workspace
+  size_t tiles, inv, x, sums, end;
+};
+inline Places places(int64_t pairs, int experts, int64_t cols) {
+  const auto up = [](size_t v) { return (v + 1023) / 1024 * 1024; };
+  const size_t rows = (size_t)most_rows(pairs, experts);
+  Places p{};
+  p.tiles = sizeof(Control);
+  p.inv = up(p.tiles + sizeof(Tile) * (size_t)most_tiles(pairs, experts));
+  p.x = up(p.inv + sizeof(float) * rows);
+  p.sums = p.x + rows * (size_t)cols * 4;
+  p.end = p.sums + rows * (size_t)((cols / kQK + 3) / 4) * 128;
+  return p;
+}
+
+template <int MODE>
+cudaError_t launch(const MoeProduct& p, void* work, float* out, cudaStream_t s) {
+  using C = Cfg<MODE>;
+  static std::atomic<uint64_t> done{0};
+  constexpr int kSmem = (int)sizeof(Smem<MODE>) + 1024;
+  cudaError_t e = allow_smem(moe_many_kernel<MODE>, kSmem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = p.plan.tokens * p.plan.top_k, nb = p.cols / kQK, all = p.rows * p.plan.experts;
+  const int64_t pitch = C::kQ6 ? q6k_gpu_row_bytes(nb) : nb * kBlockBytes, blocks = (p.rows + C::kOutRows - 1) / C::kOutRows;
+  const int64_t tiles = most_tiles(pairs, p.plan.experts);
+  if (tiles * blocks * nb * 16 >= (int64_t(1) << 31)) return cudaErrorNotSupported;        // 32-bit counters
+  uint8_t* at = static_cast<uint8_t*>(work);
+  const Places w = places(pairs, p.plan.experts, p.cols);
+  Control* control = reinterpret_cast<Control*>(at);
+  Tile* list = reinterpret_cast<Tile*>(at + w.tiles);
+  float* inv = reinterpret_cast<float*>(at + w.inv);
+  Params P{};
+  const uint64_t dims[3] = {(uint64_t)C::kSb, (uint64_t)all, (uint64_t)nb}, strides[2] = {(uint64_t)pitch, (uint64_t)C::kSb};
+  const uint32_t box[3] = {(uint32_t)C::kSb, kRows, 1};
+  if (!encode_tmap_u8_3d(&P.w, p.w, dims, strides, box)) return cudaErrorInvalidValue;
+  if (C::kUp && !encode_tmap_u8_3d(&P.up, p.up, dims, strides, box)) return cudaErrorInvalidValue;
+  P.control = control, P.tiles = list, P.inv = inv, P.x = at + w.x, P.sums = at + w.sums;
+  P.scales = p.w + nb * kQ6GpuBytes, P.out = out, P.counter = &control->counter, P.err = p.err, P.pitch = pitch;
+  P.rows = (int)p.rows, P.nb = (int)nb, P.blocks = (int)blocks;
+  const LayoutParams A{p.plan.offsets, control, list, p.err, (int)pairs, p.plan.experts};
+  moe_many_layout_kernel<<<1, kMoeMaxExperts, 0, s>>>(A);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const SplitParams B{p.x, p.plan.order, control, list, at + w.x, at + w.sums, inv, p.err, pairs, p.cols, (int)nb,
+                      C::kUp ? p.plan.top_k : 0};
+  if ((e = launch_after(moe_many_split_kernel<!C::kQ6>, dim3((unsigned)tiles, kCols / 8), 256, 0, s, B)) != cudaSuccess) return e;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  return launch_after(moe_many_kernel<MODE>, dim3((unsigned)std::min<int64_t>(tiles * blocks, device_info(dev).sm_count)), kThreads,
+                      kSmem, s, P);
+}
+
+}  // namespace many
+}  // namespace q4k

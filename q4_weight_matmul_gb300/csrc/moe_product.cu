@@ -3,6 +3,7 @@
 //
 #include "moe.cuh"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace q4k {
@@ -60,24 +61,38 @@ cudaError_t combine(const MoeProduct& p, const float* z, cudaStream_t s) {
 
 }  // namespace
 
-// The down products' rows, before they are put together, lie behind the operands.
+// Many pairs an expert go to the tensor cores' tiles of up to 128 pairs, few
+// to the kernel that streams the weights once per 16 pairs.
+constexpr int64_t kMany = 24;
+static bool many(int64_t tokens, int top_k, int experts) { return tokens * top_k >= kMany * experts; }
+
+// Operands for any number of pairs up to this one.
+static size_t operands(int64_t tokens, int top_k, int experts, int64_t cols) {
+  const int64_t pairs = tokens * top_k;
+  const size_t few = moe_few_workspace(std::min(pairs, kMany * experts), experts, cols);
+  return many(tokens, top_k, experts) ? std::max(few, moe_many_workspace(pairs, experts, cols)) : few;
+}
+// The down products' rows, before they are put together, lie behind them.
 static size_t rows_at(size_t operands) { return (operands + 255) / 256 * 256; }
 
 size_t moe_gate_up_workspace(int64_t tokens, int top_k, int experts, int64_t, int64_t cols) {
-  return moe_few_workspace(tokens * top_k, experts, cols);
+  return operands(tokens, top_k, experts, cols);
 }
 size_t moe_down_workspace(int64_t tokens, int top_k, int experts, int64_t rows, int64_t cols) {
-  return rows_at(moe_few_workspace(tokens * top_k, experts, cols)) + sizeof(float) * (size_t)(tokens * top_k) * (size_t)rows;
+  return rows_at(operands(tokens, top_k, experts, cols)) + sizeof(float) * (size_t)(tokens * top_k) * (size_t)rows;
 }
 
 cudaError_t launch_moe_gate_up(const MoeProduct& p, cudaStream_t s) {
+  if (many(p.plan.tokens, p.plan.top_k, p.plan.experts)) return launch_moe_many_gate_up(p, p.workspace, p.out, s);
   return launch_moe_few_gate_up(p, p.workspace, p.out, s);
 }
 
 cudaError_t launch_moe_down(const MoeProduct& p, cudaStream_t s) {
   float* z = reinterpret_cast<float*>(static_cast<uint8_t*>(p.workspace) +
-                                      rows_at(moe_few_workspace(p.plan.tokens * p.plan.top_k, p.plan.experts, p.cols)));
-  cudaError_t e = p.q6k ? launch_moe_few_down_q6(p, p.workspace, z, s) : launch_moe_few_down_q4(p, p.workspace, z, s);
+                                      rows_at(operands(p.plan.tokens, p.plan.top_k, p.plan.experts, p.cols)));
+  const bool m = many(p.plan.tokens, p.plan.top_k, p.plan.experts);
+  cudaError_t e = p.q6k ? (m ? launch_moe_many_down_q6 : launch_moe_few_down_q6)(p, p.workspace, z, s)
+                        : (m ? launch_moe_many_down_q4 : launch_moe_few_down_q4)(p, p.workspace, z, s);
   if (e != cudaSuccess) return e;
   return combine(p, z, s);
 }
