@@ -26,6 +26,10 @@ inline cudaError_t launch_after(K* kernel, dim3 grid, int threads, size_t smem, 
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// v / (1 + exp(-v)), within some 2e-6 of it where it is not negligible; 0 for
+// v far below 0 (exp(-v) infinite).
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+
 // A warp agrees on a wait's outcome, so that its lanes stay together; one that
 // gives up raises the block's flag and the device error word.
 __device__ __forceinline__ bool agreed(bool ok, volatile int* gave_up, int* err) {

@@ -570,7 +570,7 @@ __device__ __forceinline__ bool consume(const Params& P, Head& H, float* part, c
         const int col = 8 * n + 2 * c + (j & 1);
         if (row < P.rows && col < it.n) {
           float v = total[t][n][j];
-          if constexpr (C::kUp) v = v / (1.0f + expf(-v)) * total[1][n][j];
+          if constexpr (C::kUp) v = silu(v) * total[1][n][j];
           P.out[(int64_t)(it.first + col) * P.rows + row] = v;
         }
       }

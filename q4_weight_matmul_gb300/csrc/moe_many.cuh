@@ -24,10 +24,12 @@
 // (-1, 0, 1), two tiles that meet the hi and lo, and the hi parts of x.
 //
 // A CTA's warps: 0 copies activations, 2 weights, 3 draws items (a tile of
-// pairs times a block of rows; large tiles first), 1 issues the products, 4-7
-// convert, 8-15 run the epilogue (64 columns a thread; totals in registers).
-// Tensor memory: three sums of 128 columns in turn, four tiles of A (128 rows x
-// 64 k) in turn.  Every wait is bounded.
+// pairs times a block of rows; large tiles first), 1 issues the products, 4-11
+// convert (two groups of four that take A tiles in turn: with one, 700 cycles a
+// tile held the products up, 547 us for 4096 tokens), 12-19 run the epilogue
+// (64 columns a thread; totals in registers).
+// Tensor memory: three sums of 128 columns in turn, A of two steps (two tiles of
+// 128 rows x 64 k each) in turn.  Every wait is bounded.
 #pragma once
 
 #include "mma_sync.cuh"
@@ -42,13 +44,17 @@ namespace many {
 
 enum Mode { kGateUp, kDownQ4, kDownQ6 };
 
-constexpr int kThreads = 512;
 constexpr int kRows = 128, kCols = 128;       // of a product: weight rows, pairs
 constexpr int kStages = 4, kStageBytes = 2 * kCols * 128;   // 64 k of the activations, hi and lo
 constexpr int kSumBytes = kCols * 128;        // the sums of four superblocks, 32 bytes a pair each
-constexpr int kATiles = 4, kUnits = 3, kScaleSlots = 4, kQueue = 4;
+constexpr int kUnits = 3, kQueue = 4;
+// The products' steps: 64 k of both A tiles (Q6_K: of both parts), or (Q4_K, a
+// superblock's fifth) its min term.  A step's two A tiles take one of two
+// places; one commit a step says that its operands are free.
+constexpr int kDone = 8;
 constexpr uint32_t kAColumn = kUnits * kCols; // of the first A tile in tensor memory
-constexpr int kConverters = 4, kEpilogue = 8; // warps
+constexpr int kConverters = 8, kEpilogue = 8; // warps
+constexpr int kThreads = 32 * (4 + kConverters + kEpilogue);
 constexpr uint32_t kProduct = (1u << 4) | ((uint32_t)(kRows >> 4) << 24);      // f16 operands, f32 sums, 128 rows
 
 struct Tile {                 // pairs first .. first + n - 1 of an expert; their padded rows from `row` on
@@ -60,6 +66,7 @@ struct Control {
 
 template <int MODE>
 struct Cfg {
+  static constexpr int kSteps = MODE == kDownQ6 ? 4 : 5;     // of a superblock
   static constexpr bool kUp = MODE == kGateUp, kQ6 = MODE == kDownQ6;
   static constexpr int kSb = kQ6 ? kQ6GpuBytes : kBlockBytes;
   static constexpr int kRaw = kQ6 ? 2 : 3;                   // weight tiles (128 rows of a superblock) in flight
@@ -85,9 +92,9 @@ struct __align__(1024) Smem {
   uint8_t x[kStages][kStageBytes];
   uint8_t sums[2][kSumBytes];
   uint8_t raw[Cfg<MODE>::kRaw][kRows * Cfg<MODE>::kSb];
-  float scale[kScaleSlots][kRows];
-  uint64_t xfull[kStages], xempty[kStages], sfull[2], sempty[2], rfull[3], rempty[3], afull[kATiles], aempty[kATiles],
-      tfull[kUnits], tempty[kUnits], dfull[kScaleSlots], dempty[kScaleSlots], qfull[kQueue], qempty[kQueue], drain;
+  float scale[2][2][kRows];
+  uint64_t xfull[kStages], sfull[2], sempty[2], rfull[3], rempty[3], afull[2], done[kDone], tfull[2], tempty[kUnits],
+      dfull[2], dempty[2], qfull[kQueue], qempty[kQueue], drain;
   Tile item[kQueue];
   int block[kQueue];
   uint32_t tmem;
@@ -255,25 +262,20 @@ __global__ void __launch_bounds__(256) moe_many_split_kernel(const SplitParams P
 }
 
 // ------------------------------------------------------------- converters
-// 64 weights of a Q4_K row (32 quant bytes, sub-blocks 2 c and 2 c + 1) as
-// sc q 2^-e, pairs (0, 2), (1, 3) of every four.
-__device__ __forceinline__ void convert_q4(const uint4& q0, const uint4& q1, uint32_t s_low, uint32_t s_high,
-                                           uint32_t (&a)[32]) {
+// 32 weights of a Q4_K row (the low or high nibbles of 32 quant bytes) times
+// their scale s, pairs (0, 2), (1, 3) of every four.
+template <bool HIGH>
+__device__ __forceinline__ void convert_q4(const uint4& q0, const uint4& q1, uint32_t s, uint32_t (&a)[16]) {
   // (1024 + q) s - 1024 s, (1024 + 16 q) s / 16 - 64 s: one exact FMA each
-  const uint32_t b_low = cvt::mul_h2(s_low, 0xE400E400u), m_high = cvt::mul_h2(s_high, 0x2C002C00u),
-                 b_high = cvt::mul_h2(s_high, 0xD400D400u);
+  const uint32_t m = HIGH ? cvt::mul_h2(s, 0x2C002C00u) : s, b = cvt::mul_h2(s, HIGH ? 0xD400D400u : 0xE400E400u);
   const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t u = w[i] >> 8;
-    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
-        : "=r"(a[2 * i]) : "r"(w[i]), "r"(s_low), "r"(b_low));
-    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x000F000F, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
-        : "=r"(a[2 * i + 1]) : "r"(u), "r"(s_low), "r"(b_low));
-    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
-        : "=r"(a[16 + 2 * i]) : "r"(w[i]), "r"(m_high), "r"(b_high));
-    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, 0x00F000F0, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
-        : "=r"(a[16 + 2 * i + 1]) : "r"(u), "r"(m_high), "r"(b_high));
+    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, %4, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
+        : "=r"(a[2 * i]) : "r"(w[i]), "r"(m), "r"(b), "n"(HIGH ? 0x00F000F0 : 0x000F000F));
+    asm("{\n\t.reg .b32 t;\n\tlop3.b32 t, %1, %4, 0x64006400, 0xEA;\n\tfma.rn.f16x2 %0, t, %2, %3;\n\t}"
+        : "=r"(a[2 * i + 1]) : "r"(u), "r"(m), "r"(b), "n"(HIGH ? 0x00F000F0 : 0x000F000F));
   }
 }
 
@@ -287,7 +289,7 @@ __device__ __forceinline__ Header header_of(const uint4& h) {
   Header H;
   cvt::header_sc_m(h, H.sc[0], H.sc[1], H.m[0], H.m[1]);
   const float2 d = unpack2<false>(h.x);                        // d, dmin
-  H.r = -64.0f * d.y / d.x;
+  H.r = __fdividef(-64.0f * d.y, d.x);                         // (within 2^-22)
   H.scale = d.x;
   H.down = 0x3C003C00u;
   if (!(fabsf(H.r) <= 1024.0f) && d.y != 0.0f) {               // |r| > 16, or d = 0
@@ -318,26 +320,26 @@ __device__ __forceinline__ void convert_min(const Header& H, uint32_t (&a)[16]) 
   }
 }
 
-// 64 weights of a Q6_K row (chunk c: 32 bytes of low nibbles, 16 of bit pairs)
-// as the parts of sc (q - 32), in order.
-__device__ __forceinline__ void convert_q6(const uint4& l0, const uint4& l1, const uint4& h, uint32_t scales,
-                                           uint32_t (&hi)[32], uint32_t (&lo)[32]) {
+// Sub-block S (32 weights) of a Q6_K row's chunk (32 bytes of low nibbles, 16
+// of bit pairs; `scales` of its groups) as the parts of sc (q - 32), in order.
+__device__ __forceinline__ void convert_q6(const uint4& l0, const uint4& l1, const uint4& h, uint32_t scales, int S,
+                                           uint32_t (&hi)[16], uint32_t (&lo)[16]) {
   const uint32_t lw[8] = {l0.x, l0.y, l0.z, l0.w, l1.x, l1.y, l1.z, l1.w}, hw[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {                                // group f: sub-block f / 2, half f % 2
-    const float sf = (float)(int8_t)(scales >> (8 * f));
+  for (int g = 0; g < 2; ++g) {                                // the sub-block's groups of 16
+    const float sf = (float)(int8_t)(scales >> (16 * S + 8 * g));
     const __half2 sc = __float2half2_rn(sf), bias = __float2half2_rn(-1056.0f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // bytes of q with the top bit inverted, then two at a time under the exponent of 1024
-      const uint32_t v = ((lw[4 * (f & 1) + i] >> (4 * (f >> 1))) & 0x0F0F0F0Fu) | (((hw[i] >> (2 * f)) & 0x03030303u) << 4);
+      const uint32_t v = ((lw[4 * g + i] >> (4 * S)) & 0x0F0F0F0Fu) | (((hw[i] >> (4 * S + 2 * g)) & 0x03030303u) << 4);
       const uint32_t p0 = __byte_perm(v, 0, 0x4140) ^ 0x64206420u, p1 = __byte_perm(v, 0, 0x4342) ^ 0x64206420u;
       const __half2 q0 = __hadd2(*reinterpret_cast<const __half2*>(&p0), bias),
                     q1 = __hadd2(*reinterpret_cast<const __half2*>(&p1), bias);
       const __half2 h0 = __hmul2(q0, sc), h1 = __hmul2(q1, sc);
       const __half2 r0 = __hfma2(q0, sc, __hneg2(h0)), r1 = __hfma2(q1, sc, __hneg2(h1));
-      hi[8 * f + 2 * i] = *reinterpret_cast<const uint32_t*>(&h0), hi[8 * f + 2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-      lo[8 * f + 2 * i] = *reinterpret_cast<const uint32_t*>(&r0), lo[8 * f + 2 * i + 1] = *reinterpret_cast<const uint32_t*>(&r1);
+      hi[8 * g + 2 * i] = *reinterpret_cast<const uint32_t*>(&h0), hi[8 * g + 2 * i + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+      lo[8 * g + 2 * i] = *reinterpret_cast<const uint32_t*>(&r0), lo[8 * g + 2 * i + 1] = *reinterpret_cast<const uint32_t*>(&r1);
     }
   }
 }
@@ -354,12 +356,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(&S.xfull[i], 1), tc::mbar_init(&S.xempty[i], 1);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(&S.sfull[i], 1), tc::mbar_init(&S.sempty[i], 1);
-    for (int i = 0; i < C::kRaw; ++i) tc::mbar_init(&S.rfull[i], 1), tc::mbar_init(&S.rempty[i], kConverters);
-    for (int i = 0; i < kATiles; ++i) tc::mbar_init(&S.afull[i], kConverters), tc::mbar_init(&S.aempty[i], 1);
-    for (int i = 0; i < kUnits; ++i) tc::mbar_init(&S.tfull[i], 1), tc::mbar_init(&S.tempty[i], kEpilogue);
-    for (int i = 0; i < kScaleSlots; ++i) tc::mbar_init(&S.dfull[i], kConverters), tc::mbar_init(&S.dempty[i], kEpilogue);
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(&S.xfull[i], 1);
+    for (int i = 0; i < kDone; ++i) tc::mbar_init(&S.done[i], 1);
+    for (int i = 0; i < C::kRaw; ++i) tc::mbar_init(&S.rfull[i], 1), tc::mbar_init(&S.rempty[i], C::kQ6 ? kConverters : kConverters / 2);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&S.sfull[i], 1), tc::mbar_init(&S.sempty[i], 1), tc::mbar_init(&S.tfull[i], 1);
+      tc::mbar_init(&S.afull[i], kConverters);
+      tc::mbar_init(&S.dfull[i], C::kQ6 ? kConverters / 2 : kConverters), tc::mbar_init(&S.dempty[i], kEpilogue);
+    }
+    for (int i = 0; i < kUnits; ++i) tc::mbar_init(&S.tempty[i], kEpilogue);
     for (int i = 0; i < kQueue; ++i) tc::mbar_init(&S.qfull[i], 1), tc::mbar_init(&S.qempty[i], 3 + kConverters + kEpilogue);
     tc::mbar_init(&S.drain, 1);
     *gave_up = 0;
@@ -389,9 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
     return T.n > 0;
   };
 
-  // 512 threads x 128 registers at launch = 128 x 40 + 128 x 104 + 256 x 184
+  // Until step `k` is done with its operands.
+  auto step_done = [&](uint32_t k) { return warp_wait(&S.done[k % kDone], (k / kDone) & 1, gave_up, err); };
+
+  // 640 threads x 96 registers at launch = 128 x 32 + 256 x 64 + 256 x 160
   if (warp < 4) {
-    registers_down<40>();
+    registers_down<32>();
     if (warp == 0) {
       // ------------------------------------------------------ activations
       uint32_t j = 0, g = 0;                                   // stages, groups of sums issued
@@ -412,7 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
             ++g;
           }
           const uint32_t slot = j % kStages;
-          stop = !warp_wait(&S.xempty[slot], ((j / kStages) & 1) ^ 1, gave_up, err);
+          // (four stages before: the same 64 k of the superblock before)
+          stop = j >= kStages && !step_done((j / 4 - 1) * C::kSteps + j % 4);
           if (stop) break;
           if (elect()) {
             tc::mbar_arrive_expect_tx(&S.xfull[slot], 2 * padded * 128);
@@ -470,64 +479,67 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
       }
     } else {
       // --------------------------------------------------------- products
-      uint32_t j = 0, g = 0, a = 0, u = 0;                     // stages, groups of sums, A tiles, sums
+      uint32_t j = 0, g = 0, k = 0, u = 0, b = 0;              // stages, groups of sums, steps, sums, superblocks
       bool stop = false;
+      // the tensor memory of sum i is free
+      auto sum_free = [&](uint32_t i) { return warp_wait(&S.tempty[i % kUnits], ((i / kUnits) & 1) ^ 1, gave_up, err); };
       while (!stop && next_item()) {
         const uint32_t padded = (T.n + 15) / 16 * 16, what = kProduct | (padded >> 3) << 17;
-        for (int sb = 0; sb < nb && !stop; ++sb) {
-          for (int c = 0; c < 4 && !stop; ++c, ++j) {
-            const uint32_t slot = j % kStages;
-            stop = !warp_wait(&S.xfull[slot], (j / kStages) & 1, gave_up, err);
+        for (int sb = 0; sb < nb && !stop; ++sb, ++b) {
+          const uint32_t d0 = tmem + kCols * (u % kUnits), d1 = C::kQ6 ? d0 : tmem + kCols * ((u + 1) % kUnits);
+          for (int c = 0; c < 4; ++c, ++j, ++k) {
+            const uint32_t slot = j % kStages, x = tc::smem_u32(S.x[slot]), a = tmem + kAColumn + 64 * (k & 1);
+            stop = !warp_wait(&S.xfull[slot], (j / kStages) & 1, gave_up, err) || (c == 0 && !sum_free(u)) ||
+                   !warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
             if (stop) break;
-            const uint32_t x = tc::smem_u32(S.x[slot]);
-            for (int mt = 0; mt < 2; ++mt, ++a) {              // two tiles of rows, or (Q6_K) the two parts of one
-              const uint32_t sum = C::kQ6 ? u : u + mt;
-              if (c == 0 && !(C::kQ6 && mt)) {
-                stop = !warp_wait(&S.tempty[sum % kUnits], ((sum / kUnits) & 1) ^ 1, gave_up, err);
-                if (stop) break;
-              }
-              stop = !warp_wait(&S.afull[a % kATiles], (a / kATiles) & 1, gave_up, err);
+            tc::fence_after_sync();
+            if (elect()) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma_ts(d0, a + 8 * i, tc::desc_sw128(x + 32 * i), what, c | i ? 1 : 0);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) mma_ts(d0, a + 8 * i, tc::desc_sw128(x + padded * 128 + 32 * i), what, 1);
+            }
+            __syncwarp();
+            if (!C::kQ6 && c == 0) {
+              stop = !sum_free(u + 1);
               if (stop) break;
               tc::fence_after_sync();
-              const uint32_t d = tmem + kCols * (sum % kUnits), at = tmem + kAColumn + 32 * (a % kATiles);
-              if (elect()) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ts(d, at + 8 * k, tc::desc_sw128(x + 32 * k), what, c | k | (C::kQ6 ? mt : 0) ? 1 : 0);
-                if (!C::kQ6 || mt == 0) {
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) mma_ts(d, at + 8 * k, tc::desc_sw128(x + padded * 128 + 32 * k), what, 1);
-                }
-                tc::mma_commit(&S.aempty[a % kATiles]);
-                if (mt == 1) tc::mma_commit(&S.xempty[slot]);
-                if (C::kQ6 && mt == 1 && c == 3) tc::mma_commit(&S.tfull[u % kUnits]);
-              }
-              __syncwarp();
             }
+            if (elect()) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                mma_ts(d1, a + 32 + 8 * i, tc::desc_sw128(x + 32 * i), what, C::kQ6 || (c | i) ? 1 : 0);
+              if constexpr (!C::kQ6) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) mma_ts(d1, a + 32 + 8 * i, tc::desc_sw128(x + padded * 128 + 32 * i), what, 1);
+              }
+              tc::mma_commit(&S.done[k % kDone]);
+              if (C::kQ6 && c == 3) tc::mma_commit(&S.tfull[b & 1]);
+            }
+            __syncwarp();
           }
           if (stop) break;
           if constexpr (C::kQ6) {
             ++u;
             continue;
           }
-          stop = !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err);
+          const uint32_t a = tmem + kAColumn + 64 * (k & 1), sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
+          stop = !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err) ||
+                 !warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
           if (stop) break;
-          const uint32_t sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
-          for (int mt = 0; mt < 2; ++mt, ++a, ++u) {
-            stop = !warp_wait(&S.afull[a % kATiles], (a / kATiles) & 1, gave_up, err);
-            if (stop) break;
-            tc::fence_after_sync();
-            const uint32_t d = tmem + kCols * (u % kUnits), at = tmem + kAColumn + 32 * (a % kATiles);
-            if (elect()) {
-              mma_ts(d, at, tc::desc_sw128(sums), what, 1);
-              mma_ts(d, at + 8, tc::desc_sw128(sums), what, 1);
-              tc::mma_commit(&S.aempty[a % kATiles]);
-              tc::mma_commit(&S.tfull[u % kUnits]);
-              if (mt == 1 && ((sb & 3) == 3 || sb == nb - 1)) tc::mma_commit(&S.sempty[g & 1]);
-            }
-            __syncwarp();
+          tc::fence_after_sync();
+          const bool last = (sb & 3) == 3 || sb == nb - 1;
+          if (elect()) {
+            mma_ts(d0, a, tc::desc_sw128(sums), what, 1);
+            mma_ts(d0, a + 8, tc::desc_sw128(sums), what, 1);
+            mma_ts(d1, a + 32, tc::desc_sw128(sums), what, 1);
+            mma_ts(d1, a + 40, tc::desc_sw128(sums), what, 1);
+            tc::mma_commit(&S.tfull[b & 1]);
+            tc::mma_commit(&S.done[k % kDone]);
+            if (last) tc::mma_commit(&S.sempty[g & 1]);
           }
-          if ((sb & 3) == 3 || sb == nb - 1) ++g;
+          __syncwarp();
+          ++k, u += 2, g += last;
         }
       }
       if (elect()) tc::mma_commit(&S.drain);                   // every product is done before tensor memory goes
@@ -536,123 +548,106 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
     }
   } else if (warp < 4 + kConverters) {
     // --------------------------------------------------------------- converters
-    registers_down<104>();
-    const int quarter = warp & 3, row = 32 * quarter + lane;
+    registers_down<64>();
+    const int quarter = warp & 3, group = (warp - 4) >> 2, row = 32 * quarter + lane;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + kAColumn;
-    uint32_t n = 0, a = 0, u = 0;                              // raw tiles, A tiles, sums
-    // one A tile's turn: its place is free; it has been written
-    auto free_tile = [&] {
-      const bool ok = warp_wait(&S.aempty[a % kATiles], ((a / kATiles) & 1) ^ 1, gave_up, err);
+    uint32_t n = 0, k = 0, b = 0;                              // raw tiles, steps, superblocks
+    // step k's A tiles may be written; they have been
+    auto begin_step = [&] {
+      const bool ok = k < 2 || step_done(k - 2);
       tc::fence_after_sync();
       return ok;
     };
-    auto done_tile = [&] {
+    auto end_step = [&] {
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&S.afull[a % kATiles]);
-      ++a;
+      if (lane == 0) tc::mbar_arrive(&S.afull[k & 1]);
+      ++k;
     };
-    auto scale_of = [&](float v) -> bool {                     // of the sum u, for the epilogue
-      const uint32_t s = u % kScaleSlots;
-      if (!warp_wait(&S.dempty[s], ((u / kScaleSlots) & 1) ^ 1, gave_up, err)) return false;
-      S.scale[s][row] = v;
+    auto scale_of = [&](int mt, float v) -> bool {             // of a superblock's sum, for the epilogue
+      if (!warp_wait(&S.dempty[b & 1], ((b >> 1) & 1) ^ 1, gave_up, err)) return false;
+      S.scale[b & 1][mt][row] = v;
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&S.dfull[s]);
-      ++u;
+      if (lane == 0) tc::mbar_arrive(&S.dfull[b & 1]);
       return true;
     };
     bool stop = false;
     while (!stop && next_item()) {
-      const uint8_t* d_at = nullptr;
-      if constexpr (C::kQ6)
-        d_at = P.scales + (T.expert * (int64_t)P.rows + min(block * C::kOutRows + row, P.rows - 1)) * P.pitch;
-      for (int sb = 0; sb < nb && !stop; ++sb, n += C::kTilesM) {
-        const uint32_t slot = n % C::kRaw;
-        if constexpr (C::kQ6) {
-          const float d = __half2float(reinterpret_cast<const __half*>(d_at)[sb]);
-          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err);
+      if constexpr (C::kQ6) {
+        // a group makes the operands of one sub-block of every 64 k: half of the hi tile and of the lo tile
+        const __half* scales = reinterpret_cast<const __half*>(
+            P.scales + (T.expert * (int64_t)P.rows + min(block * C::kOutRows + row, P.rows - 1)) * P.pitch);
+        for (int sb = 0; sb < nb && !stop; ++sb, ++n, ++b) {
+          const uint32_t slot = n % C::kRaw;
+          const float d = __half2float(scales[sb]);
+          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err) || (group == 0 && !scale_of(0, d));
           if (stop) break;
           const uint8_t* w = S.raw[slot] + row * C::kSb;
-          const uint4 sc = *reinterpret_cast<const uint4*>(w);
-          const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
-          stop = !scale_of(d);
-          if (stop) break;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             const uint4* p = reinterpret_cast<const uint4*>(w + 16 + 48 * c);
             const uint4 l0 = p[0], l1 = p[1], h = p[2];
-            uint32_t hi[32], lo[32];
-            convert_q6(l0, l1, h, c == 0 ? scw[0] : c == 1 ? scw[1] : c == 2 ? scw[2] : scw[3], hi, lo);
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(w + 4 * c), at = lanes + 64 * (k & 1) + 16 * group;
             __syncwarp();
             if (c == 3 && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
-            stop = !free_tile();
+            uint32_t hi[16], lo[16];
+            convert_q6(l0, l1, h, sc, group, hi, lo);
+            stop = !begin_step();
             if (stop) break;
-            tc::tmem_st32(lanes + 32 * (a % kATiles), hi);
-            done_tile();
-            stop = !free_tile();
-            if (stop) break;
-            tc::tmem_st32(lanes + 32 * (a % kATiles), lo);
-            done_tile();
+            tc::tmem_st16(at, hi);
+            tc::tmem_st16(at + 32, lo);
+            end_step();
           }
-        } else {
-          const uint32_t slot1 = (n + 1) % C::kRaw;
-          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err);
+        }
+      } else {
+        // a group has one of the two tiles of rows
+        for (int sb = 0; sb < nb && !stop; ++sb, n += 2, ++b) {
+          const uint32_t slot = (n + group) % C::kRaw;
+          stop = !warp_wait(&S.rfull[slot], ((n + group) / C::kRaw) & 1, gave_up, err);
           if (stop) break;
-          stop = !warp_wait(&S.rfull[slot1], ((n + 1) / C::kRaw) & 1, gave_up, err);
-          if (stop) break;
-          const uint8_t* w[2] = {S.raw[slot] + row * C::kSb, S.raw[slot1] + row * C::kSb};
-          Header H[2];
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            H[mt] = header_of(*reinterpret_cast<const uint4*>(w[mt]));
-            stop = !scale_of(H[mt].scale);
-            if (stop) break;
-          }
-          if (stop) break;
+          const uint8_t* w = S.raw[slot] + row * C::kSb;
+          const Header H = header_of(*reinterpret_cast<const uint4*>(w));
 #pragma unroll 1
-          for (int c = 0; c < 4 && !stop; ++c) {
-#pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-              const uint4* p = reinterpret_cast<const uint4*>(w[mt] + 16 + 32 * c);
-              const uint4 q0 = p[0], q1 = p[1];
-              const uint32_t s = c < 2 ? H[mt].sc[0] : H[mt].sc[1];
-              uint32_t v[32];
-              convert_q4(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1)), H[mt].down),
-                         cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1) + 1), H[mt].down), v);
-              if (c == 3) {
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&S.rempty[mt ? slot1 : slot]);
-              }
-              stop = !free_tile();
-              if (stop) break;
-              tc::tmem_st32(lanes + 32 * (a % kATiles), v);
-              done_tile();
-            }
+          for (int c = 0; c < 4; ++c) {
+            const uint4* p = reinterpret_cast<const uint4*>(w + 16 + 32 * c);
+            const uint4 q0 = p[0], q1 = p[1];
+            __syncwarp();
+            if (c == 3 && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
+            const uint32_t s = c < 2 ? H.sc[0] : H.sc[1], at = lanes + 64 * (k & 1) + 32 * group;
+            uint32_t v[16];
+            convert_q4<false>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1)), H.down), v);
+            stop = !begin_step();
+            if (stop) break;
+            tc::tmem_st16(at, v);
+            convert_q4<true>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1) + 1), H.down), v);
+            tc::tmem_st16(at + 16, v);
+            end_step();
           }
           if (stop) break;
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
-            uint32_t v[16];
-            convert_min(H[mt], v);
-            stop = !free_tile();
-            if (stop) break;
-            tc::tmem_st16(lanes + 32 * (a % kATiles), v);
-            done_tile();
-          }
+          uint32_t v[16];
+          convert_min(H, v);
+          stop = !scale_of(group, H.scale) || !begin_step();
+          if (stop) break;
+          tc::tmem_st16(lanes + 64 * (k & 1) + 32 * group, v);
+          end_step();
         }
       }
     }
   } else {
     // ----------------------------------------------------------------- epilogue
-    registers_up<184>();
-    const int quarter = warp & 3, row = 32 * quarter + lane, half = (warp - 8) >> 2;
+    registers_up<160>();
+    const int quarter = warp & 3, row = 32 * quarter + lane, half = (warp - 4 - kConverters) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-    uint32_t u = 0;
+    uint32_t u = 0, b = 0;                                     // sums, superblocks
     bool stop = false;
     while (!stop && next_item()) {
       // 16 columns at a time, half of them each
       const int sixteens = (T.n + 15) / 16, first = half ? (sixteens + 1) / 2 : 0, mine = half ? sixteens / 2 : (sixteens + 1) / 2;
+      // the powers of two to take off: column 32 i + lane of the warp's in inv[i]
+      float inv[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) inv[i] = 32 * i + lane < 16 * mine ? P.inv[T.row + 16 * first + 32 * i + lane] : 0.0f;
       uint64_t total[C::kTilesM][4][8];
 #pragma unroll
       for (int mt = 0; mt < C::kTilesM; ++mt)
@@ -660,38 +655,32 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int i = 0; i < 8; ++i) total[mt][k][i] = 0;
-      for (int sb = 0; sb < nb && !stop; ++sb) {
+      for (int sb = 0; sb < nb; ++sb, ++b) {
+        stop = !warp_wait(&S.tfull[b & 1], (b >> 1) & 1, gave_up, err) ||
+               !warp_wait(&S.dfull[b & 1], (b >> 1) & 1, gave_up, err);
+        if (stop) break;
+        tc::fence_after_sync();
 #pragma unroll
         for (int mt = 0; mt < C::kTilesM; ++mt, ++u) {
-          const uint32_t s = u % kScaleSlots, t = u % kUnits;
-          stop = !warp_wait(&S.dfull[s], (u / kScaleSlots) & 1, gave_up, err);
-          if (stop) break;
-          const float d = S.scale[s][row];
+          const uint32_t t = u % kUnits;
+          const float d = S.scale[b & 1][mt][row];
           const uint64_t d2 = pair_of(d, d);
-          stop = !warp_wait(&S.tfull[t], (u / kUnits) & 1, gave_up, err);
-          if (stop) break;
-          tc::fence_after_sync();
           const uint32_t at = lanes + kCols * t + 16 * first;
 #pragma unroll
-          for (int k = 0; k < 4; k += 2) {
+          for (int k = 0; k < 4; ++k) {
             if (k < mine) {
-              uint32_t v[2][16];
-              tc::tmem_ld16(at + 16 * k, v[0]);
-              if (k + 1 < mine) tc::tmem_ld16(at + 16 * k + 16, v[1]);
+              uint32_t v[16];
+              tc::tmem_ld16(at + 16 * k, v);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) total[mt][k][i] = fma2(d2, pair_of(v[0][2 * i], v[0][2 * i + 1]), total[mt][k][i]);
-              if (k + 1 < mine)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  total[mt][k + 1][i] = fma2(d2, pair_of(v[1][2 * i], v[1][2 * i + 1]), total[mt][k + 1][i]);
+              for (int i = 0; i < 8; ++i) total[mt][k][i] = fma2(d2, pair_of(v[2 * i], v[2 * i + 1]), total[mt][k][i]);
             }
           }
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) {
             tc::mbar_arrive(&S.tempty[t]);
-            tc::mbar_arrive(&S.dempty[s]);
+            if (mt == C::kTilesM - 1) tc::mbar_arrive(&S.dempty[b & 1]);
           }
         }
       }
@@ -705,12 +694,13 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int col = 16 * (first + k) + 2 * i;
-            const float2 inv = *reinterpret_cast<const float2*>(P.inv + T.row + col);
+            const float i0 = __shfl_sync(~0u, inv[k >> 1], (16 * k + 2 * i) & 31),
+                        i1 = __shfl_sync(~0u, inv[k >> 1], (16 * k + 2 * i + 1) & 31);
             float2 v = halves(total[mt][k][i]);
-            v.x *= inv.x, v.y *= inv.y;
+            v.x *= i0, v.y *= i1;
             if constexpr (C::kUp) {
               const float2 w = halves(total[1][k][i]);
-              v.x = v.x / (1.0f + expf(-v.x)) * (w.x * inv.x), v.y = v.y / (1.0f + expf(-v.y)) * (w.y * inv.y);
+              v.x = silu(v.x) * (w.x * i0), v.y = silu(v.y) * (w.y * i1);
             }
             if (r < P.rows) {
               float* out = P.out + (int64_t)(T.first + col) * P.rows + r;
