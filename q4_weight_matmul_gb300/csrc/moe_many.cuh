@@ -115,6 +115,12 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d), "r"(a), "l"(b), "r"(what), "r"(add) : "memory");
 }
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -483,14 +489,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
       bool stop = false;
       // the tensor memory of sum i is free
       auto sum_free = [&](uint32_t i) { return warp_wait(&S.tempty[i % kUnits], ((i / kUnits) & 1) ^ 1, gave_up, err); };
+      // The operands of a step are there: `now` asks without waiting, while the
+      // products before it still run (a wait takes some 130 cycles even then,
+      // and the queue of products is short).
+      auto arrived = [&](uint64_t* other, uint32_t parity, bool now) {
+        if (now) return __all_sync(~0u, mbar_test(other, parity) && mbar_test(&S.afull[k & 1], (k >> 1) & 1)) != 0;
+        return warp_wait(other, parity, gave_up, err) && warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
+      };
+      bool ready = false;
       while (!stop && next_item()) {
         const uint32_t padded = (T.n + 15) / 16 * 16, what = kProduct | (padded >> 3) << 17;
         for (int sb = 0; sb < nb && !stop; ++sb, ++b) {
           const uint32_t d0 = tmem + kCols * (u % kUnits), d1 = C::kQ6 ? d0 : tmem + kCols * ((u + 1) % kUnits);
-          for (int c = 0; c < 4; ++c, ++j, ++k) {
+          const bool last = (sb & 3) == 3 || sb == nb - 1;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
             const uint32_t slot = j % kStages, x = tc::smem_u32(S.x[slot]), a = tmem + kAColumn + 64 * (k & 1);
-            stop = !warp_wait(&S.xfull[slot], (j / kStages) & 1, gave_up, err) || (c == 0 && !sum_free(u)) ||
-                   !warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
+            const uint32_t done = k % kDone;
+            stop = (!ready && !arrived(&S.xfull[slot], (j / kStages) & 1, false)) || (c == 0 && !sum_free(u));
             if (stop) break;
             tc::fence_after_sync();
             if (elect()) {
@@ -505,6 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
               if (stop) break;
               tc::fence_after_sync();
             }
+            ++j, ++k;
+            if (!C::kQ6 && c == 3) ready = arrived(&S.sfull[g & 1], (g >> 1) & 1, true);
+            else ready = arrived(&S.xfull[j % kStages], (j / kStages) & 1, true);
             if (elect()) {
 #pragma unroll
               for (int i = 0; i < 4; ++i)
@@ -513,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
 #pragma unroll
                 for (int i = 0; i < 4; ++i) mma_ts(d1, a + 32 + 8 * i, tc::desc_sw128(x + padded * 128 + 32 * i), what, 1);
               }
-              tc::mma_commit(&S.done[k % kDone]);
+              tc::mma_commit(&S.done[done]);
               if (C::kQ6 && c == 3) tc::mma_commit(&S.tfull[b & 1]);
             }
             __syncwarp();
@@ -524,22 +543,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
             continue;
           }
           const uint32_t a = tmem + kAColumn + 64 * (k & 1), sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
-          stop = !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err) ||
-                 !warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
+          const uint32_t done = k % kDone;
+          stop = !ready && !arrived(&S.sfull[g & 1], (g >> 1) & 1, false);
           if (stop) break;
           tc::fence_after_sync();
-          const bool last = (sb & 3) == 3 || sb == nb - 1;
+          ++k;
+          const bool next = arrived(&S.xfull[j % kStages], (j / kStages) & 1, true);
           if (elect()) {
             mma_ts(d0, a, tc::desc_sw128(sums), what, 1);
             mma_ts(d0, a + 8, tc::desc_sw128(sums), what, 1);
             mma_ts(d1, a + 32, tc::desc_sw128(sums), what, 1);
             mma_ts(d1, a + 40, tc::desc_sw128(sums), what, 1);
             tc::mma_commit(&S.tfull[b & 1]);
-            tc::mma_commit(&S.done[k % kDone]);
+            tc::mma_commit(&S.done[done]);
             if (last) tc::mma_commit(&S.sempty[g & 1]);
           }
           __syncwarp();
-          ++k, u += 2, g += last;
+          ready = next;
+          u += 2, g += last;
         }
       }
       if (elect()) tc::mma_commit(&S.drain);                   // every product is done before tensor memory goes
