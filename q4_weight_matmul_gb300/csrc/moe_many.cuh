@@ -1,9 +1,9 @@
 // Products of the experts' matrices with many rows each (prompts), on the
-// tensor cores (tcgen05): 128 or 256 weight rows times up to 128 pairs of one
+// tensor cores (tcgen05): 128 or 256 weight rows times up to 112 pairs of one
 // expert, fp32 sums of exact 16-bit products as in moe_few.cuh.
 //
 // Four launches.  (1) One CTA lays the pairs out in tiles: an expert's n pairs
-// become ceil(n / 128) tiles of equal size, a multiple of 16.  (2) Each pair's
+// become ceil(n / 112) tiles of equal size, a multiple of 16.  (2) Each pair's
 // activations, times a power of two that puts the row's largest in
 // [2^14, 2^15), become two binary16 parts, stored tile by tile as the products
 // read them (64 k of hi, then of lo, in the 128-byte-swizzled layout), with
@@ -23,13 +23,13 @@
 // Q6_K: sc (q - 32) needs up to 13 bits: hi = binary16 of it and lo = the rest
 // (-1, 0, 1), two tiles that meet the hi and lo, and the hi parts of x.
 //
-// A CTA's warps: 0 copies activations, 2 weights, 3 draws items (a tile of
-// pairs times a block of rows; large tiles first), 1 issues the products, 4-11
-// convert (two groups of four that take A tiles in turn: with one, 700 cycles a
-// tile held the products up, 547 us for 4096 tokens), 12-19 run the epilogue
-// (64 columns a thread; totals in registers).
-// Tensor memory: three sums of 128 columns in turn, A of two steps (two tiles of
-// 128 rows x 64 k each) in turn.  Every wait is bounded.
+// A CTA's warps: 0 copies activations, 2 draws items (a tile of pairs times a
+// block of rows; large tiles first) and copies weights, 1 and 3 issue the
+// products, one for each tile of rows (a burst of eight waits and starts for
+// some 400 cycles, which the other's products cover), 4-11 convert (two groups of four; with one, 700 cycles a tile held the products
+// up, 547 us for 4096 tokens), 12-19 run the epilogue (64 columns a thread;
+// totals in registers).
+// Every wait is bounded.
 #pragma once
 
 #include "mma_sync.cuh"
@@ -44,15 +44,17 @@ namespace many {
 
 enum Mode { kGateUp, kDownQ4, kDownQ6 };
 
-constexpr int kRows = 128, kCols = 128;       // of a product: weight rows, pairs
+constexpr int kRows = 128, kCols = 112;       // of a product: weight rows, pairs
 constexpr int kStages = 4, kStageBytes = 2 * kCols * 128;   // 64 k of the activations, hi and lo
 constexpr int kSumBytes = kCols * 128;        // the sums of four superblocks, 32 bytes a pair each
+// The products' steps: 64 k of both A tiles (Q6_K: of both parts), the last of
+// a superblock with its min term.  Tensor memory: three sums of kCols columns
+// in turn, the A tiles of two steps in turn, those of the min terms.  (128
+// columns a sum leave the min terms a place among the steps' only, where they
+// hold the next step up: 482 us for 4096 tokens.)
 constexpr int kUnits = 3, kQueue = 4;
-// The products' steps: 64 k of both A tiles (Q6_K: of both parts), or (Q4_K, a
-// superblock's fifth) its min term.  A step's two A tiles take one of two
-// places; one commit a step says that its operands are free.
-constexpr int kDone = 8;
-constexpr uint32_t kAColumn = kUnits * kCols; // of the first A tile in tensor memory
+constexpr uint32_t kAColumn = kUnits * kCols, kMinColumn = kAColumn + 128;
+static_assert(kMinColumn + 32 <= 512);
 constexpr int kConverters = 8, kEpilogue = 8; // warps
 constexpr int kThreads = 32 * (4 + kConverters + kEpilogue);
 constexpr uint32_t kProduct = (1u << 4) | ((uint32_t)(kRows >> 4) << 24);      // f16 operands, f32 sums, 128 rows
@@ -66,10 +68,10 @@ struct Control {
 
 template <int MODE>
 struct Cfg {
-  static constexpr int kSteps = MODE == kDownQ6 ? 4 : 5;     // of a superblock
   static constexpr bool kUp = MODE == kGateUp, kQ6 = MODE == kDownQ6;
   static constexpr int kSb = kQ6 ? kQ6GpuBytes : kBlockBytes;
-  static constexpr int kRaw = kQ6 ? 2 : 3;                   // weight tiles (128 rows of a superblock) in flight
+  static constexpr int kRaw = kQ6 ? 3 : 4;                   // weight tiles (128 rows of a superblock) in flight
+  static constexpr int kIssuers = kQ6 ? 1 : 2;               // warps that issue products
   static constexpr int kTilesM = kQ6 ? 1 : 2;                // of 128 rows each
   static constexpr int kOutRows = MODE == kDownQ4 ? 2 * kRows : kRows;
 };
@@ -93,8 +95,8 @@ struct __align__(1024) Smem {
   uint8_t sums[2][kSumBytes];
   uint8_t raw[Cfg<MODE>::kRaw][kRows * Cfg<MODE>::kSb];
   float scale[2][2][kRows];
-  uint64_t xfull[kStages], sfull[2], sempty[2], rfull[3], rempty[3], afull[2], done[kDone], tfull[2], tempty[kUnits],
-      dfull[2], dempty[2], qfull[kQueue], qempty[kQueue], drain;
+  uint64_t xfull[kStages], sfull[2], sempty[2], rfull[4], rempty[4], afull[2], mfull, done[4], tfull[kUnits],
+      tempty[kUnits], dfull[2], dempty[2], qfull[kQueue], qempty[kQueue], drain[2];
   Tile item[kQueue];
   int block[kQueue];
   uint32_t tmem;
@@ -114,12 +116,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(d), "r"(a), "l"(b), "r"(what), "r"(add) : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-               : "=r"(ok) : "r"(tc::smem_u32(bar)), "r"(parity) : "memory");
-  return ok != 0;
 }
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
   uint64_t r;
@@ -158,10 +154,10 @@ struct LayoutParams {
 };
 
 static __global__ void __launch_bounds__(kMoeMaxExperts) moe_many_layout_kernel(const LayoutParams P) {
-  __shared__ int warps[16], count[9], start[9];
+  __shared__ int warps[16], count[kCols / 16 + 1], start[kCols / 16 + 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int e = threadIdx.x, E = P.experts;
-  if (e < 9) count[e] = 0;
+  if (e <= kCols / 16) count[e] = 0;
   const int raw0 = e <= E ? P.offsets[e] : INT32_MAX, raw1 = e < E ? P.offsets[e + 1] : INT32_MAX;
   int all;
   const int before = scan_block<kMoeMaxExperts, true>(min(raw0, P.pairs), warps, all);
@@ -175,7 +171,7 @@ static __global__ void __launch_bounds__(kMoeMaxExperts) moe_many_layout_kernel(
   __syncthreads();
   if (e == 0) {
     int run = 0;
-    for (int c = 8; c > 0; --c) start[c] = run, run += count[c];
+    for (int c = kCols / 16; c > 0; --c) start[c] = run, run += count[c];
     P.control->tiles = run;
     P.control->counter = 0;
   }
@@ -363,16 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&S.xfull[i], 1);
-    for (int i = 0; i < kDone; ++i) tc::mbar_init(&S.done[i], 1);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&S.done[i], C::kIssuers);
     for (int i = 0; i < C::kRaw; ++i) tc::mbar_init(&S.rfull[i], 1), tc::mbar_init(&S.rempty[i], C::kQ6 ? kConverters : kConverters / 2);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&S.sfull[i], 1), tc::mbar_init(&S.sempty[i], 1), tc::mbar_init(&S.tfull[i], 1);
+      tc::mbar_init(&S.sfull[i], 1), tc::mbar_init(&S.sempty[i], C::kIssuers);
       tc::mbar_init(&S.afull[i], kConverters);
       tc::mbar_init(&S.dfull[i], C::kQ6 ? kConverters / 2 : kConverters), tc::mbar_init(&S.dempty[i], kEpilogue);
     }
-    for (int i = 0; i < kUnits; ++i) tc::mbar_init(&S.tempty[i], kEpilogue);
-    for (int i = 0; i < kQueue; ++i) tc::mbar_init(&S.qfull[i], 1), tc::mbar_init(&S.qempty[i], 3 + kConverters + kEpilogue);
-    tc::mbar_init(&S.drain, 1);
+    tc::mbar_init(&S.mfull, kConverters);
+    for (int i = 0; i < kUnits; ++i) tc::mbar_init(&S.tfull[i], 1), tc::mbar_init(&S.tempty[i], kEpilogue);
+    for (int i = 0; i < kQueue; ++i) tc::mbar_init(&S.qfull[i], 1), tc::mbar_init(&S.qempty[i], 1 + C::kIssuers + kConverters + kEpilogue);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&S.drain[i], 1);
     *gave_up = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -383,13 +380,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = S.tmem;
+  // Whoever has all 512 columns has them from 0 on; the address as a constant
+  // keeps the products' operands in uniform registers.
+  constexpr uint32_t tmem = 0;
+  if (threadIdx.x == 0 && S.tmem != tmem) {
+    *gave_up = 1;
+    atomicOr(err, 1);
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // The next item of a warp; false: there is none, or a wait gave up.
   uint32_t turn = 0;
   Tile T;
-  int block;
+  int block = 0;
   auto next_item = [&]() -> bool {
     const uint32_t q = turn % kQueue;
     if (!warp_wait(&S.qfull[q], (turn / kQueue) & 1, gave_up, err)) return false;
@@ -401,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
   };
 
   // Until step `k` is done with its operands.
-  auto step_done = [&](uint32_t k) { return warp_wait(&S.done[k % kDone], (k / kDone) & 1, gave_up, err); };
+  auto step_done = [&](uint32_t k) { return warp_wait(&S.done[k % 4], (k / 4) & 1, gave_up, err); };
 
   // 640 threads x 96 registers at launch = 128 x 32 + 256 x 64 + 256 x 160
   if (warp < 4) {
@@ -426,8 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
             ++g;
           }
           const uint32_t slot = j % kStages;
-          // (four stages before: the same 64 k of the superblock before)
-          stop = j >= kStages && !step_done((j / 4 - 1) * C::kSteps + j % 4);
+          stop = j >= kStages && !step_done(j - kStages);
           if (stop) break;
           if (elect()) {
             tc::mbar_arrive_expect_tx(&S.xfull[slot], 2 * padded * 128);
@@ -443,13 +445,30 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
           if (!tc::mbar_wait_sleep(&S.sfull[i & 1], (i >> 1) & 1)) break;
       }
     } else if (warp == 2) {
-      // ---------------------------------------------------------- weights
+      // ----------------------------------------------- items, and their weights
+      const int items = P.control->tiles * P.blocks;
+      int i = blockIdx.x;
       uint32_t n = 0;
       bool stop = false;
-      while (!stop && next_item()) {
-        const int w0 = T.expert * P.rows + block * C::kOutRows;
-        for (int i = 0; i < C::kTilesM * nb; ++i, ++n) {
-          const int sb = i / C::kTilesM, mt = i % C::kTilesM;
+      for (uint32_t t = 0; !stop; ++t) {
+        const uint32_t q = t % kQueue;
+        const bool have = i < items;
+        Tile tile{0, 0, 0, 0};
+        int ticket = 0;
+        if (have) {
+          tile = P.tiles[i / P.blocks], block = i % P.blocks;
+          if (lane == 0) ticket = (int)gridDim.x + atomicAdd(P.counter, 1);
+        }
+        if (!warp_wait(&S.qempty[q], ((t / kQueue) & 1) ^ 1, gave_up, err)) break;
+        if (lane == 0) {
+          S.item[q] = tile, S.block[q] = block;
+          tc::mbar_arrive(&S.qfull[q]);
+        }
+        __syncwarp();
+        if (!have) break;
+        const int w0 = tile.expert * P.rows + block * C::kOutRows;
+        for (int r = 0; r < C::kTilesM * nb; ++r, ++n) {
+          const int sb = r / C::kTilesM, mt = r % C::kTilesM;
           const uint32_t slot = n % C::kRaw;
           stop = !warp_wait(&S.rempty[slot], ((n / C::kRaw) & 1) ^ 1, gave_up, err);
           if (stop) break;
@@ -459,113 +478,57 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
           }
           __syncwarp();
         }
-      }
-      if (lane == 0)
-        for (uint32_t i = n < C::kRaw ? 0 : n - C::kRaw; i < n; ++i)
-          if (!tc::mbar_wait_sleep(&S.rfull[i % C::kRaw], (i / C::kRaw) & 1)) break;
-    } else if (warp == 3) {
-      // ------------------------------------------------------------ items
-      const int items = P.control->tiles * P.blocks;
-      int i = blockIdx.x;
-      for (uint32_t t = 0;; ++t) {
-        const uint32_t q = t % kQueue;
-        Tile tile{0, 0, 0, 0};
-        int ticket = 0;
-        if (i < items) {
-          tile = P.tiles[i / P.blocks];
-          if (lane == 0) ticket = (int)gridDim.x + atomicAdd(P.counter, 1);
-        }
-        if (!warp_wait(&S.qempty[q], ((t / kQueue) & 1) ^ 1, gave_up, err)) break;
-        if (lane == 0) {
-          S.item[q] = tile, S.block[q] = i < items ? i % P.blocks : 0;
-          tc::mbar_arrive(&S.qfull[q]);
-        }
-        if (i >= items) break;
         i = __shfl_sync(~0u, ticket, 0);
       }
-    } else {
+      if (lane == 0)
+        for (uint32_t r = n < C::kRaw ? 0 : n - C::kRaw; r < n; ++r)
+          if (!tc::mbar_wait_sleep(&S.rfull[r % C::kRaw], (r / C::kRaw) & 1)) break;
+    } else if (warp == 1 || !C::kQ6) {
       // --------------------------------------------------------- products
-      uint32_t j = 0, g = 0, k = 0, u = 0, b = 0;              // stages, groups of sums, steps, sums, superblocks
+      const uint32_t mt = C::kQ6 || warp == 1 ? 0 : 1;          // of this tile of rows (Q6_K: both parts)
+      uint32_t k = 0, g = 0, u = mt, b = 0;                    // steps, groups of sums of x, sums, superblocks
       bool stop = false;
-      // the tensor memory of sum i is free
-      auto sum_free = [&](uint32_t i) { return warp_wait(&S.tempty[i % kUnits], ((i / kUnits) & 1) ^ 1, gave_up, err); };
-      // The operands of a step are there: `now` asks without waiting, while the
-      // products before it still run (a wait takes some 130 cycles even then,
-      // and the queue of products is short).
-      auto arrived = [&](uint64_t* other, uint32_t parity, bool now) {
-        if (now) return __all_sync(~0u, mbar_test(other, parity) && mbar_test(&S.afull[k & 1], (k >> 1) & 1)) != 0;
-        return warp_wait(other, parity, gave_up, err) && warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
-      };
-      bool ready = false;
       while (!stop && next_item()) {
-        const uint32_t padded = (T.n + 15) / 16 * 16, what = kProduct | (padded >> 3) << 17;
-        for (int sb = 0; sb < nb && !stop; ++sb, ++b) {
-          const uint32_t d0 = tmem + kCols * (u % kUnits), d1 = C::kQ6 ? d0 : tmem + kCols * ((u + 1) % kUnits);
+        // (from a vote, so that it is uniform to the compiler)
+        const uint32_t padded = 16 * __popc(__ballot_sync(~0u, 16 * lane < T.n)), what = kProduct | (padded >> 3) << 17;
+        for (int sb = 0; sb < nb && !stop; ++sb, ++b, u += C::kTilesM) {
+          const uint32_t d = tmem + kCols * (u % kUnits);
           const bool last = (sb & 3) == 3 || sb == nb - 1;
+          stop = !warp_wait(&S.tempty[u % kUnits], ((u / kUnits) & 1) ^ 1, gave_up, err);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t slot = j % kStages, x = tc::smem_u32(S.x[slot]), a = tmem + kAColumn + 64 * (k & 1);
-            const uint32_t done = k % kDone;
-            stop = (!ready && !arrived(&S.xfull[slot], (j / kStages) & 1, false)) || (c == 0 && !sum_free(u));
+          for (int c = 0; c < 4; ++c, ++k) {
+            const uint32_t x = tc::smem_u32(S.x[k % kStages]), a = tmem + kAColumn + 64 * (k & 1) + 32 * mt;
+            const uint32_t sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
+            stop = stop || !warp_wait(&S.xfull[k % kStages], (k / kStages) & 1, gave_up, err) ||
+                   !warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
+            if (!C::kQ6 && c == 3)
+              stop = stop || !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err) || !warp_wait(&S.mfull, b & 1, gave_up, err);
             if (stop) break;
             tc::fence_after_sync();
             if (elect()) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_ts(d0, a + 8 * i, tc::desc_sw128(x + 32 * i), what, c | i ? 1 : 0);
+              for (int i = 0; i < 4; ++i) mma_ts(d, a + 8 * i, tc::desc_sw128(x + 32 * i), what, c | i ? 1 : 0);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) mma_ts(d0, a + 8 * i, tc::desc_sw128(x + padded * 128 + 32 * i), what, 1);
-            }
-            __syncwarp();
-            if (!C::kQ6 && c == 0) {
-              stop = !sum_free(u + 1);
-              if (stop) break;
-              tc::fence_after_sync();
-            }
-            ++j, ++k;
-            if (!C::kQ6 && c == 3) ready = arrived(&S.sfull[g & 1], (g >> 1) & 1, true);
-            else ready = arrived(&S.xfull[j % kStages], (j / kStages) & 1, true);
-            if (elect()) {
+              for (int i = 0; i < 4; ++i) mma_ts(d, a + 8 * i, tc::desc_sw128(x + padded * 128 + 32 * i), what, 1);
+              if constexpr (C::kQ6) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                mma_ts(d1, a + 32 + 8 * i, tc::desc_sw128(x + 32 * i), what, C::kQ6 || (c | i) ? 1 : 0);
-              if constexpr (!C::kQ6) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mma_ts(d1, a + 32 + 8 * i, tc::desc_sw128(x + padded * 128 + 32 * i), what, 1);
+                for (int i = 0; i < 4; ++i) mma_ts(d, a + 32 + 8 * i, tc::desc_sw128(x + 32 * i), what, 1);
+              } else if (c == 3) {
+                mma_ts(d, tmem + kMinColumn + 16 * mt, tc::desc_sw128(sums), what, 1);
+                mma_ts(d, tmem + kMinColumn + 16 * mt + 8, tc::desc_sw128(sums), what, 1);
+                if (last) tc::mma_commit(&S.sempty[g & 1]);
               }
-              tc::mma_commit(&S.done[done]);
-              if (C::kQ6 && c == 3) tc::mma_commit(&S.tfull[b & 1]);
+              tc::mma_commit(&S.done[k % 4]);
+              if (c == 3) tc::mma_commit(&S.tfull[u % kUnits]);
             }
             __syncwarp();
           }
-          if (stop) break;
-          if constexpr (C::kQ6) {
-            ++u;
-            continue;
-          }
-          const uint32_t a = tmem + kAColumn + 64 * (k & 1), sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
-          const uint32_t done = k % kDone;
-          stop = !ready && !arrived(&S.sfull[g & 1], (g >> 1) & 1, false);
-          if (stop) break;
-          tc::fence_after_sync();
-          ++k;
-          const bool next = arrived(&S.xfull[j % kStages], (j / kStages) & 1, true);
-          if (elect()) {
-            mma_ts(d0, a, tc::desc_sw128(sums), what, 1);
-            mma_ts(d0, a + 8, tc::desc_sw128(sums), what, 1);
-            mma_ts(d1, a + 32, tc::desc_sw128(sums), what, 1);
-            mma_ts(d1, a + 40, tc::desc_sw128(sums), what, 1);
-            tc::mma_commit(&S.tfull[b & 1]);
-            tc::mma_commit(&S.done[done]);
-            if (last) tc::mma_commit(&S.sempty[g & 1]);
-          }
-          __syncwarp();
-          ready = next;
-          u += 2, g += last;
+          g += !C::kQ6 && last;
         }
       }
-      if (elect()) tc::mma_commit(&S.drain);                   // every product is done before tensor memory goes
+      if (elect()) tc::mma_commit(&S.drain[mt]);               // every product is done before tensor memory goes
       __syncwarp();
-      if (!tc::mbar_wait_sleep(&S.drain, 0)) atomicOr(err, 1);
+      if (!tc::mbar_wait_sleep(&S.drain[mt], 0)) atomicOr(err, 1);
     }
   } else if (warp < 4 + kConverters) {
     // --------------------------------------------------------------- converters
@@ -636,22 +599,26 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
             __syncwarp();
             if (c == 3 && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
             const uint32_t s = c < 2 ? H.sc[0] : H.sc[1], at = lanes + 64 * (k & 1) + 32 * group;
-            uint32_t v[16];
+            uint32_t v[16], w2[16];
             convert_q4<false>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1)), H.down), v);
+            convert_q4<true>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1) + 1), H.down), w2);
             stop = !begin_step();
             if (stop) break;
             tc::tmem_st16(at, v);
-            convert_q4<true>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1) + 1), H.down), v);
-            tc::tmem_st16(at + 16, v);
+            tc::tmem_st16(at + 16, w2);
             end_step();
+            if (c == 1) {
+              // (the superblock before is done with its min tiles, as begin_step has seen)
+              convert_min(H, v);
+              tc::tmem_st16(lanes + (kMinColumn - kAColumn) + 16 * group, v);
+              stop = !scale_of(group, H.scale);
+              if (stop) break;
+              tc::tmem_wait_st();
+              tc::fence_before_sync();
+              __syncwarp();
+              if (lane == 0) tc::mbar_arrive(&S.mfull);
+            }
           }
-          if (stop) break;
-          uint32_t v[16];
-          convert_min(H, v);
-          stop = !scale_of(group, H.scale) || !begin_step();
-          if (stop) break;
-          tc::tmem_st16(lanes + 64 * (k & 1) + 32 * group, v);
-          end_step();
         }
       }
     }
@@ -676,14 +643,15 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int i = 0; i < 8; ++i) total[mt][k][i] = 0;
-      for (int sb = 0; sb < nb; ++sb, ++b) {
-        stop = !warp_wait(&S.tfull[b & 1], (b >> 1) & 1, gave_up, err) ||
-               !warp_wait(&S.dfull[b & 1], (b >> 1) & 1, gave_up, err);
+      for (int sb = 0; sb < nb && !stop; ++sb, ++b) {
+        stop = !warp_wait(&S.dfull[b & 1], (b >> 1) & 1, gave_up, err);
         if (stop) break;
-        tc::fence_after_sync();
 #pragma unroll
         for (int mt = 0; mt < C::kTilesM; ++mt, ++u) {
           const uint32_t t = u % kUnits;
+          stop = !warp_wait(&S.tfull[t], (u / kUnits) & 1, gave_up, err);
+          if (stop) break;
+          tc::fence_after_sync();
           const float d = S.scale[b & 1][mt][row];
           const uint64_t d2 = pair_of(d, d);
           const uint32_t at = lanes + kCols * t + 16 * first;
@@ -738,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
   __syncthreads();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc(S.tmem, 512);
   }
 }
 
