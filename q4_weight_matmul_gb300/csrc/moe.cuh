@@ -41,8 +41,14 @@ __device__ __forceinline__ bool agreed(bool ok, volatile int* gave_up, int* err)
   __syncwarp();
   return false;
 }
+// (Short: the code of a warp's loop is fetched anew for every turn where the
+// warps of a block do different things.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up, int* err) {
-  return agreed(tc::mbar_wait(bar, parity, gave_up), gave_up, err);
+  if (__all_sync(~0u, tc::mbar_try_wait(bar, parity))) return true;
+  const uint32_t t0 = (uint32_t)(clock64() >> 16);
+  while (!__all_sync(~0u, tc::mbar_try_wait(bar, parity)))
+    if (!agreed(!*gave_up && (uint32_t)(clock64() >> 16) - t0 < (uint32_t)(tc::kTimeoutCycles >> 16), gave_up, err)) return false;
+  return true;
 }
 
 // Exclusive sum of `v` over the block's threads before this one (`most`:

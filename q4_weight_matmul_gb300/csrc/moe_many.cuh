@@ -506,14 +506,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
             if (stop) break;
             tc::fence_after_sync();
             if (elect()) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mma_ts(d, a + 8 * i, tc::desc_sw128(x + 32 * i), what, c | i ? 1 : 0);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) mma_ts(d, a + 8 * i, tc::desc_sw128(x + padded * 128 + 32 * i), what, 1);
-              if constexpr (C::kQ6) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) mma_ts(d, a + 32 + 8 * i, tc::desc_sw128(x + 32 * i), what, 1);
-              } else if (c == 3) {
+              const uint64_t hi = tc::desc_sw128(x), lo = tc::desc_sw128(x + padded * 128);
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {                    // (2: 32 bytes in the descriptor's units)
+                mma_ts(d, a + 8 * i, hi + 2 * i, what, c | i ? 1 : 0);
+                mma_ts(d, a + 8 * i, lo + 2 * i, what, 1);
+                if constexpr (C::kQ6) mma_ts(d, a + 32 + 8 * i, hi + 2 * i, what, 1);
+              }
+              if (!C::kQ6 && c == 3) {
                 mma_ts(d, tmem + kMinColumn + 16 * mt, tc::desc_sw128(sums), what, 1);
                 mma_ts(d, tmem + kMinColumn + 16 * mt + 8, tc::desc_sw128(sums), what, 1);
                 if (last) tc::mma_commit(&S.sempty[g & 1]);
