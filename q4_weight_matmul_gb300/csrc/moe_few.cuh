@@ -377,6 +377,9 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
       m[t][r] = __byte_perm(mins, 0, (c & 1) ? 0x4342 : 0x4140);              // m[2 c], m[2 c + 1] times 2^-24
     }
   float sum[2][NT][4] = {};
+  // A chunk of 64 k has four sums in the making (two sub-blocks, two tiles of
+  // rows): taken in turn, none waits for its product before.
+  constexpr int kTogether = NT == 1 ? 2 : 1;                   // sub-blocks at a time
 #pragma unroll
   for (int ch = 0; ch < 4; ++ch) {
     uint2 q[2][2];
@@ -386,33 +389,50 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
       for (int r = 0; r < 2; ++r)
         q[t][r] = *reinterpret_cast<const uint2*>(w + t * apart + 8 * r * kBlockBytes + 16 + 32 * ch + 8 * c);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int s = 2 * ch + half;
-      const uint32_t bits = half ? 0x00F000F0u : 0x000F000Fu;
-      uint4 b[2][NT];
+    for (int first = 0; first < 2; first += kTogether) {
+      float acc[kTogether][2][NT][4] = {};
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        uint4 b[kTogether][NT];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          b[i][n] = operand<HALF>(x + n * kTileX, 2 * s + i, lane);
+        for (int h = 0; h < kTogether; ++h)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        float acc[NT][4] = {};
+          for (int n = 0; n < NT; ++n) b[h][n] = operand<HALF>(x + n * kTileX, 2 * (2 * ch + first + h) + i, lane);
+        uint32_t a[kTogether][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t u = i ? q[t][0].y : q[t][0].x, v = i ? q[t][1].y : q[t][1].x;
-          const uint32_t a[4] = {u & bits, v & bits, (u >> 8) & bits, (v >> 8) & bits};
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t u = i ? q[t][0].y : q[t][0].x, v = i ? q[t][1].y : q[t][1].x, u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<false>(acc[n], a, b[i][n].x, b[i][n].y);
-          if constexpr (!HALF)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816<false>(acc[n], a, b[i][n].z, b[i][n].w);
+          for (int h = 0; h < kTogether; ++h) {
+            const uint32_t bits = first + h ? 0x00F000F0u : 0x000F000Fu;
+            a[h][t][0] = u & bits, a[h][t][1] = v & bits, a[h][t][2] = u8 & bits, a[h][t][3] = v8 & bits;
+          }
         }
-        const float d0 = half ? d[t][0] * 0.0625f : d[t][0], d1 = half ? d[t][1] * 0.0625f : d[t][1];
-        const float s0 = fmaf(magic(sc[t][0][s >> 2], s & 3), d0, -8388608.0f * d0),
-                    s1 = fmaf(magic(sc[t][1][s >> 2], s & 3), d1, -8388608.0f * d1);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) add_scaled(sum[t][n], acc[n], s0, s1);
+        for (int h = 0; h < kTogether; ++h)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816<false>(acc[h][t][n], a[h][t], b[h][n].x, b[h][n].y);
+        if constexpr (!HALF)
+#pragma unroll
+          for (int h = 0; h < kTogether; ++h)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<false>(acc[h][t][n], a[h][t], b[h][n].z, b[h][n].w);
+      }
+#pragma unroll
+      for (int h = 0; h < kTogether; ++h) {
+        const int s = 2 * ch + first + h;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float d0 = s & 1 ? d[t][0] * 0.0625f : d[t][0], d1 = s & 1 ? d[t][1] * 0.0625f : d[t][1];
+          const float s0 = fmaf(magic(sc[t][0][s >> 2], s & 3), d0, -8388608.0f * d0),
+                      s1 = fmaf(magic(sc[t][1][s >> 2], s & 3), d1, -8388608.0f * d1);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) add_scaled(sum[t][n], acc[h][t][n], s0, s1);
+        }
       }
     }
   }
