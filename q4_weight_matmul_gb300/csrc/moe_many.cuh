@@ -44,19 +44,10 @@ namespace many {
 
 enum Mode { kGateUp, kDownQ4, kDownQ6 };
 
-constexpr int kRows = 128, kCols = 112;       // of a product: weight rows, pairs
-constexpr int kStages = 4, kStageBytes = 2 * kCols * 128;   // 64 k of the activations, hi and lo
-constexpr int kSumBytes = kCols * 128;        // the sums of four superblocks, 32 bytes a pair each
-// The products' steps: 64 k of both A tiles (Q6_K: of both parts), the last of
-// a superblock with its min term.  Tensor memory: three sums of kCols columns
-// in turn, the A tiles of two steps in turn, those of the min terms.  (128
-// columns a sum leave the min terms a place among the steps' only, where they
-// hold the next step up: 482 us for 4096 tokens.)
+constexpr int kRows = 128;                    // weight rows of a product
+constexpr int kStages = 4;                    // of 64 k of the activations, hi and lo
 constexpr int kUnits = 3, kQueue = 4;
-constexpr uint32_t kAColumn = kUnits * kCols, kMinColumn = kAColumn + 128;
-static_assert(kMinColumn + 32 <= 512);
-constexpr int kConverters = 8, kEpilogue = 8; // warps
-constexpr int kThreads = 32 * (4 + kConverters + kEpilogue);
+
 constexpr uint32_t kProduct = (1u << 4) | ((uint32_t)(kRows >> 4) << 24);      // f16 operands, f32 sums, 128 rows
 
 struct Tile {                 // pairs first .. first + n - 1 of an expert; their padded rows from `row` on
@@ -66,14 +57,36 @@ struct Control {
   int tiles, counter, pad[30];
 };
 
-template <int MODE>
+// COLS: the most pairs of a tile.  The products' steps are 64 k of both A tiles
+// (Q6_K: of both parts), the last of a superblock with its min term.  Tensor
+// memory: three sums in turn, the A tiles of some steps in turn, those of the
+// min terms.
+//  - 112: a step's products take longer than making its A.  (With 128 columns a
+//    sum the min terms' only place is among the steps', where they hold the
+//    next step up: 482 us for 4096 tokens.)
+//  - 32: the other way round, so there are twice the converters, two groups for
+//    every second step each, and four steps of A; the activations' hi and lo
+//    parts are columns of one product beside each other.
+template <int MODE, int COLS>
 struct Cfg {
   static constexpr bool kUp = MODE == kGateUp, kQ6 = MODE == kDownQ6;
+  static constexpr bool kBeside = COLS == 32;
+  static constexpr int kCols = COLS, kUnitCols = kBeside ? 2 * COLS : COLS;
+  static constexpr int kSteps = kBeside ? 4 : 2, kMins = kBeside ? 2 : 1;            // A places
+  static constexpr int kDone = 4 * kMins;                    // barriers of steps: as long as a min term's place is waited for
+  static constexpr uint32_t kAColumn = kUnits * kUnitCols, kMinColumn = kAColumn + 64 * kSteps;
+  static constexpr int kConverters = kBeside ? 16 : 8, kEpilogue = kBeside ? 4 : 8;  // warps
+  static constexpr int kThreads = 32 * (4 + kConverters + kEpilogue);
+  static constexpr int kStageBytes = 2 * COLS * 128, kSumBytes = COLS * 128;         // (the sums of four superblocks)
   static constexpr int kSb = kQ6 ? kQ6GpuBytes : kBlockBytes;
-  static constexpr int kRaw = kQ6 ? 3 : 4;                   // weight tiles (128 rows of a superblock) in flight
+  static constexpr int kRaw = kBeside ? (kQ6 ? 6 : 9) : (kQ6 ? 3 : 4);               // weight tiles (128 rows of a superblock) in flight
   static constexpr int kIssuers = kQ6 ? 1 : 2;               // warps that issue products
   static constexpr int kTilesM = kQ6 ? 1 : 2;                // of 128 rows each
   static constexpr int kOutRows = MODE == kDownQ4 ? 2 * kRows : kRows;
+  // registers of the three kinds of warps; at launch 768 x 80 and 640 x 96
+  static constexpr int kFewRegs = 32, kConvRegs = kBeside ? 72 : 64, kEpiRegs = 160;
+  static_assert(32 * (4 * kFewRegs + kConverters * kConvRegs + kEpilogue * kEpiRegs) == kThreads * (kBeside ? 80 : 96));
+  static_assert(kMinColumn + 32 * kMins <= 512);
 };
 
 struct Params {
@@ -89,20 +102,22 @@ struct Params {
   int rows, nb, blocks;
 };
 
-template <int MODE>
+template <int MODE, int COLS>
 struct __align__(1024) Smem {
-  uint8_t x[kStages][kStageBytes];
-  uint8_t sums[2][kSumBytes];
-  uint8_t raw[Cfg<MODE>::kRaw][kRows * Cfg<MODE>::kSb];
+  using C = Cfg<MODE, COLS>;
+  uint8_t x[kStages][C::kStageBytes];
+  uint8_t sums[2][C::kSumBytes];
+  uint8_t raw[C::kRaw][kRows * C::kSb];
   float scale[2][2][kRows];
-  uint64_t xfull[kStages], sfull[2], sempty[2], rfull[4], rempty[4], afull[2], mfull, done[4], tfull[kUnits],
-      tempty[kUnits], dfull[2], dempty[2], qfull[kQueue], qempty[kQueue], drain[2];
+  uint64_t xfull[kStages], sfull[2], sempty[2], rfull[C::kRaw], rempty[C::kRaw], afull[C::kSteps], mfull[C::kMins], done[C::kDone],
+      tfull[kUnits], tempty[kUnits], dfull[2], dempty[2], qfull[kQueue], qempty[kQueue], drain[2];
   Tile item[kQueue];
   int block[kQueue];
   uint32_t tmem;
   int gave_up;
 };
-static_assert(sizeof(Smem<kGateUp>) + 1024 <= 232448 && sizeof(Smem<kDownQ6>) + 1024 <= 232448);
+static_assert(sizeof(Smem<kGateUp, 112>) + 1024 <= 232448 && sizeof(Smem<kDownQ6, 112>) + 1024 <= 232448);
+static_assert(sizeof(Smem<kGateUp, 32>) + 1024 <= 232448 && sizeof(Smem<kDownQ6, 32>) + 1024 <= 232448);
 
 // One lane of a converged warp; what it issues takes its operands from uniform
 // registers.
@@ -153,7 +168,8 @@ struct LayoutParams {
   int pairs, experts;
 };
 
-static __global__ void __launch_bounds__(kMoeMaxExperts) moe_many_layout_kernel(const LayoutParams P) {
+template <int kCols>
+__global__ void __launch_bounds__(kMoeMaxExperts) moe_many_layout_kernel(const LayoutParams P) {
   __shared__ int warps[16], count[kCols / 16 + 1], start[kCols / 16 + 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int e = threadIdx.x, E = P.experts;
@@ -347,11 +363,12 @@ __device__ __forceinline__ void convert_q6(const uint4& l0, const uint4& l1, con
 }
 
 // ------------------------------------------------------------------ products
-template <int MODE>
-__global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_constant__ Params P) {
-  using C = Cfg<MODE>;
+template <int MODE, int COLS>
+__global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(const __grid_constant__ Params P) {
+  using C = Cfg<MODE, COLS>;
+  constexpr int kConverters = C::kConverters, kEpilogue = C::kEpilogue;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  Smem<MODE>& S = *reinterpret_cast<Smem<MODE>*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
+  Smem<MODE, COLS>& S = *reinterpret_cast<Smem<MODE, COLS>*>(smem_raw + ((1024u - (tc::smem_u32(smem_raw) & 1023u)) & 1023u));
   volatile int* gave_up = &S.gave_up;
   int* err = P.err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nb = P.nb;
@@ -359,14 +376,14 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&S.xfull[i], 1);
-    for (int i = 0; i < 4; ++i) tc::mbar_init(&S.done[i], C::kIssuers);
+    for (int i = 0; i < C::kDone; ++i) tc::mbar_init(&S.done[i], C::kIssuers);
     for (int i = 0; i < C::kRaw; ++i) tc::mbar_init(&S.rfull[i], 1), tc::mbar_init(&S.rempty[i], C::kQ6 ? kConverters : kConverters / 2);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&S.sfull[i], 1), tc::mbar_init(&S.sempty[i], C::kIssuers);
-      tc::mbar_init(&S.afull[i], kConverters);
-      tc::mbar_init(&S.dfull[i], C::kQ6 ? kConverters / 2 : kConverters), tc::mbar_init(&S.dempty[i], kEpilogue);
+      tc::mbar_init(&S.dfull[i], C::kQ6 ? 4 : 8), tc::mbar_init(&S.dempty[i], kEpilogue);
     }
-    tc::mbar_init(&S.mfull, kConverters);
+    for (int i = 0; i < C::kSteps; ++i) tc::mbar_init(&S.afull[i], 8);
+    for (int i = 0; i < C::kMins; ++i) tc::mbar_init(&S.mfull[i], 8);
     for (int i = 0; i < kUnits; ++i) tc::mbar_init(&S.tfull[i], 1), tc::mbar_init(&S.tempty[i], kEpilogue);
     for (int i = 0; i < kQueue; ++i) tc::mbar_init(&S.qfull[i], 1), tc::mbar_init(&S.qempty[i], 1 + C::kIssuers + kConverters + kEpilogue);
     for (int i = 0; i < 2; ++i) tc::mbar_init(&S.drain[i], 1);
@@ -404,11 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
   };
 
   // Until step `k` is done with its operands.
-  auto step_done = [&](uint32_t k) { return warp_wait(&S.done[k % 4], (k / 4) & 1, gave_up, err); };
+  auto step_done = [&](uint32_t k) { return warp_wait(&S.done[k % C::kDone], (k / C::kDone) & 1, gave_up, err); };
 
-  // 640 threads x 96 registers at launch = 128 x 32 + 256 x 64 + 256 x 160
   if (warp < 4) {
-    registers_down<32>();
+    registers_down<C::kFewRegs>();
     if (warp == 0) {
       // ------------------------------------------------------ activations
       uint32_t j = 0, g = 0;                                   // stages, groups of sums issued
@@ -490,19 +506,20 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
       bool stop = false;
       while (!stop && next_item()) {
         // (from a vote, so that it is uniform to the compiler)
-        const uint32_t padded = 16 * __popc(__ballot_sync(~0u, 16 * lane < T.n)), what = kProduct | (padded >> 3) << 17;
+        const uint32_t padded = 16 * __popc(__ballot_sync(~0u, 16 * lane < T.n)), narrow = kProduct | (padded >> 3) << 17,
+                       what = C::kBeside ? kProduct | (padded >> 2) << 17 : narrow;
         for (int sb = 0; sb < nb && !stop; ++sb, ++b, u += C::kTilesM) {
-          const uint32_t d = tmem + kCols * (u % kUnits);
+          const uint32_t d = tmem + C::kUnitCols * (u % kUnits);
           const bool last = (sb & 3) == 3 || sb == nb - 1;
           stop = !warp_wait(&S.tempty[u % kUnits], ((u / kUnits) & 1) ^ 1, gave_up, err);
 #pragma unroll 1
           for (int c = 0; c < 4; ++c, ++k) {
-            const uint32_t x = tc::smem_u32(S.x[k % kStages]), a = tmem + kAColumn + 64 * (k & 1) + 32 * mt;
+            const uint32_t x = tc::smem_u32(S.x[k % kStages]), a = tmem + C::kAColumn + 64 * (k % C::kSteps) + 32 * mt;
             const uint32_t sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
             stop = stop || !warp_wait(&S.xfull[k % kStages], (k / kStages) & 1, gave_up, err) ||
-                   !warp_wait(&S.afull[k & 1], (k >> 1) & 1, gave_up, err);
+                   !warp_wait(&S.afull[k % C::kSteps], (k / C::kSteps) & 1, gave_up, err);
             if (!C::kQ6 && c == 3)
-              stop = stop || !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err) || !warp_wait(&S.mfull, b & 1, gave_up, err);
+              stop = stop || !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err) || !warp_wait(&S.mfull[b % C::kMins], (b / C::kMins) & 1, gave_up, err);
             if (stop) break;
             tc::fence_after_sync();
             if (elect()) {
@@ -510,15 +527,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
 #pragma unroll 1
               for (int i = 0; i < 4; ++i) {                    // (2: 32 bytes in the descriptor's units)
                 mma_ts(d, a + 8 * i, hi + 2 * i, what, c | i ? 1 : 0);
-                mma_ts(d, a + 8 * i, lo + 2 * i, what, 1);
-                if constexpr (C::kQ6) mma_ts(d, a + 32 + 8 * i, hi + 2 * i, what, 1);
+                if constexpr (!C::kBeside) mma_ts(d, a + 8 * i, lo + 2 * i, what, 1);
+                if constexpr (C::kQ6) mma_ts(d, a + 32 + 8 * i, hi + 2 * i, narrow, 1);
               }
               if (!C::kQ6 && c == 3) {
-                mma_ts(d, tmem + kMinColumn + 16 * mt, tc::desc_sw128(sums), what, 1);
-                mma_ts(d, tmem + kMinColumn + 16 * mt + 8, tc::desc_sw128(sums), what, 1);
+                const uint32_t m = tmem + C::kMinColumn + 32 * (b % C::kMins) + 16 * mt;
+                mma_ts(d, m, tc::desc_sw128(sums), narrow, 1);
+                mma_ts(d, m + 8, tc::desc_sw128(sums), narrow, 1);
                 if (last) tc::mma_commit(&S.sempty[g & 1]);
               }
-              tc::mma_commit(&S.done[k % 4]);
+              tc::mma_commit(&S.done[k % C::kDone]);
               if (c == 3) tc::mma_commit(&S.tfull[u % kUnits]);
             }
             __syncwarp();
@@ -532,22 +550,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
     }
   } else if (warp < 4 + kConverters) {
     // --------------------------------------------------------------- converters
-    registers_down<64>();
-    const int quarter = warp & 3, group = (warp - 4) >> 2, row = 32 * quarter + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + kAColumn;
-    uint32_t n = 0, k = 0, b = 0;                              // raw tiles, steps, superblocks
+    registers_down<C::kConvRegs>();
+    // group: of the tiles of rows (Q6_K: sub-blocks of 64 k); turn_of: of the steps, where there are two for each
+    const int quarter = warp & 3, group = (warp - 4) >> 2 & 1, turn_of = (warp - 4) >> 3, row = 32 * quarter + lane;
+    constexpr int kTurns = kConverters / 8;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + C::kAColumn;
+    uint32_t n = 0, b = 0;                                     // raw tiles, superblocks
     // step k's A tiles may be written; they have been
-    auto begin_step = [&] {
-      const bool ok = k < 2 || step_done(k - 2);
+    auto begin_step = [&](uint32_t k) {
+      const bool ok = k < C::kSteps || step_done(k - C::kSteps);
       tc::fence_after_sync();
       return ok;
     };
-    auto end_step = [&] {
+    auto end_step = [&](uint64_t* bar) {
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&S.afull[k & 1]);
-      ++k;
+      if (lane == 0) tc::mbar_arrive(bar);
     };
     auto scale_of = [&](int mt, float v) -> bool {             // of a superblock's sum, for the epilogue
       if (!warp_wait(&S.dempty[b & 1], ((b >> 1) & 1) ^ 1, gave_up, err)) return false;
@@ -565,23 +584,23 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
         for (int sb = 0; sb < nb && !stop; ++sb, ++n, ++b) {
           const uint32_t slot = n % C::kRaw;
           const float d = __half2float(scales[sb]);
-          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err) || (group == 0 && !scale_of(0, d));
+          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err) || (group + turn_of == 0 && !scale_of(0, d));
           if (stop) break;
           const uint8_t* w = S.raw[slot] + row * C::kSb;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = turn_of; c < 4; c += kTurns) {
             const uint4* p = reinterpret_cast<const uint4*>(w + 16 + 48 * c);
             const uint4 l0 = p[0], l1 = p[1], h = p[2];
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(w + 4 * c), at = lanes + 64 * (k & 1) + 16 * group;
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(w + 4 * c), k = 4 * b + c, at = lanes + 64 * (k % C::kSteps) + 16 * group;
             __syncwarp();
-            if (c == 3 && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
+            if (c >= 4 - kTurns && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
             uint32_t hi[16], lo[16];
             convert_q6(l0, l1, h, sc, group, hi, lo);
-            stop = !begin_step();
+            stop = !begin_step(k);
             if (stop) break;
             tc::tmem_st16(at, hi);
             tc::tmem_st16(at + 32, lo);
-            end_step();
+            end_step(&S.afull[k % C::kSteps]);
           }
         }
       } else {
@@ -593,30 +612,28 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
           const uint8_t* w = S.raw[slot] + row * C::kSb;
           const Header H = header_of(*reinterpret_cast<const uint4*>(w));
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = turn_of; c < 4; c += kTurns) {
             const uint4* p = reinterpret_cast<const uint4*>(w + 16 + 32 * c);
             const uint4 q0 = p[0], q1 = p[1];
             __syncwarp();
-            if (c == 3 && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
-            const uint32_t s = c < 2 ? H.sc[0] : H.sc[1], at = lanes + 64 * (k & 1) + 32 * group;
+            if (c >= 4 - kTurns && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
+            const uint32_t s = c < 2 ? H.sc[0] : H.sc[1], k = 4 * b + c, at = lanes + 64 * (k % C::kSteps) + 32 * group;
             uint32_t v[16], w2[16];
             convert_q4<false>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1)), H.down), v);
             convert_q4<true>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1) + 1), H.down), w2);
-            stop = !begin_step();
+            stop = !begin_step(k);
             if (stop) break;
             tc::tmem_st16(at, v);
             tc::tmem_st16(at + 16, w2);
-            end_step();
-            if (c == 1) {
-              // (the superblock before is done with its min tiles, as begin_step has seen)
+            end_step(&S.afull[k % C::kSteps]);
+            if (turn_of == 0 && c == (kTurns == 1 ? 1 : 0)) {
+              // the superblock whose min term had this place before is done (one turn: as begin_step has seen)
               convert_min(H, v);
-              tc::tmem_st16(lanes + (kMinColumn - kAColumn) + 16 * group, v);
-              stop = !scale_of(group, H.scale);
+              stop = (kTurns > 1 && b >= C::kMins && !step_done(4 * (b - C::kMins) + 3)) || !scale_of(group, H.scale);
               if (stop) break;
-              tc::tmem_wait_st();
-              tc::fence_before_sync();
-              __syncwarp();
-              if (lane == 0) tc::mbar_arrive(&S.mfull);
+              tc::fence_after_sync();
+              tc::tmem_st16(lanes + (C::kMinColumn - C::kAColumn) + 32 * (b % C::kMins) + 16 * group, v);
+              end_step(&S.mfull[b % C::kMins]);
             }
           }
         }
@@ -624,23 +641,25 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
     }
   } else {
     // ----------------------------------------------------------------- epilogue
-    registers_up<160>();
+    registers_up<C::kEpiRegs>();
     const int quarter = warp & 3, row = 32 * quarter + lane, half = (warp - 4 - kConverters) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
     uint32_t u = 0, b = 0;                                     // sums, superblocks
     bool stop = false;
     while (!stop && next_item()) {
       // 16 columns at a time, half of them each
-      const int sixteens = (T.n + 15) / 16, first = half ? (sixteens + 1) / 2 : 0, mine = half ? sixteens / 2 : (sixteens + 1) / 2;
+      const int sixteens = (T.n + 15) / 16, first = half ? (sixteens + 1) / 2 : 0,
+                mine = kEpilogue == 4 ? sixteens : half ? sixteens / 2 : (sixteens + 1) / 2;
       // the powers of two to take off: column 32 i + lane of the warp's in inv[i]
       float inv[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) inv[i] = 32 * i + lane < 16 * mine ? P.inv[T.row + 16 * first + 32 * i + lane] : 0.0f;
-      uint64_t total[C::kTilesM][4][8];
+      constexpr int kMine = kEpilogue == 4 ? C::kCols / 16 : 4;
+      uint64_t total[C::kTilesM][kMine][8];
 #pragma unroll
       for (int mt = 0; mt < C::kTilesM; ++mt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kMine; ++k)
 #pragma unroll
           for (int i = 0; i < 8; ++i) total[mt][k][i] = 0;
       for (int sb = 0; sb < nb && !stop; ++sb, ++b) {
@@ -654,15 +673,19 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
           tc::fence_after_sync();
           const float d = S.scale[b & 1][mt][row];
           const uint64_t d2 = pair_of(d, d);
-          const uint32_t at = lanes + kCols * t + 16 * first;
+          const uint32_t at = lanes + C::kUnitCols * t + 16 * first;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kMine; ++k) {
             if (k < mine) {
-              uint32_t v[16];
+              uint32_t v[16], lo[16];
               tc::tmem_ld16(at + 16 * k, v);
+              if constexpr (C::kBeside) tc::tmem_ld16(at + 16 * (sixteens + k), lo);
               tc::tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 8; ++i) total[mt][k][i] = fma2(d2, pair_of(v[2 * i], v[2 * i + 1]), total[mt][k][i]);
+              for (int i = 0; i < 8; ++i) {
+                total[mt][k][i] = fma2(d2, pair_of(v[2 * i], v[2 * i + 1]), total[mt][k][i]);
+                if constexpr (C::kBeside) total[mt][k][i] = fma2(d2, pair_of(lo[2 * i], lo[2 * i + 1]), total[mt][k][i]);
+              }
             }
           }
           tc::fence_before_sync();
@@ -678,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
       for (int mt = 0; mt < (C::kUp ? 1 : C::kTilesM); ++mt) {
         const int r = block * C::kOutRows + kRows * mt + row;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kMine; ++k) {
           if (k >= mine) continue;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -711,37 +734,37 @@ __global__ void __launch_bounds__(kThreads, 1) moe_many_kernel(const __grid_cons
 }
 
 // -------------------------------------------------------------------- launches
-inline int64_t most_tiles(int64_t pairs, int experts) { return std::min(pairs, pairs / kCols + experts); }
-inline int64_t most_rows(int64_t pairs, int experts) { return (pairs + 15 * most_tiles(pairs, experts) + 15) / 16 * 16; }
+inline int64_t most_tiles(int64_t pairs, int experts, int cols) { return std::min(pairs, pairs / cols + experts); }
+inline int64_t most_rows(int64_t pairs, int experts, int cols) { return (pairs + 15 * most_tiles(pairs, experts, cols) + 15) / 16 * 16; }
 
 struct Places {               // in the workspace
   size_t tiles, inv, x, sums, end;
 };
-inline Places places(int64_t pairs, int experts, int64_t cols) {
+inline Places places(int64_t pairs, int experts, int64_t cols, int tile) {
   const auto up = [](size_t v) { return (v + 1023) / 1024 * 1024; };
-  const size_t rows = (size_t)most_rows(pairs, experts);
+  const size_t rows = (size_t)most_rows(pairs, experts, tile);
   Places p{};
   p.tiles = sizeof(Control);
-  p.inv = up(p.tiles + sizeof(Tile) * (size_t)most_tiles(pairs, experts));
+  p.inv = up(p.tiles + sizeof(Tile) * (size_t)most_tiles(pairs, experts, tile));
   p.x = up(p.inv + sizeof(float) * rows);
   p.sums = p.x + rows * (size_t)cols * 4;
   p.end = p.sums + rows * (size_t)((cols / kQK + 3) / 4) * 128;
   return p;
 }
 
-template <int MODE>
+template <int MODE, int COLS>
 cudaError_t launch(const MoeProduct& p, void* work, float* out, cudaStream_t s) {
-  using C = Cfg<MODE>;
+  using C = Cfg<MODE, COLS>;
   static std::atomic<uint64_t> done{0};
-  constexpr int kSmem = (int)sizeof(Smem<MODE>) + 1024;
-  cudaError_t e = allow_smem(moe_many_kernel<MODE>, kSmem, done);
+  constexpr int kSmem = (int)sizeof(Smem<MODE, COLS>) + 1024;
+  cudaError_t e = allow_smem(moe_many_kernel<MODE, COLS>, kSmem, done);
   if (e != cudaSuccess) return e;
   const int64_t pairs = p.plan.tokens * p.plan.top_k, nb = p.cols / kQK, all = p.rows * p.plan.experts;
   const int64_t pitch = C::kQ6 ? q6k_gpu_row_bytes(nb) : nb * kBlockBytes, blocks = (p.rows + C::kOutRows - 1) / C::kOutRows;
-  const int64_t tiles = most_tiles(pairs, p.plan.experts);
+  const int64_t tiles = most_tiles(pairs, p.plan.experts, COLS);
   if (tiles * blocks * nb * 16 >= (int64_t(1) << 31)) return cudaErrorNotSupported;        // 32-bit counters
   uint8_t* at = static_cast<uint8_t*>(work);
-  const Places w = places(pairs, p.plan.experts, p.cols);
+  const Places w = places(pairs, p.plan.experts, p.cols, COLS);
   Control* control = reinterpret_cast<Control*>(at);
   Tile* list = reinterpret_cast<Tile*>(at + w.tiles);
   float* inv = reinterpret_cast<float*>(at + w.inv);
@@ -754,14 +777,14 @@ cudaError_t launch(const MoeProduct& p, void* work, float* out, cudaStream_t s) 
   P.scales = p.w + nb * kQ6GpuBytes, P.out = out, P.counter = &control->counter, P.err = p.err, P.pitch = pitch;
   P.rows = (int)p.rows, P.nb = (int)nb, P.blocks = (int)blocks;
   const LayoutParams A{p.plan.offsets, control, list, p.err, (int)pairs, p.plan.experts};
-  moe_many_layout_kernel<<<1, kMoeMaxExperts, 0, s>>>(A);
+  moe_many_layout_kernel<COLS><<<1, kMoeMaxExperts, 0, s>>>(A);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const SplitParams B{p.x, p.plan.order, control, list, at + w.x, at + w.sums, inv, p.err, pairs, p.cols, (int)nb,
                       C::kUp ? p.plan.top_k : 0};
-  if ((e = launch_after(moe_many_split_kernel<!C::kQ6>, dim3((unsigned)tiles, kCols / 8), 256, 0, s, B)) != cudaSuccess) return e;
+  if ((e = launch_after(moe_many_split_kernel<!C::kQ6>, dim3((unsigned)tiles, COLS / 8), 256, 0, s, B)) != cudaSuccess) return e;
   int dev = 0;
   cudaGetDevice(&dev);
-  return launch_after(moe_many_kernel<MODE>, dim3((unsigned)std::min<int64_t>(tiles * blocks, device_info(dev).sm_count)), kThreads,
+  return launch_after(moe_many_kernel<MODE, COLS>, dim3((unsigned)std::min<int64_t>(tiles * blocks, device_info(dev).sm_count)), C::kThreads,
                       kSmem, s, P);
 }
 

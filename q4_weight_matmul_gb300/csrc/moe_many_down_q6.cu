@@ -4,7 +4,8 @@
 namespace q4k {
 
 cudaError_t launch_moe_many_down_q6(const MoeProduct& p, void* work, float* out, cudaStream_t s) {
-  return many::launch<many::kDownQ6>(p, work, out, s);
+  return p.plan.tokens * p.plan.top_k <= kMoeSmallTiles * p.plan.experts ? many::launch<many::kDownQ6, 32>(p, work, out, s)
+                                                                       : many::launch<many::kDownQ6, 112>(p, work, out, s);
 }
 
 }  // namespace q4k

@@ -224,6 +224,7 @@ inline size_t moe_few_workspace(int64_t pairs, int experts, int64_t cols) {
 cudaError_t launch_moe_few_gate_up(const MoeProduct& p, void* work, float* out, cudaStream_t s);
 cudaError_t launch_moe_few_down_q4(const MoeProduct& p, void* work, float* out, cudaStream_t s);
 cudaError_t launch_moe_few_down_q6(const MoeProduct& p, void* work, float* out, cudaStream_t s);
+constexpr int64_t kMoeSmallTiles = 24;                 // pairs an expert up to which the tiles are of 32 pairs, not of 112
 // The same for many pairs an expert (moe_many.cuh); `work`: moe_many_workspace() bytes.
 size_t moe_many_workspace(int64_t pairs, int experts, int64_t cols);
 cudaError_t launch_moe_many_gate_up(const MoeProduct& p, void* work, float* out, cudaStream_t s);
