@@ -51,6 +51,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return true;
 }
 
+// Two barriers, asked together at first.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
+                                          volatile int* gave_up, int* err) {
+  if (__all_sync(~0u, tc::mbar_try_wait(bar, parity) & tc::mbar_try_wait(bar2, parity2))) return true;
+  return warp_wait(bar, parity, gave_up, err) && warp_wait(bar2, parity2, gave_up, err);
+}
+
 // Exclusive sum of `v` over the block's threads before this one (`most`:
 // maximum in place of a sum); every thread gets the whole block's in `all`.
 template <int THREADS, bool MOST>

@@ -2,8 +2,14 @@
 // tensor cores (tcgen05): 128 or 256 weight rows times up to 112 pairs of one
 // expert, fp32 sums of exact 16-bit products as in moe_few.cuh.
 //
+// Measured: 4096 tokens, 8 of 128 experts of 2048 x 768: gate and up 408 us
+// (2 x 206 GFLOP with both parts: 1.0 PFLOP/s), down 302 us; 513 tokens 125 us
+// and 80 us.  Bound: a step's converters and the issue of its products, see below;
+// 45 us of the 408 are the split's, which moves 168 MB.
+//
 // Four launches.  (1) One CTA lays the pairs out in tiles: an expert's n pairs
-// become ceil(n / 112) tiles of equal size, a multiple of 16.  (2) Each pair's
+// become ceil(n / 112) tiles (or ceil(n / 32): see kMoeSmallTiles) of equal
+// size, a multiple of 16.  (2) Each pair's
 // activations, times a power of two that puts the row's largest in
 // [2^14, 2^15), become two binary16 parts, stored tile by tile as the products
 // read them (64 k of hi, then of lo, in the 128-byte-swizzled layout), with
@@ -26,10 +32,12 @@
 // A CTA's warps: 0 copies activations, 2 draws items (a tile of pairs times a
 // block of rows; large tiles first) and copies weights, 1 and 3 issue the
 // products, one for each tile of rows (a burst of eight waits and starts for
-// some 400 cycles, which the other's products cover), 4-11 convert (two groups of four; with one, 700 cycles a tile held the products
-// up, 547 us for 4096 tokens), 12-19 run the epilogue (64 columns a thread;
-// totals in registers).
-// Every wait is bounded.
+// some 400 cycles, which the other's products cover), then two groups of four
+// convert (with one, 700 cycles a tile held the products up, 547 us for 4096
+// tokens; four for tiles of 32 pairs), and eight run the epilogue (totals in
+// registers).  Every wait is bounded, and its loop short and inline: with ten
+// instructions more in each, the roles' loops did not fit the instruction
+// caches together (459 us).
 #pragma once
 
 #include "mma_sync.cuh"
@@ -57,29 +65,29 @@ struct Control {
   int tiles, counter, pad[30];
 };
 
-// COLS: the most pairs of a tile.  The products' steps are 64 k of both A tiles
-// (Q6_K: of both parts), the last of a superblock with its min term.  Tensor
-// memory: three sums in turn, the A tiles of some steps in turn, those of the
-// min terms.
+// COLS: the most pairs of a tile.  A step of the products is 64 k (or twice
+// that) of both A tiles (Q6_K: of both parts), the last of a superblock with
+// its min term.  Tensor memory: three sums in turn, the A tiles of two steps in
+// turn, those of the min terms.
 //  - 112: a step's products take longer than making its A.  (With 128 columns a
 //    sum the min terms' only place is among the steps', where they hold the
 //    next step up: 482 us for 4096 tokens.)
-//  - 32: the other way round, so there are twice the converters, two groups for
-//    every second step each, and four steps of A; the activations' hi and lo
-//    parts are columns of one product beside each other.
+//  - 32: the other way round, so there are twice the converters, steps of 128 k
+//    (a step costs the warps that issue products some 800 cycles), and the
+//    activations' hi and lo parts are columns of one product beside each other.
 template <int MODE, int COLS>
 struct Cfg {
   static constexpr bool kUp = MODE == kGateUp, kQ6 = MODE == kDownQ6;
   static constexpr bool kBeside = COLS == 32;
   static constexpr int kCols = COLS, kUnitCols = kBeside ? 2 * COLS : COLS;
-  static constexpr int kSteps = kBeside ? 4 : 2, kMins = kBeside ? 2 : 1;            // A places
-  static constexpr int kDone = 4 * kMins;                    // barriers of steps: as long as a min term's place is waited for
-  static constexpr uint32_t kAColumn = kUnits * kUnitCols, kMinColumn = kAColumn + 64 * kSteps;
+  static constexpr int kHalves = kBeside ? 2 : 1, kPerBlock = 4 / kHalves;           // 64 k of a step, steps of a superblock
+  static constexpr int kMins = kBeside ? 2 : 1;              // places of min terms
+  static constexpr uint32_t kAColumn = kUnits * kUnitCols, kMinColumn = kAColumn + 128 * kHalves;
   static constexpr int kConverters = kBeside ? 16 : 8, kEpilogue = kBeside ? 4 : 8;  // warps
   static constexpr int kThreads = 32 * (4 + kConverters + kEpilogue);
-  static constexpr int kStageBytes = 2 * COLS * 128, kSumBytes = COLS * 128;         // (the sums of four superblocks)
+  static constexpr int kStageBytes = 2 * COLS * 128 * kHalves, kSumBytes = COLS * 128;         // (the sums of four superblocks)
   static constexpr int kSb = kQ6 ? kQ6GpuBytes : kBlockBytes;
-  static constexpr int kRaw = kBeside ? (kQ6 ? 6 : 9) : (kQ6 ? 3 : 4);               // weight tiles (128 rows of a superblock) in flight
+  static constexpr int kRaw = kBeside ? (kQ6 ? 5 : 8) : (kQ6 ? 3 : 4);               // weight tiles (128 rows of a superblock) in flight
   static constexpr int kIssuers = kQ6 ? 1 : 2;               // warps that issue products
   static constexpr int kTilesM = kQ6 ? 1 : 2;                // of 128 rows each
   static constexpr int kOutRows = MODE == kDownQ4 ? 2 * kRows : kRows;
@@ -109,7 +117,7 @@ struct __align__(1024) Smem {
   uint8_t sums[2][C::kSumBytes];
   uint8_t raw[C::kRaw][kRows * C::kSb];
   float scale[2][2][kRows];
-  uint64_t xfull[kStages], sfull[2], sempty[2], rfull[C::kRaw], rempty[C::kRaw], afull[C::kSteps], mfull[C::kMins], done[C::kDone],
+  uint64_t xfull[kStages], sfull[2], sempty[2], rfull[C::kRaw], rempty[C::kRaw], afull[2], mfull[C::kMins], done[4],
       tfull[kUnits], tempty[kUnits], dfull[2], dempty[2], qfull[kQueue], qempty[kQueue], drain[2];
   Tile item[kQueue];
   int block[kQueue];
@@ -376,13 +384,13 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) tc::mbar_init(&S.xfull[i], 1);
-    for (int i = 0; i < C::kDone; ++i) tc::mbar_init(&S.done[i], C::kIssuers);
+    for (int i = 0; i < 4; ++i) tc::mbar_init(&S.done[i], C::kIssuers);
     for (int i = 0; i < C::kRaw; ++i) tc::mbar_init(&S.rfull[i], 1), tc::mbar_init(&S.rempty[i], C::kQ6 ? kConverters : kConverters / 2);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&S.sfull[i], 1), tc::mbar_init(&S.sempty[i], C::kIssuers);
       tc::mbar_init(&S.dfull[i], C::kQ6 ? 4 : 8), tc::mbar_init(&S.dempty[i], kEpilogue);
     }
-    for (int i = 0; i < C::kSteps; ++i) tc::mbar_init(&S.afull[i], 8);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(&S.afull[i], kConverters);
     for (int i = 0; i < C::kMins; ++i) tc::mbar_init(&S.mfull[i], 8);
     for (int i = 0; i < kUnits; ++i) tc::mbar_init(&S.tfull[i], 1), tc::mbar_init(&S.tempty[i], kEpilogue);
     for (int i = 0; i < kQueue; ++i) tc::mbar_init(&S.qfull[i], 1), tc::mbar_init(&S.qempty[i], 1 + C::kIssuers + kConverters + kEpilogue);
@@ -420,8 +428,9 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
     return T.n > 0;
   };
 
-  // Until step `k` is done with its operands.
-  auto step_done = [&](uint32_t k) { return warp_wait(&S.done[k % C::kDone], (k / C::kDone) & 1, gave_up, err); };
+  // Until step `k` is done with its operands.  (Four barriers: a step four later waits for this one's operands, or for
+  // the place of a min term that this one's superblock had.)
+  auto step_done = [&](uint32_t k) { return warp_wait(&S.done[k % 4], (k / 4) & 1, gave_up, err); };
 
   if (warp < 4) {
     registers_down<C::kFewRegs>();
@@ -433,7 +442,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
         const uint32_t padded = (T.n + 15) / 16 * 16;
         const uint8_t* x = P.x + (int64_t)T.row * nb * 1024;
         const uint8_t* sums = P.sums + (int64_t)T.row * ((nb + 3) / 4) * 128;
-        for (int c = 0; c < 4 * nb; ++c, ++j) {
+        for (int c = 0; c < 4 * nb; c += C::kHalves, ++j) {
           if (!C::kQ6 && c % 16 == 0) {
             stop = !warp_wait(&S.sempty[g & 1], ((g >> 1) & 1) ^ 1, gave_up, err);
             if (stop) break;
@@ -448,8 +457,9 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
           stop = j >= kStages && !step_done(j - kStages);
           if (stop) break;
           if (elect()) {
-            tc::mbar_arrive_expect_tx(&S.xfull[slot], 2 * padded * 128);
-            tc::bulk_g2s(S.x[slot], x + (int64_t)c * 2 * padded * 128, 2 * padded * 128, &S.xfull[slot]);
+            const uint32_t bytes = C::kHalves * 2 * padded * 128;
+            tc::mbar_arrive_expect_tx(&S.xfull[slot], bytes);
+            tc::bulk_g2s(S.x[slot], x + (int64_t)c * 2 * padded * 128, bytes, &S.xfull[slot]);
           }
           __syncwarp();
         }
@@ -513,31 +523,33 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
           const bool last = (sb & 3) == 3 || sb == nb - 1;
           stop = !warp_wait(&S.tempty[u % kUnits], ((u / kUnits) & 1) ^ 1, gave_up, err);
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c, ++k) {
-            const uint32_t x = tc::smem_u32(S.x[k % kStages]), a = tmem + C::kAColumn + 64 * (k % C::kSteps) + 32 * mt;
+          for (int c = 0; c < C::kPerBlock; ++c, ++k) {
+            const uint32_t x = tc::smem_u32(S.x[k % kStages]), a = tmem + C::kAColumn + 64 * C::kHalves * (k & 1) + 32 * mt;
             const uint32_t sums = tc::smem_u32(S.sums[g & 1]) + 32 * (sb & 3);
-            stop = stop || !warp_wait(&S.xfull[k % kStages], (k / kStages) & 1, gave_up, err) ||
-                   !warp_wait(&S.afull[k % C::kSteps], (k / C::kSteps) & 1, gave_up, err);
-            if (!C::kQ6 && c == 3)
-              stop = stop || !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, gave_up, err) || !warp_wait(&S.mfull[b % C::kMins], (b / C::kMins) & 1, gave_up, err);
+            stop = stop || !warp_wait(&S.xfull[k % kStages], (k / kStages) & 1, &S.afull[k & 1], (k >> 1) & 1, gave_up, err);
+            if (!C::kQ6 && c == C::kPerBlock - 1)
+              stop = stop || !warp_wait(&S.sfull[g & 1], (g >> 1) & 1, &S.mfull[b % C::kMins], (b / C::kMins) & 1, gave_up, err);
             if (stop) break;
             tc::fence_after_sync();
             if (elect()) {
-              const uint64_t hi = tc::desc_sw128(x), lo = tc::desc_sw128(x + padded * 128);
+#pragma unroll
+              for (int h = 0; h < C::kHalves; ++h) {
+                const uint64_t hi = tc::desc_sw128(x + h * 2 * padded * 128), lo = hi + padded * 8;   // (of 16 bytes)
 #pragma unroll 1
-              for (int i = 0; i < 4; ++i) {                    // (2: 32 bytes in the descriptor's units)
-                mma_ts(d, a + 8 * i, hi + 2 * i, what, c | i ? 1 : 0);
-                if constexpr (!C::kBeside) mma_ts(d, a + 8 * i, lo + 2 * i, what, 1);
-                if constexpr (C::kQ6) mma_ts(d, a + 32 + 8 * i, hi + 2 * i, narrow, 1);
+                for (int i = 0; i < 4; ++i) {                  // 16 k: 32 bytes of a row
+                  mma_ts(d, a + 64 * h + 8 * i, hi + 2 * i, what, c | h | i ? 1 : 0);
+                  if constexpr (!C::kBeside) mma_ts(d, a + 64 * h + 8 * i, lo + 2 * i, what, 1);
+                  if constexpr (C::kQ6) mma_ts(d, a + 64 * h + 32 + 8 * i, hi + 2 * i, narrow, 1);
+                }
               }
-              if (!C::kQ6 && c == 3) {
+              if (!C::kQ6 && c == C::kPerBlock - 1) {
                 const uint32_t m = tmem + C::kMinColumn + 32 * (b % C::kMins) + 16 * mt;
                 mma_ts(d, m, tc::desc_sw128(sums), narrow, 1);
                 mma_ts(d, m + 8, tc::desc_sw128(sums), narrow, 1);
                 if (last) tc::mma_commit(&S.sempty[g & 1]);
               }
-              tc::mma_commit(&S.done[k % C::kDone]);
-              if (c == 3) tc::mma_commit(&S.tfull[u % kUnits]);
+              tc::mma_commit(&S.done[k % 4]);
+              if (c == C::kPerBlock - 1) tc::mma_commit(&S.tfull[u % kUnits]);
             }
             __syncwarp();
           }
@@ -551,14 +563,15 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
   } else if (warp < 4 + kConverters) {
     // --------------------------------------------------------------- converters
     registers_down<C::kConvRegs>();
-    // group: of the tiles of rows (Q6_K: sub-blocks of 64 k); turn_of: of the steps, where there are two for each
-    const int quarter = warp & 3, group = (warp - 4) >> 2 & 1, turn_of = (warp - 4) >> 3, row = 32 * quarter + lane;
-    constexpr int kTurns = kConverters / 8;
+    // group: of the tiles of rows (Q6_K: sub-blocks of 64 k); turn_of: of a step's 64 k, where it has them twice
+    const int quarter = warp & 3, group = (warp - 4) >> 2 & 1, row = 32 * quarter + lane;
+    constexpr int kTurns = C::kHalves;
+    const int turn_of = kTurns == 1 ? 0 : (warp - 4) >> 3;
     const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16) + C::kAColumn;
     uint32_t n = 0, b = 0;                                     // raw tiles, superblocks
     // step k's A tiles may be written; they have been
     auto begin_step = [&](uint32_t k) {
-      const bool ok = k < C::kSteps || step_done(k - C::kSteps);
+      const bool ok = k < 2 || step_done(k - 2);
       tc::fence_after_sync();
       return ok;
     };
@@ -591,7 +604,8 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
           for (int c = turn_of; c < 4; c += kTurns) {
             const uint4* p = reinterpret_cast<const uint4*>(w + 16 + 48 * c);
             const uint4 l0 = p[0], l1 = p[1], h = p[2];
-            const uint32_t sc = *reinterpret_cast<const uint32_t*>(w + 4 * c), k = 4 * b + c, at = lanes + 64 * (k % C::kSteps) + 16 * group;
+            const uint32_t sc = *reinterpret_cast<const uint32_t*>(w + 4 * c), k = C::kPerBlock * b + c / C::kHalves,
+                           at = lanes + 64 * (C::kHalves * (k & 1) + turn_of) + 16 * group;
             __syncwarp();
             if (c >= 4 - kTurns && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
             uint32_t hi[16], lo[16];
@@ -600,7 +614,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
             if (stop) break;
             tc::tmem_st16(at, hi);
             tc::tmem_st16(at + 32, lo);
-            end_step(&S.afull[k % C::kSteps]);
+            end_step(&S.afull[k & 1]);
           }
         }
       } else {
@@ -617,7 +631,8 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
             const uint4 q0 = p[0], q1 = p[1];
             __syncwarp();
             if (c >= 4 - kTurns && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
-            const uint32_t s = c < 2 ? H.sc[0] : H.sc[1], k = 4 * b + c, at = lanes + 64 * (k % C::kSteps) + 32 * group;
+            const uint32_t s = c < 2 ? H.sc[0] : H.sc[1], k = C::kPerBlock * b + c / C::kHalves,
+                           at = lanes + 64 * (C::kHalves * (k & 1) + turn_of) + 32 * group;
             uint32_t v[16], w2[16];
             convert_q4<false>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1)), H.down), v);
             convert_q4<true>(q0, q1, cvt::mul_h2(cvt::byte_h2(s, 2 * (c & 1) + 1), H.down), w2);
@@ -625,14 +640,18 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
             if (stop) break;
             tc::tmem_st16(at, v);
             tc::tmem_st16(at + 16, w2);
-            end_step(&S.afull[k % C::kSteps]);
+            end_step(&S.afull[k & 1]);
             if (turn_of == 0 && c == (kTurns == 1 ? 1 : 0)) {
               // the superblock whose min term had this place before is done (one turn: as begin_step has seen)
               convert_min(H, v);
-              stop = (kTurns > 1 && b >= C::kMins && !step_done(4 * (b - C::kMins) + 3)) || !scale_of(group, H.scale);
-              if (stop) break;
-              tc::fence_after_sync();
+              if constexpr (kTurns > 1) {
+                stop = b >= C::kMins && !step_done(C::kPerBlock * (b - C::kMins + 1) - 1);
+                if (stop) break;
+                tc::fence_after_sync();
+              }
               tc::tmem_st16(lanes + (C::kMinColumn - C::kAColumn) + 32 * (b % C::kMins) + 16 * group, v);
+              stop = !scale_of(group, H.scale);
+              if (stop) break;
               end_step(&S.mfull[b % C::kMins]);
             }
           }

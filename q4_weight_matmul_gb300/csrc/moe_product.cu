@@ -61,9 +61,15 @@ cudaError_t combine(const MoeProduct& p, const float* z, cudaStream_t s) {
 
 }  // namespace
 
-// Many pairs an expert go to the tensor cores' tiles of up to 128 pairs, few
-// to the kernel that streams the weights once per 16 pairs.
-constexpr int64_t kMany = 24;
+// Many pairs an expert go to the tensor cores' tiles of up to 112 pairs, few
+// to the kernel that streams the weights once per 16 pairs: its time grows with
+// the pairs, that of a tile hardly does until it is full.  Measured (us; gate
+// and up, down Q4_K, down Q6_K), few | many:
+//   pairs an expert   128 experts, 2048 x 768              32 experts, 2560 x 1536
+//         6           74 / 51 / 80   | 82 / 53 / 73        48 / 34 / 51 | 64 / 37 / 50
+//        10           94 / 65 / 95   | 92 / 56 / 78        64 / 43 / 61 | 65 / 47 / 58
+//        16          129 / 86 / 121  | 97 / 62 / 84        87 / 53 / 75 | 67 / 48 / 59
+constexpr int64_t kMany = 10;
 static bool many(int64_t tokens, int top_k, int experts) { return tokens * top_k >= kMany * experts; }
 
 // Operands for any number of pairs up to this one.
