@@ -8,7 +8,9 @@ projection with the residual.
 reads a prompt of every request in one batch (one chunk each), then decodes
 ``--steps`` tokens of all of them, a CUDA graph per step shape, and prints the
 time of each.  Weights and inputs are random (``--hidden 2560 --heads 32
---kv-heads 8``: the 4B shape).
+--kv-heads 8``: the 4B shape).  With ``--experts 128`` (and ``--top-k``,
+``--width``) the layer goes on with routed experts in place of a dense
+feed-forward part (``expert_block.py``).
 """
 from __future__ import annotations
 
@@ -180,12 +182,24 @@ def main():
     ap.add_argument("--kv-heads", type=int, default=8)
     ap.add_argument("--head-dim", type=int, default=128)
     ap.add_argument("--page", type=int, default=16)
+    ap.add_argument("--experts", type=int, default=0, help="routed experts behind the attention block (0: none)")
+    ap.add_argument("--top-k", type=int, default=8, help="experts of a token")
+    ap.add_argument("--width", type=int, default=768, help="width of an expert")
     a = ap.parse_args()
     q4k.build()
     max_pages = -(-(a.prompt + a.steps) // a.page)
     pages = Pages(a.requests * max_pages, a.page, max_pages)
     block = random_block(a.hidden, a.heads, a.kv_heads, a.head_dim, a.requests * max_pages, a.page,
                          max_pages * a.page, torch.bfloat16, adapters=2)
+    experts = None
+    if a.experts:
+        from q4_weight_matmul_gb300.expert_block import random_experts
+        experts = random_experts(a.hidden, a.width, a.experts, a.top_k)
+
+    def layer(x, step, max_q, segments, work=None):
+        y = block(x, step, max_q, segments, work)
+        return y if experts is None else experts(y, work=work)
+
     adapter = [r % 3 - 1 for r in range(a.requests)]              # none, the first, the second, none, ...
 
     def timed(fn):
@@ -201,7 +215,7 @@ def main():
     step = {k: v.cuda() for k, v in pages.step(new).items()}
     x = torch.randn((sum(new.values()), a.hidden), device="cuda")
     segments = q4k.q4k_lora_segments([adapter[r] for r, n in new.items() for _ in range(n)])
-    y, us = timed(lambda: block(x, step, max(new.values()), segments))
+    y, us = timed(lambda: layer(x, step, max(new.values()), segments))
     print(f"prompt: {x.shape[0]} tokens, {us:.0f} us (first call)")
 
     # decoding: the step's arrays are copied into fixed buffers, the layer replays as a graph
@@ -213,11 +227,11 @@ def main():
         host = pages.step(new)
         if buffers is None:
             buffers = {k: v.cuda() for k, v in host.items()}
-            y = block(x, buffers, 1, segments, work)               # makes the workspaces
+            y = layer(x, buffers, 1, segments, work)               # makes the workspaces
             torch.cuda.synchronize()
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph):
-                y = block(x, buffers, 1, segments, work)
+                y = layer(x, buffers, 1, segments, work)
         else:
             for k, v in host.items():
                 buffers[k].copy_(v)
