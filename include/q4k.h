@@ -6,7 +6,8 @@
  * engine, §2 "the roofline that dictates strategy"): the bandwidth-bound
  * decode GEMV and the compute-bound prefill GEMM over q8_1 activations; and
  * what stands between a layer's projections: head norms with rotation,
- * attention over a paged key/value cache, low-rank adapters.
+ * attention over a paged key/value cache, low-rank adapters; and the
+ * feed-forward part with routed experts.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -26,7 +27,8 @@
  *  - Sizes of zero (rows, tokens, batch) are valid and enqueue nothing.
  *  - A call whose work takes more than one kernel launch (a q4k_gemv_seq
  *    list of more than 96 jobs, or 48 Q6_K jobs; q4k_lora_add;
- *    q4k_paged_attn of many rows) validates and plans all of it first; only a
+ *    q4k_paged_attn of many rows; q4k_moe_route, q4k_moe_gate_up and
+ *    q4k_moe_down) validates and plans all of it first; only a
  *    CUDA launch failure of a later launch can leave the earlier ones
  *    enqueued (the status is then Q4K_ERR_CUDA).
  *
@@ -722,8 +724,9 @@ typedef struct q4k_moe_plan {
 /*
  * q4k_moe_workspace_bytes - workspace of the three calls below for layers
  * with experts of hidden -> width -> hidden (gate and up: width x hidden,
- * down: hidden x width; 0, 0 for q4k_moe_route alone); it serves fewer tokens too.  0 for an invalid request.  16-byte aligned,
- * no clearing; calls that share a workspace must not overlap on the GPU.
+ * down: hidden x width; 0, 0 for q4k_moe_route alone); it serves fewer tokens
+ * too.  0 for an invalid request.  16-byte aligned, no clearing; calls that
+ * share a workspace must not overlap on the GPU.
  */
 size_t q4k_moe_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t hidden,
                                int64_t width);
@@ -741,7 +744,8 @@ size_t q4k_moe_workspace_bytes(int64_t tokens, int top_k, int experts, int64_t h
  *              *n_tokens on get no experts (expert -1, place -2): the rows
  *              behind the last request of a padded batch
  * *n_tokens out of 0..tokens is cut to that and reported by q4k_device_error
- * (Q4K_ERR_DEVICE_INDEX).  Weights are fp32, within 3e-6 |scale| of the exact value.
+ * (Q4K_ERR_DEVICE_INDEX).  Weights are fp32, within 3e-6 |scale| of the exact
+ * value.
  * Errors: Q4K_ERR_INVALID_ARG, Q4K_ERR_ALIGNMENT.  tokens == 0 enqueues
  * nothing and leaves the arrays as they are.
  */
@@ -757,8 +761,10 @@ int q4k_moe_route(const float* logits, const q4k_moe_plan* plan, int renormalize
  *   gate, up : Q4_K (BLOCK144), [experts][rows][cols/256] superblocks
  *   x        : float [tokens][cols]
  *   h        : float [tokens * top_k][rows]
- * Both products are within the bound at the top of this header (x held to 22
- * bits beside the largest value of its row).
+ * Accuracy: both products are within 1e-4 * (M + 2^-16 max|x[t]| W1) of the
+ * exact ones, with M as at the top of this header and W1 the same sum for
+ * activations of 1 (x is held to 22 bits beside the largest value of its row).
+ * Of a superblock with |dmin| > 2^24 |d| the terms with d may count as 0.
  */
 int q4k_moe_gate_up(const q4k_moe_plan* plan, const void* gate, const void* up, int64_t rows,
                     int64_t cols, const float* x, float* h, void* workspace,
@@ -775,14 +781,16 @@ int q4k_moe_gate_up(const q4k_moe_plan* plan, const void* gate, const void* up, 
  *   residual : float [tokens][rows] or NULL; may be y
  *   y        : float [tokens][rows]
  * Accuracy: |y - exact| <= 1e-4 * (|residual| + sum_j |weight_j| (M_j +
- * 2^-16 max|h_j| W1)) with M_j as at the top of this header and W1 the same
- * sum for activations of 1.
- * In both calls offsets out of range or descending are cut, an order or place
- * out of range is skipped (its row counts as zeros), and each is reported by
- * q4k_device_error (Q4K_ERR_DEVICE_INDEX).  Deterministic on one device.
+ * 2^-16 max|h_j| W1)) with M_j and W1 as above.
+ * In both calls offsets out of range or descending are cut, an order out of
+ * range, or a place of offsets[experts] or more, is skipped (its row counts as
+ * zeros), and each is reported by q4k_device_error (Q4K_ERR_DEVICE_INDEX).
+ * Values that are not finite make the rows they stand in not finite, and no
+ * others.  Deterministic on one device.
  * Errors: Q4K_ERR_INVALID_ARG, Q4K_ERR_ALIGNMENT, Q4K_ERR_UNSUPPORTED (rows *
- * experts or tokens * top_k of 2^31 or more).  tokens == 0 or rows == 0
- * enqueues nothing.
+ * experts or tokens * top_k near 2^31 or more; never where (tokens * top_k / 8
+ * + experts) * (rows / 128 + 1) * cols / 16 is less than 2^31 too).  tokens ==
+ * 0 or rows == 0 enqueues nothing.
  */
 int q4k_moe_down(const q4k_moe_plan* plan, const void* w, int format, int64_t rows, int64_t cols,
                  const float* h, const float* residual, float* y, void* workspace,

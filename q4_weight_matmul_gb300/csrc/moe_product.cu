@@ -20,11 +20,12 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const MoeProduct 
   using F = std::conditional_t<V == 4, float4, float>;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const MoePlan& L = P.plan;
-  const int64_t per = P.rows / V, at = (int64_t)blockIdx.x * kThreads + threadIdx.x, t = at / per, pairs = L.tokens * L.top_k;
+  const int64_t per = P.rows / V, at = (int64_t)blockIdx.x * kThreads + threadIdx.x, t = at / per;
   if (t >= L.tokens) return;
   const int64_t r = (at - t * per) * V;
   const int32_t* place = L.place + t * L.top_k;
   const float* weight = L.weight + t * L.top_k;
+  const int64_t pairs = min((int64_t)L.offsets[L.experts], L.tokens * L.top_k);        // rows of z that have been made
   if (place[0] == -2) return;
   alignas(16) float y[V] = {};
   if (P.residual) *reinterpret_cast<F*>(y) = *reinterpret_cast<const F*>(P.residual + t * P.rows + r);

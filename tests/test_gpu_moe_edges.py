@@ -257,3 +257,22 @@ def test_results_of_more_than_two_to_the_31_values():
     ours[mine.reshape(-1)] = rows_of.reshape(-1, cols)
     want, tol = moe.down(ours, f, "q4_k", rows, expert[some], route.weight.cpu().numpy()[some], e)
     assert np.all(np.abs(y[torch.from_numpy(some).cuda()].cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("tokens", [5, 300])
+def test_a_place_behind_the_last_pair_is_reported(tokens):
+    """The rows behind offsets[experts] of a workspace hold anything."""
+    e, k, cols, rows = 3, 2, 256, 40
+    _, w = matrices(e, rows, cols, 110)
+    expert, weight = choose(tokens, e, k, "any", 111)
+    expert[1] = -1
+    good, h = route_of(expert, weight, e), dev(synth.activations(tokens * k, cols, 112))
+    work = q4k.q4k_moe_workspace(tokens, k, e, rows, cols)
+    work.fill_(255)
+    want = q4k.q4k_moe_down(h, w, rows, good, workspace=work)
+    assert q4k.q4k_device_error() == 0
+    place = good.place.clone()
+    place[1, 0] = int(good.offsets[-1])
+    got = q4k.q4k_moe_down(h, w, rows, good._replace(place=place), workspace=work)
+    assert q4k.q4k_device_error() == 6
+    assert torch.equal(got, want) and torch.all(want[1] == 0)
