@@ -8,8 +8,11 @@
 //  - activations: x of a pair and superblock times a power of two that puts
 //    the largest in [2^14, 2^15), as two binary16 parts (22 bits);
 //  - Q4_K quants enter mma.sync m16n8k16 as binary16 subnormals: the bits of
-//    q (or 16 q) in a half are the value q 2^-24, so widening a quant is one
-//    AND for two of them, and the products are exact;
+//    4 q (or 64 q) in a half are the value q 2^-22, so widening two quants is
+//    a shift for two masks, and the products are exact.  (Sums lose what lies
+//    below the largest product's exponent, taken as that of a normal number:
+//    with q 2^-24, a shift less, the relative error of h was 1.9e-6, now 4e-7,
+//    for 4 % of the time);
 //  - a sub-block's (Q6_K: a group's) four (two) products start from zero, and
 //    fp32 FMAs add d sc times their sum up; the min term is one product of
 //    the eight m with the sub-blocks' sums of x, hi and lo;
@@ -370,11 +373,11 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
     for (int r = 0; r < 2; ++r) {
       const uint4 h = *reinterpret_cast<const uint4*>(w + t * apart + 8 * r * kBlockBytes);
       const float2 dd = unpack2<false>(h.x);
-      d[t][r] = dd.x * 16777216.0f, dmin[t][r] = dd.y * -1073741824.0f;       // 2^24; 2^24 and the sums' 2^6
+      d[t][r] = dd.x * 4194304.0f, dmin[t][r] = dd.y * -67108864.0f;          // 2^22; 2^20 and the sums' 2^6
       sc[t][r][0] = h.y & 0x3F3F3F3Fu;
       sc[t][r][1] = (h.w & 0x0F0F0F0Fu) | ((h.y >> 2) & 0x30303030u);
       const uint32_t mins = c < 2 ? h.z & 0x3F3F3F3Fu : ((h.w >> 4) & 0x0F0F0F0Fu) | ((h.z >> 2) & 0x30303030u);
-      m[t][r] = __byte_perm(mins, 0, (c & 1) ? 0x4342 : 0x4140);              // m[2 c], m[2 c + 1] times 2^-24
+      m[t][r] = __byte_perm(mins, 0, (c & 1) ? 0x4342 : 0x4140) << 4;         // m[2 c], m[2 c + 1] times 2^-20
     }
   float sum[2][NT][4] = {};
   // A chunk of 64 k has four sums in the making (two sub-blocks, two tiles of
@@ -401,11 +404,11 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
         uint32_t a[kTogether][2][4];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint32_t u = i ? q[t][0].y : q[t][0].x, v = i ? q[t][1].y : q[t][1].x, u8 = u >> 8, v8 = v >> 8;
+          const uint32_t u = i ? q[t][0].y : q[t][0].x, v = i ? q[t][1].y : q[t][1].x;
 #pragma unroll
           for (int h = 0; h < kTogether; ++h) {
-            const uint32_t bits = first + h ? 0x00F000F0u : 0x000F000Fu;
-            a[h][t][0] = u & bits, a[h][t][1] = v & bits, a[h][t][2] = u8 & bits, a[h][t][3] = v8 & bits;
+            const uint32_t bits = first + h ? 0x03C003C0u : 0x003C003Cu;
+            a[h][t][0] = u << 2 & bits, a[h][t][1] = v << 2 & bits, a[h][t][2] = u >> 6 & bits, a[h][t][3] = v >> 6 & bits;
           }
         }
 #pragma unroll

@@ -2,30 +2,35 @@
 // tensor cores (tcgen05): 128 or 256 weight rows times up to 112 pairs of one
 // expert, fp32 sums of exact 16-bit products as in moe_few.cuh.
 //
-// Measured: 4096 tokens, 8 of 128 experts of 2048 x 768: gate and up 408 us
-// (2 x 206 GFLOP with both parts: 1.0 PFLOP/s), down 302 us; 513 tokens 125 us
-// and 80 us.  Bound: a step's converters and the issue of its products, see below;
-// 45 us of the 408 are the split's, which moves 168 MB.
+// Measured: 4096 tokens, 4 of 32 experts of 2560 x 1536: gate and up 407 us
+// (2 x 258 GFLOP with both parts: 1.27 PFLOP/s), down 298 us; 513 tokens, 6 of
+// 60 experts of 2560 x 1280: 131 us, down Q6_K 109 us.  Bound: the making of a
+// step's A and the issue of its products, see below; 45 us of the 407 are the
+// split's, which moves 168 MB.
 //
 // Four launches.  (1) One CTA lays the pairs out in tiles: an expert's n pairs
 // become ceil(n / 112) tiles (or ceil(n / 32): see kMoeSmallTiles) of equal
-// size, a multiple of 16.  (2) Each pair's
-// activations, times a power of two that puts the row's largest in
-// [2^14, 2^15), become two binary16 parts, stored tile by tile as the products
-// read them (64 k of hi, then of lo, in the 128-byte-swizzled layout), with
-// the sums of every 32 of them (hi and lo, times 2^-6).  (3) The products.
-// (4) For down: the weighted rows of a token are added up (moe_product.cu).
+// size, a multiple of 16.  (2) Each pair's activations, times a power of two
+// that puts the row's largest in [2^14, 2^15), become two binary16 parts,
+// stored tile by tile as the products read them (64 k of hi, then of lo, in the
+// 128-byte-swizzled layout), with the sums of every 32 of them (hi and lo,
+// times 2^-5).  (3) The products.  (4) For down: the weighted rows of a token
+// are added up (moe_product.cu).
 //
 // The weights are the products' A and lie in tensor memory: a converter thread
-// owns a weight row, which is a lane there, and writes sc q as binary16, exact.
+// owns a weight row, which is a lane there, and writes sc q - c as binary16, exact.
 // So shared memory feeds the tensor core with B alone (with both operands
 // there, 128 columns an instruction would take all of its bandwidth).  The min
 // term dmin m sums(x) is part of the same sum: with r = dmin / d the sum over a
-// superblock is d (sum sc q x - sum r m sums(x)), r m as two binary16 parts (22
-// bits) beside the sums' parts, so a superblock takes one FMA per row and
-// column in the epilogue.  Where |r| > 16, all of it is taken 2^-e times, e =
-// floor(log2 |r|) - 3, so that r m fits binary16; sc q 2^-e stays exact up to
-// e = 20, and beyond (dmin > 2^24 d) d counts as 0.
+// superblock is d (sum (sc q - c) x - sum (r m - c) sums(x)), r m - c as two
+// binary16 parts (22 bits) beside the sums' parts, so a superblock takes one
+// FMA per row and column in the epilogue.  c, some 8 sc, is there because a sum
+// loses bits by its size: without it the quants' and the mins' parts, which
+// nearly cancel, are each several times as large as their difference (relative
+// error of h 1.95e-6 in place of 1.26e-6, for 2 to 5 % of the time).  Where
+// |r| > 16, all of it is taken 2^-e times, e = floor(log2 |r|) - 3, so that r m
+// fits binary16; sc q 2^-e stays exact up to e = 20, and beyond (dmin > 2^24 d)
+// d counts as 0.
 // Q6_K: sc (q - 32) needs up to 13 bits: hi = binary16 of it and lo = the rest
 // (-1, 0, 1), two tiles that meet the hi and lo, and the hi parts of x.
 //
@@ -91,6 +96,12 @@ struct Cfg {
   static constexpr int kIssuers = kQ6 ? 1 : 2;               // warps that issue products
   static constexpr int kTilesM = kQ6 ? 1 : 2;                // of 128 rows each
   static constexpr int kOutRows = MODE == kDownQ4 ? 2 * kRows : kRows;
+  // The tensor core drops what is below its sum's last place at every product,
+  // towards zero, so a superblock's sum comes out too small: measured, by 10
+  // (tiles of 32 pairs: 5.5) times 2^-24 of itself on average, for rows of any
+  // length and both formats.  Its scale puts the mean back: the relative error
+  // of h 1.26e-6 -> 5.2e-7 (6.2e-7 -> 3.6e-7).
+  static constexpr float kBack = 1.0f + (kBeside ? 6 : 10) * 5.9604644775390625e-8f;
   // registers of the three kinds of warps; at launch 768 x 80 and 640 x 96
   static constexpr int kFewRegs = 32, kConvRegs = kBeside ? 72 : 64, kEpiRegs = 160;
   static_assert(32 * (4 * kFewRegs + kConverters * kConvRegs + kEpilogue * kEpiRegs) == kThreads * (kBeside ? 80 : 96));
@@ -275,7 +286,7 @@ __global__ void __launch_bounds__(256) moe_many_split_kernel(const SplitParams P
       sum += __shfl_xor_sync(~0u, sum, 1);
       sum += __shfl_xor_sync(~0u, sum, 2);
       if ((lane & 3) == 0) {
-        const float x = sum * 0.015625f;
+        const float x = sum * 0.03125f;
         const __half h = __float2half_rn(x);
         // 16-byte chunk 2 (sb % 4) has the hi parts, the next one the lo parts
         const int c = 2 * (sb & 3), k = lane >> 2;
@@ -289,11 +300,11 @@ __global__ void __launch_bounds__(256) moe_many_split_kernel(const SplitParams P
 
 // ------------------------------------------------------------- converters
 // 32 weights of a Q4_K row (the low or high nibbles of 32 quant bytes) times
-// their scale s, pairs (0, 2), (1, 3) of every four.
+// their scale s, less a middle c (see middles), pairs (0, 2), (1, 3) of every four.
 template <bool HIGH>
 __device__ __forceinline__ void convert_q4(const uint4& q0, const uint4& q1, uint32_t s, uint32_t (&a)[16]) {
-  // (1024 + q) s - 1024 s, (1024 + 16 q) s / 16 - 64 s: one exact FMA each
-  const uint32_t m = HIGH ? cvt::mul_h2(s, 0x2C002C00u) : s, b = cvt::mul_h2(s, HIGH ? 0xD400D400u : 0xE400E400u);
+  // (1024 + q) s - (1024 s + c), (1024 + 16 q) s / 16 - (64 s + c): one exact FMA each
+  const uint32_t m = HIGH ? cvt::mul_h2(s, 0x2C002C00u) : s, b = cvt::mul_h2(s, HIGH ? 0xD480D480u : 0xE408E408u);
   const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -309,19 +320,19 @@ __device__ __forceinline__ void convert_q4(const uint4& q0, const uint4& q1, uin
 struct Header {
   uint32_t sc[2], m[2];       // 6-bit scales and mins
   uint32_t down;              // 2^-e twice, or 0 where d counts as 0
-  float scale, r;             // what a sum is to be multiplied with; r m 2^-e as part of it: r times 2^6
+  float scale, r;             // what a sum is to be multiplied with; r m 2^-e as part of it: r times -2^5
 };
 __device__ __forceinline__ Header header_of(const uint4& h) {
   Header H;
   cvt::header_sc_m(h, H.sc[0], H.sc[1], H.m[0], H.m[1]);
   const float2 d = unpack2<false>(h.x);                        // d, dmin
-  H.r = __fdividef(-64.0f * d.y, d.x);                         // (within 2^-22)
+  H.r = __fdividef(-32.0f * d.y, d.x);                         // (within 2^-22)
   H.scale = d.x;
   H.down = 0x3C003C00u;
-  if (!(fabsf(H.r) <= 1024.0f) && d.y != 0.0f) {               // |r| > 16, or d = 0
-    const int e = (int)(__float_as_uint(H.r) >> 23 & 0xFF) - 127 - 9;
+  if (!(fabsf(H.r) <= 512.0f) && d.y != 0.0f) {                // |r| > 16, or d = 0
+    const int e = (int)(__float_as_uint(H.r) >> 23 & 0xFF) - 127 - 8;
     if (d.x == 0.0f || e > 20) {
-      H.down = 0, H.r = -512.0f, H.scale = d.y * 0.125f;
+      H.down = 0, H.r = -512.0f, H.scale = d.y * 0.0625f;
     } else {
       H.r = __uint_as_float(__float_as_uint(H.r) - ((uint32_t)e << 23));
       H.scale = __uint_as_float(__float_as_uint(d.x) + ((uint32_t)e << 23));
@@ -334,12 +345,23 @@ __device__ __forceinline__ Header header_of(const uint4& h) {
   return H;
 }
 
-// The two binary16 parts of r m for the eight mins: [hi | hi], [lo | lo].
+// -c of sub-blocks 2 i and 2 i + 1: 8 s, as binary16 holds 1032 s (and 72 s,
+// which is exact).
+__device__ __forceinline__ float2 middles(const Header& H, int i) {
+  const uint32_t bytes = __byte_perm(H.sc[i >> 1], 0x64646464u, i & 1 ? 0x4342 : 0x4140), bias = 0xE400E400u;
+  const __half2 s = __hmul2(__hadd2(*reinterpret_cast<const __half2*>(&bytes), *reinterpret_cast<const __half2*>(&bias)),
+                            *reinterpret_cast<const __half2*>(&H.down));
+  const __half2 b = __hmul2(s, __floats2half2_rn(-1032.0f, -72.0f));
+  return __half22float2(__hfma2(s, __floats2half2_rn(1024.0f, 64.0f), b));
+}
+
+// The two binary16 parts of r m - c for the eight mins: [hi | hi], [lo | lo].
 __device__ __forceinline__ void convert_min(const Header& H, uint32_t (&a)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t w = H.m[i >> 1] >> (16 * (i & 1));
-    const float v0 = H.r * (float)(w & 0xFFu), v1 = H.r * (float)(w >> 8 & 0xFFu);
+    const float2 c = middles(H, i);
+    const float v0 = H.r * (float)(w & 0xFFu) - 32.0f * c.x, v1 = H.r * (float)(w >> 8 & 0xFFu) - 32.0f * c.y;
     a[i] = a[4 + i] = pack2<false>(v0, v1);
     const float2 h = unpack2<false>(a[i]);
     a[8 + i] = a[12 + i] = pack2<false>(v0 - h.x, v1 - h.y);
@@ -597,7 +619,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
         for (int sb = 0; sb < nb && !stop; ++sb, ++n, ++b) {
           const uint32_t slot = n % C::kRaw;
           const float d = __half2float(scales[sb]);
-          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err) || (group + turn_of == 0 && !scale_of(0, d));
+          stop = !warp_wait(&S.rfull[slot], (n / C::kRaw) & 1, gave_up, err) || (group + turn_of == 0 && !scale_of(0, d * C::kBack));
           if (stop) break;
           const uint8_t* w = S.raw[slot] + row * C::kSb;
 #pragma unroll 1
@@ -650,7 +672,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
                 tc::fence_after_sync();
               }
               tc::tmem_st16(lanes + (C::kMinColumn - C::kAColumn) + 32 * (b % C::kMins) + 16 * group, v);
-              stop = !scale_of(group, H.scale);
+              stop = !scale_of(group, H.scale * C::kBack);
               if (stop) break;
               end_step(&S.mfull[b % C::kMins]);
             }
