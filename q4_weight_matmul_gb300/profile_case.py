@@ -13,6 +13,10 @@
     python -m q4_weight_matmul_gb300.profile_case attn --requests 1 --new 512 --context 8192 --reps 3
     python -m q4_weight_matmul_gb300.profile_case attn --requests 16 --new 1 --context 8192 --f32-out --reps 3
     python -m q4_weight_matmul_gb300.profile_case lora --rows 2560 --cols 9728 --tokens 2048 --rank 32 --reps 3
+    python -m q4_weight_matmul_gb300.profile_case experts --tokens 64 --experts 128 --top-k 8 --cols 2048 --rows 768
+
+``experts`` runs a layer's routed experts, --cols -> --rows -> --cols
+(``expert_block.py``; --q6k: their down projections in Q6_K).
 
 ``seq`` runs --layers Qwen3-4B-shaped decode linear sets (q, k, v, o, gate,
 up, down; independent inputs) as one q4k_gemv_seq launch per rep, as the
@@ -101,10 +105,18 @@ def run_lora(a, dev, gen):
         q4k.q4k_lora_add(x, [w1], [w2], [base], *seg, scale, workspace=ws)
 
 
+def run_experts(a, dev, gen):
+    from q4_weight_matmul_gb300.expert_block import random_experts
+    block = random_experts(a.cols, a.rows, a.experts, a.top_k, a.q6k, device=dev)
+    x = torch.randn((a.tokens, a.cols), device=dev, generator=gen)
+    for _ in range(a.reps):
+        block(x)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("kernel", choices=["gemv", "gemm", "gemm_h16", "gemm_f16", "q8", "pack", "seq", "q6k_gemv",
-                                       "q6k_gemm_f16", "heads", "attn", "lora"])
+                                       "q6k_gemm_f16", "heads", "attn", "lora", "experts"])
     ap.add_argument("--layers", type=int, default=13)
     ap.add_argument("--rows", type=int, default=9728)
     ap.add_argument("--cols", type=int, default=2560)
@@ -116,6 +128,9 @@ def main():
     ap.add_argument("--f32-out", action="store_true")
     ap.add_argument("--rank", type=int, default=32)
     ap.add_argument("--adapters", type=int, default=4)
+    ap.add_argument("--experts", type=int, default=128)
+    ap.add_argument("--top-k", type=int, default=8)
+    ap.add_argument("--q6k", action="store_true")
     ap.add_argument("--reps", type=int, default=5)
     a = ap.parse_args()
     q4k.build()
@@ -125,8 +140,8 @@ def main():
     if a.kernel == "seq":
         run_seq(a, dev, gen)
         return
-    if a.kernel in ("heads", "attn", "lora"):
-        {"heads": run_heads, "attn": run_attn, "lora": run_lora}[a.kernel](a, dev, gen)
+    if a.kernel in ("heads", "attn", "lora", "experts"):
+        {"heads": run_heads, "attn": run_attn, "lora": run_lora, "experts": run_experts}[a.kernel](a, dev, gen)
         torch.cuda.synchronize()
         if q4k.q4k_device_error() != 0:
             raise RuntimeError("a kernel reported an error")
