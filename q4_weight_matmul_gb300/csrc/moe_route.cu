@@ -16,9 +16,15 @@
 // order: a warp ranks its own tokens' pairs within each expert as it goes, a
 // CTA of 32 warps turns the warps' counts into starts.  Up to kOneCta tokens
 // one CTA does it all in one launch.  More tokens are shared out over about an
-// SM each in chunks of whole warps; the first launch leaves every chunk's counts, and in
-// the second each CTA adds up those of the chunks before its own and of all
-// (E x chunks integers from L2) and writes the pairs' final places.
+// SM each in chunks of whole warps; the first launch leaves every chunk's
+// counts, and in the second each CTA adds up those of the chunks before its own
+// and of all (E x chunks integers from L2) and writes the pairs' final places.
+//
+// Measured: 1 token, 8 of 128 experts 3.4 us; 208 tokens, 4 of 60 experts 6.1;
+// 8192 tokens, 8 of 128 experts 12.0 (5.2 MB: 0.8 us at the copy rate).  Bound:
+// latency, of the launches, the loads that wait for one another (15.4 us before
+// the next token's logits and a chunk's pairs were asked for ahead), and top_k
+// rounds of two warp reductions a token.
 #include "moe.cuh"
 
 namespace q4k {
@@ -87,15 +93,24 @@ __global__ void __launch_bounds__(kThreads, 1) route_choose_kernel(const RoutePa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = L.experts, k = L.top_k;
   for (int e = lane; e < 32 * NV; e += 32) counts[warp][e] = 0;
   __syncwarp();
-  const int64_t live = valid_tokens(P), first = ((int64_t)blockIdx.x * kWarps + warp) * P.per_warp,
-                last = min(first + P.per_warp, L.tokens);
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + warp) * P.per_warp, last = min(first + P.per_warp, L.tokens);
+  // the next token's logits are on their way while one's experts are chosen (more than 256 experts: registers for it lack)
+  float next[NV];
+  const auto load = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) next[i] = 32 * i + lane < E && t < last ? P.logits[t * E + 32 * i + lane] : 0.0f;
+  };
+  load(first);
+  const int64_t live = valid_tokens(P);
+  int kept[2] = {-1, -1}, ranks[2] = {-1, -1};             // of the first two tokens
   for (int64_t t = first; t < last; ++t) {
     int expert = -1, rank = -1;
     float weight = 0.0f;
-    if (t < live) {
-      uint32_t key[NV];
+    uint32_t key[NV];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = 32 * i + lane < E ? key_of(P.logits[t * E + 32 * i + lane]) : 0;
+    for (int i = 0; i < NV; ++i) key[i] = 32 * i + lane < E ? key_of(next[i]) : 0;
+    if constexpr (NV <= 8) load(t + 1);
+    if (t < live) {
       uint32_t mine = 0;                                   // what round `lane` found
       float top = 0.0f, all = 0.0f;
       uint32_t left[NV];
@@ -139,6 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1) route_choose_kernel(const RoutePa
       L.weight[p] = weight;
       L.place[p] = t < live ? rank : -2;
     }
+    if constexpr (NV > 8) load(t + 1);
+    if (t == first) kept[0] = expert, ranks[0] = rank;
+    if (t == first + 1) kept[1] = expert, ranks[1] = rank;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += kThreads) {
@@ -162,9 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1) route_choose_kernel(const RoutePa
   for (int64_t t = first; t < last; ++t) {
     if (lane >= k) break;
     const int64_t p = t * k + lane;
-    const int e = L.expert[p];
+    const int e = t == first ? kept[0] : t == first + 1 ? kept[1] : L.expert[p];
     if (e < 0) continue;
-    int at = L.place[p] + counts[warp][e];
+    int at = (t == first ? ranks[0] : t == first + 1 ? ranks[1] : L.place[p]) + counts[warp][e];
     if constexpr (ONE) {
       at += off[e];
       L.order[at] = (int32_t)p;
@@ -180,9 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1) route_place_kernel(const RoutePar
   const MoePlan& L = P.plan;
   const int E = L.experts, width = (E + 31) / 32 * 32, groups = kThreads / width;
   const int g = threadIdx.x / width, e = threadIdx.x - g * width, c = blockIdx.x;
+  const int64_t first = (int64_t)c * kWarps * P.per_warp * L.top_k,
+                last = min(first + (int64_t)kWarps * P.per_warp * L.top_k, L.tokens * L.top_k), p0 = first + threadIdx.x;
+  const int expert0 = p0 < last ? L.expert[p0] : -1, rank0 = p0 < last ? L.place[p0] : 0;
   int before = 0, all = 0;
   if (g < groups && e < E) {
-#pragma unroll 8
+#pragma unroll 16
     for (int i = g; i < chunks; i += groups) {
       const int v = P.counts[(int64_t)i * E + e];
       all += v;
@@ -204,12 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1) route_place_kernel(const RoutePar
   const int pairs = off[E];
   if (threadIdx.x < width && e < E) total[e] = off[e] + before;
   __syncthreads();
-  const int64_t first = (int64_t)c * kWarps * P.per_warp * L.top_k,
-                last = min(first + (int64_t)kWarps * P.per_warp * L.top_k, L.tokens * L.top_k);
-  for (int64_t p = first + threadIdx.x; p < last; p += kThreads) {
-    const int x = L.expert[p];
+  for (int64_t p = p0; p < last; p += kThreads) {
+    const int x = p == p0 ? expert0 : L.expert[p];
     if (x >= 0) {
-      const int at = L.place[p] + total[x];
+      const int at = (p == p0 ? rank0 : L.place[p]) + total[x];
       L.place[p] = at;
       L.order[at] = (int32_t)p;
     }
