@@ -200,6 +200,14 @@ int lora_add(PyObject* const* a) {
                     address(work, at::kByte, work.numel(), "workspace"), (size_t)work.numel(), stream_of(a[10]));
 }
 
+// Tensors of a call that lie on another device than the current one, where it would be launched.
+void on_current_device(PyObject* const* a, int n) {
+  const int device = c10::cuda::current_device();
+  for (int i = 0; i < n; ++i)
+    if (THPVariable_Check(a[i]) && THPVariable_Unpack(a[i]).is_cuda() && THPVariable_Unpack(a[i]).get_device() != device)
+      refuse(PyExc_ValueError, "%s is on device %lld, not on the current one", "a tensor", THPVariable_Unpack(a[i]).get_device());
+}
+
 // (expert, weight, place, order, offsets)
 q4k_moe_plan plan_of(PyObject* const* a) {
   const at::Tensor &expert = tensor(a[0], "route.expert"), &offsets = tensor(a[4], "route.offsets");
@@ -223,6 +231,7 @@ const float* floats_or_null(PyObject* o, int64_t n, const char* name) {
 
 // (logits, expert, weight, place, order, offsets, renormalize, scale, n_tokens, workspace, stream)
 int moe_route(PyObject* const* a) {
+  on_current_device(a, 10);
   const q4k_moe_plan p = plan_of(a + 1);
   const at::Tensor &logits = tensor(a[0], "logits"), &work = tensor(a[9], "workspace");
   if (logits.dim() != 2 || logits.size(0) != p.tokens || logits.size(1) != p.experts)
@@ -235,6 +244,7 @@ int moe_route(PyObject* const* a) {
 
 // (x, gate, up, expert, weight, place, order, offsets, rows, h, workspace, stream)
 int moe_gate_up(PyObject* const* a) {
+  on_current_device(a, 11);
   const q4k_moe_plan p = plan_of(a + 3);
   const at::Tensor &x = tensor(a[0], "x"), &work = tensor(a[10], "workspace");
   if (x.dim() != 2 || x.size(0) != p.tokens) refuse(PyExc_ValueError, "%s must be [tokens][cols]", "x");
@@ -249,6 +259,7 @@ int moe_gate_up(PyObject* const* a) {
 
 // (h, w, q6k, expert, weight, place, order, offsets, rows, residual, y, workspace, stream)
 int moe_down(PyObject* const* a) {
+  on_current_device(a, 12);
   const q4k_moe_plan p = plan_of(a + 3);
   const at::Tensor &h = tensor(a[0], "h"), &work = tensor(a[11], "workspace");
   if (h.dim() != 2 || h.size(0) != p.tokens * p.top_k)

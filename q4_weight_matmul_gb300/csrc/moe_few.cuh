@@ -551,13 +551,14 @@ __device__ __forceinline__ bool consume(const Params& P, Head& H, float* part, c
                                         uint32_t first, uint32_t turn) {
   volatile int* gave_up = &H.gave_up;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp % kGroups;
-  // (the stages' shares go on from item to item, so that a slot stays one share's)
-  const int share = warp / kGroups;
+  // The stages' shares go on from item to item, so that a slot stays one share's.  `rank`: which superblocks of this item
+  // (every third) they are; the sums are put together by rank, the same way wherever the item comes.
+  const int share = warp / kGroups, rank = (share + kShares - first % kShares) % kShares;
   const int c = lane & 3, r0 = C::kQ6 ? lane >> 2 : 2 * ((lane >> 2) & 3) + (lane >> 4);
   // the warp's first row in a stage; gate and up: 16 rows of both halves
   const int base = C::kUp ? 16 * group : 32 * group;
   float total[2][N][4] = {};
-  for (uint32_t n = first + (share + kShares - first % kShares) % kShares; n < first + P.nb; n += kShares) {
+  for (uint32_t n = first + rank; n < first + P.nb; n += kShares) {
     const uint32_t slot = n % C::kSlots, sb = n - first;
     if (!C::kOwnSlots && !warp_wait_issued(&H.issued, n, gave_up, P.err)) return false;
     if (!warp_wait(&H.full[slot], (n / C::kSlots) & 1, gave_up, P.err)) return false;
@@ -567,26 +568,23 @@ __device__ __forceinline__ bool consume(const Params& P, Head& H, float* part, c
       stage_q6<N, HALF>(at + (base + r0) * C::kSb, at + C::kWeights + (base + r0) * 4 + 2 * (sb & 1), x, lane, total);
     else
       stage_q4<N, HALF>(at + (base + r0) * C::kSb, (C::kUp ? kTileRows / 2 : 16) * C::kSb, x, lane, total);
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&H.empty[slot]);
+    warp_release(&H.empty[slot]);
   }
-  // the shares' sums, one after the other through the group's place: share 2, 1, 0
+  // the ranks' sums, one after the other through the group's place: rank 2, 1, 0, when that of the item before is done
   constexpr int kSums = 8 * N;
   float* place = part + group * C::kValues * 32 + lane;
-  if (share < kShares - 1) {
-    if (!warp_wait(&H.part[group][share + 1], turn & 1, gave_up, P.err)) return false;
+  if (!warp_wait(&H.part[group][0], (turn & 1) ^ 1, gave_up, P.err)) return false;
+  if (rank < kShares - 1) {
+    if (!warp_wait(&H.part[group][rank + 1], turn & 1, gave_up, P.err)) return false;
 #pragma unroll
     for (int j = 0; j < kSums; ++j) total[j / (4 * N)][(j / 4) % N][j % 4] += place[32 * j];
-  } else if (!warp_wait(&H.part[group][0], (turn & 1) ^ 1, gave_up, P.err)) {
-    return false;
   }
-  if (share > 0) {
+  if (rank > 0) {
 #pragma unroll
     for (int j = 0; j < kSums; ++j) place[32 * j] = total[j / (4 * N)][(j / 4) % N][j % 4];
   }
-  __syncwarp();
-  if (lane == 0) tc::mbar_arrive(&H.part[group][share]);
-  if (share > 0) return true;
+  warp_release(&H.part[group][rank]);
+  if (rank > 0) return true;
   if constexpr (HALF) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -698,8 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_few_kernel(const __grid_const
       const uint32_t q = turn % kQueue;
       if (!warp_wait(&H.item_full[q], (turn / kQueue) & 1, gave_up, P.err)) break;
       const int4 it = H.item[q];
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&H.item_empty[q]);
+      warp_release(&H.item_empty[q]);
       if (it.w == 0) break;
       const int w0 = it.x * P.rows + it.y * C::kOutRows;
       uint32_t off[kEach + (kRest > 0)];                         // (128 rows are less than 2^32 bytes)
@@ -736,8 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_few_kernel(const __grid_const
       const uint32_t q = turn % kQueue;
       if (!warp_wait(&H.item_full[q], (turn / kQueue) & 1, gave_up, P.err)) break;
       const int4 v = H.item[q];
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&H.item_empty[q]);
+      warp_release(&H.item_empty[q]);
       const Item it{v.x, v.y, v.z, v.w};
       bool ok;
       if (it.n == 0) break;

@@ -444,8 +444,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
     const uint32_t q = turn % kQueue;
     if (!warp_wait(&S.qfull[q], (turn / kQueue) & 1, gave_up, err)) return false;
     T = S.item[q], block = S.block[q];
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&S.qempty[q]);
+    warp_release(&S.qempty[q]);
     ++turn;
     return T.n > 0;
   };
@@ -606,8 +605,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
     auto scale_of = [&](int mt, float v) -> bool {             // of a superblock's sum, for the epilogue
       if (!warp_wait(&S.dempty[b & 1], ((b >> 1) & 1) ^ 1, gave_up, err)) return false;
       S.scale[b & 1][mt][row] = v;
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&S.dfull[b & 1]);
+      warp_release(&S.dfull[b & 1]);
       return true;
     };
     bool stop = false;
@@ -628,8 +626,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
             const uint4 l0 = p[0], l1 = p[1], h = p[2];
             const uint32_t sc = *reinterpret_cast<const uint32_t*>(w + 4 * c), k = C::kPerBlock * b + c / C::kHalves,
                            at = lanes + 64 * (C::kHalves * (k & 1) + turn_of) + 16 * group;
-            __syncwarp();
-            if (c >= 4 - kTurns && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
+            if (c >= 4 - kTurns) warp_release(&S.rempty[slot]);
             uint32_t hi[16], lo[16];
             convert_q6(l0, l1, h, sc, group, hi, lo);
             stop = !begin_step(k);
@@ -651,8 +648,7 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
           for (int c = turn_of; c < 4; c += kTurns) {
             const uint4* p = reinterpret_cast<const uint4*>(w + 16 + 32 * c);
             const uint4 q0 = p[0], q1 = p[1];
-            __syncwarp();
-            if (c >= 4 - kTurns && lane == 0) tc::mbar_arrive(&S.rempty[slot]);
+            if (c >= 4 - kTurns) warp_release(&S.rempty[slot]);
             const uint32_t s = c < 2 ? H.sc[0] : H.sc[1], k = C::kPerBlock * b + c / C::kHalves,
                            at = lanes + 64 * (C::kHalves * (k & 1) + turn_of) + 32 * group;
             uint32_t v[16], w2[16];
@@ -730,11 +726,8 @@ __global__ void __launch_bounds__(Cfg<MODE, COLS>::kThreads, 1) moe_many_kernel(
             }
           }
           tc::fence_before_sync();
-          __syncwarp();
-          if (lane == 0) {
-            tc::mbar_arrive(&S.tempty[t]);
-            if (mt == C::kTilesM - 1) tc::mbar_arrive(&S.dempty[b & 1]);
-          }
+          warp_release(&S.tempty[t]);
+          if (mt == C::kTilesM - 1 && lane == 0) tc::mbar_arrive(&S.dempty[b & 1]);
         }
       }
       if (stop) break;

@@ -276,3 +276,24 @@ def test_a_place_behind_the_last_pair_is_reported(tokens):
     got = q4k.q4k_moe_down(h, w, rows, good._replace(place=place), workspace=work)
     assert q4k.q4k_device_error() == 6
     assert torch.equal(got, want) and torch.all(want[1] == 0)
+
+
+@pytest.mark.parametrize("tokens,experts,top_k,hidden,width", [
+    (12, 8, 2, 4096, 2048), (64, 128, 8, 2048, 768), (256, 64, 4, 2048, 768), (700, 16, 4, 2560, 1280)])
+def test_the_same_bits_every_time(tokens, experts, top_k, hidden, width):
+    """Steps with many items for every CTA, three hundred times."""
+    from q4_weight_matmul_gb300.expert_block import random_experts
+    g = torch.Generator(device="cuda").manual_seed(120)
+    x = torch.randn((tokens, hidden), generator=g, device="cuda")
+    route = q4k.q4k_moe_route(torch.randn((tokens, experts), generator=g, device="cuda"), top_k)
+    for six in (False, True):
+        block = random_experts(hidden, width, experts, top_k, six)
+        work = q4k.q4k_moe_workspace(tokens, top_k, experts, hidden, width)
+
+        def both():
+            h = q4k.q4k_moe_gate_up(x, block.gate, block.up, width, route, workspace=work)
+            return h, q4k.q4k_moe_down(h, block.down, hidden, route, x, six, workspace=work)
+
+        want = both()
+        differ = [torch.stack([(a != b).any() for a, b in zip(both(), want)]).any() for _ in range(300)]
+        assert not torch.stack(differ).any()
