@@ -34,12 +34,12 @@
 // first, so that the last to end are short; tiles of one expert lie side by
 // side and share the weights in L2.
 //
-// Measured: one token, 8 of 128 experts of 2048 x 768, gate and up 9.6 us, down
-// Q6_K 10.4; 64 tokens 63.5 us (3.6 TB/s), down 43; 12 tokens, 2 of 8 experts of
-// 4096 x 12288, 95 us (4.8 TB/s).  Bound: the unpacking of the quants (shifts,
+// Measured: one token, 8 of 128 experts of 2048 x 768, gate and up 9.7 us, down
+// Q6_K 10.6; 64 tokens 68 us (3.3 TB/s), down 46; 12 tokens, 2 of 8 experts of
+// 4096 x 12288, 97 us (4.7 TB/s).  Bound: the unpacking of the quants (shifts,
 // masks and permutes, two thirds of what a consumer does and at half the other
 // instructions' rate) beside the stream of the weights, which alone takes 70 us
-// of the 95; and latency for one token.
+// of the 97; and latency for one token.
 //
 // Waits are bounded; a warp agrees on a wait's outcome by a vote, and who
 // copies waits for its copies before it leaves.
@@ -371,7 +371,7 @@ __device__ __forceinline__ void stage_q4(const uint8_t* w, int apart, const uint
   constexpr int kSums = HALF ? 16 * 256 : 16 * 512;
   const int c = lane & 3;
   // a 4 that the compiler does not know: products go to another pipe than the shifts and masks that it would make of them
-  // (64 tokens' gate and up 66.5 -> 63.5 us; the same of >> 6, the high half of a product, is slower)
+  // (64 tokens' gate and up 69.4 -> 68.2 us; the same of >> 6, the high half of a product, is slower)
   uint32_t four;
   asm volatile("mov.u32 %0, 4;" : "=r"(four));
   uint32_t sc[2][2][2];

@@ -2,10 +2,10 @@
 // tensor cores (tcgen05): 128 or 256 weight rows times up to 112 pairs of one
 // expert, fp32 sums of exact 16-bit products as in moe_few.cuh.
 //
-// Measured: 4096 tokens, 4 of 32 experts of 2560 x 1536: gate and up 407 us
-// (2 x 258 GFLOP with both parts: 1.27 PFLOP/s), down 298 us; 513 tokens, 6 of
-// 60 experts of 2560 x 1280: 131 us, down Q6_K 109 us.  Bound: the making of a
-// step's A and the issue of its products, see below; 45 us of the 407 are the
+// Measured: 4096 tokens, 4 of 32 experts of 2560 x 1536: gate and up 410 us
+// (2 x 258 GFLOP with both parts: 1.26 PFLOP/s), down 301 us; 513 tokens, 6 of
+// 60 experts of 2560 x 1280: 132 us, down Q6_K 110 us.  Bound: the making of a
+// step's A and the issue of its products, see below; 45 us of the 410 are the
 // split's, which moves 168 MB.
 //
 // Four launches.  (1) One CTA lays the pairs out in tiles: an expert's n pairs

@@ -67,9 +67,9 @@ cudaError_t combine(const MoeProduct& p, const float* z, cudaStream_t s) {
 // the pairs, that of a tile hardly does until it is full.  Measured (us; gate
 // and up, down Q4_K, down Q6_K), few | many:
 //   pairs an expert   128 experts, 2048 x 768              32 experts, 2560 x 1536
-//         6           74 / 51 / 80   | 82 / 53 / 73        48 / 34 / 51 | 64 / 37 / 50
-//        10           94 / 65 / 95   | 92 / 56 / 78        64 / 43 / 61 | 65 / 47 / 58
-//        16          129 / 86 / 121  | 97 / 62 / 84        87 / 53 / 75 | 67 / 48 / 59
+//         6           82 / 55 / 82   | 86 / 55 / 74        50 / 35 / 52 | 67 / 39 / 51
+//        10          104 / 69 / 98   | 96 / 58 / 78        66 / 44 / 63 | 68 / 49 / 59
+//        16          141 / 91 / 124  | 101 / 65 / 85       92 / 55 / 77 | 69 / 50 / 59
 constexpr int64_t kMany = 10;
 static bool many(int64_t tokens, int top_k, int experts) { return tokens * top_k >= kMany * experts; }
 

@@ -227,7 +227,7 @@ cudaError_t launch_moe_few_down_q6(const MoeProduct& p, void* work, float* out, 
 // The same for many pairs an expert (moe_many.cuh); `work`: moe_many_workspace() bytes.
 // Up to kMoeSmallTiles pairs an expert the tiles are of 32 pairs, beyond of 112.
 // Measured (us, 128 experts of 2048 x 768; gate and up, down Q4_K, down Q6_K), 32 | 112:
-//   16 pairs  97 / 62 / 84 | 107 / 68 / 98,  24  115 / 72 / 98 | 117 / 74 / 104,  32  127 / 80 / 110 | 119 / 78 / 107
+//   16 pairs  101 / 65 / 85 | 115 / 69 / 98,  24  119 / 76 / 100 | 125 / 75 / 104,  32  133 / 84 / 111 | 127 / 80 / 107
 constexpr int64_t kMoeSmallTiles = 24;
 size_t moe_many_workspace(int64_t pairs, int experts, int64_t cols);
 cudaError_t launch_moe_many_gate_up(const MoeProduct& p, void* work, float* out, cudaStream_t s);
