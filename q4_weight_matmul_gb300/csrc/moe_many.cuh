@@ -329,7 +329,8 @@ __device__ __forceinline__ Header header_of(const uint4& h) {
   H.r = __fdividef(-32.0f * d.y, d.x);                         // (within 2^-22)
   H.scale = d.x;
   H.down = 0x3C003C00u;
-  if (!(fabsf(H.r) <= 512.0f) && d.y != 0.0f) {                // |r| > 16, or d = 0
+  // (a d or dmin that is NaN gives a ratio that is: the first stays in the scale, the second in r, and so in the sum)
+  if (fabsf(H.r) > 512.0f && d.y != 0.0f) {                    // |r| > 16, or d = 0
     const int e = (int)(__float_as_uint(H.r) >> 23 & 0xFF) - 127 - 8;
     if (d.x == 0.0f || e > 20) {
       H.down = 0, H.r = -512.0f, H.scale = d.y * 0.0625f;
@@ -340,7 +341,7 @@ __device__ __forceinline__ Header header_of(const uint4& h) {
       H.down = *reinterpret_cast<const uint32_t*>(&t);
     }
   } else if (d.y == 0.0f) {
-    H.r = 0.0f;
+    H.r = 0.0f;                                                // (d may be 0 too)
   }
   return H;
 }

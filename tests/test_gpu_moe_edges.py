@@ -297,3 +297,44 @@ def test_the_same_bits_every_time(tokens, experts, top_k, hidden, width):
         want = both()
         differ = [torch.stack([(a != b).any() for a, b in zip(both(), want)]).any() for _ in range(300)]
         assert not torch.stack(differ).any()
+
+
+@pytest.mark.parametrize("tokens", [12, 72, 300])
+def test_scales_that_are_not_finite_spoil_their_rows(tokens):
+    """NaN and infinities as d and dmin of single superblocks: the outputs of
+    those rows are not finite for the pairs of that expert; all others stay."""
+    from _gpu import pack_dev, to_dev
+    e, cols, rows, bad = 4, 768, 100, 1
+    expert, weight = with_counts([tokens // e] * e, 73)
+    route, x = route_of(expert, weight, e), dev(0.02 * synth.activations(tokens, cols, 74))
+    order = route.order.cpu().numpy()
+    hit = expert[:, 0] == bad
+    spoiled = {3: ("d", np.nan), 10: ("d", np.inf), 17: ("d", -np.inf), 24: ("dmin", np.nan), 31: ("dmin", np.inf),
+               38: ("dmin", -np.inf), 45: ("d", np.nan), 99: ("d", np.nan)}
+
+    def spoil(f):
+        f = {n: v.copy() for n, v in f.items()}
+        for i, (row, (name, value)) in enumerate(spoiled.items()):
+            if name in f:
+                f[name][bad * rows + row, i % (cols // 256)] = np.array(value, np.float16).view(np.uint16)
+        return f
+
+    def check(good, got, pairs, names):
+        wrong = np.zeros(got.shape, bool)
+        for row, (name, _) in spoiled.items():
+            if name in names:
+                wrong[pairs, row] = True
+        assert np.array_equal(got[~wrong], good[~wrong])
+        assert not np.isfinite(got[wrong]).any()
+
+    (gf, gate), (uf, up), (df, w) = (matrices(e, rows, cols, [i, 78]) for i in (1, 2, 3))
+    good = q4k.q4k_moe_gate_up(x, gate, up, rows, route).cpu().numpy()
+    for g, u in ((pack_dev(spoil(gf)), up), (gate, pack_dev(spoil(uf)))):
+        check(good, q4k.q4k_moe_gate_up(x, g, u, rows, route).cpu().numpy(), hit[order], ("d", "dmin"))
+    good = q4k.q4k_moe_down(x, w, rows, route).cpu().numpy()
+    check(good, q4k.q4k_moe_down(x, pack_dev(spoil(df)), rows, route).cpu().numpy(), hit, ("d", "dmin"))
+    f6, w6 = matrices(e, rows, cols, [4, 78], "q6_k")
+    t = to_dev(spoil(f6))
+    good = q4k.q4k_moe_down(x, w6, rows, route, q6k=True).cpu().numpy()
+    got = q4k.q4k_moe_down(x, q4k.q6k_pack(t["d"], t["sc"], t["q"]), rows, route, q6k=True).cpu().numpy()
+    check(good, got, hit, ("d",))
