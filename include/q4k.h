@@ -783,8 +783,9 @@ int q4k_moe_gate_up(const q4k_moe_plan* plan, const void* gate, const void* up, 
  * Accuracy: |y - exact| <= 1e-4 * (|residual| + sum_j |weight_j| (M_j +
  * 2^-16 max|h_j| W1)) with M_j and W1 as above.
  * In both calls offsets out of range or descending are cut, an order out of
- * range, or a place of offsets[experts] or more, is skipped (its row counts as
- * zeros), and each is reported by q4k_device_error (Q4K_ERR_DEVICE_INDEX).
+ * range, or a place below offsets[0] or of offsets[experts] or more, is skipped
+ * (its row counts as zeros), and each, and an offsets[0] that is not 0, is
+ * reported by q4k_device_error (Q4K_ERR_DEVICE_INDEX).
  * Values that are not finite make the rows they stand in not finite, and no
  * others.  Deterministic on one device.
  * Errors: Q4K_ERR_INVALID_ARG, Q4K_ERR_ALIGNMENT, Q4K_ERR_UNSUPPORTED (rows *

@@ -177,7 +177,7 @@ __device__ __forceinline__ int make_tiles(Tiles& T, const int32_t* offsets, int 
 #pragma unroll
   for (int j = 0; j < J; ++j) top = max(top, min(raw[j], pairs));             // beyond E: pairs, past every expert
   int last = scan_block<THREADS, true>(top, T.warps, all);
-  bool bad = false;
+  bool bad = e0 == 0 && raw[0] != 0;                                          // pairs before the first expert's
   int classes = 0, eighths = 0;                                               // three counts of ten bits
 #pragma unroll
   for (int j = 0; j <= J; ++j) {

@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kMoeMaxExperts) moe_many_layout_kernel(const L
   int all;
   const int before = scan_block<kMoeMaxExperts, true>(min(raw0, P.pairs), warps, all);
   const int first = max(max(before, 0), min(raw0, P.pairs)), last = max(first, min(raw1, P.pairs));
-  if (e < E && (first != raw0 || last != raw1)) atomicOr(P.err, kErrIndex);
+  if (e < E && (first != raw0 || last != raw1 || (e == 0 && raw0 != 0))) atomicOr(P.err, kErrIndex);   // (no pairs before the first expert's)
   const int n = e < E ? last - first : 0, tiles = (n + kCols - 1) / kCols;
   const int each = tiles ? ((n + tiles - 1) / tiles + 15) / 16 * 16 : 16;
   const int used = (n + each - 1) / each;                     // (rounding up can save one)

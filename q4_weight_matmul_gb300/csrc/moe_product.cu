@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const MoeProduct 
   const int64_t r = (at - t * per) * V;
   const int32_t* place = L.place + t * L.top_k;
   const float* weight = L.weight + t * L.top_k;
-  const int64_t pairs = min((int64_t)L.offsets[L.experts], L.tokens * L.top_k);        // rows of z that have been made
+  const int64_t made = L.offsets[0], pairs = min((int64_t)L.offsets[L.experts], L.tokens * L.top_k);   // rows of z from made to pairs - 1
   if (place[0] == -2) return;
   alignas(16) float y[V] = {};
   if (P.residual) *reinterpret_cast<F*>(y) = *reinterpret_cast<const F*>(P.residual + t * P.rows + r);
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(const MoeProduct 
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int p = j0 + j < L.top_k ? place[j0 + j] : -1;
-      const bool have = p >= 0 && p < pairs;
+      const bool have = p >= 0 && p >= made && p < pairs;
       if (!have && p != -1 && r == 0) atomicOr(P.err, kErrIndex);
       w[j] = have ? weight[j0 + j] : 0.0f;
       if (have) {

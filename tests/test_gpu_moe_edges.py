@@ -338,3 +338,35 @@ def test_scales_that_are_not_finite_spoil_their_rows(tokens):
     good = q4k.q4k_moe_down(x, w6, rows, route, q6k=True).cpu().numpy()
     got = q4k.q4k_moe_down(x, q4k.q6k_pack(t["d"], t["sc"], t["q"]), rows, route, q6k=True).cpu().numpy()
     check(good, got, hit, ("d",))
+
+
+@pytest.mark.parametrize("six", [False, True], ids=["q4_k", "q6_k"])
+@pytest.mark.parametrize("tokens", [5, 40, 300])
+def test_pairs_before_the_first_expert_are_reported(tokens, six):
+    """offsets[0] > 0: no expert has the positions before it, and what a
+    workspace holds there is not added up."""
+    e, k, cols, rows = 3, 2, 256, 40
+    f, w = matrices(e, rows, cols, 113, "q6_k" if six else "q4_k")
+    (gf, gate), (uf, up) = (matrices(e, rows, cols, [i, 113]) for i in (1, 2))
+    expert, weight = choose(tokens, e, k, "any", 114)
+    good, h = route_of(expert, weight, e), synth.activations(tokens * k, cols, 115)
+    work = q4k.q4k_moe_workspace(tokens, k, e, max(rows, cols), cols)
+    first = int(good.offsets[1]) - 1                                 # all but one of the first expert's pairs
+    for start in {1, max(1, first)}:
+        offsets = good.offsets.clone()
+        offsets[0] = start
+        bad = good._replace(offsets=offsets)
+        left = weight.copy()
+        left.reshape(-1)[good.order.cpu().numpy()[:start]] = 0
+        want, tol = moe.down(h, f, "q6_k" if six else "q4_k", rows, expert, left, e)
+        work.fill_(255)
+        got = q4k.q4k_moe_down(dev(h), w, rows, bad, q6k=six, workspace=work).cpu().numpy()
+        assert q4k.q4k_device_error() == 6
+        assert np.all(np.abs(got - want) <= tol)
+        x = 0.02 * synth.activations(tokens, cols, 116)
+        want, tol = moe.gate_up(x, gf, uf, rows, expert, e)
+        out = torch.full((tokens * k, rows), 7.5, device="cuda")
+        q4k.q4k_moe_gate_up(dev(x), gate, up, rows, bad, out=out)
+        assert q4k.q4k_device_error() == 6
+        assert torch.all(out[:start] == 7.5)
+        assert np.all(np.abs(out.cpu().numpy() - want)[start:] <= tol[start:])
