@@ -289,9 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_block144_kernel(
           gemv::superblock_dot_q8<B, CPL>(p, xs, xss, nb, sb, c0, acc, pout, (size_t)P.rows[0] * nb * 8);
         }
       }
-      // release the stage once every lane of the warp has read it
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty[slot]);
+      tc::warp_release(&empty[slot]);
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         if (LPR >= 2) acc[b] += __shfl_xor_sync(0xffffffffu, acc[b], 1);

@@ -284,8 +284,7 @@ __device__ __forceinline__ void consume_pass(const SeqParams& P, const uint8_t* 
         }
       }
     }
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&empty[slot]);
+    tc::warp_release(&empty[slot]);
 #pragma unroll
     for (int b = 0; b < B; ++b) part[((size_t)(s - ps) * kRB + lane) * B + b] = acc[b];
   }

@@ -58,15 +58,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64
   return warp_wait(bar, parity, gave_up, err) && warp_wait(bar2, parity2, gave_up, err);
 }
 
-// A warp is done with shared memory that `bar` guards: reads that it has made
-// must not be left for later.  (Without the fence of every lane the compiler
-// puts single loads off until after one lane's arrival, and they find what is
-// copied there next.)
-__device__ __forceinline__ void warp_release(uint64_t* bar) {
-  __threadfence_block();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
-}
+using tc::warp_release;
 
 // Exclusive sum of `v` over the block's threads before this one (`most`:
 // maximum in place of a sum); every thread gets the whole block's in `all`.

@@ -564,8 +564,7 @@ paged_attn_few_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_con
       const int slot = issued % C::kSlots;
       wait(&full[slot], (issued / C::kSlots) & 1);
       if (active) part.slot(it, ring + slot * L::kSlot, ring + slot * L::kSlot + L::kTile, u * kUnit, lane);
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty[slot]);
+      tc::warp_release(&empty[slot]);
     }
     // the groups' statistics and outputs meet: sum[group][row][D]
     part.end(stat_m + grp * ROWS, stat_l + grp * ROWS, sum + (size_t)grp * ROWS * D, lane);

@@ -29,6 +29,18 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
                ::"r"(smem_u32(bar)) : "memory");
 }
 
+// A warp is done with shared memory that `bar` guards: reads that it has made
+// must not be left for later.  (Without the fence of every lane single loads
+// were found to come after one lane's arrival, and so after the copy that it
+// lets in.)  What is read is in registers by then, so the copy that comes next,
+// through the async proxy too, needs no proxy fence: it overwrites nothing that
+// this warp wrote.
+__device__ __forceinline__ void warp_release(uint64_t* bar) {
+  __threadfence_block();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
 // One arrival that counts `count` times toward the phase's expected arrivals.
 __device__ __forceinline__ void mbar_arrive_cnt(uint64_t* bar, uint32_t count) {
   asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.shared::cta.b64 st, [%0], %1;\n\t}"

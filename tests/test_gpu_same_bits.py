@@ -1,0 +1,102 @@
+"""The kernels that stream through rings in shared memory, three hundred times
+on the same inputs: the same bits every time.  (A warp that gives a stage back
+before its last reads of it finds the next copy's bytes there, in one call of
+many.)"""
+import pytest
+import torch
+
+import q4_weight_matmul_gb300 as q4k
+
+pytestmark = pytest.mark.gpu
+CALLS = 300
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    q4k.build()
+    yield
+    assert q4k.q4k_device_error() == 0
+
+
+def rng(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def matrix(rows, cols, seed, six=False):
+    g = rng(seed)
+    i = lambda lo, hi, n, t=torch.uint8: torch.randint(lo, hi, (rows, n), generator=g, device="cuda", dtype=t)  # noqa: E731
+    d = (0.5 + torch.rand((rows, cols // 256), generator=g, device="cuda")).half().view(torch.int16)
+    if six:
+        return q4k.q6k_pack(d, i(-128, 128, cols // 16, torch.int8), i(0, 64, cols))
+    return q4k.q4k_pack(d, d, i(0, 64, cols // 32), i(0, 64, cols // 32), i(0, 16, cols))
+
+
+def floats(*shape, seed=1):
+    return torch.randn(shape, generator=rng(seed), device="cuda")
+
+
+def repeat(call):
+    """``call`` returns tensors; all of them hold the first call's bits in every later one."""
+    want = [t.clone() for t in call()]
+    assert all(bool(torch.isfinite(t.float()).all()) for t in want)
+    differ = [torch.stack([(a != b).any() for a, b in zip(call(), want)]).any() for _ in range(CALLS)]
+    assert int(torch.stack(differ).sum()) == 0
+
+
+@pytest.mark.parametrize("six", [False, True], ids=["q4_k", "q6_k"])
+@pytest.mark.parametrize("rows,cols,batch", [(9728, 2560, 1), (2560, 9728, 1), (1024, 2560, 3), (2560, 4096, 8), (4000, 4096, 4)])
+def test_decode_products(rows, cols, batch, six):
+    w, x, res = matrix(rows, cols, 10, six), floats(batch, cols), floats(batch, rows, seed=2)
+    q8 = q4k.q8_quantize(x)
+    fp, q = (q4k.q6k_gemv, q4k.q6k_gemv_q8) if six else (q4k.q4k_gemv, q4k.q4k_gemv_q8)
+    repeat(lambda: [fp(w, rows, cols, x, residual=res), q(w, rows, cols, *q8, residual=res)])
+
+
+@pytest.mark.parametrize("batch", [1, 2, 4])
+def test_several_matrices_at_once(batch):
+    rows, cols = [4096, 1024, 1000], 2560
+    ws, x = [matrix(r, cols, 20 + i) for i, r in enumerate(rows)], floats(batch, cols)
+    repeat(lambda: q4k.q4k_gemv_multi(ws, rows, cols, x))
+
+
+@pytest.mark.parametrize("mixed", [False, True], ids=["q4_k", "with q6_k"])
+@pytest.mark.parametrize("batch", [1, 4])
+def test_a_list_of_jobs(batch, mixed):
+    jobs, ys, x = [], [], {2560: floats(batch, 2560), 9728: floats(batch, 9728, seed=2)}
+    for i, (rows, cols) in enumerate([(4096, 2560), (1024, 2560), (1000, 2560), (9728, 2560), (2560, 9728), (33, 2560)]):
+        six = mixed and i % 2 == 1
+        ys.append(torch.empty((batch, rows), device="cuda"))
+        jobs.append({"w": matrix(rows, cols, 30 + i, six), "rows": rows, "cols": cols, "x": x[cols], "y": ys[-1],
+                     "wait": i in (3, 4), **({"format": 1} if six else {})})
+    seq = q4k.GemvSeq(jobs, batch)
+
+    def call():
+        for y in ys:
+            y.fill_(float("nan"))
+        seq()
+        return ys
+
+    repeat(call)
+
+
+@pytest.mark.parametrize("dim,dtype", [(128, torch.float16), (64, torch.float16), (128, torch.bfloat16), (64, torch.bfloat16)])
+@pytest.mark.parametrize("new,heads,kv_heads,kv,requests", [
+    (1, 32, 8, 4000, 7), (1, 8, 8, 1500, 40), (1, 32, 8, 60000, 1), (5, 28, 4, 3001, 8), (40, 16, 4, 2000, 3)])
+def test_attention(new, heads, kv_heads, kv, requests, dim, dtype):
+    page, pages = 16, -(-kv // 16)
+    cells = requests * pages, kv_heads, page, dim
+    k, v = floats(*cells, seed=40).to(dtype), floats(*cells, seed=41).to(dtype)
+    table = torch.randperm(requests * pages, generator=rng(42), device="cuda").int().view(requests, pages)
+    lengths = (kv - 37 * torch.arange(requests, device="cuda")).int()
+    cu = (new * torch.arange(requests + 1, device="cuda")).int()
+    q = floats(requests * new, heads, dim, seed=43).to(dtype)
+    work = {t: q4k.q4k_paged_attn_workspace(q, k, table, new, t) for t in (torch.float32, dtype)}
+    repeat(lambda: [q4k.q4k_paged_attn(q, k, v, table, cu, lengths, new, out_dtype=t, workspace=work[t]) for t in work])
+
+
+@pytest.mark.parametrize("rows,cols,tokens", [(9728, 2560, 512), (1000, 9728, 200), (2560, 4096, 77)])
+def test_prompt_products(rows, cols, tokens):
+    w, w6, x = matrix(rows, cols, 50), matrix(rows, cols, 51, True), floats(tokens, cols)
+    q8, q16, split = q4k.q8_quantize(x), q4k.q8_quantize_h16(x), q4k.x_split_f16(x)
+    repeat(lambda: [q4k.q4k_gemm(w, rows, cols, *q8), q4k.q4k_gemm_h16(w, rows, cols, *q16),
+                    q4k.q4k_gemm_f16(w, rows, cols, *split), q4k.q6k_gemm_f16(w6, rows, cols, *split)])
