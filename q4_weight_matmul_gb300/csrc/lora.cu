@@ -106,12 +106,13 @@ __device__ __forceinline__ int token_at(const LoraParams& P, int i) {
 
 constexpr float kLow = 2048.f;   // the second part of a binary16 operand is held times 2^11
 
-// The parts of a s[0] and b s[1] (s = 1: bfloat16).  CUT: the first part of a
-// value is cut off, not rounded, so that it is finite where the value is; of an
-// infinity it is all, and the others are zero (not its difference from itself).
+// The parts of a s[0] and b s[1] (s = 1: bfloat16).  CUT: in the row whose
+// cut_a or cut_b is set, the first part of a value is cut off, not rounded, so
+// that it is finite where the value is; of an infinity it is all, and the others
+// are zero (not its difference from itself).
 template <bool BF16, bool CUT>
 __device__ __forceinline__ void split_rows(const float (&a)[8], const float (&b)[8], const float (&s)[2],
-                                           uint32_t (&p)[BF16 ? 3 : 2][2][4]) {
+                                           uint32_t (&p)[BF16 ? 3 : 2][2][4], bool cut_a = false, bool cut_b = false) {
   auto pack = [](float v, float w, bool cut) {
     return cut ? __float_as_uint(v) >> 16 | (__float_as_uint(w) & 0xffff0000u) : pack2<BF16>(v, w);
   };
@@ -122,7 +123,7 @@ __device__ __forceinline__ void split_rows(const float (&a)[8], const float (&b)
 #pragma unroll
     for (int k = 0; k < (BF16 ? 3 : 2); ++k) {
       if (!BF16 && k == 1) x0 *= kLow, x1 *= kLow, y0 *= kLow, y1 *= kLow;
-      const uint32_t x = pack(x0, x1, CUT && k == 0), y = pack(y0, y1, CUT && k == 0);
+      const uint32_t x = pack(x0, x1, CUT && k == 0 && cut_a), y = pack(y0, y1, CUT && k == 0 && cut_b);
       const float2 fx = unpack2<BF16>(x), fy = unpack2<BF16>(y);
       x0 = rest(x0, fx.x), x1 = rest(x1, fx.y), y0 = rest(y0, fy.x), y1 = rest(y1, fy.y);
       p[k][i >> 1][2 * (i & 1)] = x;
@@ -142,12 +143,11 @@ __device__ __forceinline__ uint32_t split(const float (&a)[8], const float (&b)[
   float s[2] = {1.f, 1.f};
   back[0] = back[1] = 1.f;
   uint32_t apart = 0;
-  float top = 0.f;
+  float top[2] = {0.f, 0.f};
   if constexpr (BF16) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
+    for (int e = 0; e < 8; ++e) top[0] = fmaxf(top[0], fabsf(a[e])), top[1] = fmaxf(top[1], fabsf(b[e]));
   } else {
-    float top[2] = {0.f, 0.f};
     uint32_t low[2] = {0xffffffffu, 0xffffffffu};                           // twice the least magnitude but zero, less one
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -165,7 +165,9 @@ __device__ __forceinline__ uint32_t split(const float (&a)[8], const float (&b)[
     }
   }
   if constexpr (BF16) {
-    if (top > 0x1.fep127f) split_rows<true, true>(a, b, s, p);       // bfloat16's largest value
+    // past bfloat16's largest value; each row for itself: a row without a token holds anything
+    const bool cut_a = top[0] > 0x1.fep127f, cut_b = top[1] > 0x1.fep127f;
+    if (cut_a || cut_b) split_rows<true, true>(a, b, s, p, cut_a, cut_b);
     else split_rows<true, false>(a, b, s, p);
     __syncwarp();                                                    // the products are the whole warp's
   } else {

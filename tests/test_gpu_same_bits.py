@@ -100,3 +100,33 @@ def test_prompt_products(rows, cols, tokens):
     q8, q16, split = q4k.q8_quantize(x), q4k.q8_quantize_h16(x), q4k.x_split_f16(x)
     repeat(lambda: [q4k.q4k_gemm(w, rows, cols, *q8), q4k.q4k_gemm_h16(w, rows, cols, *q16),
                     q4k.q4k_gemm_f16(w, rows, cols, *split), q4k.q6k_gemm_f16(w6, rows, cols, *split)])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens,cols,rows,rank", [(3, 2560, 1000, 16), (700, 2560, 1024, 64), (1500, 4096, 999, 32)])
+def test_adapters(tokens, cols, rows, rank, dtype):
+    x, base = floats(tokens, cols), [floats(tokens, rows, seed=2)]
+    a, b = [floats(3, rank, cols, seed=60).to(dtype)], [floats(3, rows, rank, seed=61).to(dtype)]
+    segments = q4k.q4k_lora_segments([t * 7 % 4 - 1 for t in range(tokens)])
+    scale, work = torch.full((3,), 0.5, device="cuda"), q4k.q4k_lora_workspace(tokens, rank, 1)
+    repeat(lambda: q4k.q4k_lora_add(x, a, b, base, *segments, scale, workspace=work))
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("tokens,rank", [(37, 16), (700, 64), (1500, 32)])
+def test_what_other_tokens_left_behind_changes_no_bits(tokens, rank, dtype):
+    """Tiles with fewer than 16 tokens hold, in shared memory, rows that no
+    token has: a call before with activations near and beyond fp32's largest
+    leaves such values there."""
+    cols, rows = 2560, 1024
+    x, base = floats(tokens, cols), [floats(tokens, rows, seed=2)]
+    a, b = [floats(3, rank, cols, seed=60).to(dtype)], [floats(3, rows, rank, seed=61).to(dtype)]
+    segments = q4k.q4k_lora_segments([t * 7 % 4 - 1 for t in range(tokens)])
+    whole = q4k.q4k_lora_segments([0] * (tokens // 16 * 16))
+    scale, work = torch.full((3,), 0.5, device="cuda"), q4k.q4k_lora_workspace(tokens, rank, 1)
+    want = q4k.q4k_lora_add(x, a, b, base, *segments, scale, workspace=work)[0].clone()
+    for left in (3.4e38, float("inf"), float("nan"), 1e-30, 0.0):
+        full = torch.full_like(x[:whole[0].numel()], left)
+        for _ in range(3):
+            q4k.q4k_lora_add(full, a, b, [base[0][:full.shape[0]]], *whole, scale, workspace=work)
+            assert torch.equal(q4k.q4k_lora_add(x, a, b, base, *segments, scale, workspace=work)[0], want), left
