@@ -819,6 +819,20 @@ int q4k_device_error(void* stream);
  */
 int q4k_selftest_wait_timeout(void* stream);
 
+/*
+ * q4k_selftest_warp_waits - test export: the waits of whole warps that the
+ * routed experts' kernels make, by one warp, each with a limit of some 32 ms.
+ *   out : int32 [8][32] on the device; out[i][lane] is what a lane got (1: it
+ *         may go on) from wait i: 0 a barrier that nothing completes, 1 the
+ *         same where another warp has given up, 2 two barriers of which the
+ *         second is never completed, 3 two completed ones, 4 a stage that is
+ *         never issued, 5 one that has been, 6 a vote that lane 7 is against;
+ *         out[7][i]: the error word (bit 0) and the block's give-up flag (bit
+ *         8) after wait i; out[7][8 + i]: what it took, in 65536 cycles
+ * A following q4k_device_error() returns Q4K_ERR_DEVICE_TIMEOUT (wait 0).
+ */
+int q4k_selftest_warp_waits(int32_t* out, void* stream);
+
 /* Static, human-readable name of a status code. */
 const char* q4k_status_string(int status);
 

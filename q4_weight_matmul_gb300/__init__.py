@@ -104,6 +104,7 @@ SIGNATURES = {
     "q4k_moe_down": (_I, [_P, _P, _I, _I64, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "q4k_device_error": (_I, [_P]),
     "q4k_selftest_wait_timeout": (_I, [_P]),
+    "q4k_selftest_warp_waits": (_I, [_P, _P]),
     "q4k_status_string": (ctypes.c_char_p, [_I]),
     "q4k_last_error_string": (ctypes.c_char_p, []),
     "q4k_version": (ctypes.c_char_p, []),
@@ -862,6 +863,13 @@ def q4k_selftest_wait_timeout(stream=None) -> None:
     _check(lib().q4k_selftest_wait_timeout(_stream(stream)), "q4k_selftest_wait_timeout")
 
 
+def q4k_selftest_warp_waits(stream=None) -> torch.Tensor:
+    """Make the waits of whole warps run out (test of the failure path); int32 [8][32], as the C ABI describes it."""
+    out = _made_on(stream, lambda: torch.empty((8, 32), dtype=torch.int32, device="cuda"))
+    _check(lib().q4k_selftest_warp_waits(_ptr(out, torch.int32, "out"), _stream(stream)), "q4k_selftest_warp_waits")
+    return out
+
+
 def q4k_version() -> str:
     return lib().q4k_version().decode()
 
@@ -875,5 +883,5 @@ __all__ = ["build", "lib", "Q4KError", "BLOCK144", "LAYOUT_GPU", "q4k_packed_byt
            "q4k_paged_attn", "q4k_lora_segments", "q4k_lora_workspace_bytes", "q4k_lora_workspace", "q4k_lora_add",
            "MoePlan", "MoeRoute", "q4k_moe_route_out", "q4k_moe_workspace_bytes", "q4k_moe_workspace", "q4k_moe_route",
            "q4k_moe_gate_up", "q4k_moe_down",
-           "q4k_selftest_wait_timeout", "q4k_version",
+           "q4k_selftest_wait_timeout", "q4k_selftest_warp_waits", "q4k_version",
            "SIGNATURES"]

@@ -903,6 +903,15 @@ int q4k_selftest_wait_timeout(void* stream) {
   return e == cudaSuccess ? Q4K_OK : record_cuda(e);
 }
 
+int q4k_selftest_warp_waits(int32_t* out, void* stream) {
+  if (!out) return Q4K_ERR_INVALID_ARG;
+  if (!aligned16(out)) return Q4K_ERR_ALIGNMENT;
+  int* err = device_error_word();
+  if (!err) return record_cuda(cudaGetLastError());
+  cudaError_t e = launch_warp_waits_selftest(out, err, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? Q4K_OK : record_cuda(e);
+}
+
 int q4k_device_error(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return record_cuda(e);

@@ -43,19 +43,21 @@ __device__ __forceinline__ bool agreed(bool ok, volatile int* gave_up, int* err)
 }
 // (Short: the code of a warp's loop is fetched anew for every turn where the
 // warps of a block do different things.)
+template <long long kTimeoutCycles = tc::kTimeoutCycles>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up, int* err) {
   if (__all_sync(~0u, tc::mbar_try_wait(bar, parity))) return true;
   const uint32_t t0 = (uint32_t)(clock64() >> 16);
   while (!__all_sync(~0u, tc::mbar_try_wait(bar, parity)))
-    if (!agreed(!*gave_up && (uint32_t)(clock64() >> 16) - t0 < (uint32_t)(tc::kTimeoutCycles >> 16), gave_up, err)) return false;
+    if (!agreed(!*gave_up && (uint32_t)(clock64() >> 16) - t0 < (uint32_t)(kTimeoutCycles >> 16), gave_up, err)) return false;
   return true;
 }
 
 // Two barriers, asked together at first.
+template <long long kTimeoutCycles = tc::kTimeoutCycles>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
                                           volatile int* gave_up, int* err) {
   if (__all_sync(~0u, tc::mbar_try_wait(bar, parity) & tc::mbar_try_wait(bar2, parity2))) return true;
-  return warp_wait(bar, parity, gave_up, err) && warp_wait(bar2, parity2, gave_up, err);
+  return warp_wait<kTimeoutCycles>(bar, parity, gave_up, err) && warp_wait<kTimeoutCycles>(bar2, parity2, gave_up, err);
 }
 
 using tc::warp_release;

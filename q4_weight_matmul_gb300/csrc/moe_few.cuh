@@ -123,6 +123,7 @@ struct SplitParams {
 };
 
 // Until stage n has been issued.
+template <long long kTimeoutCycles = tc::kTimeoutCycles>
 __device__ __forceinline__ bool warp_wait_issued(const uint32_t* issued, uint32_t n, volatile int* gave_up, int* err) {
   bool ok = true;
   const long long t0 = clock64();
@@ -130,7 +131,7 @@ __device__ __forceinline__ bool warp_wait_issued(const uint32_t* issued, uint32_
     uint32_t v;
     asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(tc::smem_u32(issued)) : "memory");
     if ((int32_t)(v - n) > 0) break;
-    if (*gave_up || clock64() - t0 > tc::kTimeoutCycles) {
+    if (*gave_up || clock64() - t0 > kTimeoutCycles) {
       ok = false;
       break;
     }

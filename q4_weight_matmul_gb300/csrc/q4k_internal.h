@@ -237,5 +237,7 @@ cudaError_t launch_moe_many_down_q6(const MoeProduct& p, void* work, float* out,
 // One-thread kernel whose only (bounded) wait can never complete: after the
 // library's wait limit it records a timeout in `err` and returns.
 cudaError_t launch_wait_timeout_selftest(int* err, cudaStream_t s);
+// The waits of whole warps, made to run out after a short limit; out: 8 x 32.
+cudaError_t launch_warp_waits_selftest(int32_t* out, int* err, cudaStream_t s);
 
 }  // namespace q4k
