@@ -130,3 +130,66 @@ def test_what_other_tokens_left_behind_changes_no_bits(tokens, rank, dtype):
         for _ in range(3):
             q4k.q4k_lora_add(full, a, b, [base[0][:full.shape[0]]], *whole, scale, workspace=work)
             assert torch.equal(q4k.q4k_lora_add(x, a, b, base, *segments, scale, workspace=work)[0], want), left
+
+
+def calls(value):
+    """One call of every kind, on random inputs, or on activations (and keys and values) of ``value``."""
+    def x(*shape, seed=1):
+        return floats(*shape, seed=seed) if value is None else torch.full(shape, value, device="cuda")
+
+    rows, cols = 1000, 2560
+    w, w6, made = matrix(rows, cols, 70), matrix(rows, cols, 71, True), {}
+    for batch in (1, 4, 8):
+        made[f"gemv {batch}"] = lambda b=batch: [q4k.q4k_gemv(w, rows, cols, x(b, cols)), q4k.q6k_gemv(w6, rows, cols, x(b, cols))]
+    for tokens in (1, 7, 33, 200):
+        q8 = q4k.q8_quantize(floats(tokens, cols) if value is None else torch.zeros((tokens, cols), device="cuda"))
+        made[f"q8 {tokens}"] = lambda q8=q8: [q4k.q4k_gemm(w, rows, cols, *q8), q4k.q6k_gemm(w6, rows, cols, *q8)]
+        made[f"f16 {tokens}"] = lambda t=tokens: [g(m, rows, cols, *q4k.x_split_f16(x(t, cols)))
+                                                  for g, m in ((q4k.q4k_gemm_f16, w), (q4k.q6k_gemm_f16, w6))]
+    jobs, ys = [], []
+    for i in range(5):
+        ys.append(torch.empty((2, rows), device="cuda"))
+        jobs.append({"w": w6 if i == 2 else w, "rows": rows, "cols": cols, "x": x(2, cols), "y": ys[-1], "wait": i == 3,
+                     **({"format": 1} if i == 2 else {})})
+    seq = q4k.GemvSeq(jobs, 2)
+    made["jobs"] = lambda keep=jobs: (seq(), [y.clone() for y in ys])[1]
+    for dim in (64, 128):
+        for dtype in (torch.float16, torch.bfloat16):
+            fits = (lambda t, d=dtype: t.clamp(-6e4, 6e4).to(d)) if dtype == torch.float16 else (lambda t, d=dtype: t.to(d))
+            for new in (1, 2, 5, 11, 19, 150):
+                cells, kv = (40, 2, 16, dim), [300, 270]
+                k, v, q = fits(x(*cells)), fits(x(*cells, seed=2)), fits(x(2 * new, 12, dim, seed=3))
+                table = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20)
+                cu, n = torch.tensor([0, new, 2 * new], dtype=torch.int32, device="cuda"), torch.tensor(kv, dtype=torch.int32, device="cuda")
+                made[f"attention {dim} {dtype} {new}"] = lambda a=(q, k, v, table, cu, n, new), t=dtype: [
+                    q4k.q4k_paged_attn(*a, out_dtype=o) for o in (torch.float32, t)]
+            for tokens, rank in ((3, 16), (37, 16), (150, 40)):
+                a, b = [floats(2, rank, cols, seed=60).to(dtype)], [floats(2, rows, rank, seed=61).to(dtype)]
+                base, scale = [floats(tokens, rows, seed=2)], torch.full((2,), 0.5, device="cuda")
+                segments = q4k.q4k_lora_segments([t * 7 % 3 - 1 for t in range(tokens)] if value is None else [0] * tokens)
+                made[f"adapters {dtype} {tokens}"] = lambda a=(x(tokens, cols), a, b, base, *segments, scale): q4k.q4k_lora_add(*a)
+    experts, width = 6, 256
+    g, u, d = (matrix(experts * r, c, 80 + i) for i, (r, c) in enumerate(((width, cols), (width, cols), (rows, width))))
+    d6 = matrix(experts * rows, width, 84, True)
+    for tokens in (1, 11, 25, 50, 300):
+        route = q4k.q4k_moe_route(floats(tokens, experts, seed=4), 2)
+        made[f"experts {tokens}"] = lambda t=tokens, r=route: (lambda h: [h] + [
+            q4k.q4k_moe_down(h, m, rows, r, q6k=six) for m, six in ((d, False), (d6, True))])(
+                q4k.q4k_moe_gate_up(1e-4 * x(t, cols), g, u, width, r))
+    return made
+
+
+@pytest.mark.parametrize("value", [3.4e38, float("inf"), float("nan")])
+def test_what_other_calls_left_in_shared_memory_changes_no_bits(value):
+    good, bad = calls(None), calls(value)
+    want = {n: [t.clone() for t in c()] for n, c in good.items()}
+    for n, w in want.items():
+        assert all(bool(torch.isfinite(t.float()).all()) for t in w), n
+    differ = []
+    for before in bad:
+        for n, c in good.items():
+            bad[before]()
+            if not all(torch.equal(a, b) for a, b in zip(c(), want[n])):
+                differ.append((before, n))
+    q4k.q4k_device_error()
+    assert not differ
