@@ -716,7 +716,7 @@ typedef struct q4k_moe_plan {
                                  ascending in a group; -1 behind the last      */
   int32_t* offsets;           /* [experts + 1]: expert e's pairs are order[
                                  offsets[e]] .. order[offsets[e + 1] - 1]      */
-  int64_t tokens;
+  int64_t tokens;             /* 0..2^22                                       */
   int32_t top_k;              /* 1..32, at most experts                        */
   int32_t experts;            /* 1..512                                        */
 } q4k_moe_plan;

@@ -63,8 +63,8 @@ class Pages:
 
 class Workspaces:
     """Scratch memory for the calls of one stream, or of one captured graph:
-    one tensor for the attention and one for the adapters, as large as the
-    largest step so far.  Steps that share it must not overlap on the GPU, so
+    one tensor for the attention, one for the adapters and one for the routed
+    experts, each as large as the largest step so far.  Steps that share it must not overlap on the GPU, so
     one object serves all layers of a model that runs on one stream."""
 
     def __init__(self):

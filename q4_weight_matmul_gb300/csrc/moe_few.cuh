@@ -36,10 +36,14 @@
 //
 // Measured: one token, 8 of 128 experts of 2048 x 768, gate and up 9.7 us, down
 // Q6_K 10.6; 64 tokens 68 us (3.3 TB/s), down 46; 12 tokens, 2 of 8 experts of
-// 4096 x 12288, 97 us (4.7 TB/s).  Bound: the unpacking of the quants (shifts,
-// masks and permutes, two thirds of what a consumer does and at half the other
-// instructions' rate) beside the stream of the weights, which alone takes 70 us
-// of the 97; and latency for one token.
+// 4096 x 12288, 97 us (4.7 TB/s), of which the stream of the weights alone takes
+// 70.  Nothing in it is full: with 64 tokens (2048 columns) instructions issue in
+// 48 % of the cycles, the pipe of shifts and masks works in 38 % (down Q6_K 47),
+// the tensor pipe in 25 %, shared memory in 32 %, and HBM gives half its rate.
+// Bound: latency and hand-over.  The largest share of the warps' time is waits
+// for memory and barriers (3.4 of some 7 warps a scheduler has); an item of 2048
+// columns is eight stages for three warps, and ends with a chain of three
+// hand-overs of sums.  One token: the latency of two launches.
 //
 // Waits are bounded; a warp agrees on a wait's outcome by a vote, and who
 // copies waits for its copies before it leaves.

@@ -2,11 +2,14 @@
 // tensor cores (tcgen05): 128 or 256 weight rows times up to 112 pairs of one
 // expert, fp32 sums of exact 16-bit products as in moe_few.cuh.
 //
-// Measured: 4096 tokens, 4 of 32 experts of 2560 x 1536: gate and up 410 us
-// (2 x 258 GFLOP with both parts: 1.26 PFLOP/s), down 301 us; 513 tokens, 6 of
-// 60 experts of 2560 x 1280: 132 us, down Q6_K 110 us.  Bound: the making of a
-// step's A and the issue of its products, see below; 45 us of the 410 are the
-// split's, which moves 168 MB.
+// Measured: 4096 tokens, 4 of 32 experts of 2560 x 1536: gate and up 408 us
+// (2 x 258 GFLOP with both parts: 1.26 PFLOP/s; 434 us after a quarter of a
+// second, when the power limit has taken the clock from 2070 to some 1850 MHz),
+// down 299 us; 513 tokens, 6 of 60 experts of 2560 x 1280: 131 us, down Q6_K
+// 110 us.  Bound: the making of a step's A and the issue of its products, see
+// below.  The launches alone (they overlap by some us): gate and up of 4096
+// tokens layout 4, split 46 (it moves 168 MB), products 373; down layout 4,
+// split 36, products 213, putting together 45.
 //
 // Four launches.  (1) One CTA lays the pairs out in tiles: an expert's n pairs
 // become ceil(n / 112) tiles (or ceil(n / 32): see kMoeSmallTiles) of equal
@@ -40,7 +43,8 @@
 // some 400 cycles, which the other's products cover), then two groups of four
 // convert (with one, 700 cycles a tile held the products up, 547 us for 4096
 // tokens; four for tiles of 32 pairs), and eight run the epilogue (totals in
-// registers).  Every wait is bounded, and its loop short and inline: with ten
+// registers).  With 128 pairs an expert the tensor pipe works in half of the
+// cycles and instructions issue in 53 %; with 16 (tiles of 32) 21 % and 65 %.  Every wait is bounded, and its loop short and inline: with ten
 // instructions more in each, the roles' loops did not fit the instruction
 // caches together (459 us).
 #pragma once
@@ -97,10 +101,16 @@ struct Cfg {
   static constexpr int kTilesM = kQ6 ? 1 : 2;                // of 128 rows each
   static constexpr int kOutRows = MODE == kDownQ4 ? 2 * kRows : kRows;
   // The tensor core drops what is below its sum's last place at every product,
-  // towards zero, so a superblock's sum comes out too small: measured, by 10
-  // (tiles of 32 pairs: 5.5) times 2^-24 of itself on average, for rows of any
-  // length and both formats.  Its scale puts the mean back: the relative error
-  // of h 1.26e-6 -> 5.2e-7 (6.2e-7 -> 3.6e-7).
+  // towards zero, so a superblock's sum comes out too small: by half a place a
+  // product in the mean.  A sum of n products that grows steadily has lost some
+  // 0.3 n 2^-24 of itself at its end: with n = 34 (tiles of 32 pairs: 18) 10
+  // (5.5), and so it was measured for normal activations, rows of any length
+  // and both formats.  Its scale puts that mean back: the relative error of h
+  // 1.26e-6 -> 5.2e-7 (6.2e-7 -> 3.6e-7), of down 2.5e-7 and 7.3e-7 -> 1.4e-7
+  // and 4e-7.  It is a mean: sums that lose less come out too large, by 6e-7 of
+  // themselves at most, where all but one term is zero (rows with one value in
+  // 32: down 2.7e-7 -> 4.0e-7; positive values: Q4_K 0.5e-7 -> 5.9e-7, Q6_K
+  // 1.1e-6 -> 4.9e-7).
   static constexpr float kBack = 1.0f + (kBeside ? 6 : 10) * 5.9604644775390625e-8f;
   // registers of the three kinds of warps; at launch 768 x 80 and 640 x 96
   static constexpr int kFewRegs = 32, kConvRegs = kBeside ? 72 : 64, kEpiRegs = 160;

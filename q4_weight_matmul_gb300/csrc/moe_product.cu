@@ -64,8 +64,9 @@ cudaError_t combine(const MoeProduct& p, const float* z, cudaStream_t s) {
 
 // Many pairs an expert go to the tensor cores' tiles of up to 112 pairs, few
 // to the kernel that streams the weights once per 16 pairs: its time grows with
-// the pairs, that of a tile hardly does until it is full.  Measured (us; gate
-// and up, down Q4_K, down Q6_K), few | many:
+// the pairs, that of a tile hardly does until it is full.  One rule for the
+// three products; down Q6_K alone would take the other side from some 6 pairs
+// on (up to 11 %).  Measured (us; gate and up, down Q4_K, down Q6_K), few | many:
 //   pairs an expert   128 experts, 2048 x 768              32 experts, 2560 x 1536
 //         6           82 / 55 / 82   | 86 / 55 / 74        50 / 35 / 52 | 67 / 39 / 51
 //        10          104 / 69 / 98   | 96 / 58 / 78        66 / 44 / 63 | 68 / 49 / 59

@@ -32,7 +32,8 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // A warp is done with shared memory that `bar` guards: reads that it has made
 // must not be left for later.  (Without the fence of every lane single loads
 // were found to come after one lane's arrival, and so after the copy that it
-// lets in.)  What is read is in registers by then, so the copy that comes next,
+// lets in.  Not needed where every thread arrives for its own reads, or where
+// what was read has gone into tensor memory before a wait for that.)  What is read is in registers by then, so the copy that comes next,
 // through the async proxy too, needs no proxy fence: it overwrites nothing that
 // this warp wrote.
 __device__ __forceinline__ void warp_release(uint64_t* bar) {

@@ -14,7 +14,9 @@ from q4_weight_matmul_gb300.attention_block import Workspaces
 
 
 class ExpertBlock:
-    """``router`` [experts][hidden] float32; ``gate``, ``up``: the experts'
+    """``router`` [experts][hidden] float32 (its logits are torch's product, in
+    TF32 where the process lets torch's matmuls use it: tokens whose experts'
+    logits lie close together may then go to others); ``gate``, ``up``: the experts'
     packed Q4_K matrices, [experts][width] rows of ``hidden`` weights;
     ``down``: [experts][hidden] rows of ``width``, packed Q4_K or (``q6k``)
     Q6_K in the GPU layout."""
