@@ -193,3 +193,23 @@ def test_what_other_calls_left_in_shared_memory_changes_no_bits(value):
                 differ.append((before, n))
     q4k.q4k_device_error()
     assert not differ
+
+
+def test_two_streams_at_once():
+    """Calls of every kind beside every other on another stream: they share the
+    SMs, their shared memory and tensor memory, and nothing else."""
+    good = calls(None)
+    want = {n: [t.clone() for t in c()] for n, c in good.items()}
+    names, streams = list(good), [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    differ = []
+    for i, first in enumerate(names):
+        got = []
+        for second in names[i + 1::7]:                       # (one pair in seven)
+            for stream, n in zip(streams, (first, second)):
+                with torch.cuda.stream(stream):
+                    got += [(n, a, b) for _ in range(4) for a, b in zip(good[n](), want[n])]
+        torch.cuda.synchronize()
+        differ += [(first, n) for n, a, b in got if not torch.equal(a, b)]
+    assert q4k.q4k_device_error() == 0
+    assert not differ
